@@ -507,6 +507,229 @@ int zero_copy_spans(const zero_copy_span *spans, uint64_t n_spans, const void *c
                     hipStream_t stream);
 
 /* ----------------------------------------------------------------------------
+ * The owner step with 8-bit moments.
+ *
+ * Both Adam moments of an owner are held in 8 bits: ZERO_QBLOCK consecutive
+ * flat elements (an aligned block) share one fp32 scale per moment,
+ *   exp_avg           ~ exp_avg_scale * exp_avg8,
+ *   sqrt(exp_avg_sq)  ~ exp_rms_scale * exp_rms8,
+ * the codes in e4m3 (OCP, as torch.float8_e4m3fn), the scale = (the block's
+ * largest magnitude) / 448.  A root above zero never rounds to zero.  That is
+ * 2.0625 bytes of moments per parameter instead of 8.
+ *
+ * Owner-local arrays of these calls start at local_base, a multiple of
+ * ZERO_QBLOCK: codes hold (end - local_base) rounded up to a whole number of
+ * blocks, scales one value per block.  (The fp32 arrays hold end - local_base
+ * elements as elsewhere.)
+ * -------------------------------------------------------------------------- */
+#define ZERO_QBLOCK 128u  /* elements that share a scale */
+#define ZERO_PIECE 2048u  /* most elements of one piece */
+#define ZERO_PIECE_WHOLE 0xFFFFFFFFu
+
+/* One piece of an owner's work: the flat window [flat, flat + len), cut at flat
+ * multiples of ZERO_PIECE; flat is a multiple of ZERO_QBLOCK.  mask is
+ * ZERO_PIECE_WHOLE when every element is real (len is then a multiple of 8),
+ * else the index of the piece's ZERO_PIECE / 8 mask bytes: bit k of byte t is
+ * set when element flat + 8 t + k is real. */
+typedef struct {
+  uint64_t flat;
+  uint32_t len;
+  uint32_t mask;
+} zero_piece;
+
+/* ----------------------------------------------------------------------------
+ * zero_piece_table -- the owner's real elements as pieces (host only).
+ *
+ * The windows of ZERO_PIECE flat elements that hold a real element of [begin,
+ * end), in increasing order; the first starts at begin rounded down to a
+ * multiple of ZERO_QBLOCK.  Real elements are as for zero_chunk_table.
+ * numel, tensor_offset [n_tensors]  in : as from zero_shard_layout
+ * out[capacity], masks[mask_capacity * ZERO_PIECE / 8]  out; with out and masks
+ *                      NULL and both capacities 0 only the counts are computed
+ * n_pieces, n_masks    out: entries needed, also on ERANGE
+ * Errors: EINVAL (as zero_chunk_table); ERANGE when a capacity is short.
+ * -------------------------------------------------------------------------- */
+int zero_piece_table(const uint64_t *numel, const uint64_t *tensor_offset, uint32_t n_tensors, uint64_t begin,
+                     uint64_t end, zero_piece *out, uint64_t capacity, uint8_t *masks, uint64_t mask_capacity,
+                     uint64_t *n_pieces, uint64_t *n_masks);
+
+/* Arguments of zero_adam8_step; as zero_adam_args except for the piece table
+ * and the state.  Every base is <= begin; local_base is a multiple of
+ * ZERO_QBLOCK, grad_base and param_base of 8. */
+typedef struct {
+  const zero_piece *pieces; /* device table; elements outside [begin, end) are ignored */
+  uint64_t n_pieces;
+  const uint8_t *masks; /* device, n_masks * ZERO_PIECE / 8 bytes */
+  uint64_t n_masks;
+  uint64_t begin, end;
+  const void *const *rank_grads; /* R rank buffers, or ... */
+  uint32_t R;
+  int32_t grad_dtype;
+  uint64_t grad_base;
+  float divisor;
+  const float *reduced_g; /* ... an owner-local fp32 gradient (R and rank_grads are then not looked at) */
+  float *master;
+  uint8_t *exp_avg8, *exp_rms8;
+  float *exp_avg_scale, *exp_rms_scale;
+  uint64_t local_base;
+  void *param16; /* 16-bit compute copy, or ZERO_NONE */
+  int32_t param_dtype;
+  uint64_t param_base;
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t adamw;
+  uint64_t step;
+  double clip_coef;
+} zero_adam8_args;
+
+/* ----------------------------------------------------------------------------
+ * zero_adam8_step -- fused reduce + Adam/AdamW + 16-bit write-back on 8-bit moments.
+ *
+ * For every real element f, with m0 and r0 the decoded moments:
+ *   g = reduced gradient (bit-identical to zero_reduce_owned) * clip_coef
+ *   (adamw == 0 and weight_decay != 0: g += weight_decay * w)
+ *   m = beta1 m0 + (1 - beta1) g
+ *   r = sqrt(beta2 r0^2 + (1 - beta2) g^2)
+ *   w = w (1 - lr wd [adamw only]) - lr (m / (1 - beta1^t)) / (r / sqrt(1 - beta2^t) + eps)
+ *   param16[f] = round-to-nearest-even 16-bit copy of w
+ * and m, r go back into 8 bits block by block (e4m3 rounds to nearest even;
+ * a block's maxima are taken over the owner's real elements of it).  w uses m
+ * and r before that rounding.  Arithmetic is fp32.  The results do not depend
+ * on the launch, but a block that the owner's begin or end cuts scales by the
+ * owner's part alone.  A block whose largest magnitude is below 2^-100 holds
+ * zeros.  A non-finite gradient makes its whole block's moments NaN.
+ * Errors: EINVAL as for zero_adam_step, and for a missing state array or a
+ * local_base that is no multiple of ZERO_QBLOCK; EHIP.
+ * n_pieces == 0 or begin == end is a no-op.
+ * -------------------------------------------------------------------------- */
+int zero_adam8_step(const zero_adam8_args *args, hipStream_t stream);
+
+/* ----------------------------------------------------------------------------
+ * zero_moments8_pack / zero_moments8_unpack -- fp32 moments into the 8-bit form
+ * (a 32-bit checkpoint continues in 8 bits) and back (an 8-bit owner's moments
+ * leave through zero_owner_to_dense).  exp_avg, exp_avg_sq: device fp32,
+ * end - local_base elements.  Unpack writes scale * code and its square; a
+ * negative exp_avg_sq packs as NaN.  Only the owner's real elements are read
+ * and written.
+ * Errors: EINVAL (NULL or misaligned arrays, bad bases); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_moments8_pack(const zero_piece *pieces, uint64_t n_pieces, const uint8_t *masks, uint64_t n_masks,
+                       uint64_t begin, uint64_t end, uint64_t local_base, const float *exp_avg,
+                       const float *exp_avg_sq, uint8_t *exp_avg8, float *exp_avg_scale, uint8_t *exp_rms8,
+                       float *exp_rms_scale, hipStream_t stream);
+int zero_moments8_unpack(const zero_piece *pieces, uint64_t n_pieces, const uint8_t *masks, uint64_t n_masks,
+                         uint64_t begin, uint64_t end, uint64_t local_base, const uint8_t *exp_avg8,
+                         const float *exp_avg_scale, const uint8_t *exp_rms8, const float *exp_rms_scale,
+                         float *exp_avg, float *exp_avg_sq, hipStream_t stream);
+
+/* ----------------------------------------------------------------------------
+ * Losses on token log-probabilities.
+ *
+ * logits[n_rows] of `vocab` elements each (F16, BF16 or F32), row r from element
+ * r * row_stride; rows need no alignment beyond their elements'.  Row r's target
+ * is targets[r]; a target outside [0, vocab) (say -100) marks a row that counts
+ * for nothing: log-probability 0, no loss, zero gradient, its logits unread.  So
+ * does a row whose logits are all -inf.  -inf logits (masked tokens) have
+ * probability 0; NaN or +inf logits in a row that counts give NaN.
+ *   lp = logits[target] / temperature - ln sum_j exp(logits[j] / temperature)
+ * Elements are fp32; a row's sum, its logarithm and everything per row fp64;
+ * sums over rows in a fixed order, so results are identical run to run.
+ * -------------------------------------------------------------------------- */
+
+/* ----------------------------------------------------------------------------
+ * zero_token_logprobs -- logp[r] = lp of row r (fp32): what a reference model and
+ * the sampling policy hand to the losses below.
+ * n_rows == 0 is a no-op.
+ * Errors: EINVAL (bad dtype, vocab 0, row_stride < vocab, temperature not finite
+ * and > 0, NULL or misaligned arrays); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_token_logprobs(const void *logits, int dtype, uint64_t n_rows, uint32_t vocab, uint64_t row_stride,
+                        const int64_t *targets, double temperature, float *logp, hipStream_t stream);
+
+/* Arguments of zero_policy_loss.  Per-row arrays hold n_rows fp32 values. */
+typedef struct {
+  const void *logits;
+  int32_t dtype;
+  uint64_t n_rows;
+  uint32_t vocab;
+  uint64_t row_stride;
+  const int64_t *targets;
+  const float *old_logp;  /* the sampling policy's log-probabilities */
+  const float *ref_logp;  /* the reference model's; may be NULL when kl_coef is 0 */
+  const float *advantage;
+  const float *weight;    /* NULL: 1 for every row */
+  double divisor;         /* > 0 */
+  double clip_low, clip_high; /* the ratio is held in [1 - clip_low, 1 + clip_high] */
+  double kl_coef;
+  double temperature;
+  double grad_scale;      /* multiplies dlogits only (a loss scale) */
+  float *stats;           /* [4]: loss, policy part, KL part (without kl_coef), clipped share */
+  float *logp;            /* [n_rows] */
+  void *dlogits;          /* same dtype as logits; may be logits itself; NULL: no gradient */
+  uint64_t dlogits_stride;
+  void *workspace;        /* zero_policy_workspace_bytes(n_rows), 256-byte aligned */
+  size_t workspace_bytes;
+} zero_policy_args;
+
+/* ----------------------------------------------------------------------------
+ * zero_policy_loss -- clipped policy loss with a KL term, and its gradient of the
+ * logits, in one pass over them.
+ *   rho = exp(lp - old_logp),  d = ref_logp - lp
+ *   l   = -min(A rho, A clip(rho, 1 - clip_low, 1 + clip_high)) + kl_coef (exp(d) - d - 1)
+ *   loss = sum_r weight_r l_r / divisor
+ *   dlogits = grad_scale * d loss / d logits
+ * (the gradient of a clipped row's first term is 0; at the border the row is not
+ * clipped).  Rows of weight 0 give no loss and a zero gradient, and their
+ * advantage, old_logp and ref_logp are not looked at.  The caller's weights and
+ * divisor choose the mean: over tokens, or over sequences with weight 1 / length.
+ * n_rows == 0 writes stats 0.
+ * Errors: EINVAL (as zero_token_logprobs; a non-finite parameter, divisor <= 0,
+ * clip_low outside [0, 1], clip_high or kl_coef < 0, kl_coef without ref_logp,
+ * workspace missing, small or misaligned); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_policy_loss(const zero_policy_args *args, hipStream_t stream);
+int zero_policy_workspace_bytes(uint64_t n_rows, uint64_t *bytes);
+
+/* Arguments of zero_preference_loss. */
+typedef struct {
+  const void *logits;
+  int32_t dtype;
+  uint64_t n_rows;
+  uint32_t vocab;
+  uint64_t row_stride;
+  const int64_t *targets;
+  const int64_t *seq_begin; /* device [2 n_pairs + 1], increasing: sequence q is rows [seq_begin[q], seq_begin[q+1]) */
+  uint32_t n_pairs;         /* pair i: sequence 2i is the chosen one, 2i + 1 the rejected one */
+  const float *ref_logp;    /* [2 n_pairs]: each sequence's sum of the reference's log-probabilities */
+  double beta;              /* > 0 */
+  double label_smoothing;   /* in [0, 0.5] */
+  int32_t average;          /* 1: divide each sequence's sums by its number of counting rows */
+  double temperature;
+  double grad_scale;        /* multiplies dlogits only (a loss scale) */
+  float *stats;             /* [2]: loss, share of pairs whose chosen reward is the larger */
+  float *logp;              /* [n_rows] */
+  float *seq_logp, *reward; /* [2 n_pairs]: s, beta (s - ref) */
+  void *dlogits;            /* same dtype as logits; may be logits itself; NULL: no gradient */
+  uint64_t dlogits_stride;
+  void *workspace;          /* zero_preference_workspace_bytes(n_rows, n_pairs), 256-byte aligned */
+  size_t workspace_bytes;
+} zero_preference_args;
+
+/* ----------------------------------------------------------------------------
+ * zero_preference_loss -- the paired log-ratio loss and its gradient of the logits.
+ *   s_q = sum of lp over sequence q's rows (their mean with `average`)
+ *   h   = beta ((s_chosen - ref_chosen) - (s_rejected - ref_rejected))
+ *   loss = mean over pairs of -(1 - label_smoothing) ln sigma(h) - label_smoothing ln sigma(-h)
+ *   dlogits = grad_scale * d loss / d logits
+ * Rows outside every sequence get logp and a zero gradient; an empty sequence has
+ * s = 0.  Boundaries outside [0, n_rows] are taken as the nearest of the two.
+ * Errors: EINVAL (as zero_token_logprobs; a non-finite parameter, beta <= 0,
+ * label_smoothing outside [0, 0.5], no pairs, NULL or misaligned arrays,
+ * workspace missing, small or misaligned); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_preference_loss(const zero_preference_args *args, hipStream_t stream);
+int zero_preference_workspace_bytes(uint64_t n_rows, uint32_t n_pairs, uint64_t *bytes);
+
+/* ----------------------------------------------------------------------------
  * Measurement.
  * -------------------------------------------------------------------------- */
 

@@ -1,8 +1,8 @@
 """ZeRO owner-shard optimizer step on one MI355X: Python binding of libzero_shard.so.
 
 Argument marshalling only.  Every step of the path runs in the HIP library
-(``csrc/step.hip``, ``csrc/copy.hip``, ``csrc/launch.hip``, ``csrc/host.cpp``; C ABI in
-``include/zero_shard.h``);
+(``csrc/step.hip``, ``csrc/step8.hip``, ``csrc/loss.hip``, ``csrc/copy.hip``, ``csrc/launch.hip``,
+``csrc/host.cpp``; C ABI in ``include/zero_shard.h``);
 this module turns torch tensors into pointers, checks devices, dtypes,
 contiguity and extents against what the kernels will touch, passes torch's
 current stream, and raises on error codes.  There is no fallback: if the
@@ -10,7 +10,8 @@ library is missing, every call raises.
 
 The functions carry the names of the C entry points.  ``OwnerShard`` bundles
 one owner's layout, device chunk table and fp32 state for convenience; its
-methods are sequences of the same calls.
+methods are sequences of the same calls.  ``OwnerShard8`` is the same with both
+moments in 8 bits.
 """
 from __future__ import annotations
 
@@ -31,12 +32,19 @@ EXPORTED = ("zero_last_error", "zero_shard_layout", "zero_chunk_table", "zero_de
             "zero_reduce_owned", "zero_grad_check", "zero_clip_coef", "zero_step_decision", "zero_adam_step",
             "zero_owner_to_dense", "zero_dense_to_owner", "zero3_storage", "zero3_gather_spans",
             "zero3_partition_spans", "zero_copy_spans", "zero_stream_probe",
-            "zero_check_workspace_bytes", "zero_chunk_groups", "zero_span_groups", "zero_reduce_owned_noalloc")
+            "zero_check_workspace_bytes", "zero_chunk_groups", "zero_span_groups", "zero_reduce_owned_noalloc",
+            "zero_piece_table", "zero_adam8_step", "zero_moments8_pack", "zero_moments8_unpack",
+            "zero_token_logprobs", "zero_policy_loss", "zero_policy_workspace_bytes",
+            "zero_preference_loss", "zero_preference_workspace_bytes")
 
 CHUNK_DTYPE = np.dtype([("flat", "<u8"), ("len", "<u4"), ("tensor", "<u4")])
 SPAN_DTYPE = np.dtype([("src", "<u8"), ("dst", "<u8"), ("len", "<u4"), ("buf", "<u4")])
+PIECE_DTYPE = np.dtype([("flat", "<u8"), ("len", "<u4"), ("mask", "<u4")])
 ZERO_MAX_COPY_SOURCES = 128
 ZERO_MAX_PROBE_STREAMS = 64
+ZERO_QBLOCK = 128
+ZERO_PIECE = 2048
+ZERO_PIECE_WHOLE = 0xFFFFFFFF
 
 
 class ZeroShardError(RuntimeError):
@@ -58,6 +66,43 @@ class AdamArgs(ct.Structure):
         ("lr", ct.c_double), ("beta1", ct.c_double), ("beta2", ct.c_double), ("eps", ct.c_double),
         ("weight_decay", ct.c_double), ("adamw", ct.c_int32), ("step", ct.c_uint64),
         ("clip_coef", ct.c_double), ("grid_blocks", ct.c_uint32),
+    ]
+
+
+class Adam8Args(ct.Structure):
+    _fields_ = [
+        ("pieces", ct.c_void_p), ("n_pieces", ct.c_uint64), ("masks", ct.c_void_p), ("n_masks", ct.c_uint64),
+        ("begin", ct.c_uint64), ("end", ct.c_uint64),
+        ("rank_grads", ct.c_void_p), ("R", ct.c_uint32), ("grad_dtype", ct.c_int32),
+        ("grad_base", ct.c_uint64), ("divisor", ct.c_float), ("reduced_g", ct.c_void_p),
+        ("master", ct.c_void_p), ("exp_avg8", ct.c_void_p), ("exp_rms8", ct.c_void_p),
+        ("exp_avg_scale", ct.c_void_p), ("exp_rms_scale", ct.c_void_p), ("local_base", ct.c_uint64),
+        ("param16", ct.c_void_p), ("param_dtype", ct.c_int32), ("param_base", ct.c_uint64),
+        ("lr", ct.c_double), ("beta1", ct.c_double), ("beta2", ct.c_double), ("eps", ct.c_double),
+        ("weight_decay", ct.c_double), ("adamw", ct.c_int32), ("step", ct.c_uint64),
+        ("clip_coef", ct.c_double),
+    ]
+
+
+class PolicyArgs(ct.Structure):
+    _fields_ = [
+        ("logits", ct.c_void_p), ("dtype", ct.c_int32), ("n_rows", ct.c_uint64), ("vocab", ct.c_uint32),
+        ("row_stride", ct.c_uint64), ("targets", ct.c_void_p), ("old_logp", ct.c_void_p), ("ref_logp", ct.c_void_p),
+        ("advantage", ct.c_void_p), ("weight", ct.c_void_p), ("divisor", ct.c_double), ("clip_low", ct.c_double),
+        ("clip_high", ct.c_double), ("kl_coef", ct.c_double), ("temperature", ct.c_double), ("grad_scale", ct.c_double),
+        ("stats", ct.c_void_p), ("logp", ct.c_void_p), ("dlogits", ct.c_void_p), ("dlogits_stride", ct.c_uint64),
+        ("workspace", ct.c_void_p), ("workspace_bytes", ct.c_size_t),
+    ]
+
+
+class PreferenceArgs(ct.Structure):
+    _fields_ = [
+        ("logits", ct.c_void_p), ("dtype", ct.c_int32), ("n_rows", ct.c_uint64), ("vocab", ct.c_uint32),
+        ("row_stride", ct.c_uint64), ("targets", ct.c_void_p), ("seq_begin", ct.c_void_p), ("n_pairs", ct.c_uint32),
+        ("ref_logp", ct.c_void_p), ("beta", ct.c_double), ("label_smoothing", ct.c_double), ("average", ct.c_int32),
+        ("temperature", ct.c_double), ("grad_scale", ct.c_double), ("stats", ct.c_void_p), ("logp", ct.c_void_p),
+        ("seq_logp", ct.c_void_p), ("reward", ct.c_void_p), ("dlogits", ct.c_void_p), ("dlogits_stride", ct.c_uint64),
+        ("workspace", ct.c_void_p), ("workspace_bytes", ct.c_size_t),
     ]
 
 
@@ -96,6 +141,15 @@ def load(path: str):
     L.zero_stream_probe.argtypes = [P, P, U32, P, P, U32, U64, I, P]
     L.zero_check_workspace_bytes.argtypes = [U64, P]
     L.zero_chunk_groups.argtypes = [P, U64, U32, P, U64, P]
+    L.zero_piece_table.argtypes = [P, P, U32, U64, U64, P, U64, P, U64, P, P]
+    L.zero_adam8_step.argtypes = [ct.POINTER(Adam8Args), P]
+    L.zero_moments8_pack.argtypes = [P, U64, P, U64, U64, U64, U64, P, P, P, P, P, P, P]
+    L.zero_moments8_unpack.argtypes = [P, U64, P, U64, U64, U64, U64, P, P, P, P, P, P, P]
+    L.zero_token_logprobs.argtypes = [P, I, U64, U32, U64, P, D, P, P]
+    L.zero_policy_loss.argtypes = [ct.POINTER(PolicyArgs), P]
+    L.zero_policy_workspace_bytes.argtypes = [U64, P]
+    L.zero_preference_loss.argtypes = [ct.POINTER(PreferenceArgs), P]
+    L.zero_preference_workspace_bytes.argtypes = [U64, U32, P]
     return L
 
 
@@ -175,6 +229,21 @@ def zero_chunk_groups(chunks: np.ndarray, max_group: int) -> np.ndarray:
     out = np.zeros(int(count[0]) + 1, dtype=np.uint64)
     _check(lib().zero_chunk_groups(_p(ch), ch.size, max_group, _p(out), out.size, _p(count)))
     return out
+
+
+def zero_piece_table(numels: Sequence[int], offsets: Sequence[int], begin: int, end: int):
+    """The owner's pieces as a structured array (flat, len, mask) and the mask bytes of
+    those that hold padding, uint8 [n_masks, ZERO_PIECE / 8]."""
+    n, off = _u64(numels), _u64(offsets)
+    if n.size != off.size:
+        raise ValueError("numels and offsets differ in length")
+    count, n_masks = np.zeros(1, dtype=np.uint64), np.zeros(1, dtype=np.uint64)
+    args = (_p(n), _p(off), n.size, begin, end)
+    _check(lib().zero_piece_table(*args, None, 0, None, 0, _p(count), _p(n_masks)))
+    out = np.zeros(int(count[0]), dtype=PIECE_DTYPE)
+    masks = np.zeros((int(n_masks[0]), ZERO_PIECE // 8), dtype=np.uint8)
+    _check(lib().zero_piece_table(*args, _p(out), out.size, _p(masks), masks.shape[0], _p(count), _p(n_masks)))
+    return out, masks
 
 
 def zero_state_bytes(params: int, ranks: int, param: int = 2, grad: int = 2,
@@ -549,6 +618,244 @@ def zero_stream_probe(srcs, dsts, order: int = 0, src_widths=None, dst_widths=No
     _check(lib().zero_stream_probe(sa, _p(sw), len(srcs), da, _p(dw), len(dsts), unit, int(order), _stream()))
 
 
+# ---------------------------------------------------------------- the step with 8-bit moments
+def _state8(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale, exp_rms8, exp_rms_scale):
+    """Checks the piece table and the 8-bit state; returns (masks pointer or None, mask count)."""
+    torch = _torch()
+    if pieces_dev is not None:
+        _dev(pieces_dev, "pieces")
+        if pieces_dev.numel() * pieces_dev.element_size() < n_pieces * PIECE_DTYPE.itemsize:
+            raise ValueError("piece table smaller than n_pieces")
+    n_masks = 0
+    if masks_dev is not None and masks_dev.numel():
+        _dev(masks_dev, "masks", torch.uint8)
+        n_masks = masks_dev.numel() // (ZERO_PIECE // 8)
+    blocks = -(-(end - local_base) // ZERO_QBLOCK)
+    for name, t in (("exp_avg8", exp_avg8), ("exp_rms8", exp_rms8)):
+        _dev(t, name, torch.float8_e4m3fn)
+        _need(t, name, blocks * ZERO_QBLOCK)
+    for name, t in (("exp_avg_scale", exp_avg_scale), ("exp_rms_scale", exp_rms_scale)):
+        _dev(t, name, torch.float32)
+        _need(t, name, blocks)
+    return (masks_dev.data_ptr() if n_masks else None), n_masks
+
+
+def zero_adam8_step(*, pieces_dev, n_pieces: int, masks_dev=None, begin: int, end: int, master, exp_avg8,
+                    exp_avg_scale, exp_rms8, exp_rms_scale, local_base: int, step: int, lr: float, beta1: float,
+                    beta2: float, eps: float, weight_decay: float = 0.0, adamw: bool = True, rank_grads=None,
+                    grad_base: int = 0, divisor: float = 1.0, reduced_g=None, param16=None, param_base: int = 0,
+                    clip_coef: float = 1.0) -> None:
+    """Fused reduce + Adam/AdamW + 16-bit write-back whose moments are held in 8 bits:
+    ``exp_avg8``/``exp_rms8`` float8_e4m3fn codes, one fp32 scale per ZERO_QBLOCK of them,
+    over a device piece table from ``zero_piece_table``."""
+    torch = _torch()
+    _dev(master, "master", torch.float32)
+    _need(master, "master", end - local_base)
+    a = Adam8Args()
+    a.masks, a.n_masks = _state8(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale,
+                                 exp_rms8, exp_rms_scale)
+    a.pieces = pieces_dev.data_ptr() if pieces_dev is not None else None
+    a.n_pieces, a.begin, a.end = n_pieces, begin, end
+    keep = None
+    if reduced_g is not None:
+        _dev(reduced_g, "reduced_g", torch.float32)
+        _need(reduced_g, "reduced_g", end - local_base)
+        a.reduced_g = reduced_g.data_ptr()
+    else:
+        keep, code = _rank_ptrs(rank_grads, grad_base, end)
+        a.rank_grads = ct.cast(keep, ct.c_void_p)
+        a.R, a.grad_dtype, a.grad_base = len(rank_grads), code, grad_base
+    a.divisor = divisor
+    a.master, a.local_base = master.data_ptr(), local_base
+    a.exp_avg8, a.exp_rms8 = exp_avg8.data_ptr(), exp_rms8.data_ptr()
+    a.exp_avg_scale, a.exp_rms_scale = exp_avg_scale.data_ptr(), exp_rms_scale.data_ptr()
+    if param16 is not None:
+        _dev(param16, "param16")
+        if param16.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError("param16 must be float16 or bfloat16")
+        _need(param16, "param16", end - param_base)
+        a.param16, a.param_dtype, a.param_base = param16.data_ptr(), _dtype_code(param16), param_base
+    a.lr, a.beta1, a.beta2, a.eps, a.weight_decay = lr, beta1, beta2, eps, weight_decay
+    a.adamw, a.step, a.clip_coef = int(adamw), step, clip_coef
+    _check(lib().zero_adam8_step(ct.byref(a), _stream()))
+    del keep
+
+
+def _moments8(pack, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+              exp_avg_scale, exp_rms8, exp_rms_scale):
+    torch = _torch()
+    masks, n_masks = _state8(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale,
+                             exp_rms8, exp_rms_scale)
+    for name, t in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
+        _dev(t, name, torch.float32)
+        _need(t, name, end - local_base)
+    head = (pieces_dev.data_ptr() if pieces_dev is not None else None, n_pieces, masks, n_masks, begin, end, local_base)
+    wide = (exp_avg.data_ptr(), exp_avg_sq.data_ptr())
+    narrow = (exp_avg8.data_ptr(), exp_avg_scale.data_ptr(), exp_rms8.data_ptr(), exp_rms_scale.data_ptr())
+    if pack:
+        _check(lib().zero_moments8_pack(*head, *wide, *narrow, _stream()))
+    else:
+        _check(lib().zero_moments8_unpack(*head, *narrow, *wide, _stream()))
+
+
+def zero_moments8_pack(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+                       exp_avg_scale, exp_rms8, exp_rms_scale) -> None:
+    """The owner's fp32 moments into their 8-bit form."""
+    _moments8(True, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+              exp_avg_scale, exp_rms8, exp_rms_scale)
+
+
+def zero_moments8_unpack(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+                         exp_avg_scale, exp_rms8, exp_rms_scale) -> None:
+    """The owner's 8-bit moments as fp32 (scale * code, and the root's square)."""
+    _moments8(False, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+              exp_avg_scale, exp_rms8, exp_rms_scale)
+
+
+# ---------------------------------------------------------------- losses on token log-probabilities
+def _here(t, name: str, dtype, elems: int):
+    """A contiguous device tensor of one dtype with at least `elems` elements: its address."""
+    _dev(t, name, dtype)
+    _need(t, name, elems)
+    return t.data_ptr()
+
+
+def _rows(t, name: str):
+    """(rows, vocabulary, row stride) of a [rows, vocabulary] device tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, vocabulary], got {t.dim()} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index != _torch().cuda.current_device():
+        raise ValueError(f"{name} lives on {t.device}, not on the current device "
+                         f"cuda:{_torch().cuda.current_device()}")
+    n, v = t.shape
+    if v > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    stride = t.stride(0) if n > 1 else v
+    if stride < v:
+        raise ValueError(f"the rows of {name} overlap")
+    return n, v, stride
+
+
+def _logits(logits, targets):
+    torch = _torch()
+    if logits.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    n, v, stride = _rows(logits, "logits")
+    if targets.numel() != n:
+        raise ValueError(f"{targets.numel()} targets for {n} rows")
+    return n, v, stride, _here(targets, "targets", torch.int64, n)
+
+
+def _dlogits(a, dlogits, logits):
+    if dlogits is None:
+        return
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError("dlogits must have the dtype and shape of logits")
+    a.dlogits_stride = _rows(dlogits, "dlogits")[2]
+    a.dlogits = dlogits.data_ptr()
+
+
+def zero_token_logprobs(logits, targets, logp, *, temperature: float = 1.0) -> None:
+    """``logp[r]`` = log-probability of ``targets[r]`` under row r of ``logits`` / temperature.
+
+    ``logits`` [rows, vocabulary] float16, bfloat16 or float32 with contiguous rows at
+    any row stride; ``targets`` int64; ``logp`` float32.  A target outside the
+    vocabulary (-100) gives 0.
+    """
+    n, v, stride, tptr = _logits(logits, targets)
+    _check(lib().zero_token_logprobs(logits.data_ptr(), _dtype_code(logits), n, v, stride, tptr, temperature,
+                                     _here(logp, "logp", _torch().float32, n), _stream()))
+
+
+def _workspace(fn, *sizes, device=None):
+    out = np.zeros(1, dtype=np.uint64)
+    _check(fn(*sizes, _p(out)))
+    torch = _torch()
+    return torch.empty(int(out[0]), dtype=torch.uint8, device=device or "cuda")
+
+
+def policy_workspace(n_rows: int, device=None):
+    """The device workspace of ``zero_policy_loss`` over n_rows rows."""
+    return _workspace(lib().zero_policy_workspace_bytes, n_rows, device=device)
+
+
+def preference_workspace(n_rows: int, n_pairs: int, device=None):
+    """The device workspace of ``zero_preference_loss`` over n_rows rows and n_pairs pairs."""
+    return _workspace(lib().zero_preference_workspace_bytes, n_rows, n_pairs, device=device)
+
+
+def zero_policy_loss(logits, targets, *, old_logp, advantage, divisor: float, stats, logp, workspace, ref_logp=None,
+                     weight=None, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                     temperature: float = 1.0, grad_scale: float = 1.0, dlogits=None) -> None:
+    """Clipped policy loss with a KL term, and its gradient of the logits.
+
+    With lp the targets' log-probabilities, rho = exp(lp - old_logp) and
+    d = ref_logp - lp, row r adds weight * (-min(A rho, A clip(rho, 1 - clip_low,
+    1 + clip_high)) + kl_coef (exp(d) - d - 1)) / divisor to the loss.
+
+    Written: ``stats`` float32 [4] (loss, policy part, KL part without kl_coef, clipped
+    share), ``logp`` float32 [rows], and ``dlogits`` (optional; dtype and shape of
+    ``logits``, may be ``logits`` itself) = grad_scale * gradient, for
+    ``hidden_logits.backward(dlogits)``.  A target outside the vocabulary marks a row
+    that counts for nothing.  ``workspace`` from ``policy_workspace``.
+    """
+    f32 = _torch().float32
+    a = PolicyArgs()
+    n, a.vocab, a.row_stride, a.targets = _logits(logits, targets)
+    a.logits, a.dtype, a.n_rows = logits.data_ptr(), _dtype_code(logits), n
+    a.old_logp = _here(old_logp, "old_logp", f32, n)
+    a.advantage = _here(advantage, "advantage", f32, n)
+    if ref_logp is not None:
+        a.ref_logp = _here(ref_logp, "ref_logp", f32, n)
+    if weight is not None:
+        a.weight = _here(weight, "weight", f32, n)
+    a.divisor, a.clip_low, a.clip_high, a.kl_coef = divisor, clip_low, clip_high, kl_coef
+    a.temperature, a.grad_scale = temperature, grad_scale
+    a.stats, a.logp = _here(stats, "stats", f32, 4), _here(logp, "logp", f32, n)
+    _dlogits(a, dlogits, logits)
+    _dev(workspace, "workspace")
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib().zero_policy_loss(ct.byref(a), _stream()))
+
+
+def zero_preference_loss(logits, targets, seq_begin, *, ref_logp, stats, logp, seq_logp, reward, workspace,
+                         beta: float = 0.1, label_smoothing: float = 0.0, average: bool = False,
+                         temperature: float = 1.0, grad_scale: float = 1.0, dlogits=None) -> None:
+    """The paired log-ratio loss and its gradient of the logits.
+
+    ``seq_begin`` int64 [2 pairs + 1]: sequence q is rows [seq_begin[q], seq_begin[q + 1]),
+    sequences 2i and 2i + 1 the chosen and the rejected answer of pair i.  ``ref_logp``
+    float32 [2 pairs]: the reference model's sums over each sequence.  With s the
+    sequences' sums (means with ``average``; the reference's sums are then divided
+    too) and h = beta ((s_c - ref_c) - (s_r - ref_r)), the loss is the mean over pairs
+    of -(1 - label_smoothing) ln sigma(h) - label_smoothing ln sigma(-h).
+
+    Written: ``stats`` float32 [2] (loss, share of pairs with h > 0), ``logp`` float32
+    [rows], ``seq_logp`` and ``reward`` = beta (s - ref) float32 [2 pairs], and
+    ``dlogits`` as for ``zero_policy_loss``.  ``workspace`` from ``preference_workspace``.
+    """
+    torch = _torch()
+    f32 = torch.float32
+    if seq_begin.numel() % 2 != 1 or seq_begin.numel() < 3:
+        raise ValueError("seq_begin holds 2 * pairs + 1 boundaries of at least one pair")
+    pairs = seq_begin.numel() // 2
+    a = PreferenceArgs()
+    n, a.vocab, a.row_stride, a.targets = _logits(logits, targets)
+    a.logits, a.dtype, a.n_rows, a.n_pairs = logits.data_ptr(), _dtype_code(logits), n, pairs
+    a.seq_begin = _here(seq_begin, "seq_begin", torch.int64, 2 * pairs + 1)
+    a.ref_logp = _here(ref_logp, "ref_logp", f32, 2 * pairs)
+    a.beta, a.label_smoothing, a.average = beta, label_smoothing, int(average)
+    a.temperature, a.grad_scale = temperature, grad_scale
+    a.stats, a.logp = _here(stats, "stats", f32, 2), _here(logp, "logp", f32, n)
+    a.seq_logp, a.reward = _here(seq_logp, "seq_logp", f32, 2 * pairs), _here(reward, "reward", f32, 2 * pairs)
+    _dlogits(a, dlogits, logits)
+    _dev(workspace, "workspace")
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib().zero_preference_loss(ct.byref(a), _stream()))
+
+
 # ---------------------------------------------------------------- convenience
 class OwnerShard:
     """One owner's layout, device chunk table and fp32 master/moment state.
@@ -710,4 +1017,80 @@ class OwnerShard:
             self.master = torch.from_numpy(z["master"]).to(self.device)
             self.exp_avg = torch.from_numpy(z["exp_avg"]).to(self.device)
             self.exp_avg_sq = torch.from_numpy(z["exp_avg_sq"]).to(self.device)
+            return int(z["step"])
+
+
+class OwnerShard8(OwnerShard):
+    """An owner whose two moments are held in 8 bits (2.0625 bytes per parameter, not 8).
+
+    The same calls as ``OwnerShard``; the state is ``master`` (fp32), ``exp_avg8`` and
+    ``exp_rms8`` (float8_e4m3fn codes of the first moment and of the root of the
+    second) and ``exp_avg_scale`` / ``exp_rms_scale`` (fp32, one per ZERO_QBLOCK flat
+    elements).  Owner-local arrays start at ``local_base = begin`` rounded down to a
+    multiple of ZERO_QBLOCK.
+    """
+
+    def __init__(self, numels: Sequence[int], ranks: int, owner: int, align: int = 64,
+                 max_chunk: int = 2048, device=None):
+        super().__init__(numels, ranks, owner, align, max_chunk, device)
+        torch = _torch()
+        self.local_base = self.begin // ZERO_QBLOCK * ZERO_QBLOCK
+        self.local_size = self.end - self.local_base
+        self.blocks = -(-self.local_size // ZERO_QBLOCK)
+        self.pieces, masks = zero_piece_table(self.numels, self.offsets, self.begin, self.end)
+        self.pieces_dev = chunks_to_device(self.pieces, self.device)
+        self.masks_dev = torch.from_numpy(masks).to(self.device) if masks.size else None
+
+    def alloc_state(self):
+        """master, then the moments: (codes, scales) of the first and of the second's root."""
+        torch = _torch()
+        n = max(1, self.blocks)
+        mk = lambda k, dt: torch.zeros(k, dtype=dt, device=self.device)
+        self.master = mk(n * ZERO_QBLOCK, torch.float32)
+        self.exp_avg8, self.exp_rms8 = (mk(n * ZERO_QBLOCK, torch.float8_e4m3fn) for _ in range(2))
+        self.exp_avg_scale, self.exp_rms_scale = mk(n, torch.float32), mk(n, torch.float32)
+        return self.master, (self.exp_avg8, self.exp_avg_scale), (self.exp_rms8, self.exp_rms_scale)
+
+    def _state8(self) -> dict:
+        return dict(pieces_dev=self.pieces_dev, n_pieces=self.pieces.size, masks_dev=self.masks_dev, begin=self.begin,
+                    end=self.end, local_base=self.local_base, exp_avg8=self.exp_avg8,
+                    exp_avg_scale=self.exp_avg_scale, exp_rms8=self.exp_rms8, exp_rms_scale=self.exp_rms_scale)
+
+    def adam_step(self, *, step: int, hyper: dict, rank_grads=None, grad_base: int = 0,
+                  divisor: float = 1.0, reduced_g=None, param16=None, param_base: int = 0,
+                  clip_coef: float = 1.0, grid_blocks: int = 0) -> None:
+        """``grid_blocks`` is accepted for ``OwnerShard``'s callers; this step has one launch shape."""
+        zero_adam8_step(**self._state8(), master=self.master, step=step, rank_grads=rank_grads, grad_base=grad_base,
+                        divisor=divisor, reduced_g=reduced_g, param16=param16, param_base=param_base,
+                        clip_coef=clip_coef, **hyper)
+
+    def pack_moments(self, exp_avg, exp_avg_sq) -> None:
+        """Take over fp32 moments (owner-local, from ``local_base``)."""
+        zero_moments8_pack(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, **self._state8())
+
+    def unpack_moments(self, exp_avg, exp_avg_sq) -> None:
+        """Write the moments as fp32 (for ``to_dense``, or to go on in 32 bits)."""
+        zero_moments8_unpack(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, **self._state8())
+
+    _SAVED = ("master", "exp_avg8", "exp_avg_scale", "exp_rms8", "exp_rms_scale")
+
+    def save(self, path: str, step: int) -> None:
+        """Owner checkpoint: fp32 master, the codes (as bytes) and scales, the step count and the layout."""
+        torch = _torch()
+        host = lambda t: (t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t).cpu().numpy()
+        np.savez(path, **{k: host(getattr(self, k)) for k in self._SAVED}, step=np.int64(step),
+                 numels=np.array(self.numels, dtype=np.int64), ranks=np.int64(self.ranks),
+                 owner=np.int64(self.owner), align=np.int64(self.align))
+
+    def load(self, path: str) -> int:
+        """Restore a checkpoint written by save() for the same layout; returns its step."""
+        torch = _torch()
+        with np.load(path, allow_pickle=False) as z:
+            same = ("exp_avg8" in z.files and list(z["numels"]) == self.numels and int(z["ranks"]) == self.ranks
+                    and int(z["owner"]) == self.owner and int(z["align"]) == self.align)
+            if not same:
+                raise ValueError("checkpoint was written for a different layout, owner or state width")
+            for k in self._SAVED:
+                t = torch.from_numpy(z[k]).to(self.device)
+                setattr(self, k, t.view(torch.float8_e4m3fn) if k.endswith("8") else t)
             return int(z["step"])

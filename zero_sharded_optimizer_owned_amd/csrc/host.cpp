@@ -145,6 +145,80 @@ extern "C" int zero_chunk_table(const uint64_t* numel, const uint64_t* tensor_of
   return ZERO_OK;
 }
 
+// The owner's windows of ZERO_PIECE flat elements.  A run of real elements
+// (tensors without padding between them) that covers a window makes it whole;
+// any other window with a real element gets mask bytes, which the runs that
+// reach into it fill.
+extern "C" int zero_piece_table(const uint64_t* numel, const uint64_t* tensor_offset, uint32_t n_tensors,
+                                uint64_t begin, uint64_t end, zero_piece* out, uint64_t capacity, uint8_t* masks,
+                                uint64_t mask_capacity, uint64_t* n_pieces, uint64_t* n_masks) {
+  static const char* who = "zero_piece_table";
+  zs::clear_error();
+  if (!n_pieces || !n_masks) return fail(ZERO_EINVAL, "%s: n_pieces or n_masks is NULL", who);
+  if (n_tensors > 0 && (!numel || !tensor_offset)) return fail(ZERO_EINVAL, "%s: NULL tensor arrays", who);
+  if (begin > end) return fail(ZERO_EINVAL, "%s: begin > end", who);
+  if ((capacity > 0 && !out) || (mask_capacity > 0 && !masks)) return fail(ZERO_EINVAL, "%s: NULL output", who);
+  for (uint32_t k = 0; k < n_tensors; ++k) {
+    if (numel[k] == 0) return fail(ZERO_EINVAL, "%s: tensor %u has 0 elements", who, k);
+    if ((u128)tensor_offset[k] + numel[k] > (u128)(UINT64_MAX - ZERO_PIECE))
+      return fail(ZERO_EINVAL, "%s: tensor %u extends past 2^64", who, k);
+    if (k > 0 && tensor_offset[k] < tensor_offset[k - 1] + numel[k - 1])
+      return fail(ZERO_EINVAL, "%s: tensor %u overlaps or precedes tensor %u", who, k, k - 1);
+  }
+  const uint64_t base = begin / ZERO_QBLOCK * ZERO_QBLOCK, M = ZERO_PIECE / 8;
+  uint64_t pieces = 0, n_mask = 0;
+  uint64_t open = UINT64_MAX;  // the window that the last masked piece covers
+  for (uint32_t k = 0; k < n_tensors;) {
+    uint32_t j = k + 1;
+    while (j < n_tensors && tensor_offset[j] == tensor_offset[j - 1] + numel[j - 1]) ++j;
+    const uint64_t r0 = tensor_offset[k], r1 = tensor_offset[j - 1] + numel[j - 1];
+    uint64_t b = r0 > begin ? r0 : begin;
+    const uint64_t e = r1 < end ? r1 : end;
+    while (b < e) {
+      const uint64_t window = b / ZERO_PIECE, w0 = window * ZERO_PIECE, w1 = w0 + ZERO_PIECE;
+      const uint64_t flat = w0 > base ? w0 : base, stop = w1 < e ? w1 : e;
+      if (b == flat && stop == w1) {
+        if (pieces < capacity) out[pieces] = zero_piece{flat, (uint32_t)(w1 - flat), ZERO_PIECE_WHOLE};
+        ++pieces;
+      } else {
+        if (window != open) {
+          if (pieces < capacity) out[pieces] = zero_piece{flat, (uint32_t)(w1 - flat), (uint32_t)n_mask};
+          if (n_mask < mask_capacity) std::memset(masks + n_mask * M, 0, M);
+          ++pieces;
+          ++n_mask;
+          open = window;
+        }
+        if (n_mask <= mask_capacity) {
+          uint8_t* m = masks + (n_mask - 1) * M;
+          uint64_t i = b - flat;
+          const uint64_t last = stop - flat;
+          while (i < last) {  // whole bytes at once, ragged ends bit by bit
+            if (i % 8 == 0 && last - i >= 8) {
+              const uint64_t n = (last - i) / 8;
+              std::memset(m + i / 8, 0xFF, n);
+              i += 8 * n;
+            } else {
+              m[i / 8] = (uint8_t)(m[i / 8] | 1u << (i % 8));
+              ++i;
+            }
+          }
+        }
+      }
+      b = stop;
+    }
+    k = j;
+  }
+  *n_pieces = pieces;
+  *n_masks = n_mask;
+  if (n_mask >= ZERO_PIECE_WHOLE) return fail(ZERO_ERANGE, "%s: too many pieces with padding", who);
+  if (out == nullptr && masks == nullptr) return ZERO_OK;
+  if (pieces > capacity || n_mask > mask_capacity)
+    return fail(ZERO_ERANGE, "%s: %llu pieces and %llu masks needed, capacities %llu and %llu", who,
+                (unsigned long long)pieces, (unsigned long long)n_mask, (unsigned long long)capacity,
+                (unsigned long long)mask_capacity);
+  return ZERO_OK;
+}
+
 namespace {
 // Greedy grouping shared by the chunk and span group builders: consecutive
 // items go into one group while their work units total at most max_units and

@@ -1,0 +1,451 @@
+// The owner step with both Adam moments in 8 bits, and the moments' way in and
+// out of that form.
+//
+// State.  128 consecutive flat elements (an aligned block) share one fp32
+// scale per moment.  The first moment is held as m ~ ms * m8, the second as
+// its root, sqrt(v) ~ rs * r8, with m8 and r8 in e4m3 and the scale such that
+// the block's largest magnitude is the format's largest value, 448.  Holding
+// the root halves the exponent range that v needs, and the update divides by
+// the root anyway.  e4m3 keeps 4 significant bits down to 2^-15 of the block's
+// largest value and a step of 2^-18 below, so one block may span tensors of
+// very different scale.  A block's largest element is exact up to its scale's
+// fp32 rounding, so it decays as in 32 bits, and the rest keep their ratio to
+// it.  A root above zero is never rounded to zero (it takes the smallest
+// code): the update would otherwise divide its m by eps alone.
+//
+// The new weight is computed from the new fp32 moments, before they are
+// rounded to 8 bits; the rounding only reaches the next step.  A non-finite
+// gradient makes its block's scale NaN, and with it the block's moments: run
+// the overflow check first where that can happen.
+//
+// Work.  One thread takes 8 flat elements, so 16 lanes (one DPP row) hold a
+// block and its two maxima are four DPP steps each.  One 256-thread block
+// takes one piece of the piece table: up to 2048 flat elements cut at flat
+// multiples of 2048.  A piece that holds padding, or the owner's ragged end,
+// has one mask byte per 8 elements; vectors with all bits set run like a
+// whole piece's, the others element by element.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "internal.h"
+#include "launch.h"
+#include "vec.h"
+
+namespace zs {
+namespace {
+
+constexpr uint32_t kQBlock = ZERO_QBLOCK;
+constexpr uint32_t kPiece = ZERO_PIECE;
+constexpr uint32_t kMaskBytes = kPiece / 8;
+constexpr float kCodeMax = 448.0f;             // largest e4m3 value
+constexpr float kCodeTiny = 0x1p-9f;           // smallest positive one
+constexpr float kLiveMin = 0x1p-100f;          // a block whose maximum is below this holds zeros:
+                                               // 448 / maximum stays finite above it
+static_assert(kPiece == 8 * kBlock && kQBlock == 8 * 16, "one vector per thread, one DPP row per block");
+
+// ---------------------------------------------------------------------------
+// A thread's eight elements.
+// ---------------------------------------------------------------------------
+
+// The real elements among [f, f + 8) of a piece, as a bit mask: the table's
+// mask byte (all eight in a whole piece) within the piece and [begin, end).
+__device__ __forceinline__ uint32_t real_bits(const zero_piece& pc, const uint8_t* masks, uint64_t n_masks,
+                                              uint64_t begin, uint64_t end, uint64_t local_base, uint32_t t) {
+  if (pc.flat % kQBlock != 0 || pc.flat < local_base || 8 * t >= pc.len || pc.len > kPiece) return 0;
+  uint32_t bits = 0xFFu;
+  if (pc.mask != ZERO_PIECE_WHOLE) {
+    if (pc.mask >= n_masks) return 0;
+    bits = masks[(uint64_t)pc.mask * kMaskBytes + t];
+  }
+  const uint64_t f = pc.flat + 8 * t;
+  if (f < begin) bits &= f + 8 <= begin ? 0u : 0xFFu << (begin - f);
+  if (f + 8 > end) bits &= f >= end ? 0u : 0xFFu >> (8 - (end - f));
+  return bits & 0xFFu;
+}
+
+// fp32 values at index e: whole vectors as two 16-byte accesses, partial ones
+// element by element (elements not real are neither read nor written).
+template <int DT, bool NT = false>
+__device__ __forceinline__ void get8(const void* p, uint64_t e, uint32_t bits, float (&x)[8]) {
+  if (bits == 0xFFu) {
+    const auto raw = load8<DT, NT>(p, e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = Vec<DT>::get(raw, k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = (bits >> k & 1) ? Vec<DT>::load1(p, e + k) : 0.0f;
+  }
+}
+
+template <int DT, bool NT = false>
+__device__ __forceinline__ void put8(void* p, uint64_t e, uint32_t bits, const float (&x)[8]) {
+  if (bits == 0xFFu) {
+    store8<DT, NT>(p, e, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (bits >> k & 1) Vec<DT>::store1(p, e + k, x[k]);
+  }
+}
+
+// Largest of a DPP row's 16 values, in every lane of it.
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_max_step(uint32_t x) {
+  return max(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  x = row_max_step<0x128>(x);  // row_ror:8, 4, 2, 1
+  x = row_max_step<0x124>(x);
+  x = row_max_step<0x122>(x);
+  return row_max_step<0x121>(x);
+}
+
+// Encodes the row's block: this thread's eight codes and the block's scale.
+// The maximum is taken over magnitude bits, where NaN is largest.
+template <bool ROOT>
+__device__ __forceinline__ u32x2 quantise(const float (&x)[8], float* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+  const float m = __uint_as_float(row_max(top));
+  const bool dead = m < kLiveMin;  // false for NaN
+  const float inv = dead ? 0.0f : kCodeMax / m;
+  *scale = dead ? 0.0f : m / kCodeMax;
+  float q[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    q[k] = x[k] * inv;
+    if (ROOT) q[k] = x[k] > 0.0f && !dead ? fmaxf(q[k], kCodeTiny) : q[k];
+  }
+  return encode8(q);
+}
+
+struct Moments8 {
+  uint8_t *m8, *r8;
+  float *ms, *rs;
+};
+
+// The two moments of a thread's eight elements, as fp32 m and root.
+__device__ __forceinline__ void load_moments(const Moments8& s, uint64_t l, float (&m)[8], float (&r)[8]) {
+  const u32x2 cm = *reinterpret_cast<const u32x2*>(s.m8 + l), cr = *reinterpret_cast<const u32x2*>(s.r8 + l);
+  const float ms = s.ms[l / kQBlock], rs = s.rs[l / kQBlock];
+  decode8(cm, m);
+  decode8(cr, r);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    m[k] = m[k] * ms;
+    r[k] = r[k] * rs;
+  }
+}
+
+// Encodes and stores them.  Every lane of the wavefront calls it.  Vectors
+// without a real element are not written; the codes of padding inside a
+// written vector are 0.
+__device__ __forceinline__ void store_moments(const Moments8& s, uint64_t l, uint32_t bits, const float (&m)[8],
+                                              const float (&r)[8]) {
+  float ms, rs;
+  const u32x2 cm = quantise<false>(m, &ms), cr = quantise<true>(r, &rs);
+  const uint32_t row_any = row_max(bits);
+  if (bits) {
+    *reinterpret_cast<u32x2*>(s.m8 + l) = cm;
+    *reinterpret_cast<u32x2*>(s.r8 + l) = cr;
+  }
+  if ((threadIdx.x & 15) == 0 && row_any) {
+    s.ms[l / kQBlock] = ms;
+    s.rs[l / kQBlock] = rs;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The step.
+// ---------------------------------------------------------------------------
+struct Ranks8 {
+  const void* ptr[ZERO_MAX_RANKS];
+  uint32_t R;
+  uint64_t base;
+  float divisor, inv_divisor;
+  int32_t div_pow2;
+};
+
+struct Adam8Const {
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  float step_size;     // lr / (1 - beta1^t)
+  float inv_sqrt_bc2;  // 1 / sqrt(1 - beta2^t)
+  float eps;
+  float decay;  // 1 - lr * wd for AdamW, else 1
+  float l2;     // wd for classic Adam, else 0
+  float clip;
+};
+
+struct Step8Args {
+  Ranks8 rs;
+  const zero_piece* pieces;
+  uint64_t n_pieces;
+  const uint8_t* masks;
+  uint64_t n_masks;
+  uint64_t begin, end;
+  const float* reduced_g;
+  float* w;
+  Moments8 s;
+  uint64_t local_base;
+  void* p16;
+  uint64_t param_base;
+  Adam8Const c;
+};
+
+constexpr int kStored = -1;  // gradient source: a stored owner-local fp32 gradient
+
+// Sum of the ranks in rank order, from +0, one fp32 add each, then one IEEE
+// division (a product with the exact reciprocal of a power of two).
+template <int GDT>
+__device__ __forceinline__ void rank_mean(const Ranks8& rs, uint64_t f, uint32_t bits, float (&g)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = 0.0f;
+  for (uint32_t r = 0; r < rs.R; ++r) {
+    float x[8];
+    get8<GDT>(rs.ptr[r], f - rs.base, bits, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = g[k] + x[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = rs.div_pow2 ? g[k] * rs.inv_divisor : g[k] / rs.divisor;
+}
+
+template <int GDT, int PDT>
+__global__ void __launch_bounds__(kBlock) step8_kernel(const Step8Args a) {
+  const uint32_t t = threadIdx.x;
+  for (uint64_t i = blockIdx.x; i < a.n_pieces; i += gridDim.x) {
+    const zero_piece pc = a.pieces[i];
+    const uint32_t bits = real_bits(pc, a.masks, a.n_masks, a.begin, a.end, a.local_base, t);
+    const uint64_t f = pc.flat + 8 * t, l = f - a.local_base;
+    float g[8] = {}, w[8], m[8] = {}, r[8] = {};
+    if (bits) {
+      load_moments(a.s, l, m, r);
+      get8<ZERO_F32>(a.w, l, bits, w);
+      if constexpr (GDT == kStored) get8<ZERO_F32>(a.reduced_g, l, bits, g);
+      else rank_mean<GDT>(a.rs, f, bits, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool real = bits >> k & 1;
+        float gc = g[k] * a.c.clip;
+        if (a.c.l2 != 0.0f) gc = fmaf(a.c.l2, w[k], gc);
+        const float mn = fmaf(a.c.beta1, m[k], a.c.one_minus_beta1 * gc);
+        const float v = fmaf(a.c.beta2 * r[k], r[k], (a.c.one_minus_beta2 * gc) * gc);
+        const float rn = __builtin_sqrtf(v);
+        const float denom = fmaf(rn, a.c.inv_sqrt_bc2, a.c.eps);
+        w[k] = fmaf(-a.c.step_size, mn / denom, w[k] * a.c.decay);
+        m[k] = real ? mn : 0.0f;
+        r[k] = real ? rn : 0.0f;
+      }
+      put8<ZERO_F32>(a.w, l, bits, w);
+      if constexpr (PDT != ZERO_NONE) put8<PDT>(a.p16, f - a.param_base, bits, w);
+    }
+    store_moments(a.s, l, bits, m, r);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32 moments to 8 bits and back.
+// ---------------------------------------------------------------------------
+struct Convert8Args {
+  const zero_piece* pieces;
+  uint64_t n_pieces;
+  const uint8_t* masks;
+  uint64_t n_masks;
+  uint64_t begin, end, local_base;
+  float *m, *v;  // fp32 moments, owner-local
+  Moments8 s;
+};
+
+template <bool PACK>
+__global__ void __launch_bounds__(kBlock) convert8_kernel(const Convert8Args a) {
+  const uint32_t t = threadIdx.x;
+  for (uint64_t i = blockIdx.x; i < a.n_pieces; i += gridDim.x) {
+    const zero_piece pc = a.pieces[i];
+    const uint32_t bits = real_bits(pc, a.masks, a.n_masks, a.begin, a.end, a.local_base, t);
+    const uint64_t l = pc.flat + 8 * t - a.local_base;
+    float m[8] = {}, r[8] = {};
+    if constexpr (PACK) {
+      if (bits) {
+        get8<ZERO_F32>(a.m, l, bits, m);
+        get8<ZERO_F32>(a.v, l, bits, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[k] = __builtin_sqrtf(r[k]);
+      }
+      store_moments(a.s, l, bits, m, r);
+    } else if (bits) {
+      load_moments(a.s, l, m, r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[k] = r[k] * r[k];
+      put8<ZERO_F32>(a.m, l, bits, m);
+      put8<ZERO_F32>(a.v, l, bits, r);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side: validation and launch.
+// ---------------------------------------------------------------------------
+bool exact_reciprocal(float d, float* inv) {
+  int e = 0;
+  if (std::frexp(d, &e) != 0.5f) return false;
+  const float r = std::ldexp(1.0f, 1 - e);
+  if (!std::isnormal(r)) return false;
+  *inv = r;
+  return true;
+}
+
+int fill_ranks8(Ranks8* rs, const zero_adam8_args* p, const char* who) {
+  if (p->R == 0 || p->R > ZERO_MAX_RANKS)
+    return fail(ZERO_EINVAL, "%s: R = %u outside [1, %d]", who, p->R, ZERO_MAX_RANKS);
+  if (!p->rank_grads) return fail(ZERO_EINVAL, "%s: neither rank_grads nor reduced_g is given", who);
+  if (p->grad_dtype != ZERO_F16 && p->grad_dtype != ZERO_BF16 && p->grad_dtype != ZERO_F32)
+    return fail(ZERO_EINVAL, "%s: unknown gradient dtype %d", who, p->grad_dtype);
+  if (p->grad_base % 8 != 0 || p->grad_base > p->begin)
+    return fail(ZERO_EINVAL, "%s: grad_base must be a multiple of 8 and <= begin", who);
+  if (!(p->divisor > 0.0f) || !std::isfinite(p->divisor))
+    return fail(ZERO_EINVAL, "%s: divisor must be finite and > 0", who);
+  for (uint32_t r = 0; r < p->R; ++r) {
+    if (!p->rank_grads[r]) return fail(ZERO_EINVAL, "%s: rank buffer %u is NULL", who, r);
+    if (!aligned16(p->rank_grads[r]))
+      return fail(ZERO_EINVAL, "%s: rank buffer %u is not 16-byte aligned", who, r);
+    rs->ptr[r] = p->rank_grads[r];
+  }
+  rs->R = p->R;
+  rs->base = p->grad_base;
+  rs->divisor = p->divisor;
+  rs->div_pow2 = exact_reciprocal(p->divisor, &rs->inv_divisor) ? 1 : 0;
+  return ZERO_OK;
+}
+
+// The piece table, owner range and 8-bit state that every call here takes.
+int check_state8(const zero_piece* pieces, uint64_t n_pieces, const uint8_t* masks, uint64_t n_masks, uint64_t begin,
+                 uint64_t end, uint64_t local_base, const Moments8& s, const char* who) {
+  if (begin > end) return fail(ZERO_EINVAL, "%s: begin > end", who);
+  if (n_pieces > 0 && !pieces) return fail(ZERO_EINVAL, "%s: pieces is NULL", who);
+  if (n_masks > 0 && !masks) return fail(ZERO_EINVAL, "%s: masks is NULL", who);
+  if (local_base % kQBlock != 0 || local_base > begin)
+    return fail(ZERO_EINVAL, "%s: local_base must be a multiple of %u and <= begin", who, kQBlock);
+  if (!s.m8 || !s.r8 || !s.ms || !s.rs) return fail(ZERO_EINVAL, "%s: the 8-bit state arrays must be given", who);
+  if (!aligned16(s.m8) || !aligned16(s.r8) || !aligned16(s.ms) || !aligned16(s.rs))
+    return fail(ZERO_EINVAL, "%s: state arrays must be 16-byte aligned", who);
+  return ZERO_OK;
+}
+
+template <int GDT>
+void launch_step8(const Step8Args& a, int pdt, hipStream_t s) {
+  const uint32_t grid = chunk_grid(a.n_pieces, 0);
+  if (pdt == ZERO_F16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_F16>), grid, kBlock, 0, s, a);
+  else if (pdt == ZERO_BF16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_BF16>), grid, kBlock, 0, s, a);
+  else hipLaunchKernelGGL((step8_kernel<GDT, ZERO_NONE>), grid, kBlock, 0, s, a);
+}
+
+int convert8(bool pack, const zero_piece* pieces, uint64_t n_pieces, const uint8_t* masks, uint64_t n_masks,
+             uint64_t begin, uint64_t end, uint64_t local_base, float* m, float* v, const Moments8& s,
+             hipStream_t stream, const char* who) {
+  clear_error();
+  int rc = check_state8(pieces, n_pieces, masks, n_masks, begin, end, local_base, s, who);
+  if (rc) return rc;
+  if (!m || !v) return fail(ZERO_EINVAL, "%s: exp_avg and exp_avg_sq must be given", who);
+  if (!aligned16(m) || !aligned16(v)) return fail(ZERO_EINVAL, "%s: state arrays must be 16-byte aligned", who);
+  if (n_pieces == 0 || begin == end) return ZERO_OK;
+  if ((rc = begin_launch())) return rc;
+  const Convert8Args a = {pieces, n_pieces, masks, n_masks, begin, end, local_base, m, v, s};
+  const uint32_t grid = chunk_grid(n_pieces, 0);
+  if (pack) hipLaunchKernelGGL(convert8_kernel<true>, grid, kBlock, 0, stream, a);
+  else hipLaunchKernelGGL(convert8_kernel<false>, grid, kBlock, 0, stream, a);
+  return launch_status(who);
+}
+
+}  // namespace
+}  // namespace zs
+
+using namespace zs;
+
+extern "C" int zero_adam8_step(const zero_adam8_args* p, hipStream_t stream) {
+  static const char* who = "zero_adam8_step";
+  clear_error();
+  if (!p) return fail(ZERO_EINVAL, "%s: args is NULL", who);
+  if (p->step == 0) return fail(ZERO_EINVAL, "%s: step counts from 1", who);
+  Step8Args a;
+  std::memset(&a, 0, sizeof a);
+  a.s = {p->exp_avg8, p->exp_rms8, p->exp_avg_scale, p->exp_rms_scale};
+  int rc = check_state8(p->pieces, p->n_pieces, p->masks, p->n_masks, p->begin, p->end, p->local_base, a.s, who);
+  if (rc) return rc;
+  if (p->reduced_g) {
+    if (!aligned16(p->reduced_g)) return fail(ZERO_EINVAL, "%s: reduced_g is not 16-byte aligned", who);
+  } else if ((rc = fill_ranks8(&a.rs, p, who))) {
+    return rc;
+  }
+  if (!p->master) return fail(ZERO_EINVAL, "%s: master must be given", who);
+  if (!aligned16(p->master)) return fail(ZERO_EINVAL, "%s: master is not 16-byte aligned", who);
+  const int pdt = p->param_dtype;
+  if (pdt != ZERO_NONE && pdt != ZERO_F16 && pdt != ZERO_BF16)
+    return fail(ZERO_EINVAL, "%s: param_dtype must be NONE, F16 or BF16", who);
+  if (pdt != ZERO_NONE) {
+    if (!p->param16) return fail(ZERO_EINVAL, "%s: param16 is NULL", who);
+    if (!aligned16(p->param16)) return fail(ZERO_EINVAL, "%s: param16 is not 16-byte aligned", who);
+    if (p->param_base % 8 != 0 || p->param_base > p->begin)
+      return fail(ZERO_EINVAL, "%s: param_base must be a multiple of 8 and <= begin", who);
+  }
+  const double hp[] = {p->lr, p->beta1, p->beta2, p->eps, p->weight_decay, p->clip_coef};
+  for (double x : hp)
+    if (!std::isfinite(x)) return fail(ZERO_EINVAL, "%s: non-finite hyperparameter", who);
+  if (p->lr < 0 || p->eps < 0 || p->weight_decay < 0 || p->clip_coef < 0)
+    return fail(ZERO_EINVAL, "%s: lr, eps, weight_decay and clip_coef must be >= 0", who);
+  if (p->beta1 < 0 || p->beta1 >= 1 || p->beta2 < 0 || p->beta2 >= 1)
+    return fail(ZERO_EINVAL, "%s: betas must lie in [0, 1)", who);
+  if (p->n_pieces == 0 || p->begin == p->end) return ZERO_OK;
+  if ((rc = begin_launch())) return rc;
+
+  // Constants in fp64, each rounded once to fp32.
+  const double t = (double)p->step;
+  a.c.beta1 = (float)p->beta1;
+  a.c.one_minus_beta1 = (float)(1.0 - p->beta1);
+  a.c.beta2 = (float)p->beta2;
+  a.c.one_minus_beta2 = (float)(1.0 - p->beta2);
+  a.c.step_size = (float)(p->lr / (1.0 - std::pow(p->beta1, t)));
+  a.c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(p->beta2, t)));
+  a.c.eps = (float)p->eps;
+  a.c.decay = p->adamw ? (float)(1.0 - p->lr * p->weight_decay) : 1.0f;
+  a.c.l2 = p->adamw ? 0.0f : (float)p->weight_decay;
+  a.c.clip = (float)p->clip_coef;
+  a.pieces = p->pieces;
+  a.n_pieces = p->n_pieces;
+  a.masks = p->masks;
+  a.n_masks = p->n_masks;
+  a.begin = p->begin;
+  a.end = p->end;
+  a.reduced_g = p->reduced_g;
+  a.w = p->master;
+  a.local_base = p->local_base;
+  a.p16 = pdt != ZERO_NONE ? p->param16 : nullptr;
+  a.param_base = p->param_base;
+  if (p->reduced_g) launch_step8<kStored>(a, pdt, stream);
+  else if (p->grad_dtype == ZERO_F16) launch_step8<ZERO_F16>(a, pdt, stream);
+  else if (p->grad_dtype == ZERO_BF16) launch_step8<ZERO_BF16>(a, pdt, stream);
+  else launch_step8<ZERO_F32>(a, pdt, stream);
+  return launch_status(who);
+}
+
+extern "C" int zero_moments8_pack(const zero_piece* pieces, uint64_t n_pieces, const uint8_t* masks, uint64_t n_masks,
+                                  uint64_t begin, uint64_t end, uint64_t local_base, const float* exp_avg,
+                                  const float* exp_avg_sq, uint8_t* exp_avg8, float* exp_avg_scale, uint8_t* exp_rms8,
+                                  float* exp_rms_scale, hipStream_t stream) {
+  return convert8(true, pieces, n_pieces, masks, n_masks, begin, end, local_base, const_cast<float*>(exp_avg),
+                  const_cast<float*>(exp_avg_sq), Moments8{exp_avg8, exp_rms8, exp_avg_scale, exp_rms_scale}, stream,
+                  "zero_moments8_pack");
+}
+
+extern "C" int zero_moments8_unpack(const zero_piece* pieces, uint64_t n_pieces, const uint8_t* masks,
+                                    uint64_t n_masks, uint64_t begin, uint64_t end, uint64_t local_base,
+                                    const uint8_t* exp_avg8, const float* exp_avg_scale, const uint8_t* exp_rms8,
+                                    const float* exp_rms_scale, float* exp_avg, float* exp_avg_sq,
+                                    hipStream_t stream) {
+  return convert8(false, pieces, n_pieces, masks, n_masks, begin, end, local_base, exp_avg, exp_avg_sq,
+                  Moments8{const_cast<uint8_t*>(exp_avg8), const_cast<uint8_t*>(exp_rms8),
+                           const_cast<float*>(exp_avg_scale), const_cast<float*>(exp_rms_scale)},
+                  stream, "zero_moments8_unpack");
+}
