@@ -303,6 +303,22 @@ def _stream():
     return ct.c_void_p(_torch().cuda.current_stream().cuda_stream)
 
 
+def _device_stream():
+    """(current device's index, its current stream as an address)."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _addr(t, name: str, dtype, elems: int, dev: int) -> int:
+    """The address of a contiguous tensor of one dtype on device `dev` with at least
+    `elems` elements; a tensor that is not that gets the error of the check it fails."""
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous() or t.numel() < elems:
+        _dev(t, name, dtype)
+        _need(t, name, elems)
+    return t.data_ptr()
+
+
 def _need(t, name: str, elems: int) -> None:
     if t.numel() < elems:
         raise ValueError(f"{name} holds {t.numel()} elements, {elems} needed")
@@ -619,25 +635,25 @@ def zero_stream_probe(srcs, dsts, order: int = 0, src_widths=None, dst_widths=No
 
 
 # ---------------------------------------------------------------- the step with 8-bit moments
-def _state8(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale, exp_rms8, exp_rms_scale):
-    """Checks the piece table and the 8-bit state; returns (masks pointer or None, mask count)."""
+def _state8(dev, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale, exp_rms8,
+            exp_rms_scale):
+    """Checks the piece table and the 8-bit state; returns (pieces, n_pieces, masks, n_masks,
+    begin, end) and the state's addresses (codes, scales of the first; codes, scales of the second)."""
     torch = _torch()
-    if pieces_dev is not None:
-        _dev(pieces_dev, "pieces")
-        if pieces_dev.numel() * pieces_dev.element_size() < n_pieces * PIECE_DTYPE.itemsize:
-            raise ValueError("piece table smaller than n_pieces")
+    pieces = masks = None
     n_masks = 0
+    if pieces_dev is not None:
+        pieces = _addr(pieces_dev, "pieces", torch.uint8, n_pieces * PIECE_DTYPE.itemsize, dev)
     if masks_dev is not None and masks_dev.numel():
-        _dev(masks_dev, "masks", torch.uint8)
+        masks = _addr(masks_dev, "masks", torch.uint8, 0, dev)
         n_masks = masks_dev.numel() // (ZERO_PIECE // 8)
     blocks = -(-(end - local_base) // ZERO_QBLOCK)
-    for name, t in (("exp_avg8", exp_avg8), ("exp_rms8", exp_rms8)):
-        _dev(t, name, torch.float8_e4m3fn)
-        _need(t, name, blocks * ZERO_QBLOCK)
-    for name, t in (("exp_avg_scale", exp_avg_scale), ("exp_rms_scale", exp_rms_scale)):
-        _dev(t, name, torch.float32)
-        _need(t, name, blocks)
-    return (masks_dev.data_ptr() if n_masks else None), n_masks
+    e4m3, f32 = torch.float8_e4m3fn, torch.float32
+    return (pieces, n_pieces, masks, n_masks, begin, end), (
+        _addr(exp_avg8, "exp_avg8", e4m3, blocks * ZERO_QBLOCK, dev),
+        _addr(exp_avg_scale, "exp_avg_scale", f32, blocks, dev),
+        _addr(exp_rms8, "exp_rms8", e4m3, blocks * ZERO_QBLOCK, dev),
+        _addr(exp_rms_scale, "exp_rms_scale", f32, blocks, dev))
 
 
 def zero_adam8_step(*, pieces_dev, n_pieces: int, masks_dev=None, begin: int, end: int, master, exp_avg8,
@@ -649,112 +665,99 @@ def zero_adam8_step(*, pieces_dev, n_pieces: int, masks_dev=None, begin: int, en
     ``exp_avg8``/``exp_rms8`` float8_e4m3fn codes, one fp32 scale per ZERO_QBLOCK of them,
     over a device piece table from ``zero_piece_table``."""
     torch = _torch()
-    _dev(master, "master", torch.float32)
-    _need(master, "master", end - local_base)
-    a = Adam8Args()
-    a.masks, a.n_masks = _state8(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale,
-                                 exp_rms8, exp_rms_scale)
-    a.pieces = pieces_dev.data_ptr() if pieces_dev is not None else None
-    a.n_pieces, a.begin, a.end = n_pieces, begin, end
-    keep = None
+    f32 = torch.float32
+    dev, stream = _device_stream()
+    work, (m8, ms, r8, rs) = _state8(dev, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8,
+                                     exp_avg_scale, exp_rms8, exp_rms_scale)
+    ranks = None
+    R = code = 0
+    g = p16 = None
     if reduced_g is not None:
-        _dev(reduced_g, "reduced_g", torch.float32)
-        _need(reduced_g, "reduced_g", end - local_base)
-        a.reduced_g = reduced_g.data_ptr()
+        g = _addr(reduced_g, "reduced_g", f32, end - local_base, dev)
     else:
-        keep, code = _rank_ptrs(rank_grads, grad_base, end)
-        a.rank_grads = ct.cast(keep, ct.c_void_p)
-        a.R, a.grad_dtype, a.grad_base = len(rank_grads), code, grad_base
-    a.divisor = divisor
-    a.master, a.local_base = master.data_ptr(), local_base
-    a.exp_avg8, a.exp_rms8 = exp_avg8.data_ptr(), exp_rms8.data_ptr()
-    a.exp_avg_scale, a.exp_rms_scale = exp_avg_scale.data_ptr(), exp_rms_scale.data_ptr()
+        if not rank_grads:
+            raise ValueError("no rank buffers")
+        R, dt, need = len(rank_grads), rank_grads[0].dtype, end - grad_base
+        code = _dtype_code(rank_grads[0])
+        ranks = (ct.c_void_p * R)(*[_addr(x, "rank_grads", dt, need, dev) for x in rank_grads])
+    pdt = ZERO_NONE
     if param16 is not None:
-        _dev(param16, "param16")
         if param16.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("param16 must be float16 or bfloat16")
-        _need(param16, "param16", end - param_base)
-        a.param16, a.param_dtype, a.param_base = param16.data_ptr(), _dtype_code(param16), param_base
-    a.lr, a.beta1, a.beta2, a.eps, a.weight_decay = lr, beta1, beta2, eps, weight_decay
-    a.adamw, a.step, a.clip_coef = int(adamw), step, clip_coef
-    _check(lib().zero_adam8_step(ct.byref(a), _stream()))
-    del keep
+        p16, pdt = _addr(param16, "param16", param16.dtype, end - param_base, dev), _dtype_code(param16)
+    a = Adam8Args(*work, ct.addressof(ranks) if ranks is not None else None, R, code, grad_base, divisor, g,
+                  _addr(master, "master", f32, end - local_base, dev), m8, r8, ms, rs, local_base, p16, pdt,
+                  param_base, lr, beta1, beta2, eps, weight_decay, int(adamw), step, clip_coef)
+    _check(lib().zero_adam8_step(ct.byref(a), stream))
 
 
-def _moments8(pack, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
-              exp_avg_scale, exp_rms8, exp_rms_scale):
-    torch = _torch()
-    masks, n_masks = _state8(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale,
-                             exp_rms8, exp_rms_scale)
-    for name, t in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
-        _dev(t, name, torch.float32)
-        _need(t, name, end - local_base)
-    head = (pieces_dev.data_ptr() if pieces_dev is not None else None, n_pieces, masks, n_masks, begin, end, local_base)
-    wide = (exp_avg.data_ptr(), exp_avg_sq.data_ptr())
-    narrow = (exp_avg8.data_ptr(), exp_avg_scale.data_ptr(), exp_rms8.data_ptr(), exp_rms_scale.data_ptr())
+def _moments8(pack, exp_avg, exp_avg_sq, *state, local_base, **named):
+    f32 = _torch().float32
+    dev, stream = _device_stream()
+    work, narrow = _state8(dev, *state, local_base=local_base, **named)
+    need = work[5] - local_base
+    wide = _addr(exp_avg, "exp_avg", f32, need, dev), _addr(exp_avg_sq, "exp_avg_sq", f32, need, dev)
     if pack:
-        _check(lib().zero_moments8_pack(*head, *wide, *narrow, _stream()))
+        _check(lib().zero_moments8_pack(*work, local_base, *wide, *narrow, stream))
     else:
-        _check(lib().zero_moments8_unpack(*head, *narrow, *wide, _stream()))
+        _check(lib().zero_moments8_unpack(*work, local_base, *narrow, *wide, stream))
 
 
-def zero_moments8_pack(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+def zero_moments8_pack(*, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev=None, begin, end, local_base, exp_avg8,
                        exp_avg_scale, exp_rms8, exp_rms_scale) -> None:
     """The owner's fp32 moments into their 8-bit form."""
-    _moments8(True, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
-              exp_avg_scale, exp_rms8, exp_rms_scale)
+    _moments8(True, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev, begin, end, local_base=local_base,
+              exp_avg8=exp_avg8, exp_avg_scale=exp_avg_scale, exp_rms8=exp_rms8, exp_rms_scale=exp_rms_scale)
 
 
-def zero_moments8_unpack(pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
+def zero_moments8_unpack(*, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev=None, begin, end, local_base, exp_avg8,
                          exp_avg_scale, exp_rms8, exp_rms_scale) -> None:
     """The owner's 8-bit moments as fp32 (scale * code, and the root's square)."""
-    _moments8(False, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg, exp_avg_sq, exp_avg8,
-              exp_avg_scale, exp_rms8, exp_rms_scale)
+    _moments8(False, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev, begin, end, local_base=local_base,
+              exp_avg8=exp_avg8, exp_avg_scale=exp_avg_scale, exp_rms8=exp_rms8, exp_rms_scale=exp_rms_scale)
 
 
 # ---------------------------------------------------------------- losses on token log-probabilities
-def _here(t, name: str, dtype, elems: int):
-    """A contiguous device tensor of one dtype with at least `elems` elements: its address."""
-    _dev(t, name, dtype)
-    _need(t, name, elems)
-    return t.data_ptr()
-
-
-def _rows(t, name: str):
+def _rows(t, name: str, dev: int):
     """(rows, vocabulary, row stride) of a [rows, vocabulary] device tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be [rows, vocabulary], got {t.dim()} dimensions")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device.index != _torch().cuda.current_device():
-        raise ValueError(f"{name} lives on {t.device}, not on the current device "
-                         f"cuda:{_torch().cuda.current_device()}")
-    n, v = t.shape
-    if v > 1 and t.stride(1) != 1:
+    if t.get_device() != dev:
+        _dev(t, name)
+    (n, v), (stride, inner) = t.shape, t.stride()
+    if v > 1 and inner != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    stride = t.stride(0) if n > 1 else v
-    if stride < v:
+    if n <= 1:
+        stride = v
+    elif stride < v:
         raise ValueError(f"the rows of {name} overlap")
     return n, v, stride
 
 
-def _logits(logits, targets):
+def _logits(logits, targets, dlogits=None):
+    """The device's index, its stream, (logits, dtype, rows, vocabulary, row stride, targets) and (dlogits, row stride)."""
     torch = _torch()
-    if logits.dtype not in (torch.float16, torch.bfloat16, torch.float32):
-        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
-    n, v, stride = _rows(logits, "logits")
+    dt = logits.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float16 and dt is not torch.float32:
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {dt}")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a device tensor")
+    dev, stream = _device_stream()
+    n, v, stride = _rows(logits, "logits", dev)
     if targets.numel() != n:
         raise ValueError(f"{targets.numel()} targets for {n} rows")
-    return n, v, stride, _here(targets, "targets", torch.int64, n)
+    tptr = _addr(targets, "targets", torch.int64, n, dev)
+    grad = (None, 0)
+    if dlogits is not None:
+        if dlogits.dtype is not dt or dlogits.shape != logits.shape:
+            raise ValueError("dlogits must have the dtype and shape of logits")
+        grad = (dlogits.data_ptr(), _rows(dlogits, "dlogits", dev)[2])
+    return dev, stream, (logits.data_ptr(), _dtype_code(logits), n, v, stride, tptr), grad
 
 
-def _dlogits(a, dlogits, logits):
-    if dlogits is None:
-        return
-    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
-        raise ValueError("dlogits must have the dtype and shape of logits")
-    a.dlogits_stride = _rows(dlogits, "dlogits")[2]
-    a.dlogits = dlogits.data_ptr()
+def _space(t, dev: int):
+    """(address, bytes) of a workspace."""
+    return _addr(t, "workspace", t.dtype, 0, dev), t.numel() * t.element_size()
 
 
 def zero_token_logprobs(logits, targets, logp, *, temperature: float = 1.0) -> None:
@@ -764,9 +767,8 @@ def zero_token_logprobs(logits, targets, logp, *, temperature: float = 1.0) -> N
     any row stride; ``targets`` int64; ``logp`` float32.  A target outside the
     vocabulary (-100) gives 0.
     """
-    n, v, stride, tptr = _logits(logits, targets)
-    _check(lib().zero_token_logprobs(logits.data_ptr(), _dtype_code(logits), n, v, stride, tptr, temperature,
-                                     _here(logp, "logp", _torch().float32, n), _stream()))
+    dev, stream, rows, _ = _logits(logits, targets)
+    _check(lib().zero_token_logprobs(*rows, temperature, _addr(logp, "logp", _torch().float32, rows[2], dev), stream))
 
 
 def _workspace(fn, *sizes, device=None):
@@ -802,22 +804,15 @@ def zero_policy_loss(logits, targets, *, old_logp, advantage, divisor: float, st
     that counts for nothing.  ``workspace`` from ``policy_workspace``.
     """
     f32 = _torch().float32
-    a = PolicyArgs()
-    n, a.vocab, a.row_stride, a.targets = _logits(logits, targets)
-    a.logits, a.dtype, a.n_rows = logits.data_ptr(), _dtype_code(logits), n
-    a.old_logp = _here(old_logp, "old_logp", f32, n)
-    a.advantage = _here(advantage, "advantage", f32, n)
-    if ref_logp is not None:
-        a.ref_logp = _here(ref_logp, "ref_logp", f32, n)
-    if weight is not None:
-        a.weight = _here(weight, "weight", f32, n)
-    a.divisor, a.clip_low, a.clip_high, a.kl_coef = divisor, clip_low, clip_high, kl_coef
-    a.temperature, a.grad_scale = temperature, grad_scale
-    a.stats, a.logp = _here(stats, "stats", f32, 4), _here(logp, "logp", f32, n)
-    _dlogits(a, dlogits, logits)
-    _dev(workspace, "workspace")
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib().zero_policy_loss(ct.byref(a), _stream()))
+    dev, stream, rows, grad = _logits(logits, targets, dlogits)
+    n = rows[2]
+    a = PolicyArgs(*rows, _addr(old_logp, "old_logp", f32, n, dev),
+                   None if ref_logp is None else _addr(ref_logp, "ref_logp", f32, n, dev),
+                   _addr(advantage, "advantage", f32, n, dev),
+                   None if weight is None else _addr(weight, "weight", f32, n, dev), divisor, clip_low, clip_high,
+                   kl_coef, temperature, grad_scale, _addr(stats, "stats", f32, 4, dev),
+                   _addr(logp, "logp", f32, n, dev), *grad, *_space(workspace, dev))
+    _check(lib().zero_policy_loss(ct.byref(a), stream))
 
 
 def zero_preference_loss(logits, targets, seq_begin, *, ref_logp, stats, logp, seq_logp, reward, workspace,
@@ -841,19 +836,13 @@ def zero_preference_loss(logits, targets, seq_begin, *, ref_logp, stats, logp, s
     if seq_begin.numel() % 2 != 1 or seq_begin.numel() < 3:
         raise ValueError("seq_begin holds 2 * pairs + 1 boundaries of at least one pair")
     pairs = seq_begin.numel() // 2
-    a = PreferenceArgs()
-    n, a.vocab, a.row_stride, a.targets = _logits(logits, targets)
-    a.logits, a.dtype, a.n_rows, a.n_pairs = logits.data_ptr(), _dtype_code(logits), n, pairs
-    a.seq_begin = _here(seq_begin, "seq_begin", torch.int64, 2 * pairs + 1)
-    a.ref_logp = _here(ref_logp, "ref_logp", f32, 2 * pairs)
-    a.beta, a.label_smoothing, a.average = beta, label_smoothing, int(average)
-    a.temperature, a.grad_scale = temperature, grad_scale
-    a.stats, a.logp = _here(stats, "stats", f32, 2), _here(logp, "logp", f32, n)
-    a.seq_logp, a.reward = _here(seq_logp, "seq_logp", f32, 2 * pairs), _here(reward, "reward", f32, 2 * pairs)
-    _dlogits(a, dlogits, logits)
-    _dev(workspace, "workspace")
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib().zero_preference_loss(ct.byref(a), _stream()))
+    dev, stream, rows, grad = _logits(logits, targets, dlogits)
+    a = PreferenceArgs(*rows, _addr(seq_begin, "seq_begin", torch.int64, 2 * pairs + 1, dev), pairs,
+                       _addr(ref_logp, "ref_logp", f32, 2 * pairs, dev), beta, label_smoothing, int(average),
+                       temperature, grad_scale, _addr(stats, "stats", f32, 2, dev),
+                       _addr(logp, "logp", f32, rows[2], dev), _addr(seq_logp, "seq_logp", f32, 2 * pairs, dev),
+                       _addr(reward, "reward", f32, 2 * pairs, dev), *grad, *_space(workspace, dev))
+    _check(lib().zero_preference_loss(ct.byref(a), stream))
 
 
 # ---------------------------------------------------------------- convenience
@@ -868,13 +857,14 @@ class OwnerShard:
     def __init__(self, numels: Sequence[int], ranks: int, owner: int, align: int = 64,
                  max_chunk: int = 2048, device=None):
         torch = _torch()
-        self.numels = [int(x) for x in numels]
-        self.offsets, self.padded_total, begins, ends = zero_shard_layout(self.numels, ranks, align)
+        sizes = _u64(numels)  # once: each of the tables below takes the sizes
+        self.numels = sizes.tolist()
+        self.offsets, self.padded_total, begins, ends = zero_shard_layout(sizes, ranks, align)
         self.ranks, self.owner = ranks, owner
         self.begin, self.end = int(begins[owner]), int(ends[owner])
         self.local_base = self.begin & ~7
         self.local_size = self.end - self.local_base
-        self.chunks = zero_chunk_table(self.numels, self.offsets, self.begin, self.end, max_chunk)
+        self.chunks = zero_chunk_table(sizes, self.offsets, self.begin, self.end, max_chunk)
         self.device = torch.device(device or "cuda")
         self.chunks_dev = chunks_to_device(self.chunks, self.device)
         # short chunks packed several to a block, when that saves enough blocks
@@ -885,7 +875,7 @@ class OwnerShard:
             self.groups_dev = torch.from_numpy(self.groups.astype(np.int64)).to(self.device)
         self.n_real = int(self.chunks["len"].sum()) if self.chunks.size else 0
         self.align = align
-        self.dense_offsets, self.dense_total = zero_dense_offsets(self.numels)
+        self.dense_offsets, self.dense_total = zero_dense_offsets(sizes)
         self.tensor_offset_dev = torch.from_numpy(self.offsets.astype(np.int64)).to(self.device)
         self.dense_offset_dev = torch.from_numpy(self.dense_offsets.astype(np.int64)).to(self.device)
 
@@ -1032,12 +1022,13 @@ class OwnerShard8(OwnerShard):
 
     def __init__(self, numels: Sequence[int], ranks: int, owner: int, align: int = 64,
                  max_chunk: int = 2048, device=None):
-        super().__init__(numels, ranks, owner, align, max_chunk, device)
+        sizes = _u64(numels)
+        super().__init__(sizes, ranks, owner, align, max_chunk, device)
         torch = _torch()
         self.local_base = self.begin // ZERO_QBLOCK * ZERO_QBLOCK
         self.local_size = self.end - self.local_base
         self.blocks = -(-self.local_size // ZERO_QBLOCK)
-        self.pieces, masks = zero_piece_table(self.numels, self.offsets, self.begin, self.end)
+        self.pieces, masks = zero_piece_table(sizes, self.offsets, self.begin, self.end)
         self.pieces_dev = chunks_to_device(self.pieces, self.device)
         self.masks_dev = torch.from_numpy(masks).to(self.device) if masks.size else None
 

@@ -111,8 +111,8 @@ __device__ __forceinline__ u32x2 quantise(const float (&x)[8], float* scale) {
   for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7FFFFFFFu);
   const float m = __uint_as_float(row_max(top));
   const bool dead = m < kLiveMin;  // false for NaN
-  const float inv = dead ? 0.0f : kCodeMax / m;
-  *scale = dead ? 0.0f : m / kCodeMax;
+  const float inv = dead ? 0.0f : kCodeMax * (1.0f / m);
+  *scale = dead ? 0.0f : m * (1.0f / kCodeMax);
   float q[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -231,8 +231,10 @@ __global__ void __launch_bounds__(kBlock) step8_kernel(const Step8Args a) {
         const bool real = bits >> k & 1;
         float gc = g[k] * a.c.clip;
         if (a.c.l2 != 0.0f) gc = fmaf(a.c.l2, w[k], gc);
-        const float mn = fmaf(a.c.beta1, m[k], a.c.one_minus_beta1 * gc);
-        const float v = fmaf(a.c.beta2 * r[k], r[k], (a.c.one_minus_beta2 * gc) * gc);
+        // m and v round after every operation: what a code's rounding turns on
+        // is then the same in any program that evaluates the formula in fp32
+        const float mn = a.c.beta1 * m[k] + a.c.one_minus_beta1 * gc;
+        const float v = (a.c.beta2 * r[k]) * r[k] + (a.c.one_minus_beta2 * gc) * gc;
         const float rn = __builtin_sqrtf(v);
         const float denom = fmaf(rn, a.c.inv_sqrt_bc2, a.c.eps);
         w[k] = fmaf(-a.c.step_size, mn / denom, w[k] * a.c.decay);
