@@ -1,8 +1,8 @@
 // Losses on token log-probabilities and their gradient of the logits.
 //
-// For a row x of logits, its target t and a temperature T,
-//   M = max x,  S = sum_j exp((x_j - M) / T),  lp = (x_t - M) / T - ln S,
-//   d lp / d x_j = ([j = t] - exp((x_j - M) / T) / S) / T,
+// For a row x of logits, its target t, a temperature T and any reference z,
+//   S = sum_j exp((x_j - z) / T),  lp = (x_t - z) / T - ln S,
+//   d lp / d x_j = ([j = t] - exp((x_j - z) / T) / S) / T,
 // so a loss that is a function of the rows' lp has the gradient
 //   dx_j = coef * ([j = t] - p_j)
 // with one number `coef` per row.  Everything over the vocabulary is one sum
@@ -10,20 +10,28 @@
 // operations per row, done in fp64 by one thread, since the lp of hundreds of
 // tokens are added and their differences exponentiated.
 //
-// The elements are fp32 (the differences x_j - M are exact for 16-bit logits
-// near the maximum), exp is the hardware's 2^x with log2(e) / T as its factor.
-// In the sum that factor has a second word: fp32's error of log2(e), 1.3e-8,
-// moves every row's ln S the same way, and a sequence adds up hundreds of rows
+// The reference is the target's own logit: it needs no pass over the row, is
+// the same for every thread (partial sums simply add), and lp = -ln S.  It
+// serves unless the row's maximum is some 40 T above it; a sum that is not
+// below 2^60 (NaN, infinity) sends the row through a second form whose
+// reference is the maximum, found as it goes.
+//
+// The elements are fp32, exp is the hardware's 2^x with log2(e) / T as its
+// factor.  Where rows are added up to sequences that factor has a second word:
+// fp32's error of log2(e), 1.3e-8, moves every row's ln S the same way
 // (measured on 500-token sequences: rewards 5e-6 off without it, 4e-7 with
 // it).  Per-thread sums are fp32 over at most a few hundred elements and are
-// added up in fp64.  A row whose target is outside [0, vocab), or whose
-// logits are all -inf, counts for nothing: lp 0, gradient 0, and nothing of it
-// is looked at.  NaN and +inf logits in a row that counts give NaN.
+// added up in fp64.
+//
+// A row whose target is outside [0, vocab), or whose logits are all -inf,
+// counts for nothing: lp 0, gradient 0, and nothing of it is looked at.  NaN
+// and +inf logits in a row that counts give NaN.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "internal.h"
 #include "launch.h"
@@ -45,24 +53,66 @@ struct Logits {
   double inv_t;  // 1 / T
 };
 
-// One row of storage type T from its first element: `head` elements up to the
-// first 16-byte boundary, `n_vec` vectors of eight, then the tail.
+// One row: n_vec vectors of eight from its first element, then up to seven
+// elements more.
 template <int DT>
 struct Row {
   const void* x;
-  uint32_t head, n_vec, vocab;
+  uint32_t n_vec, vocab;
 
-  __device__ __forceinline__ Row(const Logits& a, uint64_t row) {
-    typedef typename Vec<DT>::T T;
-    const T* p = static_cast<const T*>(a.x) + row * a.stride;
-    x = p;
-    vocab = a.vocab;
-    const uint32_t off = (uint32_t)((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / (uint32_t)sizeof(T);
-    head = min(off, vocab);
-    n_vec = (vocab - head) / 8;
-  }
-  __device__ __forceinline__ uint32_t tail() const { return head + 8 * n_vec; }
+  __device__ __forceinline__ Row(const Logits& a, uint64_t row)
+      : x(static_cast<const typename Vec<DT>::T*>(a.x) + row * a.stride), n_vec(a.vocab / 8), vocab(a.vocab) {}
 };
+
+// ln s for finite s > 0 (NaN for NaN), and e^x - 1 and e^x, in fp64 to about
+// 1e-14, relative: s = 2^e m with m next to 1 and ln m = 2 artanh((m - 1) /
+// (m + 1)) by its series; x = n ln 2 + r and e^r - 1 by its Taylor polynomial.
+// They take some 20 registers where the general functions take 100, which a
+// block that holds a row in registers does not have.
+__device__ __forceinline__ double ln(double s) {
+  int e = __builtin_amdgcn_frexp_exp(s);
+  double m = __builtin_amdgcn_frexp_mant(s);
+  if (m < 0.70710678118654752) {
+    m += m;
+    --e;
+  }
+  const double t = (m - 1.0) / (m + 1.0), q = t * t;
+  double p = 1.0 / 17;
+  p = fma(p, q, 1.0 / 15);
+  p = fma(p, q, 1.0 / 13);
+  p = fma(p, q, 1.0 / 11);
+  p = fma(p, q, 1.0 / 9);
+  p = fma(p, q, 1.0 / 7);
+  p = fma(p, q, 1.0 / 5);
+  p = fma(p, q, 1.0 / 3);
+  const double u = t + t;
+  return fma((double)e, 0.693147180559945309, fma(u * q, p, u));
+}
+
+struct Exp {
+  double value, minus1;
+};
+
+__device__ __forceinline__ Exp exp_both(double x) {
+  x = x < -800.0 ? -800.0 : x > 800.0 ? 800.0 : x;  // beyond both ends of fp64; NaN stays
+  const double n = rint(x * 1.44269504088896341);
+  // ln 2 as its fp32 value, whose product with n is exact, and the rest
+  const double r = fma(n, 1.90465429995776805e-9, fma(n, -0.693147182464599609375, x));
+  double p = 1.0 / 479001600;
+  p = fma(p, r, 1.0 / 39916800);
+  p = fma(p, r, 1.0 / 3628800);
+  p = fma(p, r, 1.0 / 362880);
+  p = fma(p, r, 1.0 / 40320);
+  p = fma(p, r, 1.0 / 5040);
+  p = fma(p, r, 1.0 / 720);
+  p = fma(p, r, 1.0 / 120);
+  p = fma(p, r, 1.0 / 24);
+  p = fma(p, r, 1.0 / 6);
+  p = fma(p, r, 0.5);
+  p = fma(p * r, r, r);  // e^r - 1
+  const double value = ldexp(1.0 + p, (int)n);
+  return {value, n == 0.0 ? p : value - 1.0};
+}
 
 // A running (maximum, sum of exp2((x - max) c)).
 struct MaxSum {
@@ -83,9 +133,10 @@ __device__ __forceinline__ MaxSum join(const MaxSum& a, const MaxSum& b, const L
   return {m, a.s * (double)term(a.m, z, in) + b.s * (double)term(b.m, z, in)};
 }
 
-// Over the block, in a fixed tree; the result is in every thread.
+// Over a block of W wavefronts, in a fixed tree; the result is in every thread.
+template <int W>
 __device__ __forceinline__ MaxSum block_join(MaxSum v, const Logits& in) {
-  __shared__ MaxSum part[kWavesPerBlock];
+  __shared__ MaxSum part[W];
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v = join(v, MaxSum{__shfl_xor(v.m, off, 64), __shfl_xor(v.s, off, 64)}, in);
   __syncthreads();  // `part` may still be read for the row before
@@ -93,92 +144,195 @@ __device__ __forceinline__ MaxSum block_join(MaxSum v, const Logits& in) {
   __syncthreads();
   v = part[0];
 #pragma unroll
-  for (int i = 1; i < kWavesPerBlock; ++i) v = join(v, part[i], in);
+  for (int i = 1; i < W; ++i) v = join(v, part[i], in);
   return v;
 }
 
-// (M, S) of a row, in every thread of the block.
-template <int DT>
+// coef at the target's place, `at` elements after the first of these eight (if
+// it is one of them).
+__device__ __forceinline__ void add_at_target(float (&dx)[8], uint32_t at, float coef) {
+  if (at < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dx[i] += at == (uint32_t)i ? coef : 0.0f;
+  }
+}
+
+// Sum of one double per thread over a block of W wavefronts, in a fixed tree;
+// in every thread.
+template <int W = kWavesPerBlock>
+__device__ __forceinline__ double block_sum(double x) {
+  __shared__ double part[W];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) x = x + __shfl_xor(x, off, 64);
+  if (W == 1) return x;
+  __syncthreads();  // `part` may still be read for the sum before
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = part[0];
+#pragma unroll
+  for (int i = 1; i < W; ++i) x = x + part[i];
+  return x;
+}
+
+// The sum with reference z over a row by a block of 64 W threads, in every
+// thread.
+template <int DT, int W = kWavesPerBlock>
+__device__ __forceinline__ double row_sum(const Row<DT>& r, float z, const Logits& in) {
+  const uint32_t t = threadIdx.x;
+  float s = 0.0f;
+#pragma unroll 4
+  for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
+    const auto raw = load8_any<DT>(r.x, v);
+    float e = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e += term(Vec<DT>::get(raw, k), z, in);
+    s += e;
+  }
+  const uint32_t j = 8 * r.n_vec + t;
+  if (j < r.vocab) s += term(Vec<DT>::load1(r.x, j), z, in);
+  return block_sum<W>((double)s);
+}
+
+// (reference, sum) with the row's maximum as the reference, found on the way;
+// (0, 0) when every logit is -inf.
+template <int DT, int W = kWavesPerBlock>
 __device__ __forceinline__ MaxSum row_max_sum(const Row<DT>& r, const Logits& in) {
   const uint32_t t = threadIdx.x;
   float m = -INFINITY, s = 0.0f;
-  auto add = [&](float vm, auto&& sum) {
-    const float nm = fmaxf(m, vm), z = finite_or_zero(nm);
-    s = s * term(m, z, in) + sum(z);
+  auto add = [&](float x) {
+    const float nm = fmaxf(m, x), z = finite_or_zero(nm);
+    s = s * term(m, z, in) + term(x, z, in);
     m = nm;
   };
-  for (uint32_t v = t; v < r.n_vec; v += kBlock) {
-    const auto raw = load8<DT>(r.x, r.head + 8 * (uint64_t)v);
-    float vm = Vec<DT>::get(raw, 0);
+  for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
+    const auto raw = load8_any<DT>(r.x, v);
 #pragma unroll
-    for (int k = 1; k < 8; ++k) vm = fmaxf(vm, Vec<DT>::get(raw, k));
-    add(vm, [&](float z) {
-      float e = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) e += term(Vec<DT>::get(raw, k), z, in);
-      return e;
-    });
+    for (int k = 0; k < 8; ++k) add(Vec<DT>::get(raw, k));
   }
-  auto one = [&](uint32_t j) {
-    const float x = Vec<DT>::load1(r.x, j);
-    add(x, [&](float z) { return term(x, z, in); });
-  };
-  if (t < r.head) one(t);
-  for (uint32_t j = r.tail() + t; j < r.vocab; j += kBlock) one(j);
-  return block_join(MaxSum{m, (double)s}, in);
+  const uint32_t j = 8 * r.n_vec + t;
+  if (j < r.vocab) add(Vec<DT>::load1(r.x, j));
+  MaxSum all = block_join<W>(MaxSum{m, (double)s}, in);
+  all.m = finite_or_zero(all.m);
+  return all;
 }
 
-// The target's log-probability; false if the row counts for nothing.
-template <int DT>
-__device__ __forceinline__ bool row_logp(const Logits& a, const Row<DT>& r, int64_t target, const MaxSum& ms,
-                                         double* lp) {
-  *lp = 0.0;
-  if (ms.s == 0.0) return false;
-  const float d = Vec<DT>::load1(r.x, (uint64_t)target) - ms.m;
-  *lp = (double)d * a.inv_t - log(ms.s);
-  return true;
+// A sum that the reference xt serves (false for NaN).
+__device__ __forceinline__ bool served(double s) { return s < 0x1p60; }
+
+// A row's reference and sum; lp and whether the row counts follow.
+struct RowSum {
+  float z;
+  double s;
+  __device__ __forceinline__ bool counts() const { return s != 0.0; }  // true for NaN
+  __device__ __forceinline__ double logp(float xt, const Logits& in) const {
+    return counts() ? (double)(xt - z) * in.inv_t - ln(s) : 0.0;
+  }
+};
+
+template <int DT, int W = kWavesPerBlock>
+__device__ __forceinline__ RowSum row_reduce(const Row<DT>& r, float xt, const Logits& in) {
+  const double s = row_sum<DT, W>(r, xt, in);
+  if (served(s)) return {xt, s};
+  const MaxSum ms = row_max_sum<DT, W>(r, in);
+  return {ms.m, ms.s};
 }
 
 // dx = coef ([j = t] - p) over the row by the block; zeros when coef is 0.
 // `out` may be the row itself: each element is read and written by one thread.
-template <int DT>
-__device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_t target, float m, double sum, float c,
+template <int DT, int W = kWavesPerBlock>
+__device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_t target, const RowSum& rs, float c,
                                              float coef) {
   const uint32_t t = threadIdx.x;
-  const float z = finite_or_zero(m);
-  const float k = (float)(-(double)coef / sum);
-  auto one = [&](uint32_t j) {
+  const float k = (float)(-(double)coef / rs.s);
+  for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
+    float dx[8] = {};
+    if (coef != 0.0f) {
+      const auto raw = load8_any<DT>(r.x, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dx[i] = k * __builtin_amdgcn_exp2f((Vec<DT>::get(raw, i) - rs.z) * c);
+      add_at_target(dx, (uint32_t)target - 8 * v, coef);
+    }
+    store8_any<DT>(out, v, dx);
+  }
+  const uint32_t j = 8 * r.n_vec + t;
+  if (j < r.vocab) {
     float dx = 0.0f;
     if (coef != 0.0f) {
-      dx = k * __builtin_amdgcn_exp2f((Vec<DT>::load1(r.x, j) - z) * c);
+      dx = k * __builtin_amdgcn_exp2f((Vec<DT>::load1(r.x, j) - rs.z) * c);
       if (j == target) dx += coef;
     }
     Vec<DT>::store1(out, j, dx);
-  };
-  typedef typename Vec<DT>::T T;
-  const bool aligned = (reinterpret_cast<uintptr_t>(static_cast<T*>(out) + r.head) & 15u) == 0;
-  if (aligned) {
-    for (uint32_t v = t; v < r.n_vec; v += kBlock) {
-      const uint32_t j0 = r.head + 8 * v;
-      float dx[8] = {};
-      if (coef != 0.0f) {
-        const auto raw = load8<DT>(r.x, j0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dx[i] = k * __builtin_amdgcn_exp2f((Vec<DT>::get(raw, i) - z) * c);
-        if (target >= j0 && target < j0 + 8) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (j0 + i == target) dx[i] += coef;
-        }
-      }
-      store8<DT>(out, j0, dx);
-    }
-    if (t < r.head) one(t);
-    for (uint32_t j = r.tail() + t; j < r.vocab; j += kBlock) one(j);
-  } else {
-    for (uint32_t j = t; j < r.vocab; j += kBlock) one(j);
   }
 }
+
+// A row spread over a block of 64 W threads, K vectors and at most one element
+// of the tail per thread.  Threads past the row's last vector load that one
+// again and count it as 0, so that all loads are issued before the first is
+// waited for, without branches; steps that no thread of the block needs are
+// left out (only the upper half's can be: a smaller block takes the row
+// otherwise).
+template <int DT, int W, int K>
+struct Spread {
+  static constexpr uint32_t kStep = 64 * W;
+  typename Vec<DT>::Raw x[K];
+  float last;
+
+  static __device__ __forceinline__ bool step(int k, const Row<DT>& r) { return k < K / 2 || k * kStep < r.n_vec; }
+
+  __device__ __forceinline__ Spread(const Row<DT>& r, uint32_t t) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (step(k, r)) x[k] = load8_any<DT>(r.x, min(k * kStep + t, r.n_vec - 1));
+    const uint32_t j = 8 * r.n_vec + t;
+    last = j < r.vocab ? Vec<DT>::load1(r.x, j) : 0.0f;
+  }
+
+  // This thread's share of the sum; term(x) is an element's, and keep(k, i, q)
+  // sees it (k = K: the tail's).
+  template <typename T, typename F>
+  __device__ __forceinline__ float sum(const Row<DT>& r, uint32_t t, T term, F keep) const {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (step(k, r)) {
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float q = term(Vec<DT>::get(x[k], i));
+          keep(k, i, q);
+          part += q;
+        }
+        s += k * kStep + t < r.n_vec ? part : 0.0f;
+      }
+    }
+    const float q = term(last);
+    keep(K, 0, q);
+    return 8 * r.n_vec + t < r.vocab ? s + q : s;
+  }
+};
+
+// Calls fn with the block (wavefronts, vectors per thread) whose threads hold a
+// row in registers: 8 vectors each, 16 of the longest 16-bit rows.  False if
+// none does.
+template <int DT, typename F>
+bool with_spread(uint32_t vocab, F fn) {
+  const uint32_t n_vec = vocab / 8;
+  auto is = [&](auto w, auto k) {
+    if (n_vec == 0 || n_vec > 64u * decltype(w)::value * decltype(k)::value) return false;
+    fn(w, k);
+    return true;
+  };
+  using K8 = std::integral_constant<int, 8>;
+  if (is(std::integral_constant<int, 1>{}, K8{}) || is(std::integral_constant<int, 2>{}, K8{}) ||
+      is(std::integral_constant<int, 4>{}, K8{}) || is(std::integral_constant<int, 8>{}, K8{}) ||
+      is(std::integral_constant<int, 16>{}, K8{}))
+    return true;
+  if constexpr (DT != ZERO_F32) return is(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
+  return false;
+}
+
+// One block per row, as many rows to a launch as its threads may number.
+constexpr uint64_t kMostRows = 1u << 21;
 
 __device__ __forceinline__ bool in_vocab(int64_t target, uint32_t vocab) { return target >= 0 && target < (int64_t)vocab; }
 
@@ -188,33 +342,70 @@ __device__ __forceinline__ bool in_vocab(int64_t target, uint32_t vocab) { retur
 // What the preference loss keeps of a row between its passes.
 struct RowStats {
   double lp, sum;
-  float m, coef;
+  float z, coef;
 };
 
 struct LogpArgs {
   Logits in;
+  uint64_t row0;  // of a launch's first block
   float* logp;
   RowStats* stats;  // NULL unless a later pass needs them
 };
+
+__device__ __forceinline__ void logp_finish(const LogpArgs& a, uint64_t row, const RowSum& rs, float xt) {
+  const double lp = rs.logp(xt, a.in);
+  a.logp[row] = (float)lp;
+  if (a.stats) a.stats[row] = RowStats{lp, rs.s, rs.z, 0.0f};  // sum 0: does not count
+}
 
 template <int DT>
 __global__ void __launch_bounds__(kBlock) logp_kernel(const LogpArgs a) {
   for (uint64_t row = blockIdx.x; row < a.in.n_rows; row += gridDim.x) {
     const int64_t target = a.in.targets[row];
-    MaxSum ms = {-INFINITY, 0.0};
-    double lp = 0.0;
-    bool counts = false;
+    RowSum rs = {0.0f, 0.0};
+    float xt = 0.0f;
     if (in_vocab(target, a.in.vocab)) {  // the same for the whole block
       const Row<DT> r(a.in, row);
-      ms = row_max_sum(r, a.in);
-      counts = row_logp(a.in, r, target, ms, &lp);
+      xt = Vec<DT>::load1(r.x, (uint64_t)target);
+      rs = row_reduce(r, xt, a.in);
     }
-    if (threadIdx.x == 0) {
-      a.logp[row] = (float)lp;
-      // a row that does not count keeps sum 0
-      if (a.stats) a.stats[row] = RowStats{lp, counts ? ms.s : 0.0, ms.m, 0.0f};
-    }
+    if (threadIdx.x == 0) logp_finish(a, row, rs, xt);
   }
+}
+
+// TWO: with the exponent factor's second word (for sequences).  Without it the
+// factor and the reference are one fma, as in the policy loss, whose lp has
+// the same bits.
+template <int DT, int W, int K, bool TWO>
+__global__ void __launch_bounds__(64 * W, 4) logp_spread_kernel(const LogpArgs a) {
+  const uint32_t t = threadIdx.x;
+  const uint64_t row = a.row0 + blockIdx.x;
+  const int64_t target = a.in.targets[row];
+  RowSum rs = {0.0f, 0.0};
+  float xt = 0.0f;
+  if (in_vocab(target, a.in.vocab)) {
+    const Row<DT> r(a.in, row);
+    xt = Vec<DT>::load1(r.x, (uint64_t)target);
+    const Spread<DT, W, K> x(r, t);
+    const float b = -xt * a.in.c;
+    const float s = x.sum(
+        r, t, [&](float v) { return TWO ? term(v, xt, a.in) : __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
+        [](int, int, float) {});
+    rs = {xt, block_sum<W>((double)s)};
+    if (!__builtin_amdgcn_readfirstlane(served(rs.s))) rs = row_reduce<DT, W>(r, xt, a.in);
+  }
+  if (t == 0) logp_finish(a, row, rs, xt);
+}
+
+template <int DT, bool TWO>
+void launch_logp(LogpArgs a, hipStream_t s) {
+  const bool done = with_spread<DT>(a.in.vocab, [&](auto w, auto k) {
+    constexpr int W = decltype(w)::value, K = decltype(k)::value;
+    for (a.row0 = 0; a.row0 < a.in.n_rows; a.row0 += kMostRows)
+      hipLaunchKernelGGL((logp_spread_kernel<DT, W, K, TWO>), (uint32_t)std::min(kMostRows, a.in.n_rows - a.row0),
+                         64 * W, 0, s, a);
+  });
+  if (!done) hipLaunchKernelGGL(logp_kernel<DT>, chunk_grid(a.in.n_rows, 0), kBlock, 0, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -227,6 +418,7 @@ struct PolicyTerms {
 
 struct PolicyArgs {
   Logits in;
+  uint64_t row0;  // of a launch's first block
   const float *old_logp, *ref_logp, *advantage, *weight;
   double inv_divisor, low, high, kl_coef, grad_scale;
   float *logp, *stats;
@@ -243,7 +435,7 @@ __device__ __forceinline__ float policy_row(const PolicyArgs& a, uint64_t row, d
   const double adv = (double)a.advantage[row];
   double slope = 0.0;
   if (adv != 0.0) {  // 0 times an overflowed ratio is 0
-    const double ratio = exp(lp - (double)a.old_logp[row]);
+    const double ratio = exp_both(lp - (double)a.old_logp[row]).value;
     const double free = adv * ratio, held = adv * fmin(fmax(ratio, a.low), a.high);
     const bool clipped = held < free;
     out->gain = w * (clipped ? held : free);
@@ -251,11 +443,39 @@ __device__ __forceinline__ float policy_row(const PolicyArgs& a, uint64_t row, d
     slope = clipped ? 0.0 : -free;
   }
   if (a.ref_logp) {
-    const double d = (double)a.ref_logp[row] - lp, e = expm1(d);
+    const double d = (double)a.ref_logp[row] - lp, e = exp_both(d).minus1;
     out->kl = w * (isinf(e) ? e : e - d);  // d is infinite too when lp is -inf
     if (a.kl_coef != 0.0) slope -= a.kl_coef * e;
   }
   return (float)(w * slope * a.grad_scale * a.in.inv_t);
+}
+
+// The row's log-probability and terms to memory, by one thread; its coefficient.
+__device__ __forceinline__ float policy_finish(const PolicyArgs& a, uint64_t row, const RowSum& rs, float xt) {
+  const double lp = rs.logp(xt, a.in);
+  PolicyTerms terms = {0.0, 0.0, 0.0};
+  const float coef = rs.counts() ? policy_row(a, row, lp, &terms) : 0.0f;
+  a.logp[row] = (float)lp;
+  a.terms[row] = terms;
+  return coef;
+}
+
+template <int DT>
+__device__ __forceinline__ typename Vec<DT>::T* policy_out(const PolicyArgs& a, uint64_t row) {
+  return static_cast<typename Vec<DT>::T*>(a.dlogits) + row * a.dstride;
+}
+
+// A whole row by a block of 64 W threads, read from memory twice (the second
+// time mostly from the caches).  `coef` is the block's.
+template <int DT, int W>
+__device__ __forceinline__ void policy_stream(const PolicyArgs& a, uint64_t row, const Row<DT>& r, int64_t target,
+                                              float xt, bool in_range, float* s_coef) {
+  RowSum rs = {0.0f, 0.0};
+  if (in_range) rs = row_reduce<DT, W>(r, xt, a.in);
+  __syncthreads();  // s_coef may still be read for the row before
+  if (threadIdx.x == 0) *s_coef = policy_finish(a, row, rs, xt);
+  __syncthreads();
+  if (a.dlogits) row_gradient<DT, W>(r, policy_out<DT>(a, row), target, rs, a.in.c, *s_coef);
 }
 
 template <int DT>
@@ -263,41 +483,78 @@ __global__ void __launch_bounds__(kBlock) policy_kernel(const PolicyArgs a) {
   __shared__ float s_coef;
   for (uint64_t row = blockIdx.x; row < a.in.n_rows; row += gridDim.x) {
     const int64_t target = a.in.targets[row];
+    const bool in_range = in_vocab(target, a.in.vocab);
     const Row<DT> r(a.in, row);
-    MaxSum ms = {-INFINITY, 0.0};
-    float coef = 0.0f;
-    if (in_vocab(target, a.in.vocab)) {
-      ms = row_max_sum(r, a.in);
-      if (threadIdx.x == 0) {
-        double lp;
-        PolicyTerms terms = {0.0, 0.0, 0.0};
-        if (row_logp(a.in, r, target, ms, &lp)) coef = policy_row(a, row, lp, &terms);
-        a.logp[row] = (float)lp;
-        a.terms[row] = terms;
-        s_coef = coef;
-      }
-      __syncthreads();
-      coef = s_coef;
-    } else if (threadIdx.x == 0) {
-      a.logp[row] = 0.0f;
-      a.terms[row] = PolicyTerms{0.0, 0.0, 0.0};
-    }
-    if (a.dlogits)
-      row_gradient(r, static_cast<typename Vec<DT>::T*>(a.dlogits) + row * a.dstride, target, ms.m, ms.s, a.in.c, coef);
+    const float xt = in_range ? Vec<DT>::load1(r.x, (uint64_t)target) : 0.0f;
+    policy_stream<DT, kWavesPerBlock>(a, row, r, target, xt, in_range, &s_coef);
   }
 }
 
-// Sum of one double per thread over the block, in a fixed tree; in thread 0.
-__device__ __forceinline__ double block_sum(double x) {
-  __shared__ double part[kWavesPerBlock];
+// A row held in registers, so that the logits are read once.  RAW keeps the
+// 16-bit logits (4 registers a vector) and takes every exponential twice;
+// otherwise the exponentials themselves stay (8 registers a vector).
+template <int DT, int W, int K, bool RAW>
+__global__ void __launch_bounds__(64 * W, 4) policy_spread_kernel(const PolicyArgs a) {
+  __shared__ float s_coef, s_scale;
+  const uint32_t t = threadIdx.x;
+  const uint64_t row = a.row0 + blockIdx.x;
+  const int64_t target = a.in.targets[row];
+  const Row<DT> r(a.in, row);
+  if (!in_vocab(target, a.in.vocab)) return policy_stream<DT, W>(a, row, r, target, 0.0f, false, &s_coef);
+  const float xt = Vec<DT>::load1(r.x, (uint64_t)target);
+  const Spread<DT, W, K> x(r, t);
+  float e[RAW ? 1 : K][8], last = 0.0f;
+  float b = -xt * a.in.c;
+  const float s = x.sum(
+      r, t, [&](float v) { return __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
+      [&](int k, int i, float q) {
+        if (k == K) last = q;
+        else if constexpr (!RAW) e[k][i] = q;
+      });
+  const RowSum rs = {xt, block_sum<W>((double)s)};
+  if (!__builtin_amdgcn_readfirstlane(served(rs.s)))  // the same in every thread
+    return policy_stream<DT, W>(a, row, r, target, xt, true, &s_coef);
+  if (t == 0) {
+    s_coef = policy_finish(a, row, rs, xt);
+    s_scale = (float)(-(double)s_coef / rs.s);
+  }
+  __syncthreads();
+  if (!a.dlogits) return;
+  const float coef = s_coef, scale = s_scale;
+  typename Vec<DT>::T* out = policy_out<DT>(a, row);
+  const uint32_t at = (uint32_t)target - 8 * t;
+  if constexpr (RAW) asm volatile("" : "+v"(b));  // the exponentials are taken again, not kept
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) x = x + __shfl_xor(x, off, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = part[0];
-  for (int i = 1; i < kWavesPerBlock; ++i) x = x + part[i];
-  return x;
+  for (int k = 0; k < K; ++k) {
+    const uint32_t v = k * 64 * W + t;
+    if (v < r.n_vec) {
+      float dx[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (RAW) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Vec<DT>::get(x.x[k], i), a.in.c, b));
+        else dx[i] = scale * e[k][i];
+      }
+      add_at_target(dx, at - k * 64 * W * 8, coef);
+      store8_any<DT>(out, v, dx);
+    }
+  }
+  const uint32_t j = 8 * r.n_vec + t;
+  if (j < r.vocab) {
+    float dx = scale * last;
+    if (j == target) dx += coef;
+    Vec<DT>::store1(out, j, dx);
+  }
+}
+
+template <int DT>
+void launch_policy(PolicyArgs a, hipStream_t s) {
+  const bool done = with_spread<DT>(a.in.vocab, [&](auto w, auto k) {
+    constexpr int W = decltype(w)::value, K = decltype(k)::value;
+    for (a.row0 = 0; a.row0 < a.in.n_rows; a.row0 += kMostRows)
+      hipLaunchKernelGGL((policy_spread_kernel<DT, W, K, (K > 8)>), (uint32_t)std::min(kMostRows, a.in.n_rows - a.row0),
+                         64 * W, 0, s, a);
+  });
+  if (!done) hipLaunchKernelGGL(policy_kernel<DT>, chunk_grid(a.in.n_rows, 0), kBlock, 0, s, a);
 }
 
 __global__ void __launch_bounds__(kBlock) policy_fold_kernel(const PolicyTerms* terms, uint64_t n, double kl_coef,
@@ -414,8 +671,8 @@ __global__ void __launch_bounds__(kBlock) preference_grad_kernel(const GradArgs 
   for (uint64_t row = blockIdx.x - 1; row < a.in.n_rows; row += gridDim.x - 1) {
     const RowStats x = a.rows[row];
     const Row<DT> r(a.in, row);
-    row_gradient(r, static_cast<typename Vec<DT>::T*>(a.dlogits) + row * a.dstride, a.in.targets[row], x.m, x.sum,
-                 a.in.c, x.coef);
+    row_gradient(r, static_cast<typename Vec<DT>::T*>(a.dlogits) + row * a.dstride, a.in.targets[row],
+                 RowSum{x.z, x.sum}, a.in.c, x.coef);
   }
 }
 
@@ -430,7 +687,8 @@ int fill_logits(Logits* in, const void* logits, int dtype, uint64_t n_rows, uint
                 const int64_t* targets, double temperature, const char* who) {
   if (dtype != ZERO_F16 && dtype != ZERO_BF16 && dtype != ZERO_F32)
     return fail(ZERO_EINVAL, "%s: unknown logits dtype %d", who, dtype);
-  if (vocab == 0 || vocab > (uint32_t)INT32_MAX) return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^31)", who, vocab);
+  if (vocab == 0 || vocab / 8 > kMaxRowVecs)
+    return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^29]", who, vocab);
   if (stride < vocab) return fail(ZERO_EINVAL, "%s: rows of %u logits overlap at a stride of %llu", who, vocab,
                                   (unsigned long long)stride);
   if (!std::isfinite(temperature) || temperature <= 0.0)
@@ -494,9 +752,7 @@ extern "C" int zero_token_logprobs(const void* logits, int dtype, uint64_t n_row
   if (!logp || !aligned_to(logp, 4)) return fail(ZERO_EINVAL, "%s: logp is NULL or misaligned", who);
   if ((rc = begin_launch())) return rc;
   a.logp = logp;
-  by_dtype(dtype, [&](auto dt) {
-    hipLaunchKernelGGL(logp_kernel<decltype(dt)::value>, chunk_grid(n_rows, 0), kBlock, 0, stream, a);
-  });
+  by_dtype(dtype, [&](auto dt) { launch_logp<decltype(dt)::value, false>(a, stream); });
   return launch_status(who);
 }
 
@@ -549,9 +805,7 @@ extern "C" int zero_policy_loss(const zero_policy_args* p, hipStream_t stream) {
   a.dstride = p->dlogits_stride;
   a.terms = static_cast<PolicyTerms*>(p->workspace);
   if (p->n_rows > 0) {
-    by_dtype(p->dtype, [&](auto dt) {
-      hipLaunchKernelGGL(policy_kernel<decltype(dt)::value>, chunk_grid(p->n_rows, 0), kBlock, 0, stream, a);
-    });
+    by_dtype(p->dtype, [&](auto dt) { launch_policy<decltype(dt)::value>(a, stream); });
     if ((rc = launch_status(who))) return rc;
   }
   hipLaunchKernelGGL(policy_fold_kernel, 1, kBlock, 0, stream, a.terms, p->n_rows, p->kl_coef, p->stats);
@@ -596,9 +850,7 @@ extern "C" int zero_preference_loss(const zero_preference_args* p, hipStream_t s
   l.stats = rows;
   const uint32_t grid = chunk_grid(p->n_rows, 0);
   if (p->n_rows > 0) {
-    by_dtype(p->dtype, [&](auto dt) {
-      hipLaunchKernelGGL(logp_kernel<decltype(dt)::value>, grid, kBlock, 0, stream, l);
-    });
+    by_dtype(p->dtype, [&](auto dt) { launch_logp<decltype(dt)::value, true>(l, stream); });
     if ((rc = launch_status(who))) return rc;
   }
   const PairArgs q = {rows, p->n_rows, p->seq_begin, p->n_pairs, p->ref_logp, p->beta, p->label_smoothing,

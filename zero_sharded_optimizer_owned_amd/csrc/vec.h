@@ -109,6 +109,41 @@ __device__ __forceinline__ void store8(void* base, uint64_t e, const float (&x)[
   }
 }
 
+// The same at any address that suits the elements: rows of logits start where
+// an odd vocabulary puts them.  gfx950 loads and stores 16 bytes at any such
+// address in one instruction.
+// Rows are addressed by a base that is the same in every thread and a 32-bit
+// vector number, so that one register holds a thread's place in all of them.
+constexpr uint32_t kMaxRowVecs = 1u << 26;  // a row's byte offsets fit 32 bits
+
+template <int DT>
+__device__ __forceinline__ typename Vec<DT>::Raw load8_any(const void* base, uint32_t v) {
+  typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+  typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+  const char* p = static_cast<const char*>(base) + v * (uint32_t)(8 * sizeof(typename Vec<DT>::T));
+  if constexpr (DT == ZERO_F32) {
+    const f32x4_any* q = reinterpret_cast<const f32x4_any*>(p);
+    return {q[0], q[1]};
+  } else {
+    return {*reinterpret_cast<const u32x4_any*>(p)};
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8_any(void* base, uint32_t v, const float (&x)[8]) {
+  typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+  typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+  char* p = static_cast<char*>(base) + v * (uint32_t)(8 * sizeof(typename Vec<DT>::T));
+  if constexpr (DT == ZERO_F32) {
+    f32x4_any* q = reinterpret_cast<f32x4_any*>(p);
+    q[0] = f32x4{x[0], x[1], x[2], x[3]};
+    q[1] = f32x4{x[4], x[5], x[6], x[7]};
+  } else {
+    *reinterpret_cast<u32x4_any*>(p) = u32x4{Vec<DT>::pack(x[0], x[1]), Vec<DT>::pack(x[2], x[3]),
+                                             Vec<DT>::pack(x[4], x[5]), Vec<DT>::pack(x[6], x[7])};
+  }
+}
+
 // Eight e4m3 codes (8 bytes) to and from fp32, by the hardware's conversions:
 // decoding is exact, encoding rounds to nearest even.  Values beyond 464 do
 // not occur (the callers scale by the block's largest magnitude).
