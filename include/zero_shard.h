@@ -666,7 +666,8 @@ typedef struct {
   float *logp;            /* [n_rows] */
   void *dlogits;          /* same dtype as logits; may be logits itself; NULL: no gradient */
   uint64_t dlogits_stride;
-  void *workspace;        /* zero_policy_workspace_bytes(n_rows), 256-byte aligned */
+  void *workspace;        /* zero_policy_workspace_bytes(n_rows), 256-byte aligned; zeros before its first use,
+                             left ready for the next call; calls that overlap need one each */
   size_t workspace_bytes;
 } zero_policy_args;
 

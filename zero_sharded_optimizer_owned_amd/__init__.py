@@ -775,16 +775,17 @@ def _workspace(fn, *sizes, device=None):
     out = np.zeros(1, dtype=np.uint64)
     _check(fn(*sizes, _p(out)))
     torch = _torch()
-    return torch.empty(int(out[0]), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(int(out[0]), dtype=torch.uint8, device=device or "cuda")
 
 
 def policy_workspace(n_rows: int, device=None):
-    """The device workspace of ``zero_policy_loss`` over n_rows rows."""
+    """The device workspace of ``zero_policy_loss`` over up to n_rows rows: zeros before
+    its first use, then left ready for the next call (one call at a time)."""
     return _workspace(lib().zero_policy_workspace_bytes, n_rows, device=device)
 
 
 def preference_workspace(n_rows: int, n_pairs: int, device=None):
-    """The device workspace of ``zero_preference_loss`` over n_rows rows and n_pairs pairs."""
+    """The device workspace of ``zero_preference_loss`` over up to n_rows rows and n_pairs pairs."""
     return _workspace(lib().zero_preference_workspace_bytes, n_rows, n_pairs, device=device)
 
 

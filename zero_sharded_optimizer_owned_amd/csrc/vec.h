@@ -116,31 +116,42 @@ __device__ __forceinline__ void store8(void* base, uint64_t e, const float (&x)[
 // vector number, so that one register holds a thread's place in all of them.
 constexpr uint32_t kMaxRowVecs = 1u << 26;  // a row's byte offsets fit 32 bits
 
-template <int DT>
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+
+template <int DT, bool NT = false>
 __device__ __forceinline__ typename Vec<DT>::Raw load8_any(const void* base, uint32_t v) {
-  typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-  typedef f32x4 __attribute__((aligned(4))) f32x4_any;
   const char* p = static_cast<const char*>(base) + v * (uint32_t)(8 * sizeof(typename Vec<DT>::T));
   if constexpr (DT == ZERO_F32) {
     const f32x4_any* q = reinterpret_cast<const f32x4_any*>(p);
-    return {q[0], q[1]};
+    if constexpr (NT) return {__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)};
+    else return {q[0], q[1]};
   } else {
-    return {*reinterpret_cast<const u32x4_any*>(p)};
+    const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
+    if constexpr (NT) return {__builtin_nontemporal_load(q)};
+    else return {*q};
   }
 }
 
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void store8_any(void* base, uint32_t v, const float (&x)[8]) {
-  typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-  typedef f32x4 __attribute__((aligned(4))) f32x4_any;
   char* p = static_cast<char*>(base) + v * (uint32_t)(8 * sizeof(typename Vec<DT>::T));
   if constexpr (DT == ZERO_F32) {
     f32x4_any* q = reinterpret_cast<f32x4_any*>(p);
-    q[0] = f32x4{x[0], x[1], x[2], x[3]};
-    q[1] = f32x4{x[4], x[5], x[6], x[7]};
+    const f32x4 lo = {x[0], x[1], x[2], x[3]}, hi = {x[4], x[5], x[6], x[7]};
+    if constexpr (NT) {
+      __builtin_nontemporal_store((f32x4_any)lo, q);
+      __builtin_nontemporal_store((f32x4_any)hi, q + 1);
+    } else {
+      q[0] = lo;
+      q[1] = hi;
+    }
   } else {
-    *reinterpret_cast<u32x4_any*>(p) = u32x4{Vec<DT>::pack(x[0], x[1]), Vec<DT>::pack(x[2], x[3]),
-                                             Vec<DT>::pack(x[4], x[5]), Vec<DT>::pack(x[6], x[7])};
+    u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
+    const u32x4 w = {Vec<DT>::pack(x[0], x[1]), Vec<DT>::pack(x[2], x[3]), Vec<DT>::pack(x[4], x[5]),
+                     Vec<DT>::pack(x[6], x[7])};
+    if constexpr (NT) __builtin_nontemporal_store((u32x4_any)w, q);
+    else *q = w;
   }
 }
 
