@@ -53,15 +53,34 @@ struct Logits {
   double inv_t;  // 1 / T
 };
 
-// One row: n_vec vectors of eight from its first element, then up to seven
-// elements more.
+// One row of `vocab` elements: n_vec vectors of eight from the first 128-byte
+// boundary on, and up to 70 elements before and after them, one to a thread.
+// Rows of most vocabularies start anywhere.  Vectors from the row's own start
+// ran 30% slower between two 4-byte words (4096 rows of 50,001 bf16: policy
+// loss 210 us, now 168), and 9-15% slower at other odd places once the
+// gradients go past the caches (2048 rows of 128,001: 218 us and, preference
+// loss, 310; now 199 and 270, as for 128,000).
+constexpr uint32_t kRowAlign = 128;
+
 template <int DT>
 struct Row {
-  const void* x;
+  const void* x;       // the row's first element
+  const void* v;       // the first vector
+  uint32_t head;       // elements before it
   uint32_t n_vec, vocab;
 
-  __device__ __forceinline__ Row(const Logits& a, uint64_t row)
-      : x(static_cast<const typename Vec<DT>::T*>(a.x) + row * a.stride), n_vec(a.vocab / 8), vocab(a.vocab) {}
+  __device__ __forceinline__ Row(const Logits& a, uint64_t row) {
+    typedef typename Vec<DT>::T T;
+    const T* p = static_cast<const T*>(a.x) + row * a.stride;
+    vocab = a.vocab;
+    head = min((uint32_t)(-reinterpret_cast<uintptr_t>(p) & (kRowAlign - 1u)) / (uint32_t)sizeof(T), vocab);
+    x = p;
+    v = p + head;
+    n_vec = (vocab - head) / 8;
+  }
+  // Thread t's element beside the vectors, if it has one.
+  __device__ __forceinline__ bool has_side(uint32_t t) const { return t < vocab - 8 * n_vec; }
+  __device__ __forceinline__ uint32_t side(uint32_t t) const { return t < head ? t : 8 * n_vec + t; }
 };
 
 // ln s for finite s > 0 (NaN for NaN), and e^x - 1 and e^x, in fp64 to about
@@ -182,14 +201,13 @@ __device__ __forceinline__ double row_sum(const Row<DT>& r, float z, const Logit
   float s = 0.0f;
 #pragma unroll 4
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
-    const auto raw = load8_any<DT>(r.x, v);
+    const auto raw = load8_any<DT>(r.v, v);
     float e = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) e += term(Vec<DT>::get(raw, k), z, in);
     s += e;
   }
-  const uint32_t j = 8 * r.n_vec + t;
-  if (j < r.vocab) s += term(Vec<DT>::load1(r.x, j), z, in);
+  if (r.has_side(t)) s += term(Vec<DT>::load1(r.x, r.side(t)), z, in);
   return block_sum<W>((double)s);
 }
 
@@ -205,12 +223,11 @@ __device__ __forceinline__ MaxSum row_max_sum(const Row<DT>& r, const Logits& in
     m = nm;
   };
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
-    const auto raw = load8_any<DT>(r.x, v);
+    const auto raw = load8_any<DT>(r.v, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) add(Vec<DT>::get(raw, k));
   }
-  const uint32_t j = 8 * r.n_vec + t;
-  if (j < r.vocab) add(Vec<DT>::load1(r.x, j));
+  if (r.has_side(t)) add(Vec<DT>::load1(r.x, r.side(t)));
   MaxSum all = block_join<W>(MaxSum{m, (double)s}, in);
   all.m = finite_or_zero(all.m);
   return all;
@@ -244,18 +261,19 @@ __device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_
                                              float coef) {
   const uint32_t t = threadIdx.x;
   const float k = (float)(-(double)coef / rs.s);
+  void* out_v = static_cast<typename Vec<DT>::T*>(out) + r.head;
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
     float dx[8] = {};
     if (coef != 0.0f) {
-      const auto raw = load8_any<DT, NT>(r.x, v);
+      const auto raw = load8_any<DT, NT>(r.v, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) dx[i] = k * __builtin_amdgcn_exp2f((Vec<DT>::get(raw, i) - rs.z) * c);
-      add_at_target(dx, (uint32_t)target - 8 * v, coef);
+      add_at_target(dx, (uint32_t)target - r.head - 8 * v, coef);
     }
-    store8_any<DT, NT>(out, v, dx);
+    store8_any<DT, NT>(out_v, v, dx);
   }
-  const uint32_t j = 8 * r.n_vec + t;
-  if (j < r.vocab) {
+  if (r.has_side(t)) {
+    const uint32_t j = r.side(t);
     float dx = 0.0f;
     if (coef != 0.0f) {
       dx = k * __builtin_amdgcn_exp2f((Vec<DT>::load1(r.x, j) - rs.z) * c);
@@ -266,31 +284,29 @@ __device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_
 }
 
 // A row spread over a block of 64 W threads, K vectors and at most one element
-// of the tail per thread.  Threads past the row's last vector load that one
+// beside them per thread.  Threads past the row's last vector load that one
 // again and count it as 0, so that all loads are issued before the first is
-// waited for, without branches; steps that no thread of the block needs are
-// left out (only the upper half's can be: a smaller block takes the row
-// otherwise).
+// waited for, without branches; steps of the upper half that no thread of the
+// block needs are left out.
 // NT: loaded with the nontemporal hint, where no later pass reads them again
 // (log-probabilities of 4096 x 128,000: 157 us without it, 150 with it).
 template <int DT, int W, int K, bool NT>
 struct Spread {
   static constexpr uint32_t kStep = 64 * W;
   typename Vec<DT>::Raw x[K];
-  float last;
+  float side;
 
   static __device__ __forceinline__ bool step(int k, const Row<DT>& r) { return k < K / 2 || k * kStep < r.n_vec; }
 
   __device__ __forceinline__ Spread(const Row<DT>& r, uint32_t t) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (step(k, r)) x[k] = load8_any<DT, NT>(r.x, min(k * kStep + t, r.n_vec - 1));
-    const uint32_t j = 8 * r.n_vec + t;
-    last = j < r.vocab ? Vec<DT>::load1(r.x, j) : 0.0f;
+      if (step(k, r)) x[k] = load8_any<DT, NT>(r.v, min(k * kStep + t, r.n_vec - 1));
+    side = r.has_side(t) ? Vec<DT>::load1(r.x, r.side(t)) : 0.0f;
   }
 
   // This thread's share of the sum; term(x) is an element's, and keep(k, i, q)
-  // sees it (k = K: the tail's).
+  // sees it (k = K: the one beside the vectors).
   template <typename T, typename F>
   __device__ __forceinline__ float sum(const Row<DT>& r, uint32_t t, T term, F keep) const {
     float s = 0.0f;
@@ -307,27 +323,26 @@ struct Spread {
         s += k * kStep + t < r.n_vec ? part : 0.0f;
       }
     }
-    const float q = term(last);
+    const float q = term(side);
     keep(K, 0, q);
-    return 8 * r.n_vec + t < r.vocab ? s + q : s;
+    return r.has_side(t) ? s + q : s;
   }
 };
 
 // Calls fn with the block (wavefronts, vectors per thread) whose threads hold a
 // row in registers: 8 vectors each, 16 of the longest 16-bit rows.  False if
-// none does.
+// none does, or the row is so short that no vector is sure to be left.
 template <int DT, typename F>
 bool with_spread(uint32_t vocab, F fn) {
   const uint32_t n_vec = vocab / 8;
   auto is = [&](auto w, auto k) {
-    if (n_vec == 0 || n_vec > 64u * decltype(w)::value * decltype(k)::value) return false;
+    if (vocab < 128 || n_vec > 64u * decltype(w)::value * decltype(k)::value) return false;
     fn(w, k);
     return true;
   };
   using K8 = std::integral_constant<int, 8>;
-  if (is(std::integral_constant<int, 1>{}, K8{}) || is(std::integral_constant<int, 2>{}, K8{}) ||
-      is(std::integral_constant<int, 4>{}, K8{}) || is(std::integral_constant<int, 8>{}, K8{}) ||
-      is(std::integral_constant<int, 16>{}, K8{}))
+  if (is(std::integral_constant<int, 2>{}, K8{}) || is(std::integral_constant<int, 4>{}, K8{}) ||
+      is(std::integral_constant<int, 8>{}, K8{}) || is(std::integral_constant<int, 16>{}, K8{}))
     return true;
   if constexpr (DT != ZERO_F32) return is(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
   return false;
@@ -569,12 +584,12 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   if (!in_vocab(target, a.in.vocab)) return policy_stream<DT, W, NT>(a, row, r, target, in, 0.0f, false, sh);
   const float xt = Vec<DT>::load1(r.x, (uint64_t)target);
   const Spread<DT, W, K, true> x(r, t);
-  float e[RAW ? 1 : K][8], last = 0.0f;
+  float e[RAW ? 1 : K][8], side = 0.0f;
   float b = -xt * a.in.c;
   const float s = x.sum(
       r, t, [&](float v) { return __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
       [&](int k, int i, float q) {
-        if (k == K) last = q;
+        if (k == K) side = q;
         else if constexpr (!RAW) e[k][i] = q;
       });
   const RowSum rs = {xt, block_sum<W>((double)s)};
@@ -589,7 +604,8 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   if (!a.dlogits) return;
   const float coef = sh.coef, scale = sh.scale;
   typename Vec<DT>::T* out = policy_out<DT>(a, row);
-  const uint32_t at = (uint32_t)target - 8 * t;
+  void* out_v = out + r.head;
+  const uint32_t at = (uint32_t)target - r.head - 8 * t;
   if constexpr (RAW) asm volatile("" : "+v"(b));  // the exponentials are taken again, not kept
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -602,12 +618,12 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
         else dx[i] = scale * e[k][i];
       }
       add_at_target(dx, at - k * 64 * W * 8, coef);
-      store8_any<DT, NT>(out, v, dx);
+      store8_any<DT, NT>(out_v, v, dx);
     }
   }
-  const uint32_t j = 8 * r.n_vec + t;
-  if (j < r.vocab) {
-    float dx = scale * last;
+  if (r.has_side(t)) {
+    const uint32_t j = r.side(t);
+    float dx = scale * side;
     if (j == target) dx += coef;
     Vec<DT>::store1(out, j, dx);
   }

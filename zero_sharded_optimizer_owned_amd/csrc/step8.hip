@@ -193,58 +193,167 @@ struct Step8Args {
   void* p16;
   uint64_t param_base;
   Adam8Const c;
+  uint32_t run;  // consecutive pieces to an XCD
 };
 
-constexpr int kStored = -1;  // gradient source: a stored owner-local fp32 gradient
+// Gradient source, fixed at compile time:
+//   RC > 0  : exactly RC rank buffers, all loads in flight together;
+//   RC == 0 : any number of rank buffers, four in flight;
+//   RC == kStored : a stored owner-local fp32 gradient.
+constexpr int kStored = -1;
 
-// Sum of the ranks in rank order, from +0, one fp32 add each, then one IEEE
+// The rank mean: ranks added in order from +0, one fp32 add each, then one IEEE
 // division (a product with the exact reciprocal of a power of two).
-template <int GDT>
-__device__ __forceinline__ void rank_mean(const Ranks8& rs, uint64_t f, uint32_t bits, float (&g)[8]) {
+__device__ __forceinline__ void mean(float (&g)[8], const Ranks8& rs) {
+  if (rs.div_pow2) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) g[k] = 0.0f;
-  for (uint32_t r = 0; r < rs.R; ++r) {
-    float x[8];
-    get8<GDT>(rs.ptr[r], f - rs.base, bits, x);
+    for (int k = 0; k < 8; ++k) g[k] = g[k] * rs.inv_divisor;
+  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = g[k] + x[k];
+    for (int k = 0; k < 8; ++k) g[k] = g[k] / rs.divisor;
   }
-#pragma unroll
-  for (int k = 0; k < 8; ++k) g[k] = rs.div_pow2 ? g[k] * rs.inv_divisor : g[k] / rs.divisor;
 }
 
-template <int GDT, int PDT>
-__global__ void __launch_bounds__(kBlock) step8_kernel(const Step8Args a) {
-  const uint32_t t = threadIdx.x;
-  for (uint64_t i = blockIdx.x; i < a.n_pieces; i += gridDim.x) {
-    const zero_piece pc = a.pieces[i];
-    const uint32_t bits = real_bits(pc, a.masks, a.n_masks, a.begin, a.end, a.local_base, t);
-    const uint64_t f = pc.flat + 8 * t, l = f - a.local_base;
-    float g[8] = {}, w[8], m[8] = {}, r[8] = {};
-    if (bits) {
-      load_moments(a.s, l, m, r);
-      get8<ZERO_F32>(a.w, l, bits, w);
-      if constexpr (GDT == kStored) get8<ZERO_F32>(a.reduced_g, l, bits, g);
-      else rank_mean<GDT>(a.rs, f, bits, g);
+template <int GDT>
+__device__ __forceinline__ void add8(float (&g)[8], const typename Vec<GDT>::Raw& x) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = g[k] + Vec<GDT>::get(x, k);
+}
+
+// The step on eight elements in registers.  m and v round after every
+// operation: what a code's rounding turns on is then the same in any program
+// that evaluates the formula in fp32.
+__device__ __forceinline__ void adam8(const Adam8Const& c, const float (&g)[8], float (&w)[8], float (&m)[8],
+                                      float (&r)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float gc = g[k] * c.clip;
+    if (c.l2 != 0.0f) gc = fmaf(c.l2, w[k], gc);
+    const float mn = c.beta1 * m[k] + c.one_minus_beta1 * gc;
+    const float v = (c.beta2 * r[k]) * r[k] + (c.one_minus_beta2 * gc) * gc;
+    const float rn = __builtin_sqrtf(v);
+    const float denom = fmaf(rn, c.inv_sqrt_bc2, c.eps);
+    w[k] = fmaf(-c.step_size, mn / denom, w[k] * c.decay);
+    m[k] = mn;
+    r[k] = rn;
+  }
+}
+
+// Eight elements that lie inside every buffer, as vectors: every load is issued
+// before the first is used.
+template <int GDT, int RC>
+__device__ __forceinline__ void load_vectors(const Step8Args& a, uint64_t f, float (&g)[8], float (&w)[8],
+                                             float (&m)[8], float (&r)[8]) {
+  constexpr bool kStream = GDT != ZERO_F32;  // 16-bit rank data is read once: nontemporal
+  constexpr int kBatch = RC > 0 ? RC : 4;
+  const uint64_t l = f - a.local_base;
+  typename Vec<GDT>::Raw x[RC == kStored ? 1 : kBatch];
+  if constexpr (RC == kStored) {
+    x[0] = load8<GDT>(a.reduced_g, l);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (RC > 0 || (uint32_t)j < a.rs.R) x[j] = load8<GDT, kStream>(a.rs.ptr[j], f - a.rs.base);
+  }
+  const u32x2 cm = *reinterpret_cast<const u32x2*>(a.s.m8 + l), cr = *reinterpret_cast<const u32x2*>(a.s.r8 + l);
+  const float ms = a.s.ms[l / kQBlock], rs = a.s.rs[l / kQBlock];
+  const auto xw = load8<ZERO_F32>(a.w, l);
+  __builtin_amdgcn_sched_barrier(0);  // no load sinks below the adds
+  if constexpr (RC == kStored) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = Vec<GDT>::get(x[0], k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = 0.0f;
+    if constexpr (RC > 0) {
+#pragma unroll
+      for (int j = 0; j < RC; ++j) add8<GDT>(g, x[j]);
+    } else {
+      for (uint32_t r0 = 0; r0 < a.rs.R; r0 += kBatch) {
+        typename Vec<GDT>::Raw y[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)  // the next four, while these are added
+          if (r0 + kBatch + j < a.rs.R) y[j] = load8<GDT, kStream>(a.rs.ptr[r0 + kBatch + j], f - a.rs.base);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (r0 + j < a.rs.R) add8<GDT>(g, x[j]);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) x[j] = y[j];
+      }
+    }
+    mean(g, a.rs);
+  }
+  decode8(cm, m);
+  decode8(cr, r);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    w[k] = Vec<ZERO_F32>::get(xw, k);
+    m[k] = m[k] * ms;
+    r[k] = r[k] * rs;
+  }
+}
+
+// The same element by element, for the vector that the buffers' end cuts.
+template <int GDT, int RC>
+__device__ __forceinline__ void load_elements(const Step8Args& a, uint64_t f, uint32_t bits, float (&g)[8],
+                                              float (&w)[8], float (&m)[8], float (&r)[8]) {
+  const uint64_t l = f - a.local_base;
+  load_moments(a.s, l, m, r);
+  get8<ZERO_F32>(a.w, l, bits, w);
+  if constexpr (RC == kStored) {
+    get8<ZERO_F32>(a.reduced_g, l, bits, g);
+  } else {
+    for (uint32_t j = 0; j < a.rs.R; ++j) {
+      float x[8];
+      get8<GDT>(a.rs.ptr[j], f - a.rs.base, bits, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] = g[k] + x[k];
+    }
+    mean(g, a.rs);
+  }
+}
+
+// A thread's eight elements of a piece; `bits` are the real ones (all of them
+// in a WHOLE piece).  Padding beside real elements is loaded with them and
+// then left out: it lies inside the buffers, and a vector at a time keeps
+// every load of the wavefront in flight together (element by element, blocks
+// of 100-element tensors took VTIMES).
+template <int GDT, int PDT, int RC, bool WHOLE>
+__device__ __forceinline__ void step_vector(const Step8Args& a, uint64_t f, uint32_t bits) {
+  const uint64_t l = f - a.local_base;
+  float g[8] = {}, w[8], m[8] = {}, r[8] = {};
+  if (WHOLE || bits) {
+    if (WHOLE || f + 8 <= a.end) load_vectors<GDT, RC>(a, f, g, w, m, r);
+    else load_elements<GDT, RC>(a, f, bits, g, w, m, r);
+    adam8(a.c, g, w, m, r);
+    if constexpr (!WHOLE) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const bool real = bits >> k & 1;
-        float gc = g[k] * a.c.clip;
-        if (a.c.l2 != 0.0f) gc = fmaf(a.c.l2, w[k], gc);
-        // m and v round after every operation: what a code's rounding turns on
-        // is then the same in any program that evaluates the formula in fp32
-        const float mn = a.c.beta1 * m[k] + a.c.one_minus_beta1 * gc;
-        const float v = (a.c.beta2 * r[k]) * r[k] + (a.c.one_minus_beta2 * gc) * gc;
-        const float rn = __builtin_sqrtf(v);
-        const float denom = fmaf(rn, a.c.inv_sqrt_bc2, a.c.eps);
-        w[k] = fmaf(-a.c.step_size, mn / denom, w[k] * a.c.decay);
-        m[k] = real ? mn : 0.0f;
-        r[k] = real ? rn : 0.0f;
+        m[k] = (bits >> k & 1) ? m[k] : 0.0f;
+        r[k] = (bits >> k & 1) ? r[k] : 0.0f;
       }
-      put8<ZERO_F32>(a.w, l, bits, w);
-      if constexpr (PDT != ZERO_NONE) put8<PDT>(a.p16, f - a.param_base, bits, w);
     }
-    store_moments(a.s, l, bits, m, r);
+    put8<ZERO_F32>(a.w, l, WHOLE ? 0xFFu : bits, w);
+    if constexpr (PDT != ZERO_NONE) put8<PDT, true>(a.p16, f - a.param_base, WHOLE ? 0xFFu : bits, w);
+  }
+  store_moments(a.s, l, WHOLE ? 0xFFu : bits, m, r);
+}
+
+__device__ __forceinline__ bool is_whole(const zero_piece& pc, uint64_t begin, uint64_t end) {
+  return pc.mask == ZERO_PIECE_WHOLE && pc.len == kPiece && pc.flat % kQBlock == 0 && pc.flat >= begin &&
+         pc.flat <= end && end - pc.flat >= kPiece;
+}
+
+template <int GDT, int PDT, int RC>
+__global__ void __launch_bounds__(kBlock) step8_kernel(const Step8Args a) {
+  const uint32_t t = threadIdx.x;
+  for (uint64_t i = xcd_runs(blockIdx.x, gridDim.x, a.run); i < a.n_pieces; i += gridDim.x) {
+    const zero_piece pc = a.pieces[i];
+    if (is_whole(pc, a.begin, a.end))
+      step_vector<GDT, PDT, RC, true>(a, pc.flat + 8 * t, 0xFFu);
+    else
+      step_vector<GDT, PDT, RC, false>(a, pc.flat + 8 * t,
+                                       real_bits(pc, a.masks, a.n_masks, a.begin, a.end, a.local_base, t));
   }
 }
 
@@ -336,12 +445,34 @@ int check_state8(const zero_piece* pieces, uint64_t n_pieces, const uint8_t* mas
   return ZERO_OK;
 }
 
-template <int GDT>
-void launch_step8(const Step8Args& a, int pdt, hipStream_t s) {
+template <int GDT, int RC>
+void launch_step8_p(Step8Args& a, int pdt, hipStream_t s) {
   const uint32_t grid = chunk_grid(a.n_pieces, 0);
-  if (pdt == ZERO_F16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_F16>), grid, kBlock, 0, s, a);
-  else if (pdt == ZERO_BF16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_BF16>), grid, kBlock, 0, s, a);
-  else hipLaunchKernelGGL((step8_kernel<GDT, ZERO_NONE>), grid, kBlock, 0, s, a);
+  // Whole pieces: at most three blocks to a CU and runs of two pieces to an
+  // XCD.  8 bf16 ranks into 1.0e8 elements: 520 us; two blocks 523, four 531,
+  // uncapped 537, single pieces 527.  Stored gradient, 3.75e8 elements: 1177
+  // us; two 1326, four 1240, uncapped 1258, single pieces 1185.  Pieces with
+  // padding are bound by their loads' round trips, not by HBM, and want every
+  // block that fits: 100-element tensors 45 us, 56 with three blocks, and 1.5
+  // more in runs of two.
+  const bool whole = 2 * a.n_masks <= a.n_pieces;
+  const uint32_t lds = whole ? lds_for_blocks_per_cu(3, 0) : 0;
+  a.run = whole ? 2 : 1;
+  if (pdt == ZERO_F16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_F16, RC>), grid, kBlock, lds, s, a);
+  else if (pdt == ZERO_BF16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_BF16, RC>), grid, kBlock, lds, s, a);
+  else hipLaunchKernelGGL((step8_kernel<GDT, ZERO_NONE, RC>), grid, kBlock, lds, s, a);
+}
+
+// Rank counts with all loads unrolled; any other count takes four at a time.
+template <int GDT>
+void launch_step8(Step8Args& a, int pdt, hipStream_t s) {
+  switch (a.rs.R) {
+    case 1: return launch_step8_p<GDT, 1>(a, pdt, s);
+    case 2: return launch_step8_p<GDT, 2>(a, pdt, s);
+    case 4: return launch_step8_p<GDT, 4>(a, pdt, s);
+    case 8: return launch_step8_p<GDT, 8>(a, pdt, s);
+    default: return launch_step8_p<GDT, 0>(a, pdt, s);
+  }
 }
 
 int convert8(bool pack, const zero_piece* pieces, uint64_t n_pieces, const uint8_t* masks, uint64_t n_masks,
@@ -425,7 +556,7 @@ extern "C" int zero_adam8_step(const zero_adam8_args* p, hipStream_t stream) {
   a.local_base = p->local_base;
   a.p16 = pdt != ZERO_NONE ? p->param16 : nullptr;
   a.param_base = p->param_base;
-  if (p->reduced_g) launch_step8<kStored>(a, pdt, stream);
+  if (p->reduced_g) launch_step8_p<ZERO_F32, kStored>(a, pdt, stream);
   else if (p->grad_dtype == ZERO_F16) launch_step8<ZERO_F16>(a, pdt, stream);
   else if (p->grad_dtype == ZERO_BF16) launch_step8<ZERO_BF16>(a, pdt, stream);
   else launch_step8<ZERO_F32>(a, pdt, stream);
