@@ -237,13 +237,12 @@ def zero_piece_table(numels: Sequence[int], offsets: Sequence[int], begin: int, 
     n, off = _u64(numels), _u64(offsets)
     if n.size != off.size:
         raise ValueError("numels and offsets differ in length")
+    most = max(0, end - begin) // ZERO_PIECE + 2  # windows that the range can touch
+    out, masks = np.empty(most, dtype=PIECE_DTYPE), np.empty((most, ZERO_PIECE // 8), dtype=np.uint8)
     count, n_masks = np.zeros(1, dtype=np.uint64), np.zeros(1, dtype=np.uint64)
-    args = (_p(n), _p(off), n.size, begin, end)
-    _check(lib().zero_piece_table(*args, None, 0, None, 0, _p(count), _p(n_masks)))
-    out = np.zeros(int(count[0]), dtype=PIECE_DTYPE)
-    masks = np.zeros((int(n_masks[0]), ZERO_PIECE // 8), dtype=np.uint8)
-    _check(lib().zero_piece_table(*args, _p(out), out.size, _p(masks), masks.shape[0], _p(count), _p(n_masks)))
-    return out, masks
+    _check(lib().zero_piece_table(_p(n), _p(off), n.size, begin, end, _p(out), most, _p(masks), most, _p(count),
+                                  _p(n_masks)))
+    return out[:int(count[0])].copy(), masks[:int(n_masks[0])].copy()
 
 
 def zero_state_bytes(params: int, ranks: int, param: int = 2, grad: int = 2,
@@ -635,10 +634,8 @@ def zero_stream_probe(srcs, dsts, order: int = 0, src_widths=None, dst_widths=No
 
 
 # ---------------------------------------------------------------- the step with 8-bit moments
-def _state8(dev, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8, exp_avg_scale, exp_rms8,
-            exp_rms_scale):
-    """Checks the piece table and the 8-bit state; returns (pieces, n_pieces, masks, n_masks,
-    begin, end) and the state's addresses (codes, scales of the first; codes, scales of the second)."""
+def _pieces8(dev, pieces_dev, n_pieces, masks_dev, begin, end):
+    """Checks a piece table; (pieces, n_pieces, masks, n_masks, begin, end) as the calls take them."""
     torch = _torch()
     pieces = masks = None
     n_masks = 0
@@ -647,31 +644,27 @@ def _state8(dev, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_av
     if masks_dev is not None and masks_dev.numel():
         masks = _addr(masks_dev, "masks", torch.uint8, 0, dev)
         n_masks = masks_dev.numel() // (ZERO_PIECE // 8)
+    return pieces, n_pieces, masks, n_masks, begin, end
+
+
+def _state8(dev, end, local_base, exp_avg8, exp_avg_scale, exp_rms8, exp_rms_scale):
+    """Checks the 8-bit state; its addresses (codes, scales of the first moment; codes, scales of the second)."""
+    torch = _torch()
     blocks = -(-(end - local_base) // ZERO_QBLOCK)
     e4m3, f32 = torch.float8_e4m3fn, torch.float32
-    return (pieces, n_pieces, masks, n_masks, begin, end), (
-        _addr(exp_avg8, "exp_avg8", e4m3, blocks * ZERO_QBLOCK, dev),
-        _addr(exp_avg_scale, "exp_avg_scale", f32, blocks, dev),
-        _addr(exp_rms8, "exp_rms8", e4m3, blocks * ZERO_QBLOCK, dev),
-        _addr(exp_rms_scale, "exp_rms_scale", f32, blocks, dev))
+    return (_addr(exp_avg8, "exp_avg8", e4m3, blocks * ZERO_QBLOCK, dev),
+            _addr(exp_avg_scale, "exp_avg_scale", f32, blocks, dev),
+            _addr(exp_rms8, "exp_rms8", e4m3, blocks * ZERO_QBLOCK, dev),
+            _addr(exp_rms_scale, "exp_rms_scale", f32, blocks, dev))
 
 
-def zero_adam8_step(*, pieces_dev, n_pieces: int, masks_dev=None, begin: int, end: int, master, exp_avg8,
-                    exp_avg_scale, exp_rms8, exp_rms_scale, local_base: int, step: int, lr: float, beta1: float,
-                    beta2: float, eps: float, weight_decay: float = 0.0, adamw: bool = True, rank_grads=None,
-                    grad_base: int = 0, divisor: float = 1.0, reduced_g=None, param16=None, param_base: int = 0,
-                    clip_coef: float = 1.0) -> None:
-    """Fused reduce + Adam/AdamW + 16-bit write-back whose moments are held in 8 bits:
-    ``exp_avg8``/``exp_rms8`` float8_e4m3fn codes, one fp32 scale per ZERO_QBLOCK of them,
-    over a device piece table from ``zero_piece_table``."""
+def _adam8(dev, stream, work, narrow, local_base, master, hyper, step, rank_grads, grad_base, divisor, reduced_g,
+           param16, param_base, clip_coef):
+    """The call itself, after _state8's checks: checks the other tensors and marshals."""
     torch = _torch()
-    f32 = torch.float32
-    dev, stream = _device_stream()
-    work, (m8, ms, r8, rs) = _state8(dev, pieces_dev, n_pieces, masks_dev, begin, end, local_base, exp_avg8,
-                                     exp_avg_scale, exp_rms8, exp_rms_scale)
-    ranks = None
+    f32, end = torch.float32, work[5]
+    ranks = g = p16 = None
     R = code = 0
-    g = p16 = None
     if reduced_g is not None:
         g = _addr(reduced_g, "reduced_g", f32, end - local_base, dev)
     else:
@@ -685,17 +678,35 @@ def zero_adam8_step(*, pieces_dev, n_pieces: int, masks_dev=None, begin: int, en
         if param16.dtype not in (torch.float16, torch.bfloat16):
             raise TypeError("param16 must be float16 or bfloat16")
         p16, pdt = _addr(param16, "param16", param16.dtype, end - param_base, dev), _dtype_code(param16)
+    m8, ms, r8, rs = narrow
+    lr, beta1, beta2, eps, weight_decay, adamw = hyper
     a = Adam8Args(*work, ct.addressof(ranks) if ranks is not None else None, R, code, grad_base, divisor, g,
                   _addr(master, "master", f32, end - local_base, dev), m8, r8, ms, rs, local_base, p16, pdt,
                   param_base, lr, beta1, beta2, eps, weight_decay, int(adamw), step, clip_coef)
     _check(lib().zero_adam8_step(ct.byref(a), stream))
 
 
-def _moments8(pack, exp_avg, exp_avg_sq, *state, local_base, **named):
-    f32 = _torch().float32
+def _hyper(lr, beta1, beta2, eps, weight_decay=0.0, adamw=True):
+    return lr, beta1, beta2, eps, weight_decay, adamw
+
+
+def zero_adam8_step(*, pieces_dev, n_pieces: int, masks_dev=None, begin: int, end: int, master, exp_avg8,
+                    exp_avg_scale, exp_rms8, exp_rms_scale, local_base: int, step: int, lr: float, beta1: float,
+                    beta2: float, eps: float, weight_decay: float = 0.0, adamw: bool = True, rank_grads=None,
+                    grad_base: int = 0, divisor: float = 1.0, reduced_g=None, param16=None, param_base: int = 0,
+                    clip_coef: float = 1.0) -> None:
+    """Fused reduce + Adam/AdamW + 16-bit write-back whose moments are held in 8 bits:
+    ``exp_avg8``/``exp_rms8`` float8_e4m3fn codes, one fp32 scale per ZERO_QBLOCK of them,
+    over a device piece table from ``zero_piece_table``."""
     dev, stream = _device_stream()
-    work, narrow = _state8(dev, *state, local_base=local_base, **named)
-    need = work[5] - local_base
+    work = _pieces8(dev, pieces_dev, n_pieces, masks_dev, begin, end)
+    narrow = _state8(dev, end, local_base, exp_avg8, exp_avg_scale, exp_rms8, exp_rms_scale)
+    _adam8(dev, stream, work, narrow, local_base, master, (lr, beta1, beta2, eps, weight_decay, adamw), step,
+           rank_grads, grad_base, divisor, reduced_g, param16, param_base, clip_coef)
+
+
+def _moments8(pack, dev, stream, work, narrow, local_base, exp_avg, exp_avg_sq):
+    f32, need = _torch().float32, work[5] - local_base
     wide = _addr(exp_avg, "exp_avg", f32, need, dev), _addr(exp_avg_sq, "exp_avg_sq", f32, need, dev)
     if pack:
         _check(lib().zero_moments8_pack(*work, local_base, *wide, *narrow, stream))
@@ -706,15 +717,19 @@ def _moments8(pack, exp_avg, exp_avg_sq, *state, local_base, **named):
 def zero_moments8_pack(*, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev=None, begin, end, local_base, exp_avg8,
                        exp_avg_scale, exp_rms8, exp_rms_scale) -> None:
     """The owner's fp32 moments into their 8-bit form."""
-    _moments8(True, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev, begin, end, local_base=local_base,
-              exp_avg8=exp_avg8, exp_avg_scale=exp_avg_scale, exp_rms8=exp_rms8, exp_rms_scale=exp_rms_scale)
+    dev, stream = _device_stream()
+    _moments8(True, dev, stream, _pieces8(dev, pieces_dev, n_pieces, masks_dev, begin, end),
+              _state8(dev, end, local_base, exp_avg8, exp_avg_scale, exp_rms8, exp_rms_scale), local_base, exp_avg,
+              exp_avg_sq)
 
 
 def zero_moments8_unpack(*, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev=None, begin, end, local_base, exp_avg8,
                          exp_avg_scale, exp_rms8, exp_rms_scale) -> None:
     """The owner's 8-bit moments as fp32 (scale * code, and the root's square)."""
-    _moments8(False, exp_avg, exp_avg_sq, pieces_dev, n_pieces, masks_dev, begin, end, local_base=local_base,
-              exp_avg8=exp_avg8, exp_avg_scale=exp_avg_scale, exp_rms8=exp_rms8, exp_rms_scale=exp_rms_scale)
+    dev, stream = _device_stream()
+    _moments8(False, dev, stream, _pieces8(dev, pieces_dev, n_pieces, masks_dev, begin, end),
+              _state8(dev, end, local_base, exp_avg8, exp_avg_scale, exp_rms8, exp_rms_scale), local_base, exp_avg,
+              exp_avg_sq)
 
 
 # ---------------------------------------------------------------- losses on token log-probabilities
@@ -1032,6 +1047,7 @@ class OwnerShard8(OwnerShard):
         self.pieces, masks = zero_piece_table(sizes, self.offsets, self.begin, self.end)
         self.pieces_dev = chunks_to_device(self.pieces, self.device)
         self.masks_dev = torch.from_numpy(masks).to(self.device) if masks.size else None
+        self._work = None
 
     def alloc_state(self):
         """master, then the moments: (codes, scales) of the first and of the second's root."""
@@ -1044,25 +1060,33 @@ class OwnerShard8(OwnerShard):
         return self.master, (self.exp_avg8, self.exp_avg_scale), (self.exp_rms8, self.exp_rms_scale)
 
     def _state8(self) -> dict:
+        """The piece table and 8-bit state as keyword arguments of the module's calls."""
         return dict(pieces_dev=self.pieces_dev, n_pieces=self.pieces.size, masks_dev=self.masks_dev, begin=self.begin,
                     end=self.end, local_base=self.local_base, exp_avg8=self.exp_avg8,
                     exp_avg_scale=self.exp_avg_scale, exp_rms8=self.exp_rms8, exp_rms_scale=self.exp_rms_scale)
+
+    def _checked(self):
+        """(device, stream, piece table, 8-bit state) of a call; the table is this object's own, checked once."""
+        dev, stream = _device_stream()
+        if self._work is None or self._work[0] != dev:
+            self._work = dev, _pieces8(dev, self.pieces_dev, self.pieces.size, self.masks_dev, self.begin, self.end)
+        return dev, stream, self._work[1], _state8(dev, self.end, self.local_base, self.exp_avg8, self.exp_avg_scale,
+                                                   self.exp_rms8, self.exp_rms_scale)
 
     def adam_step(self, *, step: int, hyper: dict, rank_grads=None, grad_base: int = 0,
                   divisor: float = 1.0, reduced_g=None, param16=None, param_base: int = 0,
                   clip_coef: float = 1.0, grid_blocks: int = 0) -> None:
         """``grid_blocks`` is accepted for ``OwnerShard``'s callers; this step has one launch shape."""
-        zero_adam8_step(**self._state8(), master=self.master, step=step, rank_grads=rank_grads, grad_base=grad_base,
-                        divisor=divisor, reduced_g=reduced_g, param16=param16, param_base=param_base,
-                        clip_coef=clip_coef, **hyper)
+        _adam8(*self._checked(), self.local_base, self.master, _hyper(**hyper), step, rank_grads, grad_base, divisor,
+               reduced_g, param16, param_base, clip_coef)
 
     def pack_moments(self, exp_avg, exp_avg_sq) -> None:
         """Take over fp32 moments (owner-local, from ``local_base``)."""
-        zero_moments8_pack(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, **self._state8())
+        _moments8(True, *self._checked(), self.local_base, exp_avg, exp_avg_sq)
 
     def unpack_moments(self, exp_avg, exp_avg_sq) -> None:
         """Write the moments as fp32 (for ``to_dense``, or to go on in 32 bits)."""
-        zero_moments8_unpack(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, **self._state8())
+        _moments8(False, *self._checked(), self.local_base, exp_avg, exp_avg_sq)
 
     _SAVED = ("master", "exp_avg8", "exp_avg_scale", "exp_rms8", "exp_rms_scale")
 

@@ -109,6 +109,14 @@ __device__ __forceinline__ void store8(void* base, uint64_t e, const float (&x)[
   }
 }
 
+// Four elements from index e, a multiple of 4.
+template <int DT>
+__device__ __forceinline__ void store4(void* base, uint64_t e, float a, float b, float c, float d) {
+  typename Vec<DT>::T* p = static_cast<typename Vec<DT>::T*>(base) + e;
+  if constexpr (DT == ZERO_F32) *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+  else *reinterpret_cast<u32x2*>(p) = u32x2{Vec<DT>::pack(a, b), Vec<DT>::pack(c, d)};
+}
+
 // The same at any address that suits the elements: rows of logits start where
 // an odd vocabulary puts them.  gfx950 loads and stores 16 bytes at any such
 // address in one instruction.
