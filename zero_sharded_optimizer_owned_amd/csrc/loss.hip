@@ -133,6 +133,12 @@ __device__ __forceinline__ Exp exp_both(double x) {
   return {value, n == 0.0 ? p : value - 1.0};
 }
 
+// A value that is the same in every thread, in a scalar register: rows in
+// registers leave none to spare.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // A running (maximum, sum of exp2((x - max) c)).
 struct MaxSum {
   float m;
@@ -293,6 +299,9 @@ __device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_
 template <int DT, int W, int K, bool NT>
 struct Spread {
   static constexpr uint32_t kStep = 64 * W;
+  // The largest block takes rows beyond its registers too: what is past them
+  // is read where it is needed.
+  static constexpr bool kRest = W == 16 && (K == 16 || DT == ZERO_F32);
   typename Vec<DT>::Raw x[K];
   float side;
 
@@ -323,6 +332,16 @@ struct Spread {
         s += k * kStep + t < r.n_vec ? part : 0.0f;
       }
     }
+    if constexpr (kRest) {
+#pragma unroll 2
+      for (uint32_t v = K * kStep + t; v < r.n_vec; v += kStep) {
+        const auto y = load8_any<DT>(r.v, v);
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part += term(Vec<DT>::get(y, i));
+        s += part;
+      }
+    }
     const float q = term(side);
     keep(K, 0, q);
     return r.has_side(t) ? s + q : s;
@@ -330,22 +349,19 @@ struct Spread {
 };
 
 // Calls fn with the block (wavefronts, vectors per thread) whose threads hold a
-// row in registers: 8 vectors each, 16 of the longest 16-bit rows.  False if
-// none does, or the row is so short that no vector is sure to be left.
+// row in registers: 8 vectors each, 16 of 16-bit rows past 65,536 elements.
+// False if the row is so short that no vector is sure to be left.
 template <int DT, typename F>
 bool with_spread(uint32_t vocab, F fn) {
+  if (vocab < 128) return false;
   const uint32_t n_vec = vocab / 8;
-  auto is = [&](auto w, auto k) {
-    if (vocab < 128 || n_vec > 64u * decltype(w)::value * decltype(k)::value) return false;
-    fn(w, k);
-    return true;
-  };
   using K8 = std::integral_constant<int, 8>;
-  if (is(std::integral_constant<int, 2>{}, K8{}) || is(std::integral_constant<int, 4>{}, K8{}) ||
-      is(std::integral_constant<int, 8>{}, K8{}) || is(std::integral_constant<int, 16>{}, K8{}))
-    return true;
-  if constexpr (DT != ZERO_F32) return is(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
-  return false;
+  if (n_vec <= 64 * 2 * 8) fn(std::integral_constant<int, 2>{}, K8{});
+  else if (n_vec <= 64 * 4 * 8) fn(std::integral_constant<int, 4>{}, K8{});
+  else if (n_vec <= 64 * 8 * 8) fn(std::integral_constant<int, 8>{}, K8{});
+  else if (n_vec <= 64 * 16 * 8 || DT == ZERO_F32) fn(std::integral_constant<int, 16>{}, K8{});
+  else if constexpr (DT != ZERO_F32) fn(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
+  return true;
 }
 
 // One block per row, as many rows to a launch as its threads may number.
@@ -449,12 +465,11 @@ struct PolicyArgs {
 // round trip to memory of its own where it is used.
 struct PolicyRow {
   float weight, advantage, old_logp, ref_logp;
-  __device__ __forceinline__ PolicyRow(const PolicyArgs& a, uint64_t row)
-      : weight(a.weight ? a.weight[row] : 1.0f),
-        advantage(a.advantage[row]),
-        old_logp(a.old_logp[row]),
-        ref_logp(a.ref_logp ? a.ref_logp[row] : 0.0f) {}
 };
+
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, uint64_t row) {
+  return {a.weight ? a.weight[row] : 1.0f, a.advantage[row], a.old_logp[row], a.ref_logp ? a.ref_logp[row] : 0.0f};
+}
 
 // The row's terms of the loss and its coefficient.
 __device__ __forceinline__ float policy_terms(const PolicyArgs& a, const PolicyRow& in, double lp, PolicyTerms* out) {
@@ -564,7 +579,7 @@ __global__ void __launch_bounds__(kBlock) policy_kernel(const PolicyArgs a) {
     const int64_t target = a.in.targets[row];
     const bool in_range = in_vocab(target, a.in.vocab);
     const Row<DT> r(a.in, row);
-    const PolicyRow in(a, row);
+    const PolicyRow in = policy_row(a, row);
     const float xt = in_range ? Vec<DT>::load1(r.x, (uint64_t)target) : 0.0f;
     policy_stream<DT, kWavesPerBlock, NT>(a, row, r, target, in, xt, in_range, sh);
     if (sh.last) policy_fold<kWavesPerBlock>(a.terms, a.in.n_rows, a.kl_coef, a.stats);
@@ -580,12 +595,14 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   const uint64_t row = a.row0 + blockIdx.x;
   const int64_t target = a.in.targets[row];
   const Row<DT> r(a.in, row);
-  const PolicyRow in(a, row);
+  PolicyRow in = policy_row(a, row);
   if (!in_vocab(target, a.in.vocab)) return policy_stream<DT, W, NT>(a, row, r, target, in, 0.0f, false, sh);
-  const float xt = Vec<DT>::load1(r.x, (uint64_t)target);
+  float xt = Vec<DT>::load1(r.x, (uint64_t)target);
   const Spread<DT, W, K, true> x(r, t);
+  in = PolicyRow{uniform(in.weight), uniform(in.advantage), uniform(in.old_logp), uniform(in.ref_logp)};
+  xt = uniform(xt);
   float e[RAW ? 1 : K][8], side = 0.0f;
-  float b = -xt * a.in.c;
+  float b = uniform(-xt * a.in.c);
   const float s = x.sum(
       r, t, [&](float v) { return __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
       [&](int k, int i, float q) {
@@ -606,7 +623,7 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   typename Vec<DT>::T* out = policy_out<DT>(a, row);
   void* out_v = out + r.head;
   const uint32_t at = (uint32_t)target - r.head - 8 * t;
-  if constexpr (RAW) asm volatile("" : "+v"(b));  // the exponentials are taken again, not kept
+  if constexpr (RAW) asm volatile("" : "+s"(b));  // the exponentials are taken again, not kept
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t v = k * 64 * W + t;
@@ -618,6 +635,16 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
         else dx[i] = scale * e[k][i];
       }
       add_at_target(dx, at - k * 64 * W * 8, coef);
+      store8_any<DT, NT>(out_v, v, dx);
+    }
+  }
+  if constexpr (Spread<DT, W, K, true>::kRest) {
+    for (uint32_t v = K * 64 * W + t; v < r.n_vec; v += 64 * W) {
+      const auto y = load8_any<DT, NT>(r.v, v);
+      float dx[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Vec<DT>::get(y, i), a.in.c, b));
+      add_at_target(dx, (uint32_t)target - r.head - 8 * v, coef);
       store8_any<DT, NT>(out_v, v, dx);
     }
   }
