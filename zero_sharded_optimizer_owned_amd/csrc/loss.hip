@@ -53,7 +53,7 @@ struct Logits {
   double inv_t;  // 1 / T
 };
 
-// One row of `vocab` elements: n_vec vectors of eight from the first 128-byte
+// One row of `vocab` elements: n_vec 16-byte vectors from the first 128-byte
 // boundary on, and up to 70 elements before and after them, one to a thread.
 // Rows of most vocabularies start anywhere.  Vectors from the row's own start
 // ran 30% slower between two 4-byte words (4096 rows of 50,001 bf16: policy
@@ -68,6 +68,7 @@ struct Row {
   const void* v;       // the first vector
   uint32_t head;       // elements before it
   uint32_t n_vec, vocab;
+  static constexpr uint32_t N = Lane<DT>::N;
 
   __device__ __forceinline__ Row(const Logits& a, uint64_t row) {
     typedef typename Vec<DT>::T T;
@@ -76,11 +77,11 @@ struct Row {
     head = min((uint32_t)(-reinterpret_cast<uintptr_t>(p) & (kRowAlign - 1u)) / (uint32_t)sizeof(T), vocab);
     x = p;
     v = p + head;
-    n_vec = (vocab - head) / 8;
+    n_vec = (vocab - head) / N;
   }
   // Thread t's element beside the vectors, if it has one.
-  __device__ __forceinline__ bool has_side(uint32_t t) const { return t < vocab - 8 * n_vec; }
-  __device__ __forceinline__ uint32_t side(uint32_t t) const { return t < head ? t : 8 * n_vec + t; }
+  __device__ __forceinline__ bool has_side(uint32_t t) const { return t < vocab - N * n_vec; }
+  __device__ __forceinline__ uint32_t side(uint32_t t) const { return t < head ? t : N * n_vec + t; }
 };
 
 // ln s for finite s > 0 (NaN for NaN), and e^x - 1 and e^x, in fp64 to about
@@ -173,12 +174,13 @@ __device__ __forceinline__ MaxSum block_join(MaxSum v, const Logits& in) {
   return v;
 }
 
-// coef at the target's place, `at` elements after the first of these eight (if
-// it is one of them).
-__device__ __forceinline__ void add_at_target(float (&dx)[8], uint32_t at, float coef) {
-  if (at < 8) {
+// coef at the target's place, `at` elements after the first of these (if it is
+// one of them).
+template <int N>
+__device__ __forceinline__ void add_at_target(float (&dx)[N], uint32_t at, float coef) {
+  if (at < N) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dx[i] += at == (uint32_t)i ? coef : 0.0f;
+    for (int i = 0; i < N; ++i) dx[i] += at == (uint32_t)i ? coef : 0.0f;
   }
 }
 
@@ -207,10 +209,10 @@ __device__ __forceinline__ double row_sum(const Row<DT>& r, float z, const Logit
   float s = 0.0f;
 #pragma unroll 4
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
-    const auto raw = load8_any<DT>(r.v, v);
+    const auto raw = load16_any(r.v, v);
     float e = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) e += term(Vec<DT>::get(raw, k), z, in);
+    for (int k = 0; k < Lane<DT>::N; ++k) e += term(Lane<DT>::get(raw, k), z, in);
     s += e;
   }
   if (r.has_side(t)) s += term(Vec<DT>::load1(r.x, r.side(t)), z, in);
@@ -229,9 +231,9 @@ __device__ __forceinline__ MaxSum row_max_sum(const Row<DT>& r, const Logits& in
     m = nm;
   };
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
-    const auto raw = load8_any<DT>(r.v, v);
+    const auto raw = load16_any(r.v, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) add(Vec<DT>::get(raw, k));
+    for (int k = 0; k < Lane<DT>::N; ++k) add(Lane<DT>::get(raw, k));
   }
   if (r.has_side(t)) add(Vec<DT>::load1(r.x, r.side(t)));
   MaxSum all = block_join<W>(MaxSum{m, (double)s}, in);
@@ -269,14 +271,14 @@ __device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_
   const float k = (float)(-(double)coef / rs.s);
   void* out_v = static_cast<typename Vec<DT>::T*>(out) + r.head;
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
-    float dx[8] = {};
+    float dx[Lane<DT>::N] = {};
     if (coef != 0.0f) {
-      const auto raw = load8_any<DT, NT>(r.v, v);
+      const auto raw = load16_any<NT>(r.v, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dx[i] = k * __builtin_amdgcn_exp2f((Vec<DT>::get(raw, i) - rs.z) * c);
-      add_at_target(dx, (uint32_t)target - r.head - 8 * v, coef);
+      for (int i = 0; i < Lane<DT>::N; ++i) dx[i] = k * __builtin_amdgcn_exp2f((Lane<DT>::get(raw, i) - rs.z) * c);
+      add_at_target(dx, (uint32_t)target - r.head - r.N * v, coef);
     }
-    store8_any<DT, NT>(out_v, v, dx);
+    store16_any<DT, NT>(out_v, v, dx);
   }
   if (r.has_side(t)) {
     const uint32_t j = r.side(t);
@@ -301,8 +303,8 @@ struct Spread {
   static constexpr uint32_t kStep = 64 * W;
   // The largest block takes rows beyond its registers too: what is past them
   // is read where it is needed.
-  static constexpr bool kRest = W == 16 && (K == 16 || DT == ZERO_F32);
-  typename Vec<DT>::Raw x[K];
+  static constexpr bool kRest = W == 16 && K == 16;
+  u32x4 x[K];
   float side;
 
   static __device__ __forceinline__ bool step(int k, const Row<DT>& r) { return k < K / 2 || k * kStep < r.n_vec; }
@@ -310,7 +312,7 @@ struct Spread {
   __device__ __forceinline__ Spread(const Row<DT>& r, uint32_t t) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (step(k, r)) x[k] = load8_any<DT, NT>(r.v, min(k * kStep + t, r.n_vec - 1));
+      if (step(k, r)) x[k] = load16_any<NT>(r.v, min(k * kStep + t, r.n_vec - 1));
     side = r.has_side(t) ? Vec<DT>::load1(r.x, r.side(t)) : 0.0f;
   }
 
@@ -324,8 +326,8 @@ struct Spread {
       if (step(k, r)) {
         float part = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float q = term(Vec<DT>::get(x[k], i));
+        for (int i = 0; i < Lane<DT>::N; ++i) {
+          const float q = term(Lane<DT>::get(x[k], i));
           keep(k, i, q);
           part += q;
         }
@@ -335,10 +337,10 @@ struct Spread {
     if constexpr (kRest) {
 #pragma unroll 2
       for (uint32_t v = K * kStep + t; v < r.n_vec; v += kStep) {
-        const auto y = load8_any<DT>(r.v, v);
+        const auto y = load16_any(r.v, v);
         float part = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part += term(Vec<DT>::get(y, i));
+        for (int i = 0; i < Lane<DT>::N; ++i) part += term(Lane<DT>::get(y, i));
         s += part;
       }
     }
@@ -349,18 +351,18 @@ struct Spread {
 };
 
 // Calls fn with the block (wavefronts, vectors per thread) whose threads hold a
-// row in registers: 8 vectors each, 16 of 16-bit rows past 65,536 elements.
+// row in registers: 64 elements each, 128 of 16-bit rows past 65,536 elements.
 // False if the row is so short that no vector is sure to be left.
 template <int DT, typename F>
 bool with_spread(uint32_t vocab, F fn) {
+  using std::integral_constant;
+  using K = integral_constant<int, 64 / Lane<DT>::N>;
   if (vocab < 128) return false;
-  const uint32_t n_vec = vocab / 8;
-  using K8 = std::integral_constant<int, 8>;
-  if (n_vec <= 64 * 2 * 8) fn(std::integral_constant<int, 2>{}, K8{});
-  else if (n_vec <= 64 * 4 * 8) fn(std::integral_constant<int, 4>{}, K8{});
-  else if (n_vec <= 64 * 8 * 8) fn(std::integral_constant<int, 8>{}, K8{});
-  else if (n_vec <= 64 * 16 * 8 || DT == ZERO_F32) fn(std::integral_constant<int, 16>{}, K8{});
-  else if constexpr (DT != ZERO_F32) fn(std::integral_constant<int, 16>{}, std::integral_constant<int, 16>{});
+  if (vocab <= 64 * 2 * 64) fn(integral_constant<int, 2>{}, K{});
+  else if (vocab <= 64 * 4 * 64) fn(integral_constant<int, 4>{}, K{});
+  else if (vocab <= 64 * 8 * 64) fn(integral_constant<int, 8>{}, K{});
+  else if (vocab <= 64 * 16 * 64) fn(integral_constant<int, 16>{}, K{});
+  else fn(integral_constant<int, 16>{}, integral_constant<int, 16>{});
   return true;
 }
 
@@ -586,9 +588,9 @@ __global__ void __launch_bounds__(kBlock) policy_kernel(const PolicyArgs a) {
   }
 }
 
-// A row held in registers, so that the logits are read once.  RAW keeps the
-// 16-bit logits (4 registers a vector) and takes every exponential twice;
-// otherwise the exponentials themselves stay (8 registers a vector).
+// A row held in registers, so that the logits are read once.  RAW keeps 16-bit
+// logits, two to a register, and takes every exponential twice; otherwise the
+// exponentials themselves stay.
 template <int DT, int W, int K, bool RAW, bool NT>
 __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared& sh) {
   const uint32_t t = threadIdx.x;
@@ -601,7 +603,7 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   const Spread<DT, W, K, true> x(r, t);
   in = PolicyRow{uniform(in.weight), uniform(in.advantage), uniform(in.old_logp), uniform(in.ref_logp)};
   xt = uniform(xt);
-  float e[RAW ? 1 : K][8], side = 0.0f;
+  float e[RAW ? 1 : K][Lane<DT>::N], side = 0.0f;
   float b = uniform(-xt * a.in.c);
   const float s = x.sum(
       r, t, [&](float v) { return __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
@@ -622,30 +624,30 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   const float coef = sh.coef, scale = sh.scale;
   typename Vec<DT>::T* out = policy_out<DT>(a, row);
   void* out_v = out + r.head;
-  const uint32_t at = (uint32_t)target - r.head - 8 * t;
+  const uint32_t at = (uint32_t)target - r.head - r.N * t;
   if constexpr (RAW) asm volatile("" : "+s"(b));  // the exponentials are taken again, not kept
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t v = k * 64 * W + t;
     if (v < r.n_vec) {
-      float dx[8];
+      float dx[Lane<DT>::N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (RAW) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Vec<DT>::get(x.x[k], i), a.in.c, b));
+      for (int i = 0; i < Lane<DT>::N; ++i) {
+        if constexpr (RAW) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Lane<DT>::get(x.x[k], i), a.in.c, b));
         else dx[i] = scale * e[k][i];
       }
-      add_at_target(dx, at - k * 64 * W * 8, coef);
-      store8_any<DT, NT>(out_v, v, dx);
+      add_at_target(dx, at - k * 64 * W * r.N, coef);
+      store16_any<DT, NT>(out_v, v, dx);
     }
   }
   if constexpr (Spread<DT, W, K, true>::kRest) {
     for (uint32_t v = K * 64 * W + t; v < r.n_vec; v += 64 * W) {
-      const auto y = load8_any<DT, NT>(r.v, v);
-      float dx[8];
+      const auto y = load16_any<NT>(r.v, v);
+      float dx[Lane<DT>::N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Vec<DT>::get(y, i), a.in.c, b));
-      add_at_target(dx, (uint32_t)target - r.head - 8 * v, coef);
-      store8_any<DT, NT>(out_v, v, dx);
+      for (int i = 0; i < Lane<DT>::N; ++i) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Lane<DT>::get(y, i), a.in.c, b));
+      add_at_target(dx, (uint32_t)target - r.head - r.N * v, coef);
+      store16_any<DT, NT>(out_v, v, dx);
     }
   }
   if (r.has_side(t)) {
@@ -668,7 +670,7 @@ void launch_policy(PolicyArgs a, hipStream_t s) {
   const bool done = with_spread<DT>(a.in.vocab, [&](auto w, auto k) {
     constexpr int W = decltype(w)::value, K = decltype(k)::value;
     for (a.row0 = 0; a.row0 < a.in.n_rows; a.row0 += kMostRows)
-      hipLaunchKernelGGL((policy_spread_kernel<DT, W, K, (K > 8), NT>), (uint32_t)std::min(kMostRows, a.in.n_rows - a.row0),
+      hipLaunchKernelGGL((policy_spread_kernel<DT, W, K, (K > 64 / Lane<DT>::N), NT>), (uint32_t)std::min(kMostRows, a.in.n_rows - a.row0),
                          64 * W, 0, s, a);
   });
   if (!done) hipLaunchKernelGGL((policy_kernel<DT, NT>), chunk_grid(a.in.n_rows, 0), kBlock, 0, s, a);
@@ -862,8 +864,8 @@ int fill_logits(Logits* in, const void* logits, int dtype, uint64_t n_rows, uint
                 const int64_t* targets, double temperature, const char* who) {
   if (dtype != ZERO_F16 && dtype != ZERO_BF16 && dtype != ZERO_F32)
     return fail(ZERO_EINVAL, "%s: unknown logits dtype %d", who, dtype);
-  if (vocab == 0 || vocab / 8 > kMaxRowVecs)
-    return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^29]", who, vocab);
+  if (vocab == 0 || vocab / 4 > kMaxRowVecs)
+    return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^28]", who, vocab);
   if (stride < vocab) return fail(ZERO_EINVAL, "%s: rows of %u logits overlap at a stride of %llu", who, vocab,
                                   (unsigned long long)stride);
   if (!std::isfinite(temperature) || temperature <= 0.0)

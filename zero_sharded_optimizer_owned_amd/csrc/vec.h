@@ -117,50 +117,44 @@ __device__ __forceinline__ void store4(void* base, uint64_t e, float a, float b,
   else *reinterpret_cast<u32x2*>(p) = u32x2{Vec<DT>::pack(a, b), Vec<DT>::pack(c, d)};
 }
 
-// The same at any address that suits the elements: rows of logits start where
-// an odd vocabulary puts them.  gfx950 loads and stores 16 bytes at any such
-// address in one instruction.
-// Rows are addressed by a base that is the same in every thread and a 32-bit
-// vector number, so that one register holds a thread's place in all of them.
+// Rows of logits: 16 bytes to a lane, N elements, at any address that suits
+// the elements (rows start where an odd vocabulary puts them; gfx950 loads and
+// stores 16 bytes at any such address in one instruction).  A row is addressed
+// by a base that is the same in every thread and a 32-bit vector number, so
+// that one register holds a thread's place in all of them.  fp32 lanes take
+// four elements and not two halves of eight: a wavefront's instruction then
+// covers 1 KB without gaps.
 constexpr uint32_t kMaxRowVecs = 1u << 26;  // a row's byte offsets fit 32 bits
 
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 
-template <int DT, bool NT = false>
-__device__ __forceinline__ typename Vec<DT>::Raw load8_any(const void* base, uint32_t v) {
-  const char* p = static_cast<const char*>(base) + v * (uint32_t)(8 * sizeof(typename Vec<DT>::T));
-  if constexpr (DT == ZERO_F32) {
-    const f32x4_any* q = reinterpret_cast<const f32x4_any*>(p);
-    if constexpr (NT) return {__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)};
-    else return {q[0], q[1]};
-  } else {
-    const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
-    if constexpr (NT) return {__builtin_nontemporal_load(q)};
-    else return {*q};
+template <int DT>
+struct Lane {
+  static constexpr int N = DT == ZERO_F32 ? 4 : 8;
+  static __device__ __forceinline__ float get(const u32x4& r, int k) {
+    if constexpr (DT == ZERO_F32) return __uint_as_float(r[k]);
+    else return Vec<DT>::get(typename Vec<DT>::Raw{r}, k);
   }
+};
+
+template <bool NT = false>
+__device__ __forceinline__ u32x4 load16_any(const void* base, uint32_t v) {
+  const u32x4_any* q = reinterpret_cast<const u32x4_any*>(static_cast<const char*>(base) + v * 16u);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  else return *q;
 }
 
 template <int DT, bool NT = false>
-__device__ __forceinline__ void store8_any(void* base, uint32_t v, const float (&x)[8]) {
-  char* p = static_cast<char*>(base) + v * (uint32_t)(8 * sizeof(typename Vec<DT>::T));
-  if constexpr (DT == ZERO_F32) {
-    f32x4_any* q = reinterpret_cast<f32x4_any*>(p);
-    const f32x4 lo = {x[0], x[1], x[2], x[3]}, hi = {x[4], x[5], x[6], x[7]};
-    if constexpr (NT) {
-      __builtin_nontemporal_store((f32x4_any)lo, q);
-      __builtin_nontemporal_store((f32x4_any)hi, q + 1);
-    } else {
-      q[0] = lo;
-      q[1] = hi;
-    }
-  } else {
-    u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
-    const u32x4 w = {Vec<DT>::pack(x[0], x[1]), Vec<DT>::pack(x[2], x[3]), Vec<DT>::pack(x[4], x[5]),
-                     Vec<DT>::pack(x[6], x[7])};
-    if constexpr (NT) __builtin_nontemporal_store((u32x4_any)w, q);
-    else *q = w;
+__device__ __forceinline__ void store16_any(void* base, uint32_t v, const float (&x)[Lane<DT>::N]) {
+  u32x4_any* q = reinterpret_cast<u32x4_any*>(static_cast<char*>(base) + v * 16u);
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == ZERO_F32) w[i] = __float_as_uint(x[i]);
+    else w[i] = Vec<DT>::pack(x[2 * i], x[2 * i + 1]);
   }
+  if constexpr (NT) __builtin_nontemporal_store((u32x4_any)w, q);
+  else *q = w;
 }
 
 // Eight e4m3 codes (8 bytes) to and from fp32, by the hardware's conversions:
