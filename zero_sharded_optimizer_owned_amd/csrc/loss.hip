@@ -351,14 +351,17 @@ struct Spread {
 };
 
 // Calls fn with the block (wavefronts, vectors per thread) whose threads hold a
-// row in registers: 64 elements each, 128 of 16-bit rows past 65,536 elements.
+// row in registers: 64 elements each, 128 of 16-bit rows past 65,536 elements,
+// 16 up to 2048 elements, where twice as many blocks to a CU hide the rows'
+// fp64 arithmetic (8192 rows of 1000 bf16: policy loss 27.6 us, so 21.4).
 // False if the row is so short that no vector is sure to be left.
 template <int DT, typename F>
 bool with_spread(uint32_t vocab, F fn) {
   using std::integral_constant;
   using K = integral_constant<int, 64 / Lane<DT>::N>;
   if (vocab < 128) return false;
-  if (vocab <= 64 * 2 * 64) fn(integral_constant<int, 2>{}, K{});
+  if (vocab <= 64 * 2 * 16) fn(integral_constant<int, 2>{}, integral_constant<int, 16 / Lane<DT>::N>{});
+  else if (vocab <= 64 * 2 * 64) fn(integral_constant<int, 2>{}, K{});
   else if (vocab <= 64 * 4 * 64) fn(integral_constant<int, 4>{}, K{});
   else if (vocab <= 64 * 8 * 64) fn(integral_constant<int, 8>{}, K{});
   else if (vocab <= 64 * 16 * 64) fn(integral_constant<int, 16>{}, K{});
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kBlock) logp_kernel(const LogpArgs a) {
 // factor and the reference are one fma, as in the policy loss, whose lp has
 // the same bits.
 template <int DT, int W, int K, bool TWO>
-__global__ void __launch_bounds__(64 * W, 4) logp_spread_kernel(const LogpArgs a) {
+__global__ void __launch_bounds__(64 * W, K * Lane<DT>::N <= 16 ? 8 : 4) logp_spread_kernel(const LogpArgs a) {
   const uint32_t t = threadIdx.x;
   const uint64_t row = a.row0 + blockIdx.x;
   const int64_t target = a.in.targets[row];
@@ -516,31 +519,42 @@ __device__ __forceinline__ typename Vec<DT>::T* policy_out(const PolicyArgs& a, 
 }
 
 // The loss from all rows' terms, by one block of 64 W threads, each row's in a
-// fixed place of a fixed tree.  The loads are coherent across the chip: where
-// the last block of the launch adds up, other blocks have just written them.
-template <int W>
+// fixed place of a fixed tree.  COHERENT: the loads are coherent across the
+// chip, where the last block of a launch adds up what others have just written.
+template <int W, bool COHERENT>
 __device__ __forceinline__ void policy_fold(const PolicyTerms* terms, uint64_t n, double kl_coef, float* stats) {
-  auto get = [](const double* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  __shared__ PolicyTerms part[W];
+  auto get = [](const double* p) {
+    if constexpr (COHERENT) return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    else return *p;
+  };
   PolicyTerms s = {0.0, 0.0, 0.0};
-#pragma unroll 4
-  for (uint64_t i = threadIdx.x; i < n; i += 64 * W) {
-    s.gain += get(&terms[i].gain);
-    s.kl += get(&terms[i].kl);
-    s.clipped += get(&terms[i].clipped);
-  }
-  const double gain = block_sum<W>(s.gain), kl = block_sum<W>(s.kl), clipped = block_sum<W>(s.clipped);
+  auto add = [&](const PolicyTerms& x) {
+    s.gain += x.gain;
+    s.kl += x.kl;
+    s.clipped += x.clipped;
+  };
+#pragma unroll 8
+  for (uint64_t i = threadIdx.x; i < n; i += 64 * W)
+    add({get(&terms[i].gain), get(&terms[i].kl), get(&terms[i].clipped)});
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1)
+    add({__shfl_xor(s.gain, off, 64), __shfl_xor(s.kl, off, 64), __shfl_xor(s.clipped, off, 64)});
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
   if (threadIdx.x == 0) {
-    stats[0] = (float)((kl_coef != 0.0 ? kl_coef * kl : 0.0) - gain);
-    stats[1] = (float)-gain;
-    stats[2] = (float)kl;
-    stats[3] = (float)clipped;
+    for (int i = 1; i < W; ++i) add(part[i]);
+    stats[0] = (float)((kl_coef != 0.0 ? kl_coef * s.kl : 0.0) - s.gain);
+    stats[1] = (float)-s.gain;
+    stats[2] = (float)s.kl;
+    stats[3] = (float)s.clipped;
   }
 }
 
 constexpr int kFoldWaves = 16;
 __global__ void __launch_bounds__(64 * kFoldWaves) policy_fold_kernel(const PolicyTerms* terms, uint64_t n,
                                                                       double kl_coef, float* stats) {
-  policy_fold<kFoldWaves>(terms, n, kl_coef, stats);
+  policy_fold<kFoldWaves, false>(terms, n, kl_coef, stats);
 }
 
 // After a block's row is in memory (by thread 0): whether it was the last of
@@ -584,7 +598,7 @@ __global__ void __launch_bounds__(kBlock) policy_kernel(const PolicyArgs a) {
     const PolicyRow in = policy_row(a, row);
     const float xt = in_range ? Vec<DT>::load1(r.x, (uint64_t)target) : 0.0f;
     policy_stream<DT, kWavesPerBlock, NT>(a, row, r, target, in, xt, in_range, sh);
-    if (sh.last) policy_fold<kWavesPerBlock>(a.terms, a.in.n_rows, a.kl_coef, a.stats);
+    if (sh.last) policy_fold<kWavesPerBlock, true>(a.terms, a.in.n_rows, a.kl_coef, a.stats);
   }
 }
 
@@ -659,10 +673,10 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
 }
 
 template <int DT, int W, int K, bool RAW, bool NT>
-__global__ void __launch_bounds__(64 * W, 4) policy_spread_kernel(const PolicyArgs a) {
+__global__ void __launch_bounds__(64 * W, K * Lane<DT>::N <= 16 ? 8 : 4) policy_spread_kernel(const PolicyArgs a) {
   __shared__ PolicyShared sh;
   policy_spread<DT, W, K, RAW, NT>(a, sh);
-  if (sh.last) policy_fold<W>(a.terms, a.in.n_rows, a.kl_coef, a.stats);
+  if (sh.last) policy_fold<W, true>(a.terms, a.in.n_rows, a.kl_coef, a.stats);
 }
 
 template <int DT, bool NT>
