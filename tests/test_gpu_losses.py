@@ -503,3 +503,63 @@ def test_binding_refusals():
             zs.zero_policy_loss(x, t, **{**ok, **change})
     with pytest.raises(ValueError):
         zs.zero_token_logprobs(x[:1].expand(3, 8), t, o)  # overlapping rows
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^21 rows and a few: the rows of the second launch equal a call on them alone."""
+    n, v, cut = (1 << 21) + 5, 128, 1 << 21
+    g = torch.Generator(DEV).manual_seed(3)
+    x = torch.randn(n, v, generator=g, device=DEV).half()
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    a, b, c = torch.empty(n, device=DEV), torch.empty(n, device=DEV), torch.empty(5, device=DEV)
+    zs.zero_token_logprobs(x, t, a)
+    zs.zero_token_logprobs(x[cut:], t[cut:], c)
+    assert torch.equal(a[cut:], c)
+    adv, old = torch.randn(n, generator=g, device=DEV), a - 0.1
+    dx, few = torch.empty_like(x), torch.empty_like(x[cut:])
+    stats, s2 = torch.zeros(4, device=DEV), torch.zeros(4, device=DEV)
+    zs.zero_policy_loss(x, t, old_logp=old, advantage=adv, divisor=1.0, stats=stats, logp=b, dlogits=dx,
+                        workspace=zs.policy_workspace(n, DEV))
+    assert torch.equal(a, b)
+    zs.zero_policy_loss(x[cut:], t[cut:], old_logp=old[cut:], advantage=adv[cut:], divisor=1.0, stats=s2, logp=c,
+                        dlogits=few, workspace=zs.policy_workspace(5, DEV))
+    assert torch.equal(dx[cut:].view(torch.int16), few.view(torch.int16))
+    ratio = (a - old).double().exp()
+    gain = torch.minimum(adv * ratio, adv * ratio.clamp(0.8, 1.2)).sum()
+    assert abs(float(stats[0]) + float(gain)) <= 1e-6 * float((adv * ratio).abs().sum())
+
+
+def test_workspace_serves_calls_of_any_smaller_size():
+    """One workspace for calls of different row counts, one after the other."""
+    ws = zs.policy_workspace(3000, DEV)
+    for n in (3000, 7, 128, 129, 1, 3000):
+        x, t = rows_of(n, 200, 0, 0, torch.float32)
+        inp = policy_inputs(reference(x, t, 1.0))
+        got, want = torch.zeros(4, device=DEV), torch.zeros(4, device=DEV)
+        for stats, w in ((got, ws), (want, zs.policy_workspace(n, DEV))):
+            zs.zero_policy_loss(x, t, divisor=1.0, stats=stats, logp=torch.zeros(n, device=DEV), workspace=w,
+                                kl_coef=0.1, **inp)
+        assert torch.equal(got, want) and float(want[2]) > 0
+
+
+def test_many_pairs_take_the_pair_launch_and_agree_with_few():
+    """The launch for the pairs (more than 16 pairs or 1024 rows) and the form without it: the same
+    rows give the same gradient up to the number of pairs that the loss is divided by."""
+    lengths = [5, 3] * 40
+    x, t, bounds = packed(lengths, 300, "f32", seed=4)
+    n, q = len(t), len(lengths)
+    mk = lambda k: torch.zeros(k, device=DEV)
+    ref_logp = -torch.arange(q, device=DEV, dtype=torch.float32) * 0.1 - 20
+    dx, seq, reward = torch.empty_like(x), mk(q), mk(q)
+    zs.zero_preference_loss(x, t, bounds, ref_logp=ref_logp, stats=mk(2), logp=mk(n), seq_logp=seq, reward=reward,
+                            workspace=zs.preference_workspace(n, q // 2, DEV), dlogits=dx)
+    ref = reference(x, t, 1.0)
+    want = preference_reference(ref, bounds, ref_logp, 0.1, 0.0, False, 1.0, 1.0)
+    check_gradient(ref, dx, want["coef"], want["e_coef"], "f32", "many pairs")
+    k = int(bounds[20])
+    few, s2, r2 = torch.empty_like(x[:k]), mk(20), mk(20)
+    zs.zero_preference_loss(x[:k], t[:k], bounds[:21], ref_logp=ref_logp[:20], stats=mk(2), logp=mk(k), seq_logp=s2,
+                            reward=r2, workspace=zs.preference_workspace(k, 10, DEV), dlogits=few)
+    assert torch.equal(s2, seq[:20]) and torch.equal(r2, reward[:20])
+    # 40 pairs against 10: a factor of 4, a power of two; the coefficient rounds once in both
+    assert torch.equal(few, dx[:k] * 4)

@@ -1,7 +1,12 @@
 """The 8-bit step's piece table and the refusals of the 8-bit step and the losses,
 on the CPU: host calls and argument checks only, nothing is launched."""
 import ctypes as ct
+import functools
+import os
 import random
+import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -226,3 +231,54 @@ def test_binding_refuses_host_tensors_and_shapes():
     with pytest.raises(ValueError):
         zs.zero_preference_loss(x, t, torch.zeros(2, dtype=torch.int64), ref_logp=o, stats=o, logp=o, seq_logp=o,
                                 reward=o, workspace=o)
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@functools.lru_cache(maxsize=None)
+def _device_asm(source: str) -> str:
+    """gfx950 assembly of one of the library's HIP sources, built with its flags."""
+    from zero_sharded_optimizer_owned_amd.build import CSRC, HIPCC_FLAGS, INCLUDE
+
+    flags = [f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")]
+    res = subprocess.run(["hipcc", *flags, "-I", INCLUDE, "--cuda-device-only", "-S",
+                          os.path.join(CSRC, source), "-o", "-"], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
+    return res.stdout
+
+
+@pytest.mark.skipif(shutil.which("hipcc") is None, reason="hipcc not found")
+@pytest.mark.parametrize("source", ["step8.hip", "loss.hip"])
+def test_kernels_keep_to_registers(source):
+    """No kernel spills to scratch memory (rows and batches of loads live in registers), and
+    none uses packed fp32 arithmetic or an fma that rounds straight to 16 bits."""
+    asm = _device_asm(source)
+    sizes = [int(x) for x in re.findall(r"; ScratchSize: (\d+)", asm)]
+    assert sizes and max(sizes) == 0, sizes
+    assert not re.search(r"v_pk_(add|mul|fma)_f32|v_fma_mix|v_mad_mix", asm)
+
+
+@pytest.mark.skipif(shutil.which("hipcc") is None, reason="hipcc not found")
+def test_codes_use_the_hardware_conversions():
+    asm = _device_asm("step8.hip")
+    assert "v_cvt_pk_fp8_f32" in asm and "v_cvt_pk_f32_fp8" in asm
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
+                    reason="g++ or the ROCm headers not found")
+def test_piece_table_under_sanitizers(tmp_path):
+    """zero_piece_table over random layouts, built with AddressSanitizer and
+    UndefinedBehaviorSanitizer: tables of exactly the counted size, and short ones."""
+    exe = str(tmp_path / "piece_driver")
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+           "-static-libasan", "-I", os.path.join(ROOT, "include"), "-I", "/opt/rocm/include",
+           "-D__HIP_PLATFORM_AMD__", os.path.join(ROOT, "tests", "sanitize", "piece_driver.cpp"),
+           os.path.join(ROOT, "zero_sharded_optimizer_owned_amd", "csrc", "host.cpp"), "-o", exe]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0 and "sanitize" in res.stderr and ("cannot find" in res.stderr or "unrecognized" in res.stderr):
+        pytest.skip("sanitizer runtime not available: " + res.stderr[-300:])
+    assert res.returncode == 0, res.stderr[-3000:]
+    run = subprocess.run([exe], capture_output=True, text=True, timeout=600,
+                         env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0"))
+    assert run.returncode == 0 and "clean" in run.stdout, run.stdout[-2000:] + run.stderr[-4000:]
