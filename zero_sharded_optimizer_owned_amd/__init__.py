@@ -880,8 +880,14 @@ class OwnerShard:
         self.begin, self.end = int(begins[owner]), int(ends[owner])
         self.local_base = self.begin & ~7
         self.local_size = self.end - self.local_base
-        self.chunks = zero_chunk_table(sizes, self.offsets, self.begin, self.end, max_chunk)
         self.device = torch.device(device or "cuda")
+        self.align = align
+        self._tables(sizes, max_chunk)
+
+    def _tables(self, sizes, max_chunk: int) -> None:
+        """The chunk, group and offset tables of the fp32 step, the export and the import."""
+        torch = _torch()
+        self.chunks = zero_chunk_table(sizes, self.offsets, self.begin, self.end, max_chunk)
         self.chunks_dev = chunks_to_device(self.chunks, self.device)
         # short chunks packed several to a block, when that saves enough blocks
         self.groups = zero_chunk_groups(self.chunks, max_chunk)
@@ -890,7 +896,6 @@ class OwnerShard:
         if groups_pay(self.n_groups, self.chunks.size):
             self.groups_dev = torch.from_numpy(self.groups.astype(np.int64)).to(self.device)
         self.n_real = int(self.chunks["len"].sum()) if self.chunks.size else 0
-        self.align = align
         self.dense_offsets, self.dense_total = zero_dense_offsets(sizes)
         self.tensor_offset_dev = torch.from_numpy(self.offsets.astype(np.int64)).to(self.device)
         self.dense_offset_dev = torch.from_numpy(self.dense_offsets.astype(np.int64)).to(self.device)
@@ -1048,6 +1053,20 @@ class OwnerShard8(OwnerShard):
         self.pieces_dev = chunks_to_device(self.pieces, self.device)
         self.masks_dev = torch.from_numpy(masks).to(self.device) if masks.size else None
         self._work = None
+
+    # OwnerShard's tables are made when one of them is first asked for (an export, an
+    # import): the step itself needs the piece table alone.
+    _LATE = frozenset(("chunks", "chunks_dev", "groups", "n_groups", "groups_dev", "n_real", "dense_offsets",
+                       "dense_total", "tensor_offset_dev", "dense_offset_dev"))
+
+    def _tables(self, sizes, max_chunk: int) -> None:
+        self._late = sizes, max_chunk
+
+    def __getattr__(self, name):
+        if name in OwnerShard8._LATE and "_late" in self.__dict__:
+            OwnerShard._tables(self, *self.__dict__.pop("_late"))
+            return self.__dict__[name]
+        raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
 
     def alloc_state(self):
         """master, then the moments: (codes, scales) of the first and of the second's root."""

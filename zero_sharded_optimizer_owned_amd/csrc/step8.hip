@@ -461,27 +461,36 @@ int check_state8(const zero_piece* pieces, uint64_t n_pieces, const uint8_t* mas
 template <int GDT, int RC>
 void launch_step8_p(Step8Args& a, int pdt, hipStream_t s) {
   const uint32_t grid = chunk_grid(a.n_pieces, 0);
-  // Whole pieces: at most three blocks to a CU and runs of two pieces to an
-  // XCD.  8 bf16 ranks into 1.0e8 elements: 520 us; two blocks 523, four 531,
+  // Whole pieces: at most three blocks to a CU, four with up to five 16-bit
+  // rank buffers, whose loads are fewer, and runs of two pieces to an XCD.
+  // 8 bf16 ranks into 1.0e8 elements: 520 us; two blocks 523, four 531,
   // uncapped 537, single pieces 527.  Stored gradient, 3.75e8 elements: 1177
-  // us; two 1326, four 1240, uncapped 1258, single pieces 1185.  Pieces with
-  // padding wait for more round trips and want every block that fits: 200,000
-  // tensors of 100 elements 27.1 us, 28.8 with four blocks.
+  // us; two 1326, four 1240, uncapped 1258, single pieces 1185.  4 bf16 ranks
+  // into 6e7 elements: 227 us; three blocks 232, uncapped 229; 1 rank 193;
+  // three 202, uncapped 187.  Pieces with padding wait for more round trips
+  // and want every block that fits: 200,000 tensors of 100 elements 27.1 us,
+  // 28.8 with four blocks.
   const bool whole = 2 * a.n_masks <= a.n_pieces;
-  const uint32_t lds = whole ? lds_for_blocks_per_cu(3, 0) : 0;
+  const bool light = GDT != ZERO_F32 && a.rs.R <= 5;
+  const uint32_t lds = whole ? lds_for_blocks_per_cu(light ? 4 : 3, 0) : 0;
   a.run = whole ? 2 : 1;
   if (pdt == ZERO_F16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_F16, RC>), grid, kBlock, lds, s, a);
   else if (pdt == ZERO_BF16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_BF16, RC>), grid, kBlock, lds, s, a);
   else hipLaunchKernelGGL((step8_kernel<GDT, ZERO_NONE, RC>), grid, kBlock, lds, s, a);
 }
 
-// Rank counts with all loads unrolled; any other count takes four at a time.
+// Up to eight ranks have all their loads unrolled; more take four at a time
+// (taking 3 or 5 ranks so as well cost 15% and 7%).
 template <int GDT>
 void launch_step8(Step8Args& a, int pdt, hipStream_t s) {
   switch (a.rs.R) {
     case 1: return launch_step8_p<GDT, 1>(a, pdt, s);
     case 2: return launch_step8_p<GDT, 2>(a, pdt, s);
+    case 3: return launch_step8_p<GDT, 3>(a, pdt, s);
     case 4: return launch_step8_p<GDT, 4>(a, pdt, s);
+    case 5: return launch_step8_p<GDT, 5>(a, pdt, s);
+    case 6: return launch_step8_p<GDT, 6>(a, pdt, s);
+    case 7: return launch_step8_p<GDT, 7>(a, pdt, s);
     case 8: return launch_step8_p<GDT, 8>(a, pdt, s);
     default: return launch_step8_p<GDT, 0>(a, pdt, s);
   }
