@@ -369,7 +369,10 @@ bool with_spread(uint32_t vocab, F fn) {
   return true;
 }
 
-// One block per row, as many rows to a launch as its threads may number.
+// One block per row, as many rows to a launch as its threads may number; each
+// XCD takes one contiguous run of them (against rows dealt in turn: policy
+// loss of 8192 x 128,000 694 to 684 us, preference loss of 8192 x 32,000 234
+// to 228; its second pass is 1% slower so, and deals).
 constexpr uint64_t kMostRows = 1u << 21;
 
 __device__ __forceinline__ bool in_vocab(int64_t target, uint32_t vocab) { return target >= 0 && target < (int64_t)vocab; }
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kBlock) logp_kernel(const LogpArgs a) {
 template <int DT, int W, int K, bool TWO>
 __global__ void __launch_bounds__(64 * W, K * Lane<DT>::N <= 16 ? 8 : 4) logp_spread_kernel(const LogpArgs a) {
   const uint32_t t = threadIdx.x;
-  const uint64_t row = a.row0 + blockIdx.x;
+  const uint64_t row = a.row0 + xcd_contiguous(blockIdx.x, gridDim.x);
   const int64_t target = a.in.targets[row];
   RowSum rs = {0.0f, 0.0};
   float xt = 0.0f;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kBlock) policy_kernel(const PolicyArgs a) {
 template <int DT, int W, int K, bool RAW, bool NT>
 __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared& sh) {
   const uint32_t t = threadIdx.x;
-  const uint64_t row = a.row0 + blockIdx.x;
+  const uint64_t row = a.row0 + xcd_contiguous(blockIdx.x, gridDim.x);
   const int64_t target = a.in.targets[row];
   const Row<DT> r(a.in, row);
   PolicyRow in = policy_row(a, row);
