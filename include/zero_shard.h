@@ -624,7 +624,7 @@ int zero_moments8_unpack(const zero_piece *pieces, uint64_t n_pieces, const uint
 /* ----------------------------------------------------------------------------
  * Losses on token log-probabilities.
  *
- * logits[n_rows] of `vocab` elements each (F16, BF16 or F32), row r from element
+ * logits[n_rows] of `vocab` (at most 2^28) elements each (F16, BF16 or F32), row r from element
  * r * row_stride; rows need no alignment beyond their elements'.  Row r's target
  * is targets[r]; a target outside [0, vocab) (say -100) marks a row that counts
  * for nothing: log-probability 0, no loss, zero gradient, its logits unread.  So

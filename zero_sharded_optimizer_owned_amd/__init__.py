@@ -279,9 +279,15 @@ def _torch():
     return torch
 
 
+_dtype_codes = None
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    return {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}[t.dtype]
+    global _dtype_codes
+    if _dtype_codes is None:
+        torch = _torch()
+        _dtype_codes = {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+    return _dtype_codes[t.dtype]
 
 
 def _dev(t, name: str, dtype=None):

@@ -721,29 +721,55 @@ struct Pair {
   float coef[2];  // of the chosen and the rejected sequence's rows
 };
 
-// One pair by 64 W threads (a block, or with W = 1 a wavefront); in every thread.
+// One pair by 64 W threads (a block, or with W = 1 a wavefront); in every
+// thread.  Both sequences' loads go out before the first sum is formed, and
+// the four sums share one trip through LDS.
 template <int W>
 __device__ __forceinline__ Pair pair_terms(const PairArgs& a, uint32_t p, uint32_t t) {
   Pair x;
-  double part[2];
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};  // chosen lp and count, rejected lp and count
+  float ref[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint64_t q = 2 * (uint64_t)p + i;
     const int64_t n = (int64_t)a.n_rows;
     x.begin[i] = (uint64_t)min(max(a.seq_begin[q], (int64_t)0), n);
     x.end[i] = (uint64_t)min(max(a.seq_begin[q + 1], (int64_t)0), n);
-    double s = 0.0, cnt = 0.0;
+    ref[i] = a.ref_logp[q];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll 4
     for (uint64_t row = x.begin[i] + t; row < x.end[i]; row += 64 * W) {
       const RowStats r = a.rows[row];
-      s += r.sum != 0.0 ? r.lp : 0.0;
-      cnt += r.sum != 0.0 ? 1.0 : 0.0;
+      sum[2 * i] += r.sum != 0.0 ? r.lp : 0.0;
+      sum[2 * i + 1] += r.sum != 0.0 ? 1.0 : 0.0;
     }
-    s = block_sum<W>(s);
-    cnt = block_sum<W>(cnt);
-    part[i] = a.average ? 1.0 / fmax(cnt, 1.0) : 1.0;
-    x.seq[i] = s * part[i];
-    x.reward[i] = a.beta * (s - (double)a.ref_logp[q]) * part[i];
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = sum[i] + __shfl_xor(sum[i], off, 64);
+  if constexpr (W > 1) {
+    __shared__ double part[W][4];
+    __syncthreads();  // `part` may still be read for the pair before
+    if ((t & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[t >> 6][i] = sum[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum[i] = part[0][i];
+#pragma unroll
+      for (int w = 1; w < W; ++w) sum[i] = sum[i] + part[w][i];
+    }
+  }
+  double part_of[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    part_of[i] = a.average ? 1.0 / fmax(sum[2 * i + 1], 1.0) : 1.0;
+    x.seq[i] = sum[2 * i] * part_of[i];
+    x.reward[i] = a.beta * (sum[2 * i] - (double)ref[i]) * part_of[i];
   }
   const double h = x.reward[0] - x.reward[1], ex = exp_both(-fabs(h)).value;
   // -ln sigma(h) and -ln sigma(-h), without overflow
@@ -751,8 +777,8 @@ __device__ __forceinline__ Pair pair_terms(const PairArgs& a, uint32_t p, uint32
   const double sig = h >= 0.0 ? 1.0 / (1.0 + ex) : ex / (1.0 + ex);
   x.loss = {(1.0 - a.smoothing) * lose + a.smoothing * win, h > 0.0 ? 1.0 : 0.0};
   const double slope = a.beta * (sig - (1.0 - a.smoothing)) * a.grad_scale / (double)a.n_pairs;
-  x.coef[0] = (float)(slope * part[0]);
-  x.coef[1] = (float)(-slope * part[1]);
+  x.coef[0] = (float)(slope * part_of[0]);
+  x.coef[1] = (float)(-slope * part_of[1]);
   return x;
 }
 
@@ -1011,8 +1037,10 @@ extern "C" int zero_policy_loss(const zero_policy_args* p, hipStream_t stream) {
   a.stats = p->stats;
   a.dlogits = p->dlogits;
   a.dstride = p->dlogits_stride;
-  a.terms = reinterpret_cast<PolicyTerms*>(static_cast<char*>(p->workspace) + 256);
-  a.ticket = p->n_rows > 0 && p->n_rows <= kTicketRows ? static_cast<uint32_t*>(p->workspace) : nullptr;
+  if (p->n_rows > 0) {
+    a.terms = reinterpret_cast<PolicyTerms*>(static_cast<char*>(p->workspace) + 256);
+    if (p->n_rows <= kTicketRows) a.ticket = static_cast<uint32_t*>(p->workspace);
+  }
   if (p->n_rows > 0) {
     by_dtype(p->dtype, [&](auto dt) {
       if (past_cache(p->n_rows, p->vocab, p->dtype)) launch_policy<decltype(dt)::value, true>(a, stream);
