@@ -758,11 +758,11 @@ __device__ __forceinline__ Pair pair_terms(const PairArgs& a, uint32_t p, uint32
       for (int i = 0; i < 4; ++i) part[t >> 6][i] = sum[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum[i] = part[0][i];
+    for (int i = 0; i < 4; ++i) sum[i] = part[0][i];
+#pragma unroll 1
+    for (int w = 1; w < W; ++w)
 #pragma unroll
-      for (int w = 1; w < W; ++w) sum[i] = sum[i] + part[w][i];
-    }
+      for (int i = 0; i < 4; ++i) sum[i] = sum[i] + part[w][i];
   }
   double part_of[2];
 #pragma unroll
@@ -791,17 +791,18 @@ __device__ __forceinline__ void pair_store(const PairArgs& a, uint32_t p, const 
 }
 
 // One block per pair, which also hands its rows their coefficient.
-__global__ void __launch_bounds__(kBlock) pair_kernel(const PairArgs a) {
+constexpr int kPairWaves = 8;
+__global__ void __launch_bounds__(64 * kPairWaves) pair_kernel(const PairArgs a) {
   const uint32_t t = threadIdx.x;
   for (uint32_t p = blockIdx.x; p < a.n_pairs; p += gridDim.x) {
-    const Pair x = pair_terms<kWavesPerBlock>(a, p, t);
+    const Pair x = pair_terms<kPairWaves>(a, p, t);
     if (t == 0) {
       pair_store(a, p, x);
       a.pairs[p] = x.loss;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      for (uint64_t row = x.begin[i] + t; row < x.end[i]; row += kBlock)
+      for (uint64_t row = x.begin[i] + t; row < x.end[i]; row += 64 * kPairWaves)
         if (a.rows[row].sum != 0.0) a.rows[row].coef = x.coef[i];
   }
 }
@@ -1103,7 +1104,7 @@ extern "C" int zero_preference_loss(const zero_preference_args* p, hipStream_t s
     });
     return launch_status(who);
   }
-  hipLaunchKernelGGL(pair_kernel, chunk_grid(p->n_pairs, 0), kBlock, 0, stream, q);
+  hipLaunchKernelGGL(pair_kernel, std::min(p->n_pairs, 1u << 20), 64 * kPairWaves, 0, stream, q);
   if ((rc = launch_status(who))) return rc;
   by_dtype(p->dtype, [&](auto dt) {
     if (past_cache(p->n_rows, p->vocab, p->dtype))
