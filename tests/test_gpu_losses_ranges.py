@@ -1,0 +1,186 @@
+"""The losses where their rows leave the ordinary: logits far from zero, targets at the
+types' ends, low and high temperatures, long rows.
+
+Tolerances.  u = 2^-24.  With the target's logit as the reference, a term
+exp((x_j - x_t) / T), d_j = |x_j - x_t| / T, carries the rounding of the difference and of
+the exponent (2 u d_j) and one step of the exponential (2 u).  A thread adds a vector's 8
+elements and the partial sums of at most 16 vectors in fp32 (24 u), everything past those
+in fp64.  So ln S is off by at most u (2 E_p[d] + 26); lp = -ln S is stored in fp32.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import zero_sharded_optimizer_owned_amd as zs  # noqa: E402
+
+DEV = "cuda"
+U = 2.0 ** -24
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    zs.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+def full(*shape, value=9.0):
+    return torch.full(shape, value, device=DEV)
+
+
+def logprobs(x, t, temperature=1.0):
+    out = full(len(t))
+    zs.zero_token_logprobs(x, t, out, temperature=temperature)
+    return out
+
+
+def policy(x, t, old, advantage, temperature=1.0, ref=None, kl=0.0, gradient=True):
+    """(stats, logp, dlogits) of the policy loss."""
+    stats, logp, dx = full(4), full(len(t)), torch.full_like(x, 5.0) if gradient else None
+    zs.zero_policy_loss(x, t, old_logp=old, ref_logp=ref, kl_coef=kl, advantage=advantage, divisor=1.0, stats=stats,
+                        logp=logp, dlogits=dx, temperature=temperature, workspace=zs.policy_workspace(len(t), DEV))
+    return stats, logp, dx
+
+
+def preference(x, t, bounds, ref, gradient=True, **over):
+    """(stats, logp, seq_logp, reward, dlogits) of the preference loss."""
+    q = len(bounds) - 1
+    out = full(2), full(len(t)), full(q), full(q), torch.full_like(x, 5.0) if gradient else None
+    zs.zero_preference_loss(x, t, bounds, ref_logp=ref, stats=out[0], logp=out[1], seq_logp=out[2], reward=out[3],
+                            dlogits=out[4], workspace=zs.preference_workspace(len(t), q // 2, DEV), **over)
+    return out
+
+
+def bits(x):
+    return x.contiguous().view(torch.uint8)
+
+
+def exact_logp(x, t, temperature=1.0):
+    """(lp in 64 bits, its tolerance) of every row, by the definition."""
+    at = torch.arange(len(t), device=x.device), t
+    z = (x.double() - x.double()[at][:, None]) / temperature
+    top = z.max(1, keepdim=True).values
+    e = (z - top).exp()
+    total = e.sum(1)
+    lp = -top[:, 0] - total.log()
+    spread = (e * torch.where(e > 0, z.abs(), 0.0)).sum(1) / total
+    return lp, U * (2 * spread + 26) + U * lp.abs()
+
+
+def grid_rows(n, v, step, seed=1):
+    """Logits at multiples of `step` within +-15 (so that a shift leaves them exact), and targets."""
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(n, v, generator=g) * 3 / step).round().clamp(-15 / step, 15 / step) * step
+    t = torch.randint(0, v, (n,), generator=g)
+    x[torch.arange(n), t] = (x[torch.arange(n), t] + 8).clamp(max=15)
+    return x.to(DEV), t.to(DEV)
+
+
+@pytest.mark.parametrize("v", [100, 1000, 8001, 32_000, 131_072, 140_003])
+@pytest.mark.parametrize("name, shift, step", [("f32", 1000.0, 2.0 ** -6), ("f32", -4096.0, 2.0 ** -6),
+                                               ("f16", 100.0, 2.0 ** -4), ("bf16", 96.0, 0.5), ("bf16", -96.0, 0.5)])
+def test_a_common_shift_of_the_logits_changes_nothing(name, shift, step, v):
+    """All results are functions of the differences, which are exact here: the same bits."""
+    x, t = grid_rows(5, v, step)
+    near, far = x.to(DT[name]), (x + shift).to(DT[name])
+    assert torch.equal(near.double() + shift, far.double())
+    want, tol = exact_logp(near, t)
+    adv = torch.tensor([1.0, -0.5, 2.0, 0.25, -1.0], device=DEV)
+    old = (want - 0.1).float()
+    bounds = torch.tensor([0, 2, 5], device=DEV)
+    ref = full(2, value=-20.0)
+    a = [logprobs(near, t), *policy(near, t, old, adv, ref=old, kl=0.1), *preference(near, t, bounds, ref)]
+    b = [logprobs(far, t), *policy(far, t, old, adv, ref=old, kl=0.1), *preference(far, t, bounds, ref)]
+    assert bool(((b[0].double() - want).abs() <= tol).all()), (b[0].double() - want, tol)
+    for p, q in zip(a, b):
+        assert torch.equal(bits(p), bits(q))
+
+
+@pytest.mark.parametrize("v", [64, 1000, 50_001, 140_000])
+@pytest.mark.parametrize("name", list(DT))
+def test_the_calls_agree_on_a_token(name, v):
+    """The reference's sums and the policy's: one log-probability, whichever call forms it."""
+    x, t = grid_rows(6, v, 0.5, seed=2)
+    x = (x + 17).to(DT[name])
+    x[4, (t[4] + 1) % v] = 100.0  # a row whose maximum is far above its target
+    lp = logprobs(x, t)
+    want, tol = exact_logp(x, t)
+    assert bool(((lp.double() - want).abs() <= tol).all())
+    stats, again, dx = policy(x, t, lp, full(6, value=1.0), ref=lp, kl=0.5)
+    assert torch.equal(lp, again)
+    _, third, _, _, _ = preference(x, t, torch.tensor([0, 3, 6], device=DEV), full(2, value=0.0))
+    assert torch.equal(lp, third)
+
+
+@pytest.mark.parametrize("temperature", [0.1, 0.02])
+@pytest.mark.parametrize("v", [90, 4096, 131_072])
+def test_low_temperatures(v, temperature):
+    """Near-certain targets: no log-probability above zero, all within the bound."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(8, v, generator=g) * 2
+    t = torch.randint(0, v, (8,), generator=g)
+    t[6:] = t[6:].clamp(min=1)
+    x[torch.arange(8), t] = 30.0 + torch.rand(8, generator=g)
+    x[6:, 0] = 12.0  # one row's target below its maximum, one far below
+    x[6, t[6]], x[7, t[7]] = 10.5, -3.0
+    x, t = x.to(DEV), t.to(DEV)
+    want, tol = exact_logp(x, t, temperature)
+    got = logprobs(x, t, temperature)
+    assert bool((got <= 0).all()), got
+    assert bool(((got.double() - want).abs() <= tol).all()), (got.double() - want, tol)
+    assert torch.equal(policy(x, t, got, full(8, value=1.0), temperature)[1], got)
+
+
+@pytest.mark.parametrize("v", [9, 1000, 40_000, 131_072, 140_000])
+@pytest.mark.parametrize("name", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [1.0, 0.6])
+def test_a_target_at_the_types_largest_value(name, v, temperature):
+    """It is certain: lp 0, and with it the gradient; beside a second one it has half."""
+    x, t = grid_rows(4, v, 0.5, seed=3)
+    x = x.to(DT[name])
+    big = torch.finfo(DT[name]).max
+    for row in (0, 1, 3):
+        x[row, t[row]] = big
+    x[1, (t[1] + 1) % v] = big
+    x[3] = torch.finfo(DT[name]).min
+    x[3, t[3]] = big  # differences beyond fp32
+    lp = logprobs(x, t, temperature)
+    assert float(lp[0]) == 0.0 and float(lp[3]) == 0.0
+    assert abs(float(lp[1]) + math.log(2)) <= 2 * U
+    old = full(4, value=0.0)
+    old[2] = lp[2]
+    stats, again, dx = policy(x, t, old, full(4, value=1.0), temperature)
+    assert torch.equal(lp, again) and bool(torch.isfinite(dx).all()) and bool(torch.isfinite(stats).all())
+    assert int(dx[[0, 3]].count_nonzero()) == 0 and int(dx[1].count_nonzero()) == 2
+    assert abs(float(stats[1]) + 3.5) <= 4 * U * 3.5 + 1e-6  # rows 0, 2, 3 at ratio 1, row 1 at 1/2
+    lp3 = preference(x, t, torch.tensor([0, 2, 4], device=DEV), full(2, value=0.0), temperature=temperature)[1]
+    assert torch.equal(lp, lp3)
+
+
+def test_a_target_at_the_lowest_value_beside_the_largest():
+    """The difference is beyond fp32, its quotient by the temperature is not."""
+    x, t = torch.zeros(2, 300, device=DEV), torch.tensor([4, 7], device=DEV)
+    x[0, 4], x[0, 5] = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    got = logprobs(x, t, temperature=4.0)
+    want = 2.0 * torch.finfo(torch.float32).min / 4.0
+    assert abs(float(got[0]) - want) <= abs(want) * 2 * U
+
+
+@pytest.mark.parametrize("temperature", [1e6, 3.7e37, 4.4e37, 6e37, 1e38])
+@pytest.mark.parametrize("v", [50, 3000])
+def test_high_temperatures_and_masked_tokens(v, temperature):
+    """Every unmasked token is as likely as any other; masked ones are not counted."""
+    x, t = grid_rows(3, v, 0.5, seed=5)
+    x[1, (t[1] + 1) % v] = -math.inf
+    t[2] = 0
+    x[2, 1:] = -math.inf
+    lp = logprobs(x, t, temperature)
+    for row, n in enumerate((v, v - 1, 1)):
+        assert abs(float(lp[row]) + math.log(n)) <= U * (26 + math.log(n)) + 30 / temperature
+    assert torch.equal(lp, policy(x, t, lp, full(3, value=1.0), temperature)[1])

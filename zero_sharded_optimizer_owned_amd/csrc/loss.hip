@@ -17,10 +17,16 @@
 // reference is the maximum, found as it goes.
 //
 // The elements are fp32, exp is the hardware's 2^x with log2(e) / T as its
-// factor.  Where rows are added up to sequences that factor has a second word:
+// factor.  The difference to the reference comes first, so that errors go with
+// it and not with the logits' size: the target's own term is exactly 1, lp is
+// never above 0 and a shift of all logits changes nothing.  (x c - x_t c with
+// the second product rounded to fp32 costs 2^-24 |x_t| / T of lp, and the whole
+// row where that product overflows.)  In the sums the factor has a second word:
 // fp32's error of log2(e), 1.3e-8, moves every row's ln S the same way
 // (measured on 500-token sequences: rewards 5e-6 off without it, 4e-7 with
-// it).  Per-thread sums are fp32 over at most a few hundred elements and are
+// it).  Every call forms a row's sum alike: the reference model's
+// log-probabilities and the policy's agree to the bit where the logits do.
+// Per-thread sums are fp32 over at most a few hundred elements and are
 // added up in fp64.
 //
 // A row whose target is outside [0, vocab), or whose logits are all -inf,
@@ -31,6 +37,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <type_traits>
 
 #include "internal.h"
@@ -49,7 +56,7 @@ struct Logits {
   const int64_t* targets;
   float c;           // log2(e) / T
   float c_hi, c_lo;  // the same in two words: the fp32 value below it and the rest, which is
-                     // above 0, so that d = -inf gives -inf in both
+                     // held above 0, so that d = -inf gives -inf in both
   double inv_t;  // 1 / T
 };
 
@@ -250,7 +257,7 @@ struct RowSum {
   double s;
   __device__ __forceinline__ bool counts() const { return s != 0.0; }  // true for NaN
   __device__ __forceinline__ double logp(float xt, const Logits& in) const {
-    return counts() ? (double)(xt - z) * in.inv_t - ln(s) : 0.0;
+    return counts() ? ((double)xt - (double)z) * in.inv_t - ln(s) : 0.0;
   }
 };
 
@@ -414,10 +421,8 @@ __global__ void __launch_bounds__(kBlock) logp_kernel(const LogpArgs a) {
   }
 }
 
-// TWO: with the exponent factor's second word (for sequences).  Without it the
-// factor and the reference are one fma, as in the policy loss, whose lp has
-// the same bits.
-template <int DT, int W, int K, bool TWO>
+// NT: nothing reads the logits again.
+template <int DT, int W, int K, bool NT>
 __global__ void __launch_bounds__(64 * W, K * Lane<DT>::N <= 16 ? 8 : 4) logp_spread_kernel(const LogpArgs a) {
   const uint32_t t = threadIdx.x;
   const uint64_t row = a.row0 + xcd_contiguous(blockIdx.x, gridDim.x);
@@ -427,23 +432,20 @@ __global__ void __launch_bounds__(64 * W, K * Lane<DT>::N <= 16 ? 8 : 4) logp_sp
   if (in_vocab(target, a.in.vocab)) {
     const Row<DT> r(a.in, row);
     xt = Vec<DT>::load1(r.x, (uint64_t)target);
-    const Spread<DT, W, K, !TWO> x(r, t);
-    const float b = -xt * a.in.c;
-    const float s = x.sum(
-        r, t, [&](float v) { return TWO ? term(v, xt, a.in) : __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
-        [](int, int, float) {});
+    const Spread<DT, W, K, NT> x(r, t);
+    const float s = x.sum(r, t, [&](float v) { return term(v, xt, a.in); }, [](int, int, float) {});
     rs = {xt, block_sum<W>((double)s)};
     if (!__builtin_amdgcn_readfirstlane(served(rs.s))) rs = row_reduce<DT, W>(r, xt, a.in);
   }
   if (t == 0) logp_finish(a, row, rs, xt);
 }
 
-template <int DT, bool TWO>
+template <int DT, bool NT>
 void launch_logp(LogpArgs a, hipStream_t s) {
   const bool done = with_spread<DT>(a.in.vocab, [&](auto w, auto k) {
     constexpr int W = decltype(w)::value, K = decltype(k)::value;
     for (a.row0 = 0; a.row0 < a.in.n_rows; a.row0 += kMostRows)
-      hipLaunchKernelGGL((logp_spread_kernel<DT, W, K, TWO>), (uint32_t)std::min(kMostRows, a.in.n_rows - a.row0),
+      hipLaunchKernelGGL((logp_spread_kernel<DT, W, K, NT>), (uint32_t)std::min(kMostRows, a.in.n_rows - a.row0),
                          64 * W, 0, s, a);
   });
   if (!done) hipLaunchKernelGGL(logp_kernel<DT>, chunk_grid(a.in.n_rows, 0), kBlock, 0, s, a);
@@ -621,9 +623,8 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   in = PolicyRow{uniform(in.weight), uniform(in.advantage), uniform(in.old_logp), uniform(in.ref_logp)};
   xt = uniform(xt);
   float e[RAW ? 1 : K][Lane<DT>::N], side = 0.0f;
-  float b = uniform(-xt * a.in.c);
   const float s = x.sum(
-      r, t, [&](float v) { return __builtin_amdgcn_exp2f(fmaf(v, a.in.c, b)); },
+      r, t, [&](float v) { return term(v, xt, a.in); },
       [&](int k, int i, float q) {
         if (k == K) side = q;
         else if constexpr (!RAW) e[k][i] = q;
@@ -642,7 +643,7 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   typename Vec<DT>::T* out = policy_out<DT>(a, row);
   void* out_v = out + r.head;
   const uint32_t at = (uint32_t)target - r.head - r.N * t;
-  if constexpr (RAW) asm volatile("" : "+s"(b));  // the exponentials are taken again, not kept
+  if constexpr (RAW) asm volatile("" : "+s"(xt));  // the exponentials are taken again, not kept
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t v = k * 64 * W + t;
@@ -650,7 +651,7 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
       float dx[Lane<DT>::N];
 #pragma unroll
       for (int i = 0; i < Lane<DT>::N; ++i) {
-        if constexpr (RAW) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Lane<DT>::get(x.x[k], i), a.in.c, b));
+        if constexpr (RAW) dx[i] = scale * __builtin_amdgcn_exp2f((Lane<DT>::get(x.x[k], i) - xt) * a.in.c);
         else dx[i] = scale * e[k][i];
       }
       add_at_target(dx, at - k * 64 * W * r.N, coef);
@@ -662,7 +663,7 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
       const auto y = load16_any<NT>(r.v, v);
       float dx[Lane<DT>::N];
 #pragma unroll
-      for (int i = 0; i < Lane<DT>::N; ++i) dx[i] = scale * __builtin_amdgcn_exp2f(fmaf(Lane<DT>::get(y, i), a.in.c, b));
+      for (int i = 0; i < Lane<DT>::N; ++i) dx[i] = scale * __builtin_amdgcn_exp2f((Lane<DT>::get(y, i) - xt) * a.in.c);
       add_at_target(dx, (uint32_t)target - r.head - r.N * v, coef);
       store16_any<DT, NT>(out_v, v, dx);
     }
@@ -927,7 +928,8 @@ int fill_logits(Logits* in, const void* logits, int dtype, uint64_t n_rows, uint
   }
   float hi = (float)c;
   if ((double)hi >= c) hi = std::nextafterf(hi, 0.0f);
-  *in = Logits{logits, n_rows, stride, vocab, targets, (float)c, hi, (float)(c - (double)hi), 1.0 / temperature};
+  const float lo = std::max((float)(c - (double)hi), std::numeric_limits<float>::denorm_min());  // 0 at T past 1e37
+  *in = Logits{logits, n_rows, stride, vocab, targets, (float)c, hi, lo, 1.0 / temperature};
   return ZERO_OK;
 }
 
@@ -990,7 +992,7 @@ extern "C" int zero_token_logprobs(const void* logits, int dtype, uint64_t n_row
   if (!logp || !aligned_to(logp, 4)) return fail(ZERO_EINVAL, "%s: logp is NULL or misaligned", who);
   if ((rc = begin_launch())) return rc;
   a.logp = logp;
-  by_dtype(dtype, [&](auto dt) { launch_logp<decltype(dt)::value, false>(a, stream); });
+  by_dtype(dtype, [&](auto dt) { launch_logp<decltype(dt)::value, true>(a, stream); });
   return launch_status(who);
 }
 
@@ -1094,7 +1096,7 @@ extern "C" int zero_preference_loss(const zero_preference_args* p, hipStream_t s
   l.logp = p->logp;
   l.stats = rows;
   if (p->n_rows > 0) {
-    by_dtype(p->dtype, [&](auto dt) { launch_logp<decltype(dt)::value, true>(l, stream); });
+    by_dtype(p->dtype, [&](auto dt) { launch_logp<decltype(dt)::value, false>(l, stream); });
     if ((rc = launch_status(who))) return rc;
   }
   const PairArgs q = {rows, p->n_rows, p->seq_begin, p->n_pairs, p->ref_logp, p->beta, p->label_smoothing,
