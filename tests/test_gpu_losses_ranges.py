@@ -184,3 +184,35 @@ def test_high_temperatures_and_masked_tokens(v, temperature):
     for row, n in enumerate((v, v - 1, 1)):
         assert abs(float(lp[row]) + math.log(n)) <= U * (26 + math.log(n)) + 30 / temperature
     assert torch.equal(lp, policy(x, t, lp, full(3, value=1.0), temperature)[1])
+
+
+@pytest.mark.parametrize("pairs", [2, 40])  # with the pairs in the gradient's launch, and in one of their own
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+def test_a_masked_target_in_a_pair(pairs, smoothing):
+    """A rejected answer of probability 0 leaves no loss and no gradient (with smoothing, an infinite loss: its
+    -ln sigma(-h) counts); a chosen one an infinite loss and the full slope."""
+    v, n = 200, 4 * pairs  # two tokens to a sequence
+    x, t = grid_rows(n, v, 0.5, seed=6)
+    bounds, ref = torch.arange(0, n + 1, 2, device=DEV), full(2 * pairs, value=-9.0)
+    plain = preference(x, t, bounds, ref, label_smoothing=smoothing)
+    y = x.clone()
+    y[3, t[3]] = -math.inf  # pair 0's rejected sequence
+    stats, logp, seq, reward, dx = preference(y, t, bounds, ref, label_smoothing=smoothing)
+    assert float(logp[3]) == float(seq[1]) == float(reward[1]) == -math.inf
+    others = [q for q in range(2 * pairs) if q != 1]
+    assert torch.equal(reward[others], plain[3][others])
+    h = (reward[0::2] - reward[1::2]).double()[1:]
+    rest = -((1 - smoothing) * torch.nn.functional.logsigmoid(h) + smoothing * torch.nn.functional.logsigmoid(-h)).sum()
+    if smoothing == 0.0:
+        assert abs(float(stats[0]) - float(rest) / pairs) <= 1e-6
+        assert int(dx[:4].count_nonzero()) == 0
+    else:
+        assert float(stats[0]) == math.inf and bool(torch.isfinite(dx).all())
+        assert torch.equal(dx[4:], plain[4][4:])
+    z = x.clone()
+    z[0, t[0]] = -math.inf  # pair 0's chosen sequence
+    stats, _, seq, reward, dx = preference(z, t, bounds, ref, label_smoothing=smoothing)
+    assert float(stats[0]) == math.inf and float(reward[0]) == -math.inf
+    assert bool(torch.isfinite(dx).all()) and torch.equal(dx[4:], plain[4][4:])
+    slope = -0.1 * (1 - smoothing) / pairs
+    assert abs(float(dx[0, t[0]]) - slope) <= 4 * U * abs(slope)

@@ -776,7 +776,9 @@ __device__ __forceinline__ Pair pair_terms(const PairArgs& a, uint32_t p, uint32
   // -ln sigma(h) and -ln sigma(-h), without overflow
   const double soft = ln(1.0 + ex), lose = soft + fmax(-h, 0.0), win = soft + fmax(h, 0.0);
   const double sig = h >= 0.0 ? 1.0 / (1.0 + ex) : ex / (1.0 + ex);
-  x.loss = {(1.0 - a.smoothing) * lose + a.smoothing * win, h > 0.0 ? 1.0 : 0.0};
+  // without smoothing an infinite -ln sigma(-h) (a rejected answer of probability 0) is not part of the loss
+  const double smooth = a.smoothing != 0.0 ? a.smoothing * win : 0.0;
+  x.loss = {(1.0 - a.smoothing) * lose + smooth, h > 0.0 ? 1.0 : 0.0};
   const double slope = a.beta * (sig - (1.0 - a.smoothing)) * a.grad_scale / (double)a.n_pairs;
   x.coef[0] = (float)(slope * part_of[0]);
   x.coef[1] = (float)(-slope * part_of[1]);
