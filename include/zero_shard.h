@@ -607,9 +607,9 @@ int zero_adam8_step(const zero_adam8_args *args, hipStream_t stream);
  * zero_moments8_pack / zero_moments8_unpack -- fp32 moments into the 8-bit form
  * (a 32-bit checkpoint continues in 8 bits) and back (an 8-bit owner's moments
  * leave through zero_owner_to_dense).  exp_avg, exp_avg_sq: device fp32,
- * end - local_base elements.  Unpack writes scale * code and its square; a
- * negative exp_avg_sq packs as NaN.  Only the owner's real elements are read
- * and written.
+ * end - local_base elements.  Unpack writes scale * code and its square.  A value
+ * that is not finite (for exp_avg_sq, or negative) makes its block of that moment
+ * NaN.  Only the owner's real elements are read and written.
  * Errors: EINVAL (NULL or misaligned arrays, bad bases); EHIP.
  * -------------------------------------------------------------------------- */
 int zero_moments8_pack(const zero_piece *pieces, uint64_t n_pieces, const uint8_t *masks, uint64_t n_masks,

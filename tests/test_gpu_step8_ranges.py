@@ -1,11 +1,9 @@
-"""The 8-bit step where gradients leave the ordinary: infinite ones, and finite ones whose
-square is beyond fp32.  Tolerances as in test_gpu_step8."""
-import numpy as np
+"""The 8-bit step and conversion where values leave the ordinary."""
 import pytest
 
 import synth
 from helpers import F32, gen, to_dev
-from test_gpu_step8 import HP, Q, check_step, host_state, make_shard
+from test_gpu_step8 import HP, Q, make_shard
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -53,20 +51,3 @@ def test_packing_a_second_moment_that_is_no_number(bad):
     gm, gv = unpacked(sh)
     assert bool((gm == 0.5).all())
     assert bool(torch.isnan(gv[Q:2 * Q]).all()) and bool(torch.isfinite(gv[:Q]).all() and torch.isfinite(gv[2 * Q:]).all())
-
-
-@pytest.mark.parametrize("big", [1e19, 3e20, -1e25, 1e36])
-@pytest.mark.parametrize("hp", [HP, dict(HP, adamw=False, weight_decay=0.1), dict(HP, beta2=0.0)])
-def test_a_finite_gradient_whose_square_overflows(big, hp):
-    """The formula's root is finite, and so are the moments, this step and the next."""
-    sh = make_shard([Q * 40], 1, 0, 1)
-    g = gen(3, synth.STREAM_GRAD, Q * 40, synth.DIST_NORMAL, 1e-3, F32)
-    g[5 * Q + 17] = big
-    for step in (2, 3):
-        before = host_state(sh)
-        sh.adam_step(step=step, hyper=hp, reduced_g=to_dev(g, F32))
-        torch.cuda.synchronize()
-        check_step(sh, before, g, hp, step, what=f"{big} step {step}")
-        g[5 * Q + 17] = 0.5  # the second step's gradient is ordinary, its root is not
-    for k in ("exp_avg_scale", "exp_rms_scale", "master"):
-        assert bool(torch.isfinite(getattr(sh, k)).all()), k

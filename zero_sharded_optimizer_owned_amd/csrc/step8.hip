@@ -15,7 +15,7 @@
 //
 // The new weight is computed from the new fp32 moments, before they are
 // rounded to 8 bits; the rounding only reaches the next step.  A non-finite
-// gradient makes its block's scale NaN, and with it the block's moments: run
+// gradient makes its block's scales NaN, and with them the block's moments: run
 // the overflow check first where that can happen.
 //
 // Work.  One thread takes 8 flat elements, so 16 lanes (one DPP row) hold a
@@ -111,7 +111,8 @@ __device__ __forceinline__ uint32_t row_max(uint32_t x) {
 }
 
 // Encodes the row's block: this thread's eight codes and the block's scale.
-// The maximum is taken over magnitude bits, where NaN is largest.
+// The maximum is taken over magnitude bits, where NaN is largest.  A maximum
+// that is not finite makes the scale NaN, so that every code decodes to NaN.
 template <bool ROOT>
 __device__ __forceinline__ u32x2 quantise(const float (&x)[8], float* scale) {
   uint32_t top = 0;
@@ -120,7 +121,7 @@ __device__ __forceinline__ u32x2 quantise(const float (&x)[8], float* scale) {
   const float m = __uint_as_float(row_max(top));
   const bool dead = m < kLiveMin;  // false for NaN
   const float inv = dead ? 0.0f : kCodeMax * (1.0f / m);
-  *scale = dead ? 0.0f : m * (1.0f / kCodeMax);
+  *scale = dead ? 0.0f : m * (1.0f / kCodeMax) + (m - m);
   float q[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
