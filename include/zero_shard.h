@@ -596,7 +596,9 @@ typedef struct {
  * and r before that rounding.  Arithmetic is fp32.  The results do not depend
  * on the launch, but a block that the owner's begin or end cuts scales by the
  * owner's part alone.  A block whose largest magnitude is below 2^-100 holds
- * zeros.  A non-finite gradient makes its whole block's moments NaN.
+ * zeros.  A non-finite gradient makes its whole block's moments NaN; a finite one
+ * whose square is beyond fp32 has a finite root (unpacked, its exp_avg_sq is then
+ * infinite).
  * Errors: EINVAL as for zero_adam_step, and for a missing state array or a
  * local_base that is no multiple of ZERO_QBLOCK; EHIP.
  * n_pieces == 0 or begin == end is a no-op.

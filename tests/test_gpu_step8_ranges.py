@@ -1,4 +1,5 @@
 """The 8-bit step and conversion where values leave the ordinary."""
+import numpy as np
 import pytest
 
 import synth
@@ -20,6 +21,12 @@ def _gpu():
     zs.lib()
     yield
     torch.cuda.synchronize()
+
+
+def decoded(sh):
+    """(first moment, root of the second) as the codes and scales stand for them."""
+    return [(c.float().view(-1, Q) * s.view(-1, 1)).view(-1)
+            for c, s in ((sh.exp_avg8, sh.exp_avg_scale), (sh.exp_rms8, sh.exp_rms_scale))]
 
 
 def unpacked(sh):
@@ -51,3 +58,36 @@ def test_packing_a_second_moment_that_is_no_number(bad):
     gm, gv = unpacked(sh)
     assert bool((gm == 0.5).all())
     assert bool(torch.isnan(gv[Q:2 * Q]).all()) and bool(torch.isfinite(gv[:Q]).all() and torch.isfinite(gv[2 * Q:]).all())
+
+
+@pytest.mark.parametrize("big", [1e19, 3e20, -1e25, 1e36])
+@pytest.mark.parametrize("hp", [HP, dict(HP, adamw=False, weight_decay=0.1), dict(HP, beta2=0.0)])
+def test_a_finite_gradient_whose_square_overflows(big, hp):
+    """The formula's root is finite, and so are the moments, this step and the next.
+
+    Against 64 bits, u = 2^-24: the new m and r are off by 6 u of their terms' sums, the quotient by 12 u more, a
+    scale by 8 u of its block's largest; a code by half an e4m3 step (2^-4, below the normal range 2^-10 scale, up to
+    2^-9 scale where a root above zero takes the smallest code) and by 2^-18 for the scale's and x's own rounding."""
+    at, u, shape = 5 * Q + 17, 2.0 ** -24, (-1, Q)
+    sh = make_shard([Q * 40], 1, 0, 1)
+    g = gen(3, synth.STREAM_GRAD, Q * 40, synth.DIST_NORMAL, 1e-3, F32).astype(np.float64)
+    for step, value in ((2, big), (3, 0.5)):  # the second step's gradient is ordinary, its root is not
+        g[at] = np.float32(value)
+        m0, r0 = (x.cpu().numpy().astype(np.float64) for x in decoded(sh))
+        w0 = sh.master.cpu().numpy().astype(np.float64)
+        sh.adam_step(step=step, hyper=hp, reduced_g=to_dev(g.astype(np.float32), F32))
+        b1, b2 = hp["beta1"], hp["beta2"]
+        gd = g if hp["adamw"] else g + hp["weight_decay"] * w0
+        m, r = b1 * m0 + (1 - b1) * gd, np.sqrt(b2 * r0 ** 2 + (1 - b2) * gd ** 2)
+        a = b1 * np.abs(m0) + (1 - b1) * np.abs(gd)
+        size, denom = hp["lr"] / (1 - b1 ** step), r / np.sqrt(1 - b2 ** step) + hp["eps"]
+        w = w0 * (1 - hp["lr"] * hp["weight_decay"] if hp["adamw"] else 1.0) - size * m / denom
+        got = sh.master.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - w) <= 3 * u * np.abs(w0) + 20 * u * size * a / denom)
+        for x, amp, back, root in zip((m, r), (a, r), decoded(sh), (False, True)):
+            back = back.cpu().numpy().astype(np.float64)
+            scale = np.repeat(np.abs(x).reshape(shape).max(1) / 448, Q)
+            off = 8 * u * np.repeat(amp.reshape(shape).max(1) / 448, Q)
+            half = np.maximum(np.abs(x) * 2.0 ** -4, (scale + off) * (2.0 ** -9 if root else 2.0 ** -10))
+            assert np.all(np.abs(back - x) <= half + 2.0 ** -18 * np.abs(x) + 8 * u * amp)
+            assert not root or np.all(back[x > 0] > 0)

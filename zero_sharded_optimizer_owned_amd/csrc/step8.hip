@@ -229,6 +229,13 @@ __device__ __forceinline__ void add8(float (&g)[8], const typename Vec<GDT>::Raw
   for (int k = 0; k < 8; ++k) g[k] = g[k] + Vec<GDT>::get(x, k);
 }
 
+// sqrt(beta2 r^2 + (1 - beta2) g^2) where the sum is beyond fp32 and the root is
+// not (g past 6e20 with beta2 = 0.999): the same with both scaled by a power of two.
+__device__ __forceinline__ float large_root(const Adam8Const& c, float g, float r) {
+  const float gs = g * 0x1p-66f, rs = r * 0x1p-66f;
+  return __builtin_sqrtf((c.beta2 * rs) * rs + (c.one_minus_beta2 * gs) * gs) * 0x1p66f;
+}
+
 // The step on eight elements in registers.  m and v round after every
 // operation: what a code's rounding turns on is then the same in any program
 // that evaluates the formula in fp32.
@@ -240,7 +247,8 @@ __device__ __forceinline__ void adam8(const Adam8Const& c, const float (&g)[8], 
     if (c.l2 != 0.0f) gc = fmaf(c.l2, w[k], gc);
     const float mn = c.beta1 * m[k] + c.one_minus_beta1 * gc;
     const float v = (c.beta2 * r[k]) * r[k] + (c.one_minus_beta2 * gc) * gc;
-    const float rn = __builtin_sqrtf(v);
+    float rn = __builtin_sqrtf(v);
+    if (__builtin_expect(v == INFINITY, 0)) rn = large_root(c, gc, r[k]);
     const float denom = fmaf(rn, c.inv_sqrt_bc2, c.eps);
     w[k] = fmaf(-c.step_size, mn / denom, w[k] * c.decay);
     m[k] = mn;
