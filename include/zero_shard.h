@@ -633,8 +633,9 @@ int zero_moments8_unpack(const zero_piece *pieces, uint64_t n_pieces, const uint
  * does a row whose logits are all -inf.  -inf logits (masked tokens) have
  * probability 0; NaN or +inf logits in a row that counts give NaN.
  *   lp = logits[target] / temperature - ln sum_j exp(logits[j] / temperature)
- * Elements are fp32; a row's sum, its logarithm and everything per row fp64;
- * sums over rows in a fixed order, so results are identical run to run.
+ * Elements, and partial sums of at most 129 of them, are fp32; a row's sum, its
+ * logarithm and everything per row fp64; sums over rows in a fixed order, so
+ * results are identical run to run.
  * -------------------------------------------------------------------------- */
 
 /* ----------------------------------------------------------------------------

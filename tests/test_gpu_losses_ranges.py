@@ -216,3 +216,27 @@ def test_a_masked_target_in_a_pair(pairs, smoothing):
     assert bool(torch.isfinite(dx).all()) and torch.equal(dx[4:], plain[4][4:])
     slope = -0.1 * (1 - smoothing) / pairs
     assert abs(float(dx[0, t[0]]) - slope) <= 4 * U * abs(slope)
+
+
+@pytest.mark.parametrize("name, v", [("f16", (1 << 26) + 5), ("f32", 1 << 25)])
+def test_sums_of_very_long_rows(name, v):
+    """Equal terms that fp32 does not hold exactly: adding thousands of them up in fp32 rounds the same way
+    again and again (6e-5 of the sum at 65,536 terms to a thread)."""
+    up = float(torch.tensor(0.3).to(DT[name]))
+    x = torch.zeros(2, v, dtype=DT[name], device=DEV)
+    t = torch.tensor([v // 3, 7], device=DEV)
+    x[0, t[0]] = up  # the target's own logit serves as the reference
+    x[1, v // 2], x[1, 7] = up, -60.0  # the maximum has to
+    rest = math.exp(-up)
+    total = [1 + (v - 1) * rest, 1 + (v - 2) * rest + math.exp(-60.0 - up)]
+    want = [-math.log(total[0]), -60.0 - up - math.log(total[1])]
+    got = logprobs(x, t)
+    for row in range(2):
+        assert abs(float(got[row]) - want[row]) <= U * (2 * abs(want[row] + math.log(v)) + 2 + 26 + abs(want[row]))
+    old = got - 0.1
+    stats, lp, dx = policy(x, t, old, full(2, value=1.0))
+    assert torch.equal(got, lp)
+    ratio = math.exp(want[0] - float(old[0]))
+    p = rest / total[0]
+    e = 40 * U
+    assert abs(float(dx[0, 0]) - ratio * p) <= ratio * p * (e + torch.finfo(DT[name]).eps / 2) + 2.0 ** -25

@@ -26,8 +26,8 @@
 // (measured on 500-token sequences: rewards 5e-6 off without it, 4e-7 with
 // it).  Every call forms a row's sum alike: the reference model's
 // log-probabilities and the policy's agree to the bit where the logits do.
-// Per-thread sums are fp32 over at most a few hundred elements and are
-// added up in fp64.
+// A thread adds a vector's 4 or 8 elements in fp32, and the vectors that it
+// holds in registers (at most 16); everything past that is added up in fp64.
 //
 // A row whose target is outside [0, vocab), or whose logits are all -inf,
 // counts for nothing: lp 0, gradient 0, and nothing of it is looked at.  NaN
@@ -213,37 +213,48 @@ __device__ __forceinline__ double block_sum(double x) {
 template <int DT, int W = kWavesPerBlock>
 __device__ __forceinline__ double row_sum(const Row<DT>& r, float z, const Logits& in) {
   const uint32_t t = threadIdx.x;
-  float s = 0.0f;
+  double s = 0.0;
 #pragma unroll 4
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
     const auto raw = load16_any(r.v, v);
     float e = 0.0f;
 #pragma unroll
     for (int k = 0; k < Lane<DT>::N; ++k) e += term(Lane<DT>::get(raw, k), z, in);
-    s += e;
+    s += (double)e;
   }
-  if (r.has_side(t)) s += term(Vec<DT>::load1(r.x, r.side(t)), z, in);
-  return block_sum<W>((double)s);
+  if (r.has_side(t)) s += (double)term(Vec<DT>::load1(r.x, r.side(t)), z, in);
+  return block_sum<W>(s);
 }
 
 // (reference, sum) with the row's maximum as the reference, found on the way;
 // (0, 0) when every logit is -inf.
 template <int DT, int W = kWavesPerBlock>
 __device__ __forceinline__ MaxSum row_max_sum(const Row<DT>& r, const Logits& in) {
+  constexpr int N = Lane<DT>::N;
   const uint32_t t = threadIdx.x;
-  float m = -INFINITY, s = 0.0f;
-  auto add = [&](float x) {
-    const float nm = fmaxf(m, x), z = finite_or_zero(nm);
-    s = s * term(m, z, in) + term(x, z, in);
-    m = nm;
+  MaxSum own = {-INFINITY, 0.0};
+  // the sum so far goes over to the larger maximum, then a vector's terms join it
+  auto raise = [&](float top) {
+    const float nm = fmaxf(own.m, top), z = finite_or_zero(nm);
+    own.s *= (double)term(own.m, z, in);
+    own.m = nm;
+    return z;
   };
   for (uint32_t v = t; v < r.n_vec; v += 64 * W) {
     const auto raw = load16_any(r.v, v);
+    float top = -INFINITY, e = 0.0f;
 #pragma unroll
-    for (int k = 0; k < Lane<DT>::N; ++k) add(Lane<DT>::get(raw, k));
+    for (int k = 0; k < N; ++k) top = fmaxf(top, Lane<DT>::get(raw, k));
+    const float z = raise(top);
+#pragma unroll
+    for (int k = 0; k < N; ++k) e += term(Lane<DT>::get(raw, k), z, in);
+    own.s += (double)e;
   }
-  if (r.has_side(t)) add(Vec<DT>::load1(r.x, r.side(t)));
-  MaxSum all = block_join<W>(MaxSum{m, (double)s}, in);
+  if (r.has_side(t)) {
+    const float x = Vec<DT>::load1(r.x, r.side(t)), z = raise(x);
+    own.s += (double)term(x, z, in);
+  }
+  MaxSum all = block_join<W>(own, in);
   all.m = finite_or_zero(all.m);
   return all;
 }
@@ -326,7 +337,7 @@ struct Spread {
   // This thread's share of the sum; term(x) is an element's, and keep(k, i, q)
   // sees it (k = K: the one beside the vectors).
   template <typename T, typename F>
-  __device__ __forceinline__ float sum(const Row<DT>& r, uint32_t t, T term, F keep) const {
+  __device__ __forceinline__ double sum(const Row<DT>& r, uint32_t t, T term, F keep) const {
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -341,6 +352,9 @@ struct Spread {
         s += k * kStep + t < r.n_vec ? part : 0.0f;
       }
     }
+    const float q = term(side);
+    keep(K, 0, q);
+    double all = (double)(r.has_side(t) ? s + q : s);
     if constexpr (kRest) {
 #pragma unroll 2
       for (uint32_t v = K * kStep + t; v < r.n_vec; v += kStep) {
@@ -348,12 +362,10 @@ struct Spread {
         float part = 0.0f;
 #pragma unroll
         for (int i = 0; i < Lane<DT>::N; ++i) part += term(Lane<DT>::get(y, i));
-        s += part;
+        all += (double)part;
       }
     }
-    const float q = term(side);
-    keep(K, 0, q);
-    return r.has_side(t) ? s + q : s;
+    return all;
   }
 };
 
@@ -433,8 +445,7 @@ __global__ void __launch_bounds__(64 * W, K * Lane<DT>::N <= 16 ? 8 : 4) logp_sp
     const Row<DT> r(a.in, row);
     xt = Vec<DT>::load1(r.x, (uint64_t)target);
     const Spread<DT, W, K, NT> x(r, t);
-    const float s = x.sum(r, t, [&](float v) { return term(v, xt, a.in); }, [](int, int, float) {});
-    rs = {xt, block_sum<W>((double)s)};
+    rs = {xt, block_sum<W>(x.sum(r, t, [&](float v) { return term(v, xt, a.in); }, [](int, int, float) {}))};
     if (!__builtin_amdgcn_readfirstlane(served(rs.s))) rs = row_reduce<DT, W>(r, xt, a.in);
   }
   if (t == 0) logp_finish(a, row, rs, xt);
@@ -619,17 +630,17 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   PolicyRow in = policy_row(a, row);
   if (!in_vocab(target, a.in.vocab)) return policy_stream<DT, W, NT>(a, row, r, target, in, 0.0f, false, sh);
   float xt = Vec<DT>::load1(r.x, (uint64_t)target);
-  const Spread<DT, W, K, true> x(r, t);
+  Spread<DT, W, K, true> x(r, t);
   in = PolicyRow{uniform(in.weight), uniform(in.advantage), uniform(in.old_logp), uniform(in.ref_logp)};
   xt = uniform(xt);
   float e[RAW ? 1 : K][Lane<DT>::N], side = 0.0f;
-  const float s = x.sum(
+  const double s = x.sum(
       r, t, [&](float v) { return term(v, xt, a.in); },
       [&](int k, int i, float q) {
         if (k == K) side = q;
         else if constexpr (!RAW) e[k][i] = q;
       });
-  const RowSum rs = {xt, block_sum<W>((double)s)};
+  const RowSum rs = {xt, block_sum<W>(s)};
   if (!__builtin_amdgcn_readfirstlane(served(rs.s)))  // the same in every thread
     return policy_stream<DT, W, NT>(a, row, r, target, in, xt, true, sh);
   if (t == 0) {
@@ -643,7 +654,10 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   typename Vec<DT>::T* out = policy_out<DT>(a, row);
   void* out_v = out + r.head;
   const uint32_t at = (uint32_t)target - r.head - r.N * t;
-  if constexpr (RAW) asm volatile("" : "+s"(xt));  // the exponentials are taken again, not kept
+  if constexpr (RAW) {  // the elements are unpacked again, and nothing of them kept but the 16 bits
+#pragma unroll
+    for (int k = 0; k < K; ++k) asm volatile("" : "+v"(x.x[k]));
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const uint32_t v = k * 64 * W + t;
