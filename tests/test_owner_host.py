@@ -1,0 +1,31 @@
+"""OwnerShard and OwnerShard8 as objects: what they are made from, saved to and refuse.  On the CPU:
+layouts, tables and checkpoints only, nothing is launched."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import zero_sharded_optimizer_owned_amd as zs  # noqa: E402
+
+CLASSES = [zs.OwnerShard, zs.OwnerShard8]
+
+
+@pytest.mark.parametrize("cls", CLASSES)
+def test_sizes_from_any_iterable(cls):
+    want = cls([1000, 37, 5003], 4, 1, device="cpu")
+    model = [torch.zeros(1000), torch.zeros(37), torch.zeros(5003)]
+    for numels in ((p.numel() for p in model), map(len, model), {k: len(p) for k, p in enumerate(model)}.values(),
+                   (1000, 37, 5003), torch.Size([1000, 37, 5003]), np.array([1000, 37, 5003]),
+                   np.array([1000, 37, 5003], dtype=np.uint64), [torch.tensor(1000), np.int32(37), 5003]):
+        got = cls(numels, 4, 1, device="cpu")
+        assert got.numels == want.numels == [1000, 37, 5003] and all(type(n) is int for n in got.numels)
+        assert (got.begin, got.end, got.local_base) == (want.begin, want.end, want.local_base)
+        assert np.array_equal(got.chunks, want.chunks) and np.array_equal(got.dense_offsets, want.dense_offsets)
+
+
+@pytest.mark.parametrize("cls", CLASSES)
+@pytest.mark.parametrize("numels, error", [([-5], OverflowError), (np.array([3, -5]), OverflowError), (5, TypeError),
+                                           ([[1, 2], [3, 4]], TypeError), ([4, 0], zs.ZeroShardError)])
+def test_sizes_that_are_none(cls, numels, error):
+    with pytest.raises(error):
+        cls(numels, 1, 0, device="cpu")

@@ -173,6 +173,13 @@ def _u64(a) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=np.uint64))
 
 
+def _sizes(numels) -> np.ndarray:
+    """Tensor sizes as uint64, from any iterable of numbers (a generator over a model's parameters)."""
+    if isinstance(numels, np.ndarray) and numels.dtype == np.uint64 and numels.ndim == 1:
+        return np.ascontiguousarray(numels)
+    return np.fromiter(map(int, numels), dtype=np.uint64)
+
+
 def _p(a: np.ndarray):
     return ct.c_void_p(a.ctypes.data) if a is not None and a.size else None
 
@@ -879,7 +886,7 @@ class OwnerShard:
     def __init__(self, numels: Sequence[int], ranks: int, owner: int, align: int = 64,
                  max_chunk: int = 2048, device=None):
         torch = _torch()
-        sizes = _u64(numels)  # once: each of the tables below takes the sizes
+        sizes = _sizes(numels)  # once: each of the tables below takes the sizes
         self.numels = sizes.tolist()
         self.offsets, self.padded_total, begins, ends = zero_shard_layout(sizes, ranks, align)
         self.ranks, self.owner = ranks, owner
@@ -1049,7 +1056,7 @@ class OwnerShard8(OwnerShard):
 
     def __init__(self, numels: Sequence[int], ranks: int, owner: int, align: int = 64,
                  max_chunk: int = 2048, device=None):
-        sizes = _u64(numels)
+        sizes = _sizes(numels)
         super().__init__(sizes, ranks, owner, align, max_chunk, device)
         torch = _torch()
         self.local_base = self.begin // ZERO_QBLOCK * ZERO_QBLOCK
