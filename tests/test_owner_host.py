@@ -29,3 +29,19 @@ def test_sizes_from_any_iterable(cls):
 def test_sizes_that_are_none(cls, numels, error):
     with pytest.raises(error):
         cls(numels, 1, 0, device="cpu")
+
+
+@pytest.mark.parametrize("cls, other", [CLASSES, CLASSES[::-1]])
+def test_a_checkpoint_of_the_other_width_is_refused_whole(cls, other, tmp_path):
+    """Nothing of the owner changes when its load is refused."""
+    saved, mine = other([300, 7], 2, 1, device="cpu"), cls([300, 7], 2, 1, device="cpu")
+    saved.alloc_state()
+    saved.master.fill_(7.0)
+    saved.save(str(tmp_path / "s.npz"), 3)
+    mine.alloc_state()
+    before = mine.master.clone()
+    with pytest.raises(ValueError):
+        mine.load(str(tmp_path / "s.npz"))
+    assert torch.equal(mine.master, before)
+    again = other([300, 7], 2, 1, device="cpu")
+    assert again.load(str(tmp_path / "s.npz")) == 3 and torch.equal(again.master, saved.master)

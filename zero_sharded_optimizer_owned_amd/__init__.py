@@ -1034,10 +1034,10 @@ class OwnerShard:
         """Restore a checkpoint written by save() for the same layout; returns its step."""
         torch = _torch()
         with np.load(path, allow_pickle=False) as z:
-            same = (list(z["numels"]) == self.numels and int(z["ranks"]) == self.ranks
+            same = ("exp_avg" in z.files and list(z["numels"]) == self.numels and int(z["ranks"]) == self.ranks
                     and int(z["owner"]) == self.owner and int(z["align"]) == self.align)
             if not same:
-                raise ValueError("checkpoint was written for a different layout or owner")
+                raise ValueError("checkpoint was written for a different layout, owner or state width")
             self.master = torch.from_numpy(z["master"]).to(self.device)
             self.exp_avg = torch.from_numpy(z["exp_avg"]).to(self.device)
             self.exp_avg_sq = torch.from_numpy(z["exp_avg_sq"]).to(self.device)
