@@ -91,3 +91,23 @@ def test_a_finite_gradient_whose_square_overflows(big, hp):
             half = np.maximum(np.abs(x) * 2.0 ** -4, (scale + off) * (2.0 ** -9 if root else 2.0 ** -10))
             assert np.all(np.abs(back - x) <= half + 2.0 ** -18 * np.abs(x) + 8 * u * amp)
             assert not root or np.all(back[x > 0] > 0)
+
+
+def test_the_first_export_can_be_captured():
+    sh = make_shard([100, 37, 5003], 2, 1, 64)
+    dense, back = torch.zeros(sh.dense_total, device=DEV), torch.zeros_like(sh.master)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sh.to_dense(sh.master, dense)
+        sh.from_dense(dense, back)
+    want_dense, want_back = torch.zeros_like(dense), torch.zeros_like(back)
+    sh.to_dense(sh.master, want_dense)
+    sh.from_dense(want_dense, want_back)
+    assert int(want_dense.count_nonzero()) > 0
+    for _ in range(3):
+        dense.zero_()
+        back.zero_()
+        torch.randn(4096, device=DEV).sum()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dense, want_dense) and torch.equal(back, want_back)

@@ -45,3 +45,18 @@ def test_a_checkpoint_of_the_other_width_is_refused_whole(cls, other, tmp_path):
     assert torch.equal(mine.master, before)
     again = other([300, 7], 2, 1, device="cpu")
     assert again.load(str(tmp_path / "s.npz")) == 3 and torch.equal(again.master, saved.master)
+
+
+@pytest.mark.parametrize("cls", CLASSES)
+def test_the_constructor_makes_every_table(cls, monkeypatch):
+    """An export or import later builds nothing (it may run under a graph's capture, or on several threads)."""
+    sh = cls([100] * 50 + [5003], 2, 1, device="cpu")
+
+    def no(*a, **k):
+        raise AssertionError("a table made after construction")
+
+    for name in ("zero_chunk_table", "zero_chunk_groups", "zero_dense_offsets", "zero_piece_table", "chunks_to_device"):
+        monkeypatch.setattr(zs, name, no)
+    assert sh.chunks.size and sh.n_groups == sh.groups.size - 1 and sh.dense_total == 10_003 and sh.n_real
+    assert sh.chunks_dev.numel() == 16 * sh.chunks.size
+    assert sh.tensor_offset_dev.numel() == sh.dense_offset_dev.numel() == 51

@@ -895,11 +895,6 @@ class OwnerShard:
         self.local_size = self.end - self.local_base
         self.device = torch.device(device or "cuda")
         self.align = align
-        self._tables(sizes, max_chunk)
-
-    def _tables(self, sizes, max_chunk: int) -> None:
-        """The chunk, group and offset tables of the fp32 step, the export and the import."""
-        torch = _torch()
         self.chunks = zero_chunk_table(sizes, self.offsets, self.begin, self.end, max_chunk)
         self.chunks_dev = chunks_to_device(self.chunks, self.device)
         # short chunks packed several to a block, when that saves enough blocks
@@ -1066,20 +1061,6 @@ class OwnerShard8(OwnerShard):
         self.pieces_dev = chunks_to_device(self.pieces, self.device)
         self.masks_dev = torch.from_numpy(masks).to(self.device) if masks.size else None
         self._work = None
-
-    # OwnerShard's tables are made when one of them is first asked for (an export, an
-    # import): the step itself needs the piece table alone.
-    _LATE = frozenset(("chunks", "chunks_dev", "groups", "n_groups", "groups_dev", "n_real", "dense_offsets",
-                       "dense_total", "tensor_offset_dev", "dense_offset_dev"))
-
-    def _tables(self, sizes, max_chunk: int) -> None:
-        self._late = sizes, max_chunk
-
-    def __getattr__(self, name):
-        if name in OwnerShard8._LATE and "_late" in self.__dict__:
-            OwnerShard._tables(self, *self.__dict__.pop("_late"))
-            return self.__dict__[name]
-        raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
 
     def alloc_state(self):
         """master, then the moments: (codes, scales) of the first and of the second's root."""
