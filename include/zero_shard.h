@@ -670,7 +670,8 @@ typedef struct {
   void *dlogits;          /* same dtype as logits; may be logits itself; NULL: no gradient */
   uint64_t dlogits_stride;
   void *workspace;        /* zero_policy_workspace_bytes(n_rows), 256-byte aligned; zeros before its first use,
-                             left ready for the next call; calls that overlap need one each */
+                             left ready for the next call; calls that overlap need one each.  The first 8 bytes
+                             count rows: with anything else in them a call of up to 128 rows leaves stats NaN */
   size_t workspace_bytes;
 } zero_policy_args;
 

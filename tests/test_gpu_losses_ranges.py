@@ -240,3 +240,37 @@ def test_sums_of_very_long_rows(name, v):
     p = rest / total[0]
     e = 40 * U
     assert abs(float(dx[0, 0]) - ratio * p) <= ratio * p * (e + torch.finfo(DT[name]).eps / 2) + 2.0 ** -25
+
+
+@pytest.mark.parametrize("v", [50, 3000, 140_000])
+@pytest.mark.parametrize("n", [1, 24, 128])
+def test_a_workspace_that_was_not_zero_shows(n, v):
+    """The loss of few rows is formed by the last block to finish, which a count in the workspace names.  A count
+    that does not start at 0 leaves NaN, never the values of an earlier call; the rest of the results hold."""
+    x, t = grid_rows(n, v, 0.5, seed=10)
+    adv, old = full(n, value=1.0), full(n, value=-2.0)
+    want, logp, dx = policy(x, t, old, adv)
+    for left in (0x0101010101010101, -1, 1, 23, 127):  # bytes, or the small numbers of some other tensor
+        ws = zs.policy_workspace(n, DEV)
+        ws[:ws.numel() // 8 * 8].view(torch.int64).fill_(left)
+        stats, lp, d = full(4), full(n), torch.full_like(x, 5.0)
+        for _ in range(2):  # nor does a second call with it
+            zs.zero_policy_loss(x, t, old_logp=old, advantage=adv, divisor=1.0, stats=stats, logp=lp, dlogits=d,
+                                workspace=ws)
+            assert bool(torch.isnan(stats).all()), stats
+            assert torch.equal(lp, logp) and torch.equal(d, dx)
+    ws = zs.policy_workspace(n, DEV)
+    for _ in range(3):
+        zs.zero_policy_loss(x, t, old_logp=old, advantage=adv, divisor=1.0, stats=stats, logp=lp, dlogits=d, workspace=ws)
+        assert torch.equal(stats, want)
+
+
+def test_more_rows_need_no_count():
+    """Past 128 rows a launch of its own adds up: any contents of the workspace will do."""
+    x, t = grid_rows(129, 300, 0.5, seed=11)
+    adv, old = full(129, value=1.0), full(129, value=-2.0)
+    want, _, _ = policy(x, t, old, adv)
+    stats, lp = full(4), full(129)
+    zs.zero_policy_loss(x, t, old_logp=old, advantage=adv, divisor=1.0, stats=stats, logp=lp,
+                        workspace=zs.policy_workspace(129, DEV).fill_(0xFF))
+    assert torch.equal(stats, want)

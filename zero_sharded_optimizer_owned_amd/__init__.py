@@ -808,7 +808,8 @@ def _workspace(fn, *sizes, device=None):
 
 def policy_workspace(n_rows: int, device=None):
     """The device workspace of ``zero_policy_loss`` over up to n_rows rows: zeros before
-    its first use, then left ready for the next call (one call at a time)."""
+    its first use, then left ready for the next call (one call at a time).  Any other
+    contents show as NaN in ``stats``."""
     return _workspace(lib().zero_policy_workspace_bytes, n_rows, device=device)
 
 

@@ -485,7 +485,7 @@ struct PolicyArgs {
   void* dlogits;
   uint64_t dstride;
   PolicyTerms* terms;
-  uint32_t* ticket;  // NULL: a launch of its own adds up the terms
+  uint64_t* ticket;  // NULL: a launch of its own adds up the terms
 };
 
 // What a row brings besides its logits, loaded ahead of them: each would be a
@@ -520,6 +520,17 @@ __device__ __forceinline__ float policy_terms(const PolicyArgs& a, const PolicyR
   return (float)(w * slope * a.grad_scale * a.in.inv_t);
 }
 
+// Stores and loads that are coherent across the chip: what one block of a launch
+// leaves for another.
+template <typename T>
+__device__ __forceinline__ void put_agent(T* p, T x) {
+  __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T get_agent(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // The row's log-probability and terms to memory, by one thread; its coefficient.
 __device__ __forceinline__ float policy_finish(const PolicyArgs& a, uint64_t row, const PolicyRow& in, const RowSum& rs,
                                                float xt) {
@@ -527,11 +538,9 @@ __device__ __forceinline__ float policy_finish(const PolicyArgs& a, uint64_t row
   PolicyTerms terms = {0.0, 0.0, 0.0};
   const float coef = rs.counts() ? policy_terms(a, in, lp, &terms) : 0.0f;
   a.logp[row] = (float)lp;
-  // coherent across the chip, for the block that adds the terms up
-  auto put = [](double* p, double x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  put(&a.terms[row].gain, terms.gain);
-  put(&a.terms[row].kl, terms.kl);
-  put(&a.terms[row].clipped, terms.clipped);
+  put_agent(&a.terms[row].gain, terms.gain);  // for the block that adds the terms up
+  put_agent(&a.terms[row].kl, terms.kl);
+  put_agent(&a.terms[row].clipped, terms.clipped);
   return coef;
 }
 
@@ -547,7 +556,7 @@ template <int W, bool COHERENT>
 __device__ __forceinline__ void policy_fold(const PolicyTerms* terms, uint64_t n, double kl_coef, float* stats) {
   __shared__ PolicyTerms part[W];
   auto get = [](const double* p) {
-    if constexpr (COHERENT) return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if constexpr (COHERENT) return get_agent(p);
     else return *p;
   };
   PolicyTerms s = {0.0, 0.0, 0.0};
@@ -566,10 +575,10 @@ __device__ __forceinline__ void policy_fold(const PolicyTerms* terms, uint64_t n
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < W; ++i) add(part[i]);
-    stats[0] = (float)((kl_coef != 0.0 ? kl_coef * s.kl : 0.0) - s.gain);
-    stats[1] = (float)-s.gain;
-    stats[2] = (float)s.kl;
-    stats[3] = (float)s.clipped;
+    put_agent(stats, (float)((kl_coef != 0.0 ? kl_coef * s.kl : 0.0) - s.gain));
+    put_agent(stats + 1, (float)-s.gain);
+    put_agent(stats + 2, (float)s.kl);
+    put_agent(stats + 3, (float)s.clipped);
   }
 }
 
@@ -581,11 +590,32 @@ __global__ void __launch_bounds__(64 * kFoldWaves) policy_fold_kernel(const Poli
 
 // After a block's row is in memory (by thread 0): whether it was the last of
 // the launch's rows.  The last one puts the count back to 0 for the next call.
-__device__ __forceinline__ bool policy_last(const PolicyArgs& a) {
+// A count that did not start at 0 (a workspace that was never zeroed, or that
+// two calls share at once) must not leave the stats of an earlier call: the
+// first row's block sets them to NaN ahead of its own count, and so does every
+// block that finds a count beyond the rows.  The count goes in steps of an odd
+// constant, so that memory with small numbers in it is such a count too.
+constexpr uint64_t kTicketStep = 0x9E3779B97F4A7C15u;
+constexpr uint64_t odd_inverse(uint64_t x) {  // modulo 2^64, by Newton's iteration
+  uint64_t y = x;
+  for (int i = 0; i < 5; ++i) y *= 2 - x * y;
+  return y;
+}
+static_assert(odd_inverse(kTicketStep) * kTicketStep == 1, "");
+
+__device__ __forceinline__ void policy_spoil(const PolicyArgs& a) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) put_agent(a.stats + i, __builtin_nanf(""));
+}
+
+__device__ __forceinline__ bool policy_last(const PolicyArgs& a, uint64_t row) {
   if (!a.ticket) return false;
-  const uint32_t before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-  if (before + 1 != (uint32_t)a.in.n_rows) return false;
-  __hip_atomic_store(a.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (row == 0) policy_spoil(a);
+  const uint64_t before =
+      __hip_atomic_fetch_add(a.ticket, kTicketStep, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) * odd_inverse(kTicketStep);
+  if (before >= a.in.n_rows) policy_spoil(a);
+  if (before + 1 != a.in.n_rows) return false;
+  put_agent(a.ticket, (uint64_t)0);
   return true;
 }
 
@@ -602,7 +632,7 @@ __device__ __forceinline__ void policy_stream(const PolicyArgs& a, uint64_t row,
   __syncthreads();  // sh may still be read for the row before
   if (threadIdx.x == 0) {
     sh.coef = policy_finish(a, row, in, rs, xt);
-    sh.last = policy_last(a);
+    sh.last = policy_last(a, row);
   }
   __syncthreads();
   if (a.dlogits) row_gradient<DT, W, NT>(r, policy_out<DT>(a, row), target, rs, a.in.c, sh.coef);
@@ -652,7 +682,7 @@ __device__ __forceinline__ void policy_spread(const PolicyArgs& a, PolicyShared&
   if (t == 0) {
     sh.coef = policy_finish(a, row, in, rs, xt);
     sh.scale = (float)(-(double)sh.coef / rs.s);
-    sh.last = policy_last(a);
+    sh.last = policy_last(a, row);
   }
   __syncthreads();
   if (!a.dlogits) return;
@@ -1067,7 +1097,7 @@ extern "C" int zero_policy_loss(const zero_policy_args* p, hipStream_t stream) {
   a.dstride = p->dlogits_stride;
   if (p->n_rows > 0) {
     a.terms = reinterpret_cast<PolicyTerms*>(static_cast<char*>(p->workspace) + 256);
-    if (p->n_rows <= kTicketRows) a.ticket = static_cast<uint32_t*>(p->workspace);
+    if (p->n_rows <= kTicketRows) a.ticket = static_cast<uint64_t*>(p->workspace);
   }
   if (p->n_rows > 0) {
     by_dtype(p->dtype, [&](auto dt) {
