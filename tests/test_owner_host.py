@@ -60,3 +60,20 @@ def test_the_constructor_makes_every_table(cls, monkeypatch):
     assert sh.chunks.size and sh.n_groups == sh.groups.size - 1 and sh.dense_total == 10_003 and sh.n_real
     assert sh.chunks_dev.numel() == 16 * sh.chunks.size
     assert sh.tensor_offset_dev.numel() == sh.dense_offset_dev.numel() == 51
+
+
+def test_device_0_is_a_device(monkeypatch):
+    """Not the current one."""
+    seen = []
+    make = lambda *a, device, **k: seen.append(device)  # noqa: E731
+    monkeypatch.setattr(torch, "zeros", make)
+    monkeypatch.setattr(torch, "empty", make)
+    for call in (lambda d: zs.policy_workspace(3, device=d), lambda d: zs.preference_workspace(3, 1, device=d),
+                 lambda d: zs.check_workspace(3, device=d)):
+        for device, want in ((0, 0), (1, 1), (None, "cuda"), ("cuda:0", "cuda:0")):
+            call(device)
+            assert seen.pop() == want
+    monkeypatch.undo()
+    monkeypatch.setattr(torch, "device", lambda d: seen.append(d) or "cpu")
+    zs.OwnerShard([5], 1, 0, device=0)
+    assert seen == [0]

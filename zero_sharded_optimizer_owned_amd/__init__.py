@@ -297,6 +297,11 @@ def _dtype_code(t) -> int:
     return _dtype_codes[t.dtype]
 
 
+def _device(device):
+    """Where a call puts what it makes: the current device unless one is named (0 is one)."""
+    return "cuda" if device is None else device
+
+
 def _dev(t, name: str, dtype=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -424,13 +429,13 @@ def check_workspace_bytes(n: int) -> int:
 def check_workspace(n: int, device=None):
     """A device buffer for the overflow / norm reduction over n elements."""
     torch = _torch()
-    return torch.empty(check_workspace_bytes(n), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(check_workspace_bytes(n), dtype=torch.uint8, device=_device(device))
 
 
 def chunks_to_device(chunks: np.ndarray, device=None):
     torch = _torch()
     flat = np.ascontiguousarray(chunks).view(np.uint8)
-    t = torch.from_numpy(flat.copy()).to(device or "cuda")
+    t = torch.from_numpy(flat.copy()).to(_device(device))
     return t
 
 
@@ -578,7 +583,7 @@ def zero3_partition_spans(numels, ranks: int, rank: int, max_span: int = DEFAULT
 
 def spans_to_device(spans: np.ndarray, device=None):
     torch = _torch()
-    return torch.from_numpy(np.ascontiguousarray(spans).view(np.uint8).copy()).to(device or "cuda")
+    return torch.from_numpy(np.ascontiguousarray(spans).view(np.uint8).copy()).to(_device(device))
 
 
 def zero_span_groups(spans: np.ndarray, elem_bytes: int, max_group: int = DEFAULT_SPAN) -> np.ndarray:
@@ -803,7 +808,7 @@ def _workspace(fn, *sizes, device=None):
     out = np.zeros(1, dtype=np.uint64)
     _check(fn(*sizes, _p(out)))
     torch = _torch()
-    return torch.zeros(int(out[0]), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(int(out[0]), dtype=torch.uint8, device=_device(device))
 
 
 def policy_workspace(n_rows: int, device=None):
@@ -894,7 +899,7 @@ class OwnerShard:
         self.begin, self.end = int(begins[owner]), int(ends[owner])
         self.local_base = self.begin & ~7
         self.local_size = self.end - self.local_base
-        self.device = torch.device(device or "cuda")
+        self.device = torch.device(_device(device))
         self.align = align
         self.chunks = zero_chunk_table(sizes, self.offsets, self.begin, self.end, max_chunk)
         self.chunks_dev = chunks_to_device(self.chunks, self.device)
