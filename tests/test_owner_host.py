@@ -1,5 +1,7 @@
 """OwnerShard and OwnerShard8 as objects: what they are made from, saved to and refuse.  On the CPU:
 layouts, tables and checkpoints only, nothing is launched."""
+import copy
+
 import numpy as np
 import pytest
 
@@ -77,3 +79,17 @@ def test_device_0_is_a_device(monkeypatch):
     monkeypatch.setattr(torch, "device", lambda d: seen.append(d) or "cpu")
     zs.OwnerShard([5], 1, 0, device=0)
     assert seen == [0]
+
+
+def test_a_copy_of_an_owner_uses_its_own_tables(monkeypatch):
+    """No address outlives the tensor it belongs to: a deep copy after a call, or one with a new table."""
+    sh = zs.OwnerShard8([100] * 40, 2, 1, device="cpu")
+    sh.alloc_state()
+    monkeypatch.setattr(zs, "_device_stream", lambda: (-1, 0))  # where a host tensor's get_device() is
+    tables = lambda s: s._checked()[2][0:3:2]  # noqa: E731
+    own = lambda s: (s.pieces_dev.data_ptr(), s.masks_dev.data_ptr())  # noqa: E731
+    assert tables(sh) == own(sh)
+    twin = copy.deepcopy(sh)
+    assert tables(twin) == own(twin) and not set(own(twin)) & set(own(sh))
+    sh.pieces_dev = sh.pieces_dev.clone()
+    assert tables(sh) == own(sh)

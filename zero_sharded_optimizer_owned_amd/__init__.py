@@ -1066,7 +1066,6 @@ class OwnerShard8(OwnerShard):
         self.pieces, masks = zero_piece_table(sizes, self.offsets, self.begin, self.end)
         self.pieces_dev = chunks_to_device(self.pieces, self.device)
         self.masks_dev = torch.from_numpy(masks).to(self.device) if masks.size else None
-        self._work = None
 
     def alloc_state(self):
         """master, then the moments: (codes, scales) of the first and of the second's root."""
@@ -1085,12 +1084,12 @@ class OwnerShard8(OwnerShard):
                     exp_avg_scale=self.exp_avg_scale, exp_rms8=self.exp_rms8, exp_rms_scale=self.exp_rms_scale)
 
     def _checked(self):
-        """(device, stream, piece table, 8-bit state) of a call; the table is this object's own, checked once."""
+        """(device, stream, piece table, 8-bit state) of a call."""
         dev, stream = _device_stream()
-        if self._work is None or self._work[0] != dev:
-            self._work = dev, _pieces8(dev, self.pieces_dev, self.pieces.size, self.masks_dev, self.begin, self.end)
-        return dev, stream, self._work[1], _state8(dev, self.end, self.local_base, self.exp_avg8, self.exp_avg_scale,
-                                                   self.exp_rms8, self.exp_rms_scale)
+        return (dev, stream,
+                _pieces8(dev, self.pieces_dev, self.pieces.size, self.masks_dev, self.begin, self.end),
+                _state8(dev, self.end, self.local_base, self.exp_avg8, self.exp_avg_scale, self.exp_rms8,
+                        self.exp_rms_scale))
 
     def adam_step(self, *, step: int, hyper: dict, rank_grads=None, grad_base: int = 0,
                   divisor: float = 1.0, reduced_g=None, param16=None, param_base: int = 0,
