@@ -93,3 +93,20 @@ def test_a_copy_of_an_owner_uses_its_own_tables(monkeypatch):
     assert tables(twin) == own(twin) and not set(own(twin)) & set(own(sh))
     sh.pieces_dev = sh.pieces_dev.clone()
     assert tables(sh) == own(sh)
+
+
+@pytest.mark.parametrize("change", [dict(n_pieces=-1), dict(begin=-8, end=-8), dict(end=-1)])
+def test_negative_counts_are_refused(change, monkeypatch):
+    """They are unsigned for the library: -1 pieces would be all there is of memory."""
+    sh = zs.OwnerShard8([1000], 1, 0, device="cpu")
+    sh.alloc_state()
+    monkeypatch.setattr(zs, "_device_stream", lambda: (-1, 0))
+    monkeypatch.setattr(zs, "_check", lambda rc: None)
+    monkeypatch.setattr(zs, "lib", lambda: pytest.fail("reached the library"))
+    state, moments = {**sh._state8(), **change}, [torch.zeros(1024), torch.zeros(1024)]
+    hyper = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+    for call in (lambda: zs.zero_adam8_step(**state, master=sh.master, step=1, reduced_g=moments[0], **hyper),
+                 lambda: zs.zero_moments8_pack(**state, exp_avg=moments[0], exp_avg_sq=moments[1]),
+                 lambda: zs.zero_moments8_unpack(**state, exp_avg=moments[0], exp_avg_sq=moments[1])):
+        with pytest.raises(ValueError):
+            call()

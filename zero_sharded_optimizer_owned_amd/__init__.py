@@ -655,6 +655,8 @@ def zero_stream_probe(srcs, dsts, order: int = 0, src_widths=None, dst_widths=No
 def _pieces8(dev, pieces_dev, n_pieces, masks_dev, begin, end):
     """Checks a piece table; (pieces, n_pieces, masks, n_masks, begin, end) as the calls take them."""
     torch = _torch()
+    if n_pieces < 0 or begin < 0 or end < 0:  # as unsigned they would pass the checks of sizes
+        raise ValueError(f"negative n_pieces, begin or end: {n_pieces}, {begin}, {end}")
     pieces = masks = None
     n_masks = 0
     if pieces_dev is not None:
