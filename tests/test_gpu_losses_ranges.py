@@ -274,3 +274,94 @@ def test_more_rows_need_no_count():
     zs.zero_policy_loss(x, t, old_logp=old, advantage=adv, divisor=1.0, stats=stats, logp=lp,
                         workspace=zs.policy_workspace(129, DEV).fill_(0xFF))
     assert torch.equal(stats, want)
+
+
+def past_cache_rows(name, v):
+    """Rows that are a little more than the 256 MB from which gradients are stored past the cache, and a slice of
+    them that is less."""
+    n = (1 << 28) // (v * torch.tensor([], dtype=DT[name]).element_size()) + 8
+    g = torch.Generator(DEV).manual_seed(7)
+    x = torch.empty(n, v, dtype=DT[name], device=DEV).normal_(0.0, 2.0, generator=g)
+    t = torch.randint(0, v, (n,), generator=g, device=DEV)
+    t[torch.rand(n, generator=g, device=DEV) < 0.1] = -100
+    x[:, v - 3] = -math.inf
+    t[t == v - 3] = 0
+    return x, t
+
+
+@pytest.mark.parametrize("name, v", [("f16", 50_001), ("bf16", 32_000), ("bf16", 131_080), ("f32", 8_000),
+                                     ("f32", 131_079)])
+def test_policy_gradient_past_the_cache(name, v):
+    """A row's results do not depend on the others: the same bits as a call on the slice alone."""
+    x, t = past_cache_rows(name, v)
+    n, k = len(t), len(t) // 3
+    g = torch.Generator(DEV).manual_seed(8)
+    adv = torch.randn(n, generator=g, device=DEV)
+    old = logprobs(x, t) + 0.2 * torch.randn(n, generator=g, device=DEV)
+    _, logp, dx = policy(x, t, old, adv, ref=old, kl=0.1)
+    for rows in (slice(0, k), slice(n - k, n)):
+        _, lp, d = policy(x[rows], t[rows], old[rows], adv[rows], ref=old[rows], kl=0.1)
+        assert torch.equal(lp, logp[rows]) and torch.equal(bits(d), bits(dx[rows]))
+    assert int(dx[t < 0].count_nonzero()) == 0
+    _, alone, _ = policy(x, t, old, adv, ref=old, kl=0.1, gradient=False)
+    assert torch.equal(alone, logp)
+    stats = policy(x, t, old, adv, ref=old, kl=0.1)[0], policy(x, t, old, adv, ref=old, kl=0.1, gradient=False)[0]
+    assert torch.equal(*stats)
+
+
+@pytest.mark.parametrize("name, v", [("f16", 50_001), ("bf16", 32_000), ("f32", 8_000), ("f32", 131_079)])
+def test_preference_gradient_past_the_cache(name, v):
+    """16 times the pairs of a slice at 16 times its gradient scale: the slice's rows have the same coefficients and
+    with them the same bits."""
+    x, t = past_cache_rows(name, v)
+    n = len(t)
+    few = 4
+    pairs = 16 * few
+    cuts = torch.linspace(0, n - 3, 2 * pairs + 1).long()
+    cuts[2 * few] = max(2 * few, n // 3)  # the first pairs' rows are a third of all
+    cuts[:2 * few] = torch.linspace(0, int(cuts[2 * few]) - 1, 2 * few + 1).long()[:2 * few]
+    cuts = cuts.cummax(0).values.to(DEV)
+    k = int(cuts[2 * few])
+    ref = torch.linspace(-3000.0, -2990.0, 2 * pairs, device=DEV)
+    every = preference(x, t, cuts, ref, grad_scale=16.0, beta=0.01)
+    part = preference(x[:k], t[:k], cuts[:2 * few + 1], ref[:2 * few], grad_scale=1.0, beta=0.01)
+    for i in (1, 2, 3):
+        m = len(part[i])
+        assert torch.equal(every[i][:m], part[i])
+    assert torch.equal(bits(every[4][:k]), bits(part[4]))
+    assert int(part[4].count_nonzero()) > 0 and bool(torch.isfinite(every[4]).all())
+    assert int(every[4][n - 3:].count_nonzero()) == 0 and int(every[4][t < 0].count_nonzero()) == 0
+    # the slice itself, by the definition
+    lp, tol = exact_logp(x[:k], t[:k].clamp(min=0))
+    counts = t[:k] >= 0
+    assert bool(((part[1].double() - lp).abs() <= tol)[counts].all())
+    sign = torch.zeros(k, dtype=torch.float64, device=DEV)
+    h = (part[3][0::2] - part[3][1::2]).double()
+    slope = 0.01 / few * (torch.sigmoid(h) - 1)
+    for q in range(2 * few):
+        sign[int(cuts[q]):int(cuts[q + 1])] = slope[q // 2] * (1 - 2 * (q % 2))
+    coef = torch.where(counts, sign, 0.0)
+    # h from rewards stored in fp32: u |reward| each, a quarter of it in sigmoid's slope
+    e_h = U * part[3].double().abs().max() * 2
+    for row in (0, 1, k // 2, k - 1):
+        p = (x[row].double()).softmax(0)
+        want = -coef[row] * p
+        want[t[row].clamp(min=0)] += coef[row]
+        spread = (x[row].double() - x[row, t[row].clamp(min=0)].double()).abs()
+        e_p = U * (2 * torch.where(torch.isfinite(spread), spread, 0.0) + 6) + tol[row]
+        err = coef[row].abs() * p * e_p + 0.01 / few * e_h + 4 * U * want.abs()
+        err = err + (want.abs() + err) * torch.finfo(DT[name]).eps / 2 + (2.0 ** -25 if name == "f16" else 2.0 ** -126)
+        assert bool(((part[4][row].double() - want).abs() <= err).all())
+
+
+def test_many_pairs_without_a_gradient():
+    """The launch for the pairs, only their statistics wanted."""
+    x, t = grid_rows(100, 257, 0.5, seed=9)
+    bounds = torch.arange(0, 101, 2, device=DEV)
+    ref = torch.linspace(-30.0, -5.0, 50, device=DEV)
+    a, b = preference(x, t, bounds, ref), preference(x, t, bounds, ref, gradient=False)
+    for p, q in zip(a[:4], b[:4]):
+        assert torch.equal(p, q)
+    h = (a[3][0::2] - a[3][1::2]).double()
+    assert abs(float(a[0][0]) + float(torch.nn.functional.logsigmoid(h).mean())) <= 1e-6
+    assert float(a[0][1]) == float((h > 0).float().mean())

@@ -3,8 +3,8 @@ import numpy as np
 import pytest
 
 import synth
-from helpers import F32, gen, to_dev
-from test_gpu_step8 import HP, Q, make_shard
+from helpers import F16, F32, gen, to_dev
+from test_gpu_step8 import HP, LAYOUTS, Q, make_shard, rank_buffers, real_mask
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -111,3 +111,50 @@ def test_the_first_export_can_be_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(dense, want_dense) and torch.equal(back, want_back)
+
+
+@pytest.mark.parametrize("layout", range(len(LAYOUTS)))
+def test_codes_and_scales_beside_the_real_elements(layout):
+    """A vector with a real element has code 0 at its padding; vectors and blocks without one are not written."""
+    numels, ranks, owner, align = LAYOUTS[layout]
+    sh = make_shard(numels, ranks, owner, align, moments=False)
+    left = 0x39  # 1.125
+    for k in ("exp_avg8", "exp_rms8"):
+        getattr(sh, k).view(torch.uint8).fill_(left)
+    for k in ("exp_avg_scale", "exp_rms_scale"):
+        getattr(sh, k).fill_(1e-6)
+    real = real_mask(sh)
+    sh.adam_step(step=3, hyper=HP, rank_grads=rank_buffers(sh, 3, F16, sh.local_base), grad_base=sh.local_base,
+                 divisor=3.0)
+    written = np.repeat(real.reshape(-1, 8).any(1), 8)
+    for k in ("exp_avg8", "exp_rms8"):
+        codes = getattr(sh, k).view(torch.uint8).cpu().numpy()
+        assert np.all((codes & 0x7F)[written & ~real] == 0) and np.all(codes[~written] == left), k
+    touched = real.reshape(-1, Q).any(1)
+    for k in ("exp_avg_scale", "exp_rms_scale"):
+        scale = getattr(sh, k).cpu().numpy()
+        assert np.all(scale[~touched] == np.float32(1e-6)) and np.all(scale[touched] != np.float32(1e-6)), k
+
+
+@pytest.mark.parametrize("noise", [0.0, 0.3])
+def test_a_fit_ends_as_with_32_bit_moments(noise):
+    """The 8-bit fit's loss against the 32-bit one's, step for step the same problem.  Without noise both go
+    towards 0 and the 8-bit one ends within a factor of two; with noise both end at its floor, to a thousandth."""
+    torch.manual_seed(0)
+    n, k = 512, 64
+    x = torch.randn(n, k, device=DEV)
+    y = x @ torch.randn(k, 32, device=DEV)
+    y = y + noise * torch.randn(n, 32, device=DEV)
+    end = {}
+    for cls in (zs.OwnerShard, zs.OwnerShard8):
+        sh = cls([k * 32], 1, 0, align=64, device=DEV)
+        sh.alloc_state()
+        for step in range(1, 301):
+            e = x @ sh.master[:k * 32].view(k, 32) - y
+            g = (x.t() @ e / n).reshape(-1).contiguous()
+            hp = dict(HP, lr=0.05 * (1 - step / 320), beta1=0.9, beta2=0.99, weight_decay=0.0)
+            sh.adam_step(step=step, hyper=hp, rank_grads=[g])
+        end[cls] = float((x @ sh.master[:k * 32].view(k, 32) - y).square().mean())
+    wide, narrow = end[zs.OwnerShard], end[zs.OwnerShard8]
+    assert wide < 2e-3 * float(y.square().mean())
+    assert narrow <= (2 * wide if noise == 0.0 else 1.001 * wide)
