@@ -64,10 +64,9 @@ struct Logits {
 // One row of `vocab` elements: n_vec 16-byte vectors from the first 128-byte
 // boundary on, and up to 70 elements before and after them, one to a thread.
 // Rows of most vocabularies start anywhere.  Vectors from the row's own start
-// ran 30% slower between two 4-byte words (4096 rows of 50,001 bf16: policy
-// loss 210 us, now 168), and 9-15% slower at other odd places once the
-// gradients go past the caches (2048 rows of 128,001: 218 us and, preference
-// loss, 310; now 199 and 270, as for 128,000).
+// run 25-30% slower there (4096 rows of 50,001 bf16: policy loss 210 us, so 168;
+// 2048 rows of 128,001: 246 us and, preference loss, 362; so 198 and 276, as for
+// 128,000).
 constexpr uint32_t kRowAlign = 128;
 
 template <int DT>
@@ -321,7 +320,7 @@ __device__ __forceinline__ void row_gradient(const Row<DT>& r, void* out, int64_
 // waited for, without branches; steps of the upper half that no thread of the
 // block needs are left out.
 // NT: loaded with the nontemporal hint, where no later pass reads them again
-// (log-probabilities of 4096 x 128,000: 157 us without it, 150 with it).
+// (log-probabilities of 4096 x 128,000: 162 us without it, 155 with it).
 template <int DT, int W, int K, bool NT>
 struct Spread {
   static constexpr uint32_t kStep = 64 * W;
@@ -378,7 +377,7 @@ struct Spread {
 // Calls fn with the block (wavefronts, vectors per thread) whose threads hold a
 // row in registers: 64 elements each, 128 of 16-bit rows past 65,536 elements,
 // 16 up to 2048 elements, where twice as many blocks to a CU hide the rows'
-// fp64 arithmetic (8192 rows of 1000 bf16: policy loss 27.6 us, so 21.4).
+// fp64 arithmetic (8192 rows of 1000 bf16: policy loss 25.3 us, so 17.8).
 // False if the row is so short that no vector is sure to be left.
 template <int DT, typename F>
 bool with_spread(uint32_t vocab, F fn) {
@@ -396,8 +395,8 @@ bool with_spread(uint32_t vocab, F fn) {
 
 // One block per row, as many rows to a launch as its threads may number; each
 // XCD takes one contiguous run of them (against rows dealt in turn: policy
-// loss of 8192 x 128,000 694 to 684 us, preference loss of 8192 x 32,000 234
-// to 228; its second pass is 1% slower so, and deals).
+// loss of 8192 x 128,000 715 to 708 us, preference loss of 8067 x 32,000 234
+// to 226; its second pass is 1% slower so, and deals).
 constexpr uint64_t kMostRows = 1u << 21;
 
 __device__ __forceinline__ bool in_vocab(int64_t target, uint32_t vocab) { return target >= 0 && target < (int64_t)vocab; }
@@ -949,10 +948,10 @@ uint32_t elem_bytes(int dtype) { return dtype == ZERO_F32 ? 4 : 2; }
 // Whether rows of logits are more than the 256 MB memory-side cache holds.
 // dlogits are then stored (and, in the preference loss, the logits read the
 // last time) with the nontemporal hint.  Measured on bf16 rows of 32,000, with
-// a pass over dlogits after the call: 4096 rows (250 MB) 152 us, 163 with the
-// hint; 8192 rows 327 us, 305 with it.  Calls alone, without and with it:
-// policy loss of 8192 x 128,000 762 and 704 us, preference loss of 8192 x
-// 32,000 282 and 235 us (its first pass no longer waits for the dirty lines
+// a pass over dlogits after the call: 4096 rows (250 MB) 164 us, 188 with the
+// hint; 8192 rows 363 us, 360 with it.  Calls alone, without and with it:
+// policy loss of 8192 x 128,000 738 and 708 us, preference loss of 8067 x
+// 32,000 282 and 226 us (its first pass no longer waits for the dirty lines
 // of the call before).
 bool past_cache(uint64_t n_rows, uint32_t vocab, int dtype) {
   return n_rows * vocab * elem_bytes(dtype) > (uint64_t(256) << 20);
@@ -1004,9 +1003,9 @@ int check_space(const void* ws, size_t have, uint64_t need, const char* who) {
 uint64_t policy_space(uint64_t n_rows) { return 256 + n_rows * sizeof(PolicyTerms); }
 
 // Up to this many rows the last block to finish adds up the terms, instead of
-// a launch of its own.  Counting at one address costs some 30 ns a row
-// (measured, 4096 logits a row: 16 rows 7.9 against 10.4 us, 128 rows 8.3
-// against 10.7, 512 rows 16.8 against 10.9).
+// a launch of its own.  Counting at one address costs some 20 ns a row
+// (measured, 4096 logits a row: 16 rows 8.3 against 11.6 us, 128 rows 8.6
+// against 11.7, 512 rows 15.5 against 10.9).
 constexpr uint64_t kTicketRows = 128;
 
 // Row statistics, then the pairs' losses.

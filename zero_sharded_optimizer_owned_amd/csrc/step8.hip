@@ -334,7 +334,7 @@ __device__ __forceinline__ void load_elements(const Step8Args& a, uint64_t f, ui
 // in a WHOLE piece).  Padding beside real elements is loaded with them and
 // then left out: it lies inside the buffers, and a vector at a time keeps
 // every load of the wavefront in flight together (200,000 tensors of 100
-// elements: 45 us element by element, 29 so).
+// elements: 45 us element by element, 27 so).
 template <int GDT, int PDT, int RC, bool WHOLE>
 __device__ __forceinline__ void step_vector(const Step8Args& a, uint64_t f, uint32_t bits) {
   const uint64_t l = f - a.local_base;
@@ -472,17 +472,17 @@ void launch_step8_p(Step8Args& a, int pdt, hipStream_t s) {
   const uint32_t grid = chunk_grid(a.n_pieces, 0);
   // Whole pieces: at most three blocks to a CU, four with up to five 16-bit
   // rank buffers, whose loads are fewer, and runs of two pieces to an XCD.
-  // 8 bf16 ranks into 1.0e8 elements: 520 us; two blocks 523, four 531,
-  // uncapped 537, single pieces 527.  Stored gradient, 3.75e8 elements: 1177
-  // us; two 1326, four 1240, uncapped 1258, single pieces 1185.  4 bf16 ranks
-  // into 6e7 elements: 227 us; three blocks 232, uncapped 229; 1 rank 193;
-  // three 202, uncapped 187.  Pieces with padding wait for more round trips
-  // and want every block that fits: 200,000 tensors of 100 elements 27.1 us,
-  // 28.8 with four blocks.
+  // 8 bf16 ranks into 1.0e8 elements: 512 us; two blocks 562, four 533,
+  // uncapped 538, single pieces 516.  4 bf16 ranks into 6e7 elements: 226 us;
+  // three blocks 229, uncapped 230; 1 rank 184; three 194, uncapped 178.  The
+  // stored gradient goes by single pieces: 3.75e8 elements 1118 us, in runs
+  // 1147 (and so 1479 with two blocks, 1221 with four, 1259 uncapped).  Pieces
+  // with padding wait for more round trips and want every block that fits:
+  // 200,000 tensors of 100 elements 27.4 us, 29.0 with four blocks.
   const bool whole = 2 * a.n_masks <= a.n_pieces;
   const bool light = GDT != ZERO_F32 && a.rs.R <= 5;
   const uint32_t lds = whole ? lds_for_blocks_per_cu(light ? 4 : 3, 0) : 0;
-  a.run = whole ? 2 : 1;
+  a.run = whole && RC != kStored ? 2 : 1;
   if (pdt == ZERO_F16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_F16, RC>), grid, kBlock, lds, s, a);
   else if (pdt == ZERO_BF16) hipLaunchKernelGGL((step8_kernel<GDT, ZERO_BF16, RC>), grid, kBlock, lds, s, a);
   else hipLaunchKernelGGL((step8_kernel<GDT, ZERO_NONE, RC>), grid, kBlock, lds, s, a);
