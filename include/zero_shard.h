@@ -735,6 +735,151 @@ int zero_preference_loss(const zero_preference_args *args, hipStream_t stream);
 int zero_preference_workspace_bytes(uint64_t n_rows, uint32_t n_pairs, uint64_t *bytes);
 
 /* ----------------------------------------------------------------------------
+ * The model's two ends, and what its backward pass keeps.
+ *
+ * Tables and rows are F16, BF16 or F32.  Sums are fp32 or wider, in an order that
+ * depends on the sizes alone, so results are identical run to run.
+ * -------------------------------------------------------------------------- */
+
+/* ----------------------------------------------------------------------------
+ * zero_embedding -- out[n] = scale * table[tokens[n]]; a token outside
+ * [0, vocab) (say -1, padding) gives zeros.
+ * table[vocab] of `dim` elements each, row v from element v * stride; out dense.
+ * Neither needs alignment beyond its elements'.  vocab < 2^31, dim <= 2^20.
+ * n_tokens == 0 is a no-op.
+ * Errors: EINVAL (bad dtype, vocab or dim, stride < dim, scale not finite, NULL
+ * or misaligned arrays); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_embedding(const void *table, int dtype, uint32_t vocab, uint32_t dim, uint64_t stride,
+                   const int64_t *tokens, uint64_t n_tokens, double scale, void *out, hipStream_t stream);
+
+/* Arguments of zero_embedding_grad. */
+typedef struct {
+  const void *dout; /* [n_tokens][dim], dense */
+  int32_t dtype;
+  const int64_t *tokens;
+  uint64_t n_tokens; /* below 2^31 */
+  uint32_t vocab, dim;
+  double scale;
+  void *dtable;     /* row v from element v * stride */
+  int32_t table_dtype; /* dtype, or F32 */
+  uint64_t stride;
+  int32_t accumulate;
+  void *workspace;  /* zero_embedding_workspace_bytes(n_tokens, dim), 256-byte aligned */
+  size_t workspace_bytes;
+} zero_embedding_grad_args;
+
+/* ----------------------------------------------------------------------------
+ * zero_embedding_grad -- the lookup's gradient of the table:
+ *   dtable[v] = scale * sum of dout[n] over the n with tokens[n] == v
+ * accumulate != 0: that is added to dtable[v], rounded once, and rows that no
+ * token names are left as they are (a tied table takes its output head's gradient
+ * first); else those rows are zero.  Tokens outside [0, vocab) count for nothing.
+ * Errors: EINVAL (as zero_embedding; table_dtype neither dtype nor F32, workspace
+ * missing, small or misaligned); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_embedding_grad(const zero_embedding_grad_args *args, hipStream_t stream);
+int zero_embedding_workspace_bytes(uint64_t n_tokens, uint32_t dim, uint64_t *bytes);
+
+/* ----------------------------------------------------------------------------
+ * zero_rms_norm -- root-mean-square norm with the residual's addition:
+ *   h = x + residual, rounded to dtype (without residual: x)
+ *   rstd = 1 / sqrt(mean of h^2 + eps),  out = h * rstd * gain
+ * All arrays are dense [n_rows][dim], gain [dim], rstd [n_rows] fp32 (may be NULL);
+ * they need no alignment beyond their elements'.  h may be residual or x itself.
+ * With codes and scales (both or neither) h is also kept in 8 bits: of each 128
+ * consecutive elements of a row (the last run of a row may be shorter) scales
+ * holds max|h| / 448 (fp32, [n_rows][ceil(dim / 128)]) and codes
+ * e4m3(h * (448 / max|h|)).  Runs whose maximum is below 2^-100 are zeros; a value
+ * that is not finite makes its run NaN.
+ * dim <= 2^14.  n_rows == 0 is a no-op.
+ * Errors: EINVAL (bad dtype or dim, eps not finite or negative, NULL or misaligned
+ * arrays, residual without h or codes without scales); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_rms_norm(const void *x, const void *residual, const void *gain, int dtype, uint64_t n_rows, uint32_t dim,
+                  double eps, void *h, void *out, float *rstd, uint8_t *codes, float *scales, hipStream_t stream);
+
+/* zero_rms_norm_restore -- out = code * scale * rstd * gain: the norm's output again, from
+ * what was kept (the next product's input, for its weights' gradient). */
+int zero_rms_norm_restore(const uint8_t *codes, const float *scales, const float *rstd, const void *gain, int dtype,
+                          uint64_t n_rows, uint32_t dim, void *out, hipStream_t stream);
+
+/* Arguments of zero_rms_norm_backward. */
+typedef struct {
+  const void *dy, *gain;
+  const void *h;            /* the residual stream, or ... */
+  const uint8_t *codes;     /* ... its kept form */
+  const float *scales;
+  const float *rstd;
+  const void *upstream;     /* gradient that reaches h past the norm, or NULL */
+  int32_t dtype;
+  uint64_t n_rows;
+  uint32_t dim;
+  void *dx;                 /* may be dy or upstream itself */
+  void *dgain;              /* [dim], dtype */
+  void *workspace;          /* zero_rms_norm_workspace_bytes(n_rows, dim), 256-byte aligned */
+  size_t workspace_bytes;
+} zero_rms_norm_backward_args;
+
+/* ----------------------------------------------------------------------------
+ * zero_rms_norm_backward -- with n = h * rstd and d = dy * gain:
+ *   dx = rstd * (d - n * mean of d n) + upstream   (the gradient of x and of residual)
+ *   dgain = sum over rows of dy * n
+ * n_rows == 0 writes dgain 0.
+ * Errors: EINVAL (as zero_rms_norm; neither or both of h and codes, workspace
+ * missing, small or misaligned); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_rms_norm_backward(const zero_rms_norm_backward_args *args, hipStream_t stream);
+int zero_rms_norm_workspace_bytes(uint64_t n_rows, uint32_t dim, uint64_t *bytes);
+
+/* Arguments of zero_linear_cross_entropy. */
+typedef struct {
+  const void *hidden; /* [n_rows], row r from element r * hidden_stride */
+  const void *weight; /* [vocab], row v from element v * weight_stride */
+  int32_t dtype;      /* F16 or BF16 */
+  uint64_t n_rows;    /* below 2^31 */
+  uint32_t vocab;     /* at most 2^20 */
+  uint32_t dim;       /* a multiple of 8, at most 2^15 */
+  uint64_t hidden_stride, weight_stride; /* multiples of 8, at most 2^22; rows 16-byte aligned */
+  const int64_t *targets;
+  const float *row_weight; /* [n_rows]; NULL: 1 for every row */
+  double divisor;     /* > 0 */
+  double temperature;
+  double grad_scale;  /* multiplies the gradients only (a loss scale) */
+  float *stats;       /* [2]: loss, number of rows that count */
+  float *logp;        /* [n_rows] */
+  void *dhidden, *dweight; /* dtype and shape of hidden and weight; NULL: not wanted */
+  uint64_t dhidden_stride, dweight_stride;
+  uint32_t piece_rows; /* rows whose logits exist at a time, in [1, 16384] */
+  void *workspace;    /* zero_linear_cross_entropy_workspace_bytes(...), 256-byte aligned */
+  size_t workspace_bytes;
+} zero_linear_cross_entropy_args;
+
+/* ----------------------------------------------------------------------------
+ * zero_linear_cross_entropy -- softmax cross entropy from hidden states and output
+ * weights, and the gradients of both:
+ *   x = hidden weight^T / temperature
+ *   lp_r = x[r][targets[r]] - ln sum_j exp(x[r][j])
+ *   loss = -sum_r row_weight_r lp_r / divisor
+ *   dhidden, dweight = grad_scale * d loss / d hidden, d weight
+ * A target outside [0, vocab) (say -100) marks a row that counts for nothing: logp
+ * 0, no loss, zero dhidden, its hidden state unread.  Products add in fp32.  The
+ * gradients' second factor, softmax - onehot, is rounded to dtype once more on the
+ * way (from 11 significant bits), relative to the largest |row_weight|.  Logits
+ * that are NaN or +inf give NaN; -inf has probability 0.
+ * Rows go in pieces of piece_rows; per row of a piece the workspace holds vocab 16-bit
+ * values (without gradients: vocab / 32 bytes) and the hidden state, and with more than
+ * one piece fp32 sums of dweight.
+ * n_rows == 0 writes stats 0 and a zero dweight.
+ * Errors: EINVAL (sizes, strides and alignment as above, divisor or temperature
+ * not finite and > 0, grad_scale not finite, NULL arrays, workspace missing, small
+ * or misaligned); EHIP.
+ * -------------------------------------------------------------------------- */
+int zero_linear_cross_entropy(const zero_linear_cross_entropy_args *args, hipStream_t stream);
+int zero_linear_cross_entropy_workspace_bytes(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows,
+                                              int grad, uint64_t *bytes);
+
+/* ----------------------------------------------------------------------------
  * Measurement.
  * -------------------------------------------------------------------------- */
 

@@ -1,8 +1,8 @@
 """ZeRO owner-shard optimizer step on one MI355X: Python binding of libzero_shard.so.
 
 Argument marshalling only.  Every step of the path runs in the HIP library
-(``csrc/step.hip``, ``csrc/step8.hip``, ``csrc/loss.hip``, ``csrc/copy.hip``, ``csrc/launch.hip``,
-``csrc/host.cpp``; C ABI in ``include/zero_shard.h``);
+(``csrc/step.hip``, ``csrc/step8.hip``, ``csrc/loss.hip``, ``csrc/embed.hip``, ``csrc/norm.hip``,
+``csrc/head.hip``, ``csrc/copy.hip``, ``csrc/launch.hip``, ``csrc/host.cpp``; C ABI in ``include/zero_shard.h``);
 this module turns torch tensors into pointers, checks devices, dtypes,
 contiguity and extents against what the kernels will touch, passes torch's
 current stream, and raises on error codes.  There is no fallback: if the
@@ -35,7 +35,10 @@ EXPORTED = ("zero_last_error", "zero_shard_layout", "zero_chunk_table", "zero_de
             "zero_check_workspace_bytes", "zero_chunk_groups", "zero_span_groups", "zero_reduce_owned_noalloc",
             "zero_piece_table", "zero_adam8_step", "zero_moments8_pack", "zero_moments8_unpack",
             "zero_token_logprobs", "zero_policy_loss", "zero_policy_workspace_bytes",
-            "zero_preference_loss", "zero_preference_workspace_bytes")
+            "zero_preference_loss", "zero_preference_workspace_bytes",
+            "zero_embedding", "zero_embedding_grad", "zero_embedding_workspace_bytes", "zero_rms_norm",
+            "zero_rms_norm_restore", "zero_rms_norm_backward", "zero_rms_norm_workspace_bytes",
+            "zero_linear_cross_entropy", "zero_linear_cross_entropy_workspace_bytes")
 
 CHUNK_DTYPE = np.dtype([("flat", "<u8"), ("len", "<u4"), ("tensor", "<u4")])
 SPAN_DTYPE = np.dtype([("src", "<u8"), ("dst", "<u8"), ("len", "<u4"), ("buf", "<u4")])
@@ -106,6 +109,35 @@ class PreferenceArgs(ct.Structure):
     ]
 
 
+class EmbeddingGradArgs(ct.Structure):
+    _fields_ = [
+        ("dout", ct.c_void_p), ("dtype", ct.c_int32), ("tokens", ct.c_void_p), ("n_tokens", ct.c_uint64),
+        ("vocab", ct.c_uint32), ("dim", ct.c_uint32), ("scale", ct.c_double), ("dtable", ct.c_void_p),
+        ("table_dtype", ct.c_int32), ("stride", ct.c_uint64), ("accumulate", ct.c_int32), ("workspace", ct.c_void_p),
+        ("workspace_bytes", ct.c_size_t),
+    ]
+
+
+class RmsNormBackwardArgs(ct.Structure):
+    _fields_ = [
+        ("dy", ct.c_void_p), ("gain", ct.c_void_p), ("h", ct.c_void_p), ("codes", ct.c_void_p),
+        ("scales", ct.c_void_p), ("rstd", ct.c_void_p), ("upstream", ct.c_void_p), ("dtype", ct.c_int32),
+        ("n_rows", ct.c_uint64), ("dim", ct.c_uint32), ("dx", ct.c_void_p), ("dgain", ct.c_void_p),
+        ("workspace", ct.c_void_p), ("workspace_bytes", ct.c_size_t),
+    ]
+
+
+class LinearCrossEntropyArgs(ct.Structure):
+    _fields_ = [
+        ("hidden", ct.c_void_p), ("weight", ct.c_void_p), ("dtype", ct.c_int32), ("n_rows", ct.c_uint64),
+        ("vocab", ct.c_uint32), ("dim", ct.c_uint32), ("hidden_stride", ct.c_uint64), ("weight_stride", ct.c_uint64),
+        ("targets", ct.c_void_p), ("row_weight", ct.c_void_p), ("divisor", ct.c_double), ("temperature", ct.c_double),
+        ("grad_scale", ct.c_double), ("stats", ct.c_void_p), ("logp", ct.c_void_p), ("dhidden", ct.c_void_p),
+        ("dweight", ct.c_void_p), ("dhidden_stride", ct.c_uint64), ("dweight_stride", ct.c_uint64),
+        ("piece_rows", ct.c_uint32), ("workspace", ct.c_void_p), ("workspace_bytes", ct.c_size_t),
+    ]
+
+
 class Ratio(ct.Structure):
     _fields_ = [("num", ct.c_uint64), ("den", ct.c_uint64)]
 
@@ -150,6 +182,15 @@ def load(path: str):
     L.zero_policy_workspace_bytes.argtypes = [U64, P]
     L.zero_preference_loss.argtypes = [ct.POINTER(PreferenceArgs), P]
     L.zero_preference_workspace_bytes.argtypes = [U64, U32, P]
+    L.zero_embedding.argtypes = [P, I, U32, U32, U64, P, U64, D, P, P]
+    L.zero_embedding_grad.argtypes = [ct.POINTER(EmbeddingGradArgs), P]
+    L.zero_embedding_workspace_bytes.argtypes = [U64, U32, P]
+    L.zero_rms_norm.argtypes = [P, P, P, I, U64, U32, D, P, P, P, P, P, P]
+    L.zero_rms_norm_restore.argtypes = [P, P, P, P, I, U64, U32, P, P]
+    L.zero_rms_norm_backward.argtypes = [ct.POINTER(RmsNormBackwardArgs), P]
+    L.zero_rms_norm_workspace_bytes.argtypes = [U64, U32, P]
+    L.zero_linear_cross_entropy.argtypes = [ct.POINTER(LinearCrossEntropyArgs), P]
+    L.zero_linear_cross_entropy_workspace_bytes.argtypes = [U64, U32, U32, U32, I, P]
     return L
 
 
@@ -880,6 +921,214 @@ def zero_preference_loss(logits, targets, seq_begin, *, ref_logp, stats, logp, s
                        _addr(logp, "logp", f32, rows[2], dev), _addr(seq_logp, "seq_logp", f32, 2 * pairs, dev),
                        _addr(reward, "reward", f32, 2 * pairs, dev), *grad, *_space(workspace, dev))
     _check(lib().zero_preference_loss(ct.byref(a), stream))
+
+
+# ---------------------------------------------------------------- the model's two ends
+def _matrix(t, name: str, dev: int, dtype=None, shape=None):
+    """(address, rows, width, row stride) of a [rows, width] device tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if t.get_device() != dev:
+        _dev(t, name)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    (n, d), (stride, inner) = t.shape, t.stride()
+    if shape is not None and (n, d) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {[n, d]}")
+    if d > 1 and inner != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if n <= 1:
+        stride = d
+    elif stride < d:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), n, d, stride
+
+
+def _kind(t, name: str) -> int:
+    """The dtype code of a float16, bfloat16 or float32 tensor."""
+    torch = _torch()
+    if t.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+    return _dtype_code(t)
+
+
+def _dense(t, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of one dtype and shape."""
+    p = _addr(t, name, dtype, 0, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+def zero_embedding(table, tokens, out, *, scale: float = 1.0) -> None:
+    """``out[n] = scale * table[tokens[n]]``, zeros for a token outside the table (-1).
+
+    ``table`` [vocabulary, dim] float16, bfloat16 or float32 with contiguous rows at any
+    row stride (a view of the flat 16-bit parameters); ``tokens`` int64 [n]; ``out``
+    [n, dim] of the table's dtype.
+    """
+    dt = _kind(table, "table")
+    dev, stream = _device_stream()
+    ptr, v, d, stride = _matrix(table, "table", dev)
+    n = tokens.numel()
+    _check(lib().zero_embedding(ptr, dt, v, d, stride, _addr(tokens, "tokens", _torch().int64, n, dev), n, scale,
+                                _dense(out, "out", table.dtype, (n, d), dev), stream))
+
+
+def embedding_workspace(n_tokens: int, vocab: int, dim: int, device=None):
+    """The device workspace of ``zero_embedding_grad`` for up to n_tokens tokens (its size
+    does not depend on the vocabulary)."""
+    return _workspace(lib().zero_embedding_workspace_bytes, n_tokens, dim, device=device)
+
+
+def zero_embedding_grad(dout, tokens, dtable, *, workspace, scale: float = 1.0, accumulate: bool = False) -> None:
+    """``dtable[v]`` = scale * sum of ``dout[n]`` over the n with ``tokens[n] == v``.
+
+    With ``accumulate`` that is added to ``dtable`` (rows that no token names stay as
+    they are: a tied table takes its output head's gradient first); without it those
+    rows become zero.  ``dout`` [n, dim]; ``dtable`` [vocabulary, dim] of its dtype or
+    float32, rows contiguous at any row stride (a view of a rank's flat gradient).
+    Sums are fp32 in a fixed order.  ``workspace`` from ``embedding_workspace``.
+    """
+    dt, table_dt = _kind(dout, "dout"), _kind(dtable, "dtable")
+    dev, stream = _device_stream()
+    ptr, v, d, stride = _matrix(dtable, "dtable", dev)
+    n = tokens.numel()
+    a = EmbeddingGradArgs(_dense(dout, "dout", dout.dtype, (n, d), dev), dt,
+                          _addr(tokens, "tokens", _torch().int64, n, dev), n, v, d, scale, ptr, table_dt, stride,
+                          int(accumulate), *_space(workspace, dev))
+    _check(lib().zero_embedding_grad(ct.byref(a), stream))
+
+
+def _kept(codes, scales, n: int, d: int, dev: int):
+    """Addresses of the 8-bit form of [n, d] rows, or (None, None)."""
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    if codes is None:
+        return None, None
+    torch = _torch()
+    return (_dense(codes, "codes", torch.float8_e4m3fn, (n, d), dev),
+            _dense(scales, "scales", torch.float32, (n, -(-d // ZERO_QBLOCK)), dev))
+
+
+def zero_rms_norm(x, gain, out, *, residual=None, h=None, eps: float = 1e-6, rstd=None, codes=None,
+                  scales=None) -> None:
+    """Root-mean-square norm with the residual's addition.
+
+    h = x + residual (rounded; ``h`` may be ``residual`` or ``x`` itself; without a
+    residual h is x), rstd = 1 / sqrt(mean of h^2 + eps), ``out`` = h rstd gain.  All
+    [rows, dim] of one dtype, ``gain`` [dim].  ``rstd`` (optional) float32 [rows].
+
+    ``codes`` float8_e4m3fn [rows, dim] and ``scales`` float32 [rows, ceil(dim /
+    ZERO_QBLOCK)] (optional) keep h in 8 bits for ``zero_rms_norm_restore`` and
+    ``zero_rms_norm_backward``: 1.03 bytes an element in place of h's and out's four.
+    """
+    torch = _torch()
+    dt = _kind(x, "x")
+    dev, stream = _device_stream()
+    px, n, d, stride = _matrix(x, "x", dev)
+    _dense(x, "x", x.dtype, (n, d), dev)
+    if (residual is None) != (h is None):
+        raise ValueError("residual and h go together")
+    same = lambda t, name: None if t is None else _dense(t, name, x.dtype, (n, d), dev)  # noqa: E731
+    _check(lib().zero_rms_norm(px, same(residual, "residual"), _dense(gain, "gain", x.dtype, (d,), dev), dt, n, d, eps,
+                               same(h, "h"), same(out, "out"),
+                               None if rstd is None else _dense(rstd, "rstd", torch.float32, (n,), dev),
+                               *_kept(codes, scales, n, d, dev), stream))
+
+
+def zero_rms_norm_restore(codes, scales, rstd, gain, out) -> None:
+    """``out`` = the norm's output again, from the 8-bit form: the next product's input,
+    for the gradient of its weights."""
+    torch = _torch()
+    dt = _kind(out, "out")
+    dev, stream = _device_stream()
+    p, n, d, _ = _matrix(out, "out", dev)
+    _dense(out, "out", out.dtype, (n, d), dev)
+    _check(lib().zero_rms_norm_restore(*_kept(codes, scales, n, d, dev),
+                                       _dense(rstd, "rstd", torch.float32, (n,), dev),
+                                       _dense(gain, "gain", out.dtype, (d,), dev), dt, n, d, p, stream))
+
+
+def rms_norm_workspace(n_rows: int, dim: int, device=None):
+    """The device workspace of ``zero_rms_norm_backward`` over up to n_rows rows."""
+    return _workspace(lib().zero_rms_norm_workspace_bytes, n_rows, dim, device=device)
+
+
+def zero_rms_norm_backward(dy, gain, rstd, dx, dgain, *, workspace, h=None, codes=None, scales=None,
+                           upstream=None) -> None:
+    """The norm's gradients, from ``h`` or from its 8-bit form (``codes``, ``scales``).
+
+    With n = h rstd and d = dy gain: ``dx`` = rstd (d - n mean(d n)) + upstream, the
+    gradient of x and of the residual (``upstream``: the gradient that reaches h past
+    the norm; ``dx`` may be ``dy`` or ``upstream`` itself), and ``dgain`` = sum over rows
+    of dy n.  ``workspace`` from ``rms_norm_workspace``.
+    """
+    torch = _torch()
+    dt = _kind(dy, "dy")
+    dev, stream = _device_stream()
+    p, n, d, _ = _matrix(dy, "dy", dev)
+    _dense(dy, "dy", dy.dtype, (n, d), dev)
+    if (h is None) == (codes is None):
+        raise ValueError("either h or codes and scales")
+    same = lambda t, name: None if t is None else _dense(t, name, dy.dtype, (n, d), dev)  # noqa: E731
+    row = lambda t, name: _dense(t, name, dy.dtype, (d,), dev)  # noqa: E731
+    a = RmsNormBackwardArgs(p, row(gain, "gain"), same(h, "h"), *_kept(codes, scales, n, d, dev),
+                            _dense(rstd, "rstd", torch.float32, (n,), dev), same(upstream, "upstream"), dt, n, d,
+                            same(dx, "dx"), row(dgain, "dgain"), *_space(workspace, dev))
+    _check(lib().zero_rms_norm_backward(ct.byref(a), stream))
+
+
+PIECE_ROWS = 8192
+
+
+def linear_cross_entropy_workspace(n_rows: int, vocab: int, dim: int, *, grad: bool = True,
+                                   piece_rows: int = PIECE_ROWS, device=None):
+    """The device workspace of ``zero_linear_cross_entropy`` over up to n_rows rows.
+
+    With gradients it holds 2 bytes for each logit of ``piece_rows`` rows and, with more
+    rows than that, 4 bytes for each weight; without them vocab / 32 bytes a row."""
+    return _workspace(lib().zero_linear_cross_entropy_workspace_bytes, n_rows, vocab, dim, piece_rows, int(grad),
+                      device=device)
+
+
+def zero_linear_cross_entropy(hidden, weight, targets, *, divisor: float, stats, logp, workspace, row_weight=None,
+                              temperature: float = 1.0, grad_scale: float = 1.0, dhidden=None, dweight=None,
+                              piece_rows: int = PIECE_ROWS) -> None:
+    """Softmax cross entropy of ``hidden @ weight.T / temperature`` and its gradients,
+    without keeping the logits.
+
+    ``hidden`` [rows, dim], ``weight`` [vocabulary, dim], both float16 or bfloat16, rows
+    contiguous and 16-byte aligned, dim a multiple of 8; ``targets`` int64 [rows]; a
+    target outside the vocabulary (-100) marks a row that counts for nothing.  With lp
+    the targets' log-probabilities the loss is -sum of row_weight lp / divisor.
+
+    Written: ``stats`` float32 [2] (loss, number of rows that count), ``logp`` float32
+    [rows], and, each optional, ``dhidden`` and ``dweight`` (shape and dtype of ``hidden``
+    and ``weight``) = grad_scale * gradient.  Rows go in pieces of ``piece_rows``;
+    ``workspace`` from ``linear_cross_entropy_workspace`` with the same ``piece_rows``.
+    """
+    torch = _torch()
+    f32 = torch.float32
+    dt = _kind(hidden, "hidden")
+    dev, stream = _device_stream()
+    ph, n, d, hs = _matrix(hidden, "hidden", dev)
+    pw, v, _, ws = _matrix(weight, "weight", dev, hidden.dtype, (weight.shape[0], d))
+    if targets.numel() != n:
+        raise ValueError(f"{targets.numel()} targets for {n} rows")
+    grads = [(None, 0), (None, 0)]
+    for i, (t, name, shape) in enumerate(((dhidden, "dhidden", (n, d)), (dweight, "dweight", (v, d)))):
+        if t is not None:
+            p, _, _, s = _matrix(t, name, dev, hidden.dtype, shape)
+            grads[i] = (p, s)
+    a = LinearCrossEntropyArgs(ph, pw, dt, n, v, d, hs, ws, _addr(targets, "targets", torch.int64, n, dev),
+                               None if row_weight is None else _addr(row_weight, "row_weight", f32, n, dev), divisor,
+                               temperature, grad_scale, _addr(stats, "stats", f32, 2, dev),
+                               _addr(logp, "logp", f32, n, dev), grads[0][0], grads[1][0], grads[0][1], grads[1][1],
+                               piece_rows, *_space(workspace, dev))
+    _check(lib().zero_linear_cross_entropy(ct.byref(a), stream))
 
 
 # ---------------------------------------------------------------- convenience

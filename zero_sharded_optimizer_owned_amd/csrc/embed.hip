@@ -1,0 +1,540 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   out[n]    = scale table[token[n]]            (0 for a token outside the table)
+//   dtable[v] = scale sum of dout[n] over the n with token[n] = v, n ascending
+//
+// Both are bound by HBM: the lookup reads and writes each row once; the
+// gradient reads dout once and writes the table once (or, added onto another
+// gradient, reads and writes the rows that tokens name).  The sum over equal
+// tokens has a fixed order, so tokens are sorted (a stable radix sort of
+// (token, position), whole numbers only) and no float is added atomically.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "launch.h"
+#include "rows.h"
+
+namespace zs {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Lookup.
+// ---------------------------------------------------------------------------
+struct EmbedArgs {
+  const void* table;
+  const int64_t* tokens;
+  void* out;
+  uint64_t n_tokens, stride;  // stride: of the table's rows
+  uint32_t vocab, dim, vecs;  // vecs: 16-byte vectors of a row
+  float scale;
+};
+
+// 2^SH threads to a row, one vector each at a time.
+template <int DT, bool NT>
+__global__ void __launch_bounds__(kBlock) embed_kernel(const EmbedArgs a, const uint32_t shift) {
+  constexpr int N = Lane<DT>::N;
+  typedef typename Vec<DT>::T T;
+  const uint32_t lanes = 1u << shift, rows = kBlock >> shift;
+  for (uint64_t n = (uint64_t)blockIdx.x * rows + (threadIdx.x >> shift); n < a.n_tokens; n += (uint64_t)gridDim.x * rows) {
+    const int64_t token = a.tokens[n];
+    const bool has = token >= 0 && token < (int64_t)a.vocab;
+    const T* from = static_cast<const T*>(a.table) + (has ? (uint64_t)token * a.stride : 0);
+    T* to = static_cast<T*>(a.out) + n * a.dim;
+    for (uint32_t v = threadIdx.x & (lanes - 1); v < a.vecs; v += lanes) {
+      float x[N] = {};
+      if (has) {
+        const u32x4 r = load_cut<DT>(from, v, a.dim);
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = Lane<DT>::get(r, k) * a.scale;
+      }
+      store_cut<DT, NT>(to, v, a.dim, x);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Stable radix sort of (token, position).
+//
+// A pass takes up to 9 bits.  Blocks of 256 threads take 2048 consecutive
+// keys; a wavefront takes 512 of them in 8 rounds of 64.  In a round a lane
+// finds the lanes with its digit by one ballot per bit, its rank among them by
+// a population count, and the count so far in its wavefront's own counters:
+// the order within a digit is the order of the keys.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kSortKeys = 2048, kRounds = kSortKeys / kBlock, kMaxBits = 9, kDigits = 1u << kMaxBits;
+
+struct SortArgs {
+  const int64_t* tokens;      // the first pass reads these,
+  const uint32_t *keys, *at;  // the others these
+  uint32_t *keys_out, *at_out;
+  uint32_t* hist;  // [1 << bits][blocks]
+  uint32_t n, vocab, blocks, shift, bits;
+};
+
+// A token outside the table sorts behind all others.
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, uint32_t i) {
+  if (a.tokens) {
+    const int64_t t = a.tokens[i];
+    return t >= 0 && t < (int64_t)a.vocab ? (uint32_t)t : a.vocab;
+  }
+  return a.keys[i];
+}
+
+__global__ void __launch_bounds__(kBlock) histogram_kernel(const SortArgs a) {
+  __shared__ uint32_t count[kDigits];
+  const uint32_t digits = 1u << a.bits;
+  for (uint32_t d = threadIdx.x; d < digits; d += kBlock) count[d] = 0;
+  __syncthreads();
+  const uint32_t begin = blockIdx.x * kSortKeys;
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    const uint32_t i = begin + r * kBlock + threadIdx.x;
+    if (i < a.n) atomicAdd(&count[sort_key(a, i) >> a.shift & (digits - 1)], 1u);
+  }
+  __syncthreads();
+  for (uint32_t d = threadIdx.x; d < digits; d += kBlock) a.hist[(uint64_t)d * a.blocks + blockIdx.x] = count[d];
+}
+
+__global__ void __launch_bounds__(kBlock) scatter_kernel(const SortArgs a) {
+  __shared__ uint32_t count[kWavesPerBlock][kDigits];  // of a wavefront, then where its keys of a digit begin
+  __shared__ uint32_t sums[kWavesPerBlock];
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, digits = 1u << a.bits;
+  for (uint32_t d = t; d < kWavesPerBlock * kDigits; d += kBlock) (&count[0][0])[d] = 0;
+  __syncthreads();
+  uint32_t key[kRounds], rank[kRounds];
+  const uint32_t begin = blockIdx.x * kSortKeys + wave * (kSortKeys / kWavesPerBlock) + lane;
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    const uint32_t i = begin + r * 64;
+    key[r] = i < a.n ? sort_key(a, i) : 0;
+  }
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    const bool has = begin + r * 64 < a.n;
+    const uint32_t d = key[r] >> a.shift & (digits - 1);
+    uint64_t same = __ballot(has);
+    for (uint32_t b = 0; b < a.bits; ++b) {
+      const uint64_t one = __ballot(d >> b & 1);
+      same &= (d >> b & 1) ? one : ~one;
+    }
+    const uint32_t before = __popcll(same & ((1ull << lane) - 1));
+    const uint32_t seen = count[wave][d];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (has && before == 0) count[wave][d] = seen + (uint32_t)__popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    rank[r] = seen + before;
+  }
+  __syncthreads();
+  // Where each digit of this block begins: behind all smaller digits, and
+  // behind the earlier blocks' keys of the same one.  A thread takes two
+  // neighbouring digits.
+  uint32_t total[2] = {0, 0}, mine[2] = {0, 0};
+#pragma unroll
+  for (uint32_t j = 0; j < 2; ++j) {
+    const uint32_t d = 2 * t + j;
+    if (d < digits)
+      for (uint32_t b = 0; b < a.blocks; ++b) {
+        const uint32_t c = a.hist[(uint64_t)d * a.blocks + b];
+        mine[j] += b < blockIdx.x ? c : 0;
+        total[j] += c;
+      }
+  }
+  uint32_t sum = total[0] + total[1];
+#pragma unroll
+  for (uint32_t s = 1; s < 64; s <<= 1) {
+    const uint32_t up = __shfl_up(sum, s, 64);
+    if (lane >= s) sum += up;
+  }
+  if (lane == 63) sums[wave] = sum;
+  __syncthreads();
+  for (uint32_t w = 0; w < wave; ++w) sum += sums[w];
+  uint32_t start = sum - total[0] - total[1];
+#pragma unroll
+  for (uint32_t j = 0; j < 2; ++j) {
+    const uint32_t d = 2 * t + j;
+    if (d < digits) {
+      uint32_t at = start + mine[j];
+#pragma unroll
+      for (int w = 0; w < kWavesPerBlock; ++w) {
+        const uint32_t c = count[w][d];
+        count[w][d] = at;
+        at += c;
+      }
+    }
+    start += total[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    const uint32_t i = begin + r * 64;
+    if (i < a.n) {
+      const uint32_t to = count[wave][key[r] >> a.shift & (digits - 1)] + rank[r];
+      a.keys_out[to] = key[r];
+      a.at_out[to] = a.tokens ? i : a.at[i];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over the sorted positions.
+//
+// They are cut into tiles of kTile.  A run of equal tokens that lies within a
+// tile is summed and written there; one that a tile's end cuts leaves partial
+// sums (fp32), the tile's first run in slot 0, its last one in slot 1, which
+// join_kernel adds in the order of the tiles.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kTile = 32;
+
+struct GradArgs {
+  const uint32_t *keys, *at;  // sorted
+  const void* dout;
+  void* dtable;
+  float* partial;  // [tiles][2][vecs * N]
+  uint64_t stride;
+  uint32_t n, vocab, dim, vecs;
+  float scale;
+  bool accumulate;
+};
+
+template <int DT, int OUT>
+__device__ __forceinline__ void write_row(const GradArgs& a, uint32_t key, uint32_t v, const float (&sum)[Lane<DT>::N]) {
+  constexpr int N = Lane<DT>::N;
+  typedef typename Vec<OUT>::T T;
+  T* row = static_cast<T*>(a.dtable) + (uint64_t)key * a.stride;
+  float x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = sum[k] * a.scale;
+  if constexpr (OUT == DT) {
+    if (a.accumulate) {
+      const u32x4 old = load_cut<OUT>(row, v, a.dim);
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] += Lane<OUT>::get(old, k);
+    }
+    store_cut<OUT>(row, v, a.dim, x);
+  } else {  // a 16-bit gradient into an fp32 table
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (v * N + k < a.dim) row[v * N + k] = a.accumulate ? row[v * N + k] + x[k] : x[k];
+  }
+}
+
+template <int DT, int OUT>
+__global__ void __launch_bounds__(kBlock) sum_kernel(const GradArgs a) {
+  constexpr int N = Lane<DT>::N;
+  typedef typename Vec<DT>::T T;
+  __shared__ uint32_t key[kTile + 2], at[kTile];
+  const uint32_t begin = blockIdx.x * kTile, end = min(begin + kTile, a.n), n = end - begin;
+  // key[0] and key[n + 1]: the neighbours' (a number that no key has, at the ends)
+  for (uint32_t i = threadIdx.x; i < n + 2; i += kBlock) {
+    const int64_t p = (int64_t)begin + i - 1;
+    key[i] = p >= 0 && p < (int64_t)a.n ? a.keys[p] : 0xFFFFFFFFu;
+    if (i >= 1 && i <= n) at[i - 1] = a.at[p];
+  }
+  __syncthreads();
+  for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.vecs; v += gridDim.y * kBlock) {
+    float sum[N] = {};
+    bool cut = key[0] == key[1];  // the run at hand began in an earlier tile
+    constexpr uint32_t B = 8;     // rows in flight
+    for (uint32_t i0 = 0; i0 < n; i0 += B) {
+      u32x4 r[B];
+#pragma unroll
+      for (uint32_t j = 0; j < B; ++j) {
+        r[j] = u32x4{0, 0, 0, 0};
+        if (i0 + j < n && key[i0 + j + 1] < a.vocab)
+          r[j] = load_cut<DT>(static_cast<const T*>(a.dout) + (uint64_t)at[i0 + j] * a.dim, v, a.dim);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < B; ++j) {
+        const uint32_t i = i0 + j;
+        if (i >= n) break;
+        const uint32_t k0 = key[i + 1];
+        if (k0 >= a.vocab) break;
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] += Lane<DT>::get(r[j], k);
+        const bool last = key[i + 2] != k0;
+        if (last && !cut) write_row<DT, OUT>(a, k0, v, sum);
+        else if (last || i + 1 == n) {
+          f32x4* to = reinterpret_cast<f32x4*>(a.partial + (((uint64_t)blockIdx.x * 2 + (cut ? 0 : 1)) * a.vecs + v) * N);
+#pragma unroll
+          for (int k = 0; k < N; k += 4) to[k / 4] = f32x4{sum[k], sum[k + 1], sum[k + 2], sum[k + 3]};
+        }
+        if (last) {
+          cut = false;
+#pragma unroll
+          for (int k = 0; k < N; ++k) sum[k] = 0.0f;
+        }
+      }
+    }
+  }
+}
+
+// Tile b's last run, where it began in the tile and goes on behind it.
+template <int DT, int OUT>
+__global__ void __launch_bounds__(kBlock) join_kernel(const GradArgs a) {
+  constexpr int N = Lane<DT>::N;
+  const uint32_t begin = blockIdx.x * kTile, end = begin + kTile;
+  if (end >= a.n) return;
+  const uint32_t key = a.keys[end - 1];
+  if (key >= a.vocab || a.keys[end] != key) return;           // ends here
+  if (begin > 0 && a.keys[begin - 1] == key) return;  // began earlier
+  // the run's last tile: the first whose last key is another one
+  uint32_t last = blockIdx.x + 1;
+  while ((uint64_t)(last + 1) * kTile <= a.n && a.keys[(last + 1) * kTile - 1] == key &&
+         (uint64_t)(last + 1) * kTile < a.n && a.keys[(last + 1) * kTile] == key)
+    ++last;
+  for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.vecs; v += gridDim.y * kBlock) {
+    float sum[N];
+    const auto part = [&](uint32_t tile, uint32_t slot, int k) {
+      return reinterpret_cast<const f32x4*>(a.partial + (((uint64_t)tile * 2 + slot) * a.vecs + v) * N)[k];
+    };
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const f32x4 p = part(blockIdx.x, 1, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[4 * k + j] = p[j];
+    }
+#pragma unroll 8
+    for (uint32_t b = blockIdx.x + 1; b <= last; ++b) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const f32x4 p = part(b, 0, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[4 * k + j] += p[j];
+      }
+    }
+    write_row<DT, OUT>(a, key, v, sum);
+  }
+}
+
+// The rows of the table that no token names are zero.  A block takes kFillRows
+// of them and finds the sorted keys of that range by bisection, 64 probes at a time.
+constexpr uint32_t kFillRows = 16;
+
+// The first position in [lo, hi] whose key is at least x (hi: none), for a whole wavefront.
+__device__ __forceinline__ uint32_t first_at_least(const uint32_t* keys, uint32_t lo, uint32_t hi, uint32_t x) {
+  const uint32_t lane = threadIdx.x & 63;
+  while (hi > lo) {
+    const uint32_t step = (hi - lo + 63) / 64, p = lo + lane * step;
+    const uint32_t c = (uint32_t)__popcll(__ballot(p < hi && keys[p] < x));  // probes 0 .. c - 1 are below x
+    if (c == 0) break;
+    hi = min(hi, lo + c * step);
+    lo += (c - 1) * step + 1;
+  }
+  return lo;
+}
+
+template <int OUT, bool NT>
+__global__ void __launch_bounds__(kBlock) fill_kernel(const GradArgs a, uint32_t vecs) {
+  constexpr int N = Lane<OUT>::N;
+  typedef typename Vec<OUT>::T T;
+  __shared__ uint32_t named;
+  const uint32_t lane = threadIdx.x & 63;
+  for (uint32_t row0 = blockIdx.x * kFillRows; row0 < a.vocab; row0 += gridDim.x * kFillRows) {
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      uint32_t p = first_at_least(a.keys, 0, a.n, row0);
+      uint32_t bits = 0;
+      while (p < a.n) {
+        const uint32_t k = p + lane < a.n ? a.keys[p + lane] : 0xFFFFFFFFu;
+        if (k < row0 + kFillRows) bits |= 1u << (k - row0);
+        if (__ballot(k >= row0 + kFillRows)) break;
+        p += 64;
+        const uint32_t last = (uint32_t)__builtin_amdgcn_readlane((int)k, 63);
+        if ((uint32_t)__builtin_amdgcn_readfirstlane((int)k) == last) p = first_at_least(a.keys, p, a.n, last + 1);
+      }
+#pragma unroll
+      for (uint32_t s = 1; s < 64; s <<= 1) bits |= (uint32_t)__shfl_xor((int)bits, s, 64);
+      if (lane == 0) named = bits;
+    }
+    __syncthreads();
+    const uint32_t skip = named, rows = min(kFillRows, a.vocab - row0);
+    const float zero[N] = {};
+    for (uint32_t r = 0; r < rows; ++r) {
+      if (skip >> r & 1) continue;
+      T* row = static_cast<T*>(a.dtable) + (uint64_t)(row0 + r) * a.stride;
+      for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) store_cut<OUT, NT>(row, v, a.dim, zero);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kMaxDim = 1u << 20;
+
+uint64_t up256(uint64_t n) { return (n + 255) / 256 * 256; }
+
+// Workspace: two copies of (keys, positions), the histogram, the partial sums.
+struct Space {
+  uint64_t keys[2], at[2], hist, partial, bytes;
+  uint32_t blocks, tiles, row;  // row: floats of a partial row
+};
+Space space_of(uint64_t n, uint32_t dim) {
+  Space s;
+  s.blocks = (uint32_t)((n + kSortKeys - 1) / kSortKeys);
+  s.tiles = (uint32_t)((n + kTile - 1) / kTile);
+  s.row = (dim + 7) / 8 * 8;
+  uint64_t at = 0;
+  const auto take = [&](uint64_t bytes) {
+    const uint64_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  for (int i = 0; i < 2; ++i) {
+    s.keys[i] = take(n * 4);
+    s.at[i] = take(n * 4);
+  }
+  s.hist = take((uint64_t)kDigits * s.blocks * 4);
+  s.partial = take((uint64_t)s.tiles * 2 * s.row * 4);
+  s.bytes = std::max<uint64_t>(at, 256);
+  return s;
+}
+
+int check_table(const void* table, int dtype, uint32_t vocab, uint32_t dim, uint64_t stride, const char* who) {
+  if (!known_dtype(dtype)) return fail(ZERO_EINVAL, "%s: unknown dtype %d", who, dtype);
+  if (vocab == 0 || vocab > (uint32_t)INT32_MAX) return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^31)", who, vocab);
+  if (dim == 0 || dim > kMaxDim) return fail(ZERO_EINVAL, "%s: dim %u outside [1, 2^20]", who, dim);
+  if (stride < dim) return fail(ZERO_EINVAL, "%s: rows of %u elements overlap at a stride of %llu", who, dim,
+                                (unsigned long long)stride);
+  if (vocab > UINT64_MAX / 8 / stride) return fail(ZERO_EINVAL, "%s: vocab * stride overflows", who);
+  if (!table || !multiple_of(table, dtype_bytes(dtype)))
+    return fail(ZERO_EINVAL, "%s: the table is NULL or not aligned to its elements", who);
+  return ZERO_OK;
+}
+
+// Bytes past which what is written will not be found in the 256 MB memory-side cache.
+bool past_cache(uint64_t bytes) { return bytes > (uint64_t(256) << 20); }
+
+}  // namespace
+}  // namespace zs
+
+using namespace zs;
+
+extern "C" int zero_embedding(const void* table, int dtype, uint32_t vocab, uint32_t dim, uint64_t stride,
+                              const int64_t* tokens, uint64_t n_tokens, double scale, void* out, hipStream_t stream) {
+  static const char* who = "zero_embedding";
+  clear_error();
+  int rc = check_table(table, dtype, vocab, dim, stride, who);
+  if (rc) return rc;
+  if (!std::isfinite(scale)) return fail(ZERO_EINVAL, "%s: scale must be finite", who);
+  if (n_tokens > UINT64_MAX / 8 / dim) return fail(ZERO_EINVAL, "%s: n_tokens * dim overflows", who);
+  if (n_tokens == 0) return ZERO_OK;
+  if (!tokens || !multiple_of(tokens, 8) || !out || !multiple_of(out, dtype_bytes(dtype)))
+    return fail(ZERO_EINVAL, "%s: tokens or out is NULL or not aligned to its elements", who);
+  if ((rc = begin_launch())) return rc;
+  with_dtype(dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const uint32_t vecs = (dim + Lane<DT>::N - 1) / Lane<DT>::N;
+    uint32_t shift = 0;
+    while ((1u << shift) < vecs && (1u << shift) < (uint32_t)kBlock) ++shift;
+    const EmbedArgs a = {table, tokens, out, n_tokens, stride, vocab, dim, vecs, (float)scale};
+    const uint64_t rows = kBlock >> shift;
+    const uint32_t grid = chunk_grid((n_tokens + rows - 1) / rows, 0);
+    if (past_cache(n_tokens * dim * dtype_bytes(dtype)))
+      hipLaunchKernelGGL((embed_kernel<DT, true>), grid, kBlock, 0, stream, a, shift);
+    else
+      hipLaunchKernelGGL((embed_kernel<DT, false>), grid, kBlock, 0, stream, a, shift);
+  });
+  return launch_status(who);
+}
+
+extern "C" int zero_embedding_workspace_bytes(uint64_t n_tokens, uint32_t dim, uint64_t* bytes) {
+  static const char* who = "zero_embedding_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(ZERO_EINVAL, "%s: bytes is NULL", who);
+  if (dim == 0 || dim > kMaxDim) return fail(ZERO_EINVAL, "%s: dim %u outside [1, 2^20]", who, dim);
+  if (n_tokens > (uint64_t)INT32_MAX) return fail(ZERO_ERANGE, "%s: n_tokens beyond 2^31 - 1", who);
+  *bytes = space_of(n_tokens, dim).bytes;
+  return ZERO_OK;
+}
+
+extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_t stream) {
+  static const char* who = "zero_embedding_grad";
+  clear_error();
+  if (!p) return fail(ZERO_EINVAL, "%s: args is NULL", who);
+  int rc = check_table(p->dtable, p->table_dtype, p->vocab, p->dim, p->stride, who);
+  if (rc) return rc;
+  if (!known_dtype(p->dtype)) return fail(ZERO_EINVAL, "%s: unknown dtype %d", who, p->dtype);
+  if (p->table_dtype != p->dtype && p->table_dtype != ZERO_F32)
+    return fail(ZERO_EINVAL, "%s: dtable must have the dtype of dout or fp32", who);
+  if (!std::isfinite(p->scale)) return fail(ZERO_EINVAL, "%s: scale must be finite", who);
+  if (p->n_tokens > (uint64_t)INT32_MAX) return fail(ZERO_EINVAL, "%s: n_tokens beyond 2^31 - 1", who);
+  const Space s = space_of(p->n_tokens, p->dim);
+  if (p->n_tokens > 0) {
+    if (!p->dout || !p->tokens || !multiple_of(p->dout, dtype_bytes(p->dtype)) || !multiple_of(p->tokens, 8))
+      return fail(ZERO_EINVAL, "%s: dout or tokens is NULL or not aligned to its elements", who);
+    if (!p->workspace) return fail(ZERO_EINVAL, "%s: workspace is NULL", who);
+    if (p->workspace_bytes < s.bytes)
+      return fail(ZERO_EINVAL, "%s: workspace needs %llu bytes, got %zu", who, (unsigned long long)s.bytes,
+                  p->workspace_bytes);
+    if (!multiple_of(p->workspace, 256)) return fail(ZERO_EINVAL, "%s: workspace must be 256-byte aligned", who);
+  }
+  if (p->n_tokens == 0 && p->accumulate) return ZERO_OK;
+  if ((rc = begin_launch())) return rc;
+  char* ws = static_cast<char*>(p->workspace);
+  GradArgs g = {};
+  g.dout = p->dout;
+  g.dtable = p->dtable;
+  g.stride = p->stride;
+  g.n = (uint32_t)p->n_tokens;
+  g.vocab = p->vocab;
+  g.dim = p->dim;
+  g.scale = (float)p->scale;
+  g.accumulate = p->accumulate != 0;
+  if (g.n > 0) {
+    // keys are 0 .. vocab: passes of equal width, 9 bits at most
+    uint32_t bits = 1;
+    while (bits < 32 && p->vocab >> bits) ++bits;
+    const uint32_t passes = (bits + kMaxBits - 1) / kMaxBits;
+    SortArgs a = {p->tokens, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<uint32_t*>(ws + s.hist),
+                  g.n, p->vocab, s.blocks, 0, 0};
+    for (uint32_t i = 0, done = 0; i < passes; ++i) {
+      a.shift = done;
+      a.bits = (bits - done + passes - i - 1) / (passes - i);
+      done += a.bits;
+      a.keys_out = reinterpret_cast<uint32_t*>(ws + s.keys[i & 1]);
+      a.at_out = reinterpret_cast<uint32_t*>(ws + s.at[i & 1]);
+      hipLaunchKernelGGL(histogram_kernel, s.blocks, kBlock, 0, stream, a);
+      hipLaunchKernelGGL(scatter_kernel, s.blocks, kBlock, 0, stream, a);
+      a.tokens = nullptr;
+      a.keys = a.keys_out;
+      a.at = a.at_out;
+    }
+    if ((rc = launch_status(who))) return rc;
+    g.keys = a.keys;
+    g.at = a.at;
+    g.partial = reinterpret_cast<float*>(ws + s.partial);
+  }
+  if (!g.accumulate) {
+    const uint32_t grid = (uint32_t)std::min<uint64_t>((p->vocab + kFillRows - 1) / kFillRows, 1u << 20);
+    with_dtype(p->table_dtype, [&](auto dt) {
+      constexpr int OUT = decltype(dt)::value;
+      const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
+      if (past_cache((uint64_t)p->vocab * p->dim * dtype_bytes(p->table_dtype)))
+        hipLaunchKernelGGL((fill_kernel<OUT, true>), grid, kBlock, 0, stream, g, vecs);
+      else
+        hipLaunchKernelGGL((fill_kernel<OUT, false>), grid, kBlock, 0, stream, g, vecs);
+    });
+    if ((rc = launch_status(who))) return rc;
+  }
+  if (g.n == 0) return ZERO_OK;
+  with_dtype(p->dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    g.vecs = (p->dim + Lane<DT>::N - 1) / Lane<DT>::N;
+    const dim3 grid(s.tiles, std::min(65535u, (g.vecs + kBlock - 1) / kBlock));
+    if (p->table_dtype == ZERO_F32 && DT != ZERO_F32) {
+      hipLaunchKernelGGL((sum_kernel<DT, ZERO_F32>), grid, kBlock, 0, stream, g);
+      hipLaunchKernelGGL((join_kernel<DT, ZERO_F32>), grid, kBlock, 0, stream, g);
+    } else {
+      hipLaunchKernelGGL((sum_kernel<DT, DT>), grid, kBlock, 0, stream, g);
+      hipLaunchKernelGGL((join_kernel<DT, DT>), grid, kBlock, 0, stream, g);
+    }
+  });
+  return launch_status(who);
+}

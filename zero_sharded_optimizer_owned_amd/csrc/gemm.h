@@ -1,0 +1,179 @@
+// Matrix products on the matrix cores: out[m][n] = sum over k of P[m][k] Q[n][k],
+// operands in 16 bits, sums in fp32.
+//
+// A block of 512 threads makes a 256 x 256 tile, k in steps of 64.  Its eight
+// wavefronts take 128 x 64 each (two in m, four in n).  A step's tile of each
+// operand (32 KB) is loaded straight into LDS, 16 bytes to a lane, one step
+// ahead of the products; two steps fill 128 KB of LDS.
+//
+// An operand is laid out either with k contiguous (Rows: element (r, k) at r
+// stride + k) or with r contiguous (Columns: at k stride + r).  Rows' tiles hold
+// 64 k of a row in 128 bytes and are read by ds_read_b128; Columns' tiles hold
+// 256 r of a k in 512 bytes and are read by the transposing read
+// (ds_read_b64_tr_b16: 16 lanes fetch 4 k by 16 r and get 4 k of one r each).
+// Either way a lane then holds 8 consecutive k of one r.  The direct load
+// writes LDS in lane order, so the exclusive-or that spreads the banks is
+// applied to the global address: 16-byte piece c of a row lies at piece
+// c ^ swizzle(row).
+//
+// The products are formed with Q first, so that a lane's four results are four
+// consecutive n of one m.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "vec.h"
+
+namespace zs {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kGemmThreads = 512;
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+constexpr int kOperandBytes = 256 * kTileK * 2;
+constexpr int kGemmLds = 4 * kOperandBytes;
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: reads zero
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(const u32x4 a, const u32x4 b, const f32x4 c) {
+  if constexpr (DT == ZERO_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, lds_char* to) {
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7FFFFFFF, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, offset, 0, 0, 0);
+}
+
+// k contiguous.  `base`: row 0 of the tile; rows from `rows` on and k from
+// `depth` (a multiple of 8) on are zero.  256 rows are under 2 GB.
+struct Rows {
+  const char* base;
+  uint32_t offset[4], k;
+  uint32_t depth;
+
+  __device__ __forceinline__ void begin(const void* p, uint64_t row0, uint32_t n_rows, uint64_t stride, uint32_t depth_) {
+    base = static_cast<const char*>(p) + row0 * stride * 2;
+    depth = depth_;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t rows = n_rows > row0 ? (uint32_t)min((uint64_t)n_rows - row0, (uint64_t)256) : 0;
+    k = ((lane % 8) ^ (lane / 8)) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t row = (wave * 4 + i) * 8 + lane / 8;
+      offset[i] = row < rows ? (uint32_t)(row * stride * 2) + k * 2 : kNowhere;
+    }
+  }
+  __device__ __forceinline__ void load(uint32_t k0, lds_char* tile) const {
+    const uint32_t wave = threadIdx.x >> 6;
+    const bool in = k0 + k < depth;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_to_lds(base + (uint64_t)k0 * 2, in ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
+  }
+  // Eight k from 32 kk + 8 (lane / 16) on of row r0 + lane % 16.
+  static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
+    const uint32_t lane = threadIdx.x & 63, row = r0 + lane % 16, piece = (lane / 16 + 4 * kk) ^ (row % 8);
+    return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(tile + row * 128 + piece * 16);
+  }
+};
+
+// r contiguous.  `base`: column r0 of row 0; columns from `columns` (a multiple
+// of 8) on and k from `depth` on are zero.
+struct Columns {
+  const char* base;
+  uint64_t stride;
+  uint32_t offset[4];
+  uint32_t depth;
+
+  __device__ __forceinline__ void begin(const void* p, uint64_t column0, uint32_t n_columns, uint64_t stride_, uint32_t depth_) {
+    base = static_cast<const char*>(p) + column0 * 2;
+    stride = stride_;
+    depth = depth_;
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t columns = n_columns > column0 ? (uint32_t)min((uint64_t)n_columns - column0, (uint64_t)256) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t row = (wave * 4 + i) * 2 + lane / 32, c = (lane % 32) ^ swizzle(row);
+      offset[i] = c * 8 < columns ? (uint32_t)(row * stride * 2) + c * 16 : kNowhere;
+    }
+  }
+  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) { return (row % 4) << 1 | (row / 8 % 2) << 3; }
+  __device__ __forceinline__ void load(uint32_t k0, lds_char* tile) const {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const char* at = base + k0 * stride * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t row = (wave * 4 + i) * 2 + lane / 32;
+      load_to_lds(at, k0 + row < depth ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
+    }
+  }
+  static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
+    const uint32_t lane = threadIdx.x & 63;
+    u32x4 f;
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h) {
+      const uint32_t row = 32 * kk + 8 * (lane / 16) + 4 * h + lane % 16 / 4;
+      const uint32_t piece = (r0 / 8 + lane % 4 / 2) ^ swizzle(row);
+      const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)(tile + row * 512 + piece * 16 + lane % 2 * 8));
+      const u32x2 w = __builtin_bit_cast(u32x2, q);
+      f[2 * h] = w[0];
+      f[2 * h + 1] = w[1];
+    }
+    return f;
+  }
+};
+
+// acc[i][j][x]: m = 128 (wave / 4) + 16 i + lane % 16, n = 64 (wave % 4) + 16 j +
+// 4 (lane / 16) + x.  k runs over [k_begin, k_end), k_begin a multiple of 64.
+typedef f32x4 Acc[8][4];
+
+template <int DT, class P, class Q>
+__device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_begin, uint32_t k_end, lds_char* lds, Acc& acc) {
+  const uint32_t wave = threadIdx.x >> 6, m0 = wave / 4 * 128, n0 = wave % 4 * 64;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  if (k_begin >= k_end) return;
+  lds_char* now = lds;
+  lds_char* next = lds + 2 * kOperandBytes;
+  p.load(k_begin, now);
+  q.load(k_begin, now + kOperandBytes);
+  for (uint32_t k = k_begin; k < k_end; k += kTileK) {
+    // this wavefront's loads of the step have arrived and its reads of the
+    // other half are done; behind the barrier that holds for all of them
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (k + kTileK < k_end) {
+      p.load(k + kTileK, next);
+      q.load(k + kTileK, next + kOperandBytes);
+    }
+#pragma unroll
+    for (uint32_t kk = 0; kk < 2; ++kk) {
+      u32x4 a[4], b[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[j] = Q::fragment(now + kOperandBytes, n0 + 16 * j, kk);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = P::fragment(now, m0 + 16 * i, kk);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(a[j], b[i], acc[i][j]);
+    }
+    lds_char* t = now;
+    now = next;
+    next = t;
+  }
+}
+
+}  // namespace zs

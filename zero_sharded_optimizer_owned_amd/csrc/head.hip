@@ -1,0 +1,520 @@
+// Softmax cross entropy from hidden states and output weights, with the
+// gradients of both, without the logits of more than a piece of the rows.
+//
+//   x = hidden weight^T / T      lp = x[target] - ln sum_j exp(x_j)
+//   loss = -sum_r w_r lp_r / divisor
+//   dx = grad_scale w / (divisor T) (softmax(x) - onehot)
+//   dhidden = dx weight          dweight = dx^T hidden
+//
+// Three matrix products bound it: 2 N V D operations each.  Rows whose target
+// lies outside the vocabulary are left out of all of them: the others are
+// gathered first.  A piece of rows goes through
+//   prepare, gather   the rows that count, their targets and weights
+//   logits            product one; its epilogue leaves exp(x - m) of each
+//                     256-column tile in 16 bits, m the row's maximum in the
+//                     tile, with m and the sum
+//   softmax           the rows' log-probabilities; the tiles' exponentials
+//                     become dx in place
+//   dhidden, dweight  products two and three
+// dx is held as (softmax - onehot) w / max|w| 2^14 in 16 bits; the common factor
+// comes back in the epilogues, so that fp16 keeps probabilities down to 2^-38
+// whatever the loss scale.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "gemm.h"
+#include "launch.h"
+#include "rows.h"
+
+namespace zs {
+namespace {
+
+constexpr double kLog2e = 1.4426950408889634074;
+constexpr float kHeld = 0x1p14f;   // of dx as it is held
+constexpr float kTileExp = 0x1p15f;  // of a tile's exponentials, at most 1 before
+
+struct Meta {
+  uint32_t live;  // rows that count, of the piece
+  float factor;   // dx = factor * what is held
+};
+
+struct HeadArgs {
+  const void *hidden, *weight;
+  uint64_t hidden_stride, weight_stride;
+  const int64_t* targets;
+  const float* row_weight;
+  uint32_t rows, vocab, dim;  // rows: of the piece
+  uint32_t tiles, padded;     // 256-column tiles of the vocabulary, 256 * tiles
+  double inv_temperature, coef;  // coef = grad_scale / (divisor temperature)
+  float c;                    // log2(e) / temperature
+  float* logp;
+  void *dhidden, *dweight;
+  uint64_t dhidden_stride, dweight_stride;
+  // workspace
+  Meta* meta;
+  uint32_t *row_of, *target;  // of each row that counts
+  float *omega, *said;        // w / max|w|; the target's logit
+  double* terms;              // w lp of the piece's rows
+  uint8_t* counts;            // of the piece's rows
+  uint16_t *kept, *held;      // rows that count [rows][dim8]; exponentials, then dx [rows][padded]
+  f32x2* stats;               // [rows][tiles]: a tile's maximum and sum without the target
+  float* sum;                 // fp32 dweight of the pieces so far
+  int first, last;            // whether the piece is the first, the last
+};
+
+// ---------------------------------------------------------------------------
+// The rows that count, in order.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
+  __shared__ uint32_t part[16];
+  __shared__ float most[16];
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  uint32_t before = 0;
+  float top = 0.0f;
+  for (uint32_t r0 = 0; r0 < a.rows; r0 += 1024) {
+    const uint32_t r = r0 + t;
+    const int64_t target = r < a.rows ? a.targets[r] : -1;
+    const bool has = target >= 0 && target < (int64_t)a.vocab;
+    const float w = has && a.row_weight ? fabsf(a.row_weight[r]) : (has ? 1.0f : 0.0f);
+    if (w < INFINITY) top = fmaxf(top, w);
+    const uint64_t ballot = __ballot(has);
+    __syncthreads();
+    if (lane == 0) part[wave] = (uint32_t)__popcll(ballot);
+    __syncthreads();
+    uint32_t at = before + (uint32_t)__popcll(ballot & ((1ull << lane) - 1)), all = 0;
+    for (uint32_t i = 0; i < 16; ++i) {
+      at += i < wave ? part[i] : 0;
+      all += part[i];
+    }
+    before += all;
+    if (r < a.rows) {
+      a.counts[r] = has;
+      if (!has) {
+        a.logp[r] = 0.0f;
+        a.terms[r] = 0.0;
+      } else {
+        a.row_of[at] = r;
+        a.target[at] = (uint32_t)target;
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
+  if (lane == 0) most[wave] = top;
+  __syncthreads();
+  for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
+  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld)};
+  for (uint32_t i = t; i < before; i += 1024) {
+    const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f;
+    a.omega[i] = top > 0.0f ? w / top : w;  // all weights 0 or not finite
+  }
+}
+
+// Block i: the i-th row that counts is copied; row i's gradient, if it does not
+// count, is zero.
+__global__ void __launch_bounds__(kBlock) gather_kernel(const HeadArgs a) {
+  const uint32_t vecs = a.dim / 8;
+  for (uint32_t i = blockIdx.x; i < a.rows; i += gridDim.x) {
+    if (i < a.meta->live) {
+      const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.hidden) + a.row_of[i] * a.hidden_stride);
+      u32x4* to = reinterpret_cast<u32x4*>(a.kept + (uint64_t)i * a.dim);
+      for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) to[v] = from[v];
+    }
+    if (a.dhidden && !a.counts[i]) {
+      u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.dhidden) + i * a.dhidden_stride);
+      for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) to[v] = u32x4{0, 0, 0, 0};
+    }
+  }
+}
+
+// Tile numbers in an order that keeps a group of tiles on one XCD: each XCD
+// takes a contiguous run, in which eight m tiles go along n together.
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, uint32_t* m, uint32_t* n) {
+  const uint32_t i = (uint32_t)xcd_contiguous(b, (uint64_t)mt * nt);
+  constexpr uint32_t G = 8;
+  const uint32_t group = i / (G * nt), in = i % (G * nt), size = min(G, mt - group * G);
+  *m = group * G + in % size;
+  *n = in / size;
+}
+
+// ---------------------------------------------------------------------------
+// Product one.
+// ---------------------------------------------------------------------------
+template <int DT, bool KEEP>
+__global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const uint32_t live = a.meta->live, mt = (live + 255) / 256;
+  if (blockIdx.x >= mt * a.tiles) return;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, mt, a.tiles, &tm, &tn);
+  Rows p, q;
+  p.begin(a.kept, (uint64_t)tm * 256, live, a.dim, a.dim);
+  q.begin(a.weight, (uint64_t)tn * 256, a.vocab, a.weight_stride, a.dim);
+  Acc acc;
+  gemm_tile<DT>(p, q, 0, a.dim, (lds_char*)lds, acc);
+  // the tile's maximum of each row, over the four wavefronts that share it
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t m0 = wave / 4 * 128 + lane % 16, n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  float* red = reinterpret_cast<float*>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (n0 + 16 * j + x < a.vocab) top = fmaxf(top, acc[i][j][x]);
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    if (lane < 16) red[wave % 4 * 256 + m0 + 16 * i] = top;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t r = m0 + 16 * i, row = tm * 256 + r;
+    const bool has = row < live;
+    const float top = fmaxf(fmaxf(red[r], red[256 + r]), fmaxf(red[512 + r], red[768 + r]));
+    const float m = top == -INFINITY ? 0.0f : top;
+    const uint32_t target = has ? a.target[row] : 0xFFFFFFFFu;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float e[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t n = n0 + 16 * j + x;
+        e[x] = n < a.vocab ? __builtin_amdgcn_exp2f((acc[i][j][x] - m) * a.c) : 0.0f;
+        if (n == target) a.said[row] = acc[i][j][x];
+        else sum += e[x];
+      }
+      if (KEEP && has)
+        store4<ZERO_F16>(a.held, (uint64_t)row * a.padded + n0 + 16 * j, e[0] * kTileExp, e[1] * kTileExp, e[2] * kTileExp,
+                         e[3] * kTileExp);
+    }
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if (lane < 16) red[1024 + wave % 4 * 256 + r] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < 256 && tm * 256 + threadIdx.x < live) {
+    const uint32_t r = threadIdx.x;
+    const float top = fmaxf(fmaxf(red[r], red[256 + r]), fmaxf(red[512 + r], red[768 + r]));
+    const float* s = red + 1024 + r;
+    a.stats[(uint64_t)(tm * 256 + r) * a.tiles + tn] = f32x2{top, s[0] + s[256] + s[512] + s[768]};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Log-probabilities, and dx in place of the exponentials.  One block to a row.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kMaxTiles = 1u << 12;  // a vocabulary of 2^20
+
+template <int DT, bool KEEP>
+__global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
+  __shared__ float scale[KEEP ? kMaxTiles : 1];
+  __shared__ double part[kWavesPerBlock];
+  __shared__ float tops[kWavesPerBlock];
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  for (uint32_t row = blockIdx.x; row < a.meta->live; row += gridDim.x) {
+    const f32x2* stats = a.stats + (uint64_t)row * a.tiles;
+    float top = -INFINITY;
+    for (uint32_t i = t; i < a.tiles; i += kBlock) top = fmaxf(top, stats[i][0]);
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
+    __syncthreads();
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    for (int i = 0; i < kWavesPerBlock; ++i) top = fmaxf(top, tops[i]);
+    double sum = 0.0;
+    for (uint32_t i = t; i < a.tiles; i += kBlock) {
+      const f32x2 s = stats[i];
+      if (!(s[1] == 0.0f && s[0] == -INFINITY)) sum += (double)s[1] * (double)__builtin_amdgcn_exp2f((s[0] - top) * a.c);
+    }
+    sum = row_sum<kWavesPerBlock>(sum, part);
+    const uint32_t target = a.target[row], from = a.row_of[row];
+    const double d = (double)(a.said[row] - top) * a.inv_temperature;
+    const double all = sum + exp(d);
+    if (t == 0) {
+      const double lp = d == 0.0 ? -log1p(sum) : d - log(all);
+      a.logp[from] = (float)lp;
+      a.terms[from] = lp * (a.row_weight ? (double)a.row_weight[from] : 1.0);
+    }
+    if constexpr (KEEP) {
+      const float omega = a.omega[row] * kHeld;
+      const float unit = (float)((double)omega / all) * (1.0f / kTileExp);
+      for (uint32_t i = t; i < a.tiles; i += kBlock) {
+        const float m = stats[i][0];
+        scale[i] = m == -INFINITY ? 0.0f : unit * __builtin_amdgcn_exp2f((m - top) * a.c);
+      }
+      __syncthreads();
+      const float other = -(float)((double)omega * (sum / all));  // at the target: p - 1, without cancellation
+      uint16_t* held = a.held + (uint64_t)row * a.padded;
+      for (uint32_t v = t; v < a.padded / 8; v += kBlock) {
+        const Vec<ZERO_F16>::Raw e = load8<ZERO_F16>(held, (uint64_t)v * 8);
+        const float f = scale[v / 32];
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = v * 8 + k == target ? other : Vec<ZERO_F16>::get(e, k) * f;
+        store8<DT>(held, (uint64_t)v * 8, x);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Products two and three.
+// ---------------------------------------------------------------------------
+template <int DT>
+__global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const uint32_t live = a.meta->live, mt = (live + 255) / 256, nt = (a.dim + 255) / 256;
+  if (blockIdx.x >= mt * nt) return;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, mt, nt, &tm, &tn);
+  Rows p;
+  Columns q;
+  p.begin(a.held, (uint64_t)tm * 256, live, a.padded, a.padded);
+  q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, a.vocab);
+  Acc acc;
+  gemm_tile<DT>(p, q, 0, a.vocab, (lds_char*)lds, acc);
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  const float f = a.meta->factor;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
+    if (row >= live) continue;
+    const uint64_t at = a.row_of[row] * a.dhidden_stride;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4 x = acc[i][j] * f;
+      if (n0 + 16 * j < a.dim) store4<DT>(a.dhidden, at + n0 + 16 * j, x[0], x[1], x[2], x[3]);
+    }
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  const uint32_t live = a.meta->live, mt = a.tiles, nt = (a.dim + 255) / 256;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, mt, nt, &tm, &tn);
+  Columns p, q;
+  p.begin(a.held, (uint64_t)tm * 256, a.padded, a.padded, live);
+  q.begin(a.kept, (uint64_t)tn * 256, a.dim, a.dim, live);
+  Acc acc;
+  gemm_tile<DT>(p, q, 0, live, (lds_char*)lds, acc);
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  const float f = a.meta->factor;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
+    if (row >= a.vocab) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t n = n0 + 16 * j;
+      if (n >= a.dim) continue;
+      f32x4 x = acc[i][j] * f;
+      f32x4* sum = reinterpret_cast<f32x4*>(a.sum + (uint64_t)row * a.dim + n);
+      if (!a.first) x += *sum;
+      if (a.last) store4<DT>(a.dweight, row * a.dweight_stride + n, x[0], x[1], x[2], x[3]);
+      else *sum = x;
+    }
+  }
+}
+
+// stats[0] = -sum of the rows' terms / divisor, stats[1] = how many rows count;
+// each thread adds a fixed set of rows.
+__global__ void __launch_bounds__(1024) loss_kernel(const double* terms, const uint8_t* counts, uint64_t n, double inv_divisor,
+                                                    float* stats) {
+  __shared__ double part[16];
+  double sum = 0.0, count = 0.0;
+  for (uint64_t i = threadIdx.x; i < n; i += 1024) {
+    sum += terms[i];
+    count += (double)counts[i];
+  }
+  sum = row_sum<16>(sum, part);
+  count = row_sum<16>(count, part);
+  if (threadIdx.x == 0) {
+    stats[0] = (float)(-sum * inv_divisor);
+    stats[1] = (float)count;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kMaxDim = 1u << 15;
+
+struct Space {
+  uint64_t meta, row_of, target, omega, said, terms, counts, kept, held, stats, sum, bytes;
+  uint32_t piece;
+};
+
+// Where the pieces of `piece_rows` rows have their intermediates.
+Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows, bool grad) {
+  Space s;
+  s.piece = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(n_rows, piece_rows));
+  const uint64_t tiles = (vocab + 255) / 256, p = s.piece;
+  uint64_t at = 0;
+  const auto take = [&](uint64_t bytes) {
+    const uint64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  s.meta = take(sizeof(Meta));
+  s.row_of = take(p * 4);
+  s.target = take(p * 4);
+  s.omega = take(p * 4);
+  s.said = take(p * 4);
+  s.terms = take(n_rows * 8);
+  s.counts = take(n_rows);
+  s.kept = take(p * dim * 2);
+  s.stats = take(p * tiles * 8);
+  s.held = take(grad ? p * tiles * 512 : 0);
+  s.sum = take(grad && n_rows > p ? (uint64_t)vocab * dim * 4 : 0);
+  s.bytes = at;
+  return s;
+}
+
+int check_shape(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows, const char* who) {
+  if (vocab == 0 || vocab > kMaxTiles * 256) return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^20]", who, vocab);
+  if (dim == 0 || dim > kMaxDim || dim % 8)
+    return fail(ZERO_EINVAL, "%s: dim %u is not a multiple of 8 in [8, %u]", who, dim, kMaxDim);
+  if (piece_rows == 0 || piece_rows > 16384) return fail(ZERO_EINVAL, "%s: piece_rows %u outside [1, 16384]", who, piece_rows);
+  if (n_rows > (uint64_t)INT32_MAX) return fail(ZERO_EINVAL, "%s: n_rows beyond 2^31 - 1", who);
+  return ZERO_OK;
+}
+
+int check_matrix(const void* p, uint64_t rows, uint32_t dim, uint64_t stride, const char* name, const char* who) {
+  if (!p || !multiple_of(p, 16) || stride % 8)
+    return fail(ZERO_EINVAL, "%s: %s is NULL, or its rows are not 16-byte aligned", who, name);
+  if (stride < dim || stride > (1u << 22))
+    return fail(ZERO_EINVAL, "%s: %s has a row stride of %llu outside [dim, 2^22]", who, name, (unsigned long long)stride);
+  (void)rows;
+  return ZERO_OK;
+}
+
+template <int DT>
+void launch_piece(const HeadArgs& a, bool grad, hipStream_t stream) {
+  const uint32_t mt = (a.rows + 255) / 256, nt = (a.dim + 255) / 256;
+  hipLaunchKernelGGL(prepare_kernel, 1, 1024, 0, stream, a);
+  hipLaunchKernelGGL(gather_kernel, a.rows, kBlock, 0, stream, a);
+  if (grad) {
+    hipLaunchKernelGGL((logits_kernel<DT, true>), mt * a.tiles, kGemmThreads, kGemmLds, stream, a);
+    hipLaunchKernelGGL((softmax_kernel<DT, true>), a.rows, kBlock, 0, stream, a);
+    if (a.dhidden) hipLaunchKernelGGL(dhidden_kernel<DT>, mt * nt, kGemmThreads, kGemmLds, stream, a);
+    if (a.dweight) hipLaunchKernelGGL(dweight_kernel<DT>, a.tiles * nt, kGemmThreads, kGemmLds, stream, a);
+  } else {
+    hipLaunchKernelGGL((logits_kernel<DT, false>), mt * a.tiles, kGemmThreads, kGemmLds, stream, a);
+    hipLaunchKernelGGL((softmax_kernel<DT, false>), a.rows, kBlock, 0, stream, a);
+  }
+}
+
+}  // namespace
+}  // namespace zs
+
+using namespace zs;
+
+extern "C" int zero_linear_cross_entropy_workspace_bytes(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows,
+                                                         int grad, uint64_t* bytes) {
+  static const char* who = "zero_linear_cross_entropy_workspace_bytes";
+  clear_error();
+  if (!bytes) return fail(ZERO_EINVAL, "%s: bytes is NULL", who);
+  const int rc = check_shape(n_rows, vocab, dim, piece_rows, who);
+  if (rc) return rc;
+  *bytes = space_of(n_rows, vocab, dim, piece_rows, grad != 0).bytes;
+  return ZERO_OK;
+}
+
+extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p, hipStream_t stream) {
+  static const char* who = "zero_linear_cross_entropy";
+  clear_error();
+  if (!p) return fail(ZERO_EINVAL, "%s: args is NULL", who);
+  if (p->dtype != ZERO_F16 && p->dtype != ZERO_BF16) return fail(ZERO_EINVAL, "%s: dtype %d is not fp16 or bf16", who, p->dtype);
+  int rc = check_shape(p->n_rows, p->vocab, p->dim, p->piece_rows, who);
+  if (rc) return rc;
+  const double nums[] = {p->divisor, p->temperature, p->grad_scale};
+  for (double x : nums)
+    if (!std::isfinite(x)) return fail(ZERO_EINVAL, "%s: non-finite parameter", who);
+  if (p->divisor <= 0.0) return fail(ZERO_EINVAL, "%s: divisor must be > 0", who);
+  if (p->temperature <= 0.0 || !std::isnormal((float)(kLog2e / p->temperature)))
+    return fail(ZERO_EINVAL, "%s: temperature %g is out of range", who, p->temperature);
+  if (!p->stats || !multiple_of(p->stats, 4)) return fail(ZERO_EINVAL, "%s: stats is NULL or misaligned", who);
+  if ((rc = check_matrix(p->weight, p->vocab, p->dim, p->weight_stride, "weight", who))) return rc;
+  if (p->dweight && (rc = check_matrix(p->dweight, p->vocab, p->dim, p->dweight_stride, "dweight", who))) return rc;
+  const bool grad = p->dhidden || p->dweight;
+  const Space s = space_of(p->n_rows, p->vocab, p->dim, p->piece_rows, grad);
+  if (p->n_rows > 0) {
+    if ((rc = check_matrix(p->hidden, p->n_rows, p->dim, p->hidden_stride, "hidden", who))) return rc;
+    if (p->dhidden && (rc = check_matrix(p->dhidden, p->n_rows, p->dim, p->dhidden_stride, "dhidden", who))) return rc;
+    if (!p->targets || !multiple_of(p->targets, 8)) return fail(ZERO_EINVAL, "%s: targets is NULL or misaligned", who);
+    if (!p->logp || !multiple_of(p->logp, 4) || !multiple_of(p->row_weight, 4))
+      return fail(ZERO_EINVAL, "%s: logp is NULL, or a per-row array is misaligned", who);
+  }
+  if (!p->workspace) return fail(ZERO_EINVAL, "%s: workspace is NULL", who);
+  if (p->workspace_bytes < s.bytes)
+    return fail(ZERO_EINVAL, "%s: workspace needs %llu bytes, got %zu", who, (unsigned long long)s.bytes, p->workspace_bytes);
+  if (!multiple_of(p->workspace, 256)) return fail(ZERO_EINVAL, "%s: workspace must be 256-byte aligned", who);
+  if ((rc = begin_launch())) return rc;
+  char* ws = static_cast<char*>(p->workspace);
+  HeadArgs a = {};
+  a.weight = p->weight;
+  a.hidden_stride = p->hidden_stride;
+  a.weight_stride = p->weight_stride;
+  a.vocab = p->vocab;
+  a.dim = p->dim;
+  a.tiles = (p->vocab + 255) / 256;
+  a.padded = a.tiles * 256;
+  a.inv_temperature = 1.0 / p->temperature;
+  a.coef = p->grad_scale / (p->divisor * p->temperature);
+  a.c = (float)(kLog2e / p->temperature);
+  a.dweight = p->dweight;
+  a.dhidden_stride = p->dhidden_stride;
+  a.dweight_stride = p->dweight_stride;
+  a.meta = reinterpret_cast<Meta*>(ws + s.meta);
+  a.row_of = reinterpret_cast<uint32_t*>(ws + s.row_of);
+  a.target = reinterpret_cast<uint32_t*>(ws + s.target);
+  a.omega = reinterpret_cast<float*>(ws + s.omega);
+  a.said = reinterpret_cast<float*>(ws + s.said);
+  a.kept = reinterpret_cast<uint16_t*>(ws + s.kept);
+  a.stats = reinterpret_cast<f32x2*>(ws + s.stats);
+  a.held = reinterpret_cast<uint16_t*>(ws + s.held);
+  a.sum = reinterpret_cast<float*>(ws + s.sum);
+  double* terms = reinterpret_cast<double*>(ws + s.terms);
+  uint8_t* counts = reinterpret_cast<uint8_t*>(ws + s.counts);
+  // without rows, one empty piece: dweight is then zero
+  uint64_t row = 0;
+  do {
+    a.rows = (uint32_t)std::min<uint64_t>(s.piece, p->n_rows - row);
+    a.first = row == 0;
+    a.last = row + a.rows == p->n_rows;
+    a.hidden = static_cast<const uint16_t*>(p->hidden) + row * p->hidden_stride;
+    a.targets = p->targets + row;
+    a.row_weight = p->row_weight ? p->row_weight + row : nullptr;
+    a.logp = p->logp + row;
+    a.dhidden = p->dhidden ? static_cast<uint16_t*>(p->dhidden) + row * p->dhidden_stride : nullptr;
+    a.terms = terms + row;
+    a.counts = counts + row;
+    if (a.rows > 0) {
+      if (p->dtype == ZERO_F16) launch_piece<ZERO_F16>(a, grad, stream);
+      else launch_piece<ZERO_BF16>(a, grad, stream);
+    } else if (a.dweight) {
+      hipLaunchKernelGGL(prepare_kernel, 1, 1024, 0, stream, a);
+      const uint32_t nt = (a.dim + 255) / 256;
+      if (p->dtype == ZERO_F16) hipLaunchKernelGGL(dweight_kernel<ZERO_F16>, a.tiles * nt, kGemmThreads, kGemmLds, stream, a);
+      else hipLaunchKernelGGL(dweight_kernel<ZERO_BF16>, a.tiles * nt, kGemmThreads, kGemmLds, stream, a);
+    }
+    if ((rc = launch_status(who))) return rc;
+    row += a.rows;
+  } while (row < p->n_rows);
+  hipLaunchKernelGGL(loss_kernel, 1, 1024, 0, stream, terms, counts, p->n_rows, 1.0 / p->divisor, p->stats);
+  return launch_status(who);
+}
