@@ -38,8 +38,10 @@ constexpr float kHeld = 0x1p14f;   // of dx as it is held
 constexpr float kTileExp = 0x1p15f;  // of a tile's exponentials, at most 1 before
 
 struct Meta {
-  uint32_t live;  // rows that count, of the piece
-  float factor;   // dx = factor * what is held
+  uint32_t live;    // rows that count, of the piece
+  float factor;     // dx = factor * what is held
+  uint32_t splits;  // of dhidden's sums over the vocabulary
+  uint32_t done;    // rows whose terms are stored (few rows only)
 };
 
 struct HeadArgs {
@@ -48,7 +50,8 @@ struct HeadArgs {
   const int64_t* targets;
   const float* row_weight;
   uint32_t rows, vocab, dim;  // rows: of the piece
-  uint32_t tiles, padded;     // 256-column tiles of the vocabulary, 256 * tiles
+  uint32_t tiles, padded;     // tiles of the vocabulary, its columns up to a multiple of 256
+  uint32_t shift;             // a tile is 1 << shift columns
   double inv_temperature, coef;  // coef = grad_scale / (divisor temperature)
   float c;                    // log2(e) / temperature
   float* logp;
@@ -62,9 +65,30 @@ struct HeadArgs {
   uint8_t* counts;            // of the piece's rows
   uint16_t *kept, *held;      // rows that count [rows][dim8]; exponentials, then dx [rows][padded]
   f32x2* stats;               // [rows][tiles]: a tile's maximum and sum without the target
+  float* part;                // [splits][rows][dim]: dhidden's sums over parts of the vocabulary
   float* sum;                 // fp32 dweight of the pieces so far
   int first, last;            // whether the piece is the first, the last
+  float* stats_out;           // few rows: the last block of softmax_kernel writes the loss
+  double inv_divisor;
 };
+
+// How many parts the vocabulary of dhidden's product is cut into, so that the
+// launch fills the 256 CUs evenly: of up to 64, the one with the least time in
+// steps of the product.  A part's sums go through memory in fp32, which takes
+// a CU as long as some 25 steps (256 KB written and read at its share of HBM).
+__host__ __device__ inline uint32_t splits_of(uint32_t live, uint32_t vocab, uint32_t dim) {
+  const uint32_t tiles = ((live + 255) / 256) * ((dim + 255) / 256), steps = (vocab + 63) / 64;
+  uint32_t best = 1;
+  uint32_t least = (tiles + 255) / 256 * steps;
+  for (uint32_t s = 2; s <= 64 && s * 8 <= steps && tiles * s <= 2048; ++s) {
+    const uint32_t t = (tiles * s + 255) / 256 * ((steps + s - 1) / s + 25);
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
 
 // ---------------------------------------------------------------------------
 // The rows that count, in order.
@@ -107,7 +131,7 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
   if (lane == 0) most[wave] = top;
   __syncthreads();
   for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
-  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld)};
+  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), splits_of(before, a.vocab, a.dim), 0};
   for (uint32_t i = t; i < before; i += 1024) {
     const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f;
     a.omega[i] = top > 0.0f ? w / top : w;  // all weights 0 or not finite
@@ -209,18 +233,112 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
   }
 }
 
+// The same for up to 16 rows, bound by the reading of the weights: a wavefront
+// takes 16 columns and reads their weights straight into registers, 16 bytes
+// to a lane, kFewSteps steps of 32 k in flight; the rows' hidden states come
+// from the caches.  Tiles are 64 columns, so that a vocabulary of 32,000 makes
+// 500 blocks.
+constexpr uint32_t kFewRows = 16, kFewShift = 6;
+constexpr int kFewSteps = 8;
+
+template <int DT, bool KEEP>
+__global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
+  __shared__ float red[2][kWavesPerBlock][16];
+  const uint32_t live = a.meta->live, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (live == 0) return;
+  const uint32_t tn = blockIdx.x, column = tn * 64 + wave * 16, row = lane % 16, k0 = lane / 16 * 8;
+  const bool has = row < live, in = column + lane % 16 < a.vocab;
+  const uint16_t* w = static_cast<const uint16_t*>(a.weight) + (uint64_t)(in ? column + lane % 16 : 0) * a.weight_stride + k0;
+  const uint16_t* h = a.kept + (uint64_t)(has ? row : 0) * a.dim + k0;
+  f32x4 acc = {0, 0, 0, 0};
+  uint32_t k = 0;
+  for (; k + 32 * kFewSteps <= a.dim; k += 32 * kFewSteps) {
+    u32x4 x[kFewSteps], y[kFewSteps];
+#pragma unroll
+    for (int i = 0; i < kFewSteps; ++i) x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + k + 32 * i));
+#pragma unroll
+    for (int i = 0; i < kFewSteps; ++i) y[i] = has ? *reinterpret_cast<const u32x4*>(h + k + 32 * i) : u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kFewSteps; ++i) acc = mfma16<DT>(x[i], y[i], acc);
+  }
+  for (; k < a.dim; k += 32) {
+    u32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+    if (k + k0 < a.dim) {
+      x = *reinterpret_cast<const u32x4*>(w + k);
+      if (has) y = *reinterpret_cast<const u32x4*>(h + k);
+    }
+    acc = mfma16<DT>(x, y, acc);
+  }
+  // acc[x]: column + 4 (lane / 16) + x of row lane % 16
+  const uint32_t n0 = column + lane / 16 * 4;
+  float top = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (n0 + x < a.vocab) top = fmaxf(top, acc[x]);
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = fmaxf(top, __shfl_xor(top, 32, 64));
+  if (lane < 16) red[0][wave][lane] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWavesPerBlock; ++i) top = fmaxf(top, red[0][i][row]);
+  const float m = top == -INFINITY ? 0.0f : top;
+  const uint32_t target = has ? a.target[row] : 0xFFFFFFFFu;
+  float sum = 0.0f, e[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    e[x] = n0 + x < a.vocab ? __builtin_amdgcn_exp2f((acc[x] - m) * a.c) : 0.0f;
+    if (n0 + x == target) a.said[row] = acc[x];
+    else sum += e[x];
+  }
+  if (KEEP && has)
+    store4<ZERO_F16>(a.held, (uint64_t)row * a.padded + n0, e[0] * kTileExp, e[1] * kTileExp, e[2] * kTileExp,
+                     e[3] * kTileExp);
+  sum += __shfl_xor(sum, 16, 64);
+  sum += __shfl_xor(sum, 32, 64);
+  if (lane < 16) red[1][wave][lane] = sum;
+  __syncthreads();
+  if (threadIdx.x < live && tn < a.tiles) {  // the blocks behind the vocabulary only store zeros
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWavesPerBlock; ++i) sum += red[1][i][threadIdx.x];
+    a.stats[(uint64_t)threadIdx.x * a.tiles + tn] = f32x2{top, sum};
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Log-probabilities, and dx in place of the exponentials.  One block to a row.
+// Log-probabilities, and dx in place of the exponentials.  Blocks (row, part of
+// the row): each goes over the row's tile statistics and then its own part.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kMaxTiles = 1u << 12;  // a vocabulary of 2^20
+constexpr uint32_t kPartTiles = 512;      // most tiles of one part
+
+// Up to this many rows the last block to finish adds up the rows' terms.
+constexpr uint32_t kTicketRows = 128;
+
+__device__ __forceinline__ void loss_of(const double* terms, const uint8_t* counts, uint64_t n, double inv_divisor,
+                                        double* part, float* stats) {
+  double sum = 0.0, count = 0.0;
+  for (uint64_t i = threadIdx.x; i < n; i += kBlock) {
+    sum += terms[i];
+    count += (double)counts[i];
+  }
+  sum = row_sum<kWavesPerBlock>(sum, part);
+  count = row_sum<kWavesPerBlock>(count, part);
+  if (threadIdx.x == 0) {
+    stats[0] = (float)(-sum * inv_divisor);
+    stats[1] = (float)count;
+  }
+}
 
 template <int DT, bool KEEP>
 __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
-  __shared__ float scale[KEEP ? kMaxTiles : 1];
+  __shared__ float scale[KEEP ? kPartTiles : 1];
   __shared__ double part[kWavesPerBlock];
   __shared__ float tops[kWavesPerBlock];
-  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  for (uint32_t row = blockIdx.x; row < a.meta->live; row += gridDim.x) {
+  __shared__ uint32_t rank;
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, live = a.meta->live;
+  // this block's tiles
+  const uint32_t per = (a.tiles + gridDim.y - 1) / gridDim.y, tile0 = blockIdx.y * per, tile1 = min(tile0 + per, a.tiles);
+  for (uint32_t row = blockIdx.x; row < live; row += gridDim.x) {
     const f32x2* stats = a.stats + (uint64_t)row * a.tiles;
     float top = -INFINITY;
     for (uint32_t i = t; i < a.tiles; i += kBlock) top = fmaxf(top, stats[i][0]);
@@ -239,7 +357,7 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
     const uint32_t target = a.target[row], from = a.row_of[row];
     const double d = (double)(a.said[row] - top) * a.inv_temperature;
     const double all = sum + exp(d);
-    if (t == 0) {
+    if (t == 0 && blockIdx.y == 0) {
       const double lp = d == 0.0 ? -log1p(sum) : d - log(all);
       a.logp[from] = (float)lp;
       a.terms[from] = lp * (a.row_weight ? (double)a.row_weight[from] : 1.0);
@@ -247,24 +365,45 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
     if constexpr (KEEP) {
       const float omega = a.omega[row] * kHeld;
       const float unit = (float)((double)omega / all) * (1.0f / kTileExp);
-      for (uint32_t i = t; i < a.tiles; i += kBlock) {
-        const float m = stats[i][0];
-        scale[i] = m == -INFINITY ? 0.0f : unit * __builtin_amdgcn_exp2f((m - top) * a.c);
-      }
-      __syncthreads();
       const float other = -(float)((double)omega * (sum / all));  // at the target: p - 1, without cancellation
       uint16_t* held = a.held + (uint64_t)row * a.padded;
-      for (uint32_t v = t; v < a.padded / 8; v += kBlock) {
-        const Vec<ZERO_F16>::Raw e = load8<ZERO_F16>(held, (uint64_t)v * 8);
-        const float f = scale[v / 32];
-        float x[8];
+      for (uint32_t first = tile0; first < tile1; first += kPartTiles) {
+        const uint32_t end = min(first + kPartTiles, tile1);
+        __syncthreads();
+        for (uint32_t i = t; i < end - first; i += kBlock) {
+          const float m = stats[first + i][0];
+          scale[i] = m == -INFINITY ? 0.0f : unit * __builtin_amdgcn_exp2f((m - top) * a.c);
+        }
+        __syncthreads();
+        const uint32_t v0 = (first << a.shift) / 8, v1 = min(end << a.shift, a.padded) / 8;
+#pragma unroll 4
+        for (uint32_t v = v0 + t; v < v1; v += kBlock) {
+          const Vec<ZERO_F16>::Raw e = load8<ZERO_F16>(held, (uint64_t)v * 8);
+          const float f = scale[(v - v0) >> (a.shift - 3)];
+          float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = v * 8 + k == target ? other : Vec<ZERO_F16>::get(e, k) * f;
-        store8<DT>(held, (uint64_t)v * 8, x);
+          for (int k = 0; k < 8; ++k) x[k] = v * 8 + k == target ? other : Vec<ZERO_F16>::get(e, k) * f;
+          store8<DT>(held, (uint64_t)v * 8, x);
+        }
       }
-      __syncthreads();
     }
   }
+  if (!a.stats_out || blockIdx.y != 0) return;
+  // few rows: a block to each, and one at least; the last one adds up
+  if (t == 0) {
+    __threadfence();
+    rank = atomicAdd(&a.meta->done, 1u);
+  }
+  __syncthreads();
+  if (rank + 1 != gridDim.x) return;
+  __threadfence();
+  loss_of(a.terms, a.counts, a.rows, a.inv_divisor, part, a.stats_out);
+}
+
+__global__ void __launch_bounds__(kBlock) loss_kernel(const double* terms, const uint8_t* counts, uint64_t n, double inv_divisor,
+                                                      float* stats) {
+  __shared__ double part[kWavesPerBlock];
+  loss_of(terms, counts, n, inv_divisor, part, stats);
 }
 
 // ---------------------------------------------------------------------------
@@ -273,28 +412,57 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
 template <int DT>
 __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t live = a.meta->live, mt = (live + 255) / 256, nt = (a.dim + 255) / 256;
-  if (blockIdx.x >= mt * nt) return;
-  uint32_t tm, tn;
-  tile_of(blockIdx.x, mt, nt, &tm, &tn);
-  Rows p;
-  Columns q;
-  p.begin(a.held, (uint64_t)tm * 256, live, a.padded, a.padded);
-  q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, a.vocab);
-  Acc acc;
-  gemm_tile<DT>(p, q, 0, a.vocab, (lds_char*)lds, acc);
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  const uint32_t live = a.meta->live, splits = a.meta->splits, mt = (live + 255) / 256, nt = (a.dim + 255) / 256;
+  const uint32_t steps = (a.vocab + 63) / 64, per = (steps + splits - 1) / splits;
+  for (uint32_t b = blockIdx.x; b < mt * nt * splits; b += gridDim.x) {
+    const uint32_t split = b / (mt * nt);
+    uint32_t tm, tn;
+    tile_of(b % (mt * nt), mt, nt, &tm, &tn);
+    Rows p;
+    Columns q;
+    p.begin(a.held, (uint64_t)tm * 256, live, a.padded, a.padded);
+    q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, a.vocab);
+    Acc acc;
+    __syncthreads();
+    gemm_tile<DT>(p, q, split * per * 64, min((split + 1) * per * 64, a.vocab), (lds_char*)lds, acc);
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+    const float f = a.meta->factor;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
+      if (row >= live) continue;
+      const uint64_t at = a.row_of[row] * a.dhidden_stride;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t n = n0 + 16 * j;
+        if (n >= a.dim) continue;
+        if (splits > 1) {
+          *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
+        } else {
+          const f32x4 x = acc[i][j] * f;
+          store4<DT>(a.dhidden, at + n, x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+  }
+}
+
+// dhidden from the sums over parts of the vocabulary, in their order.
+template <int DT>
+__global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
+  const uint32_t live = a.meta->live, splits = a.meta->splits;
+  if (splits <= 1) return;
   const float f = a.meta->factor;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
-    if (row >= live) continue;
+  for (uint32_t row = blockIdx.x; row < live; row += gridDim.x) {
     const uint64_t at = a.row_of[row] * a.dhidden_stride;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const f32x4 x = acc[i][j] * f;
-      if (n0 + 16 * j < a.dim) store4<DT>(a.dhidden, at + n0 + 16 * j, x[0], x[1], x[2], x[3]);
+    for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.dim / 4; v += gridDim.y * kBlock) {
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll 8
+      for (uint32_t s = 0; s < splits; ++s)
+        x += *reinterpret_cast<const f32x4*>(a.part + ((uint64_t)s * live + row) * a.dim + v * 4);
+      x *= f;
+      store4<DT>(a.dhidden, at + v * 4, x[0], x[1], x[2], x[3]);
     }
   }
 }
@@ -302,7 +470,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
 template <int DT>
 __global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t live = a.meta->live, mt = a.tiles, nt = (a.dim + 255) / 256;
+  const uint32_t live = a.meta->live, mt = a.padded / 256, nt = (a.dim + 255) / 256;
   uint32_t tm, tn;
   tile_of(blockIdx.x, mt, nt, &tm, &tn);
   Columns p, q;
@@ -330,39 +498,23 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs
   }
 }
 
-// stats[0] = -sum of the rows' terms / divisor, stats[1] = how many rows count;
-// each thread adds a fixed set of rows.
-__global__ void __launch_bounds__(1024) loss_kernel(const double* terms, const uint8_t* counts, uint64_t n, double inv_divisor,
-                                                    float* stats) {
-  __shared__ double part[16];
-  double sum = 0.0, count = 0.0;
-  for (uint64_t i = threadIdx.x; i < n; i += 1024) {
-    sum += terms[i];
-    count += (double)counts[i];
-  }
-  sum = row_sum<16>(sum, part);
-  count = row_sum<16>(count, part);
-  if (threadIdx.x == 0) {
-    stats[0] = (float)(-sum * inv_divisor);
-    stats[1] = (float)count;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kMaxDim = 1u << 15;
 
 struct Space {
-  uint64_t meta, row_of, target, omega, said, terms, counts, kept, held, stats, sum, bytes;
-  uint32_t piece;
+  uint64_t meta, row_of, target, omega, said, terms, counts, kept, held, stats, part, sum, bytes;
+  uint32_t piece, tiles, shift, blocks;  // blocks: most of dhidden's product
 };
 
 // Where the pieces of `piece_rows` rows have their intermediates.
 Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows, bool grad) {
   Space s;
   s.piece = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(n_rows, piece_rows));
-  const uint64_t tiles = (vocab + 255) / 256, p = s.piece;
+  s.shift = s.piece <= kFewRows ? kFewShift : 8;
+  s.tiles = (vocab + (1u << s.shift) - 1) >> s.shift;
+  const uint64_t p = s.piece, padded = (vocab + 255) / 256 * 256;
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
@@ -377,15 +529,23 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.terms = take(n_rows * 8);
   s.counts = take(n_rows);
   s.kept = take(p * dim * 2);
-  s.stats = take(p * tiles * 8);
-  s.held = take(grad ? p * tiles * 512 : 0);
+  s.stats = take(p * s.tiles * 8);
+  s.held = take(grad ? p * padded * 2 : 0);
+  uint64_t part = 0;  // dhidden's parts, for whatever number of rows counts
+  s.blocks = 0;
+  for (uint32_t m = 256; grad && m < p + 256; m += 256) {
+    const uint32_t live = (uint32_t)std::min<uint64_t>(m, p), n = splits_of(live, vocab, dim);
+    if (n > 1) part = std::max(part, (uint64_t)n * live);
+    s.blocks = std::max(s.blocks, m / 256 * ((dim + 255) / 256) * n);
+  }
+  s.part = take(part * dim * 4);
   s.sum = take(grad && n_rows > p ? (uint64_t)vocab * dim * 4 : 0);
   s.bytes = at;
   return s;
 }
 
 int check_shape(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows, const char* who) {
-  if (vocab == 0 || vocab > kMaxTiles * 256) return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^20]", who, vocab);
+  if (vocab == 0 || vocab > 1u << 20) return fail(ZERO_EINVAL, "%s: vocab %u outside [1, 2^20]", who, vocab);
   if (dim == 0 || dim > kMaxDim || dim % 8)
     return fail(ZERO_EINVAL, "%s: dim %u is not a multiple of 8 in [8, %u]", who, dim, kMaxDim);
   if (piece_rows == 0 || piece_rows > 16384) return fail(ZERO_EINVAL, "%s: piece_rows %u outside [1, 16384]", who, piece_rows);
@@ -402,20 +562,28 @@ int check_matrix(const void* p, uint64_t rows, uint32_t dim, uint64_t stride, co
   return ZERO_OK;
 }
 
+template <int DT, bool KEEP>
+void launch_rows(const HeadArgs& a, hipStream_t stream) {
+  if (a.shift == kFewShift) hipLaunchKernelGGL((few_logits_kernel<DT, KEEP>), a.padded / 64, kBlock, 0, stream, a);
+  else
+    hipLaunchKernelGGL((logits_kernel<DT, KEEP>), (a.rows + 255) / 256 * a.tiles, kGemmThreads, kGemmLds, stream, a);
+  // with few rows, parts of them: 1024 blocks, of 2048 columns at least
+  const uint32_t parts = KEEP ? std::min((a.padded + 2047) / 2048, std::max(1024 / a.rows, 1u)) : 1;
+  hipLaunchKernelGGL((softmax_kernel<DT, KEEP>), dim3(a.rows, parts), kBlock, 0, stream, a);
+}
+
 template <int DT>
-void launch_piece(const HeadArgs& a, bool grad, hipStream_t stream) {
-  const uint32_t mt = (a.rows + 255) / 256, nt = (a.dim + 255) / 256;
+void launch_piece(const HeadArgs& a, bool grad, uint32_t blocks, hipStream_t stream) {
+  const uint32_t nt = (a.dim + 255) / 256;
   hipLaunchKernelGGL(prepare_kernel, 1, 1024, 0, stream, a);
   hipLaunchKernelGGL(gather_kernel, a.rows, kBlock, 0, stream, a);
-  if (grad) {
-    hipLaunchKernelGGL((logits_kernel<DT, true>), mt * a.tiles, kGemmThreads, kGemmLds, stream, a);
-    hipLaunchKernelGGL((softmax_kernel<DT, true>), a.rows, kBlock, 0, stream, a);
-    if (a.dhidden) hipLaunchKernelGGL(dhidden_kernel<DT>, mt * nt, kGemmThreads, kGemmLds, stream, a);
-    if (a.dweight) hipLaunchKernelGGL(dweight_kernel<DT>, a.tiles * nt, kGemmThreads, kGemmLds, stream, a);
-  } else {
-    hipLaunchKernelGGL((logits_kernel<DT, false>), mt * a.tiles, kGemmThreads, kGemmLds, stream, a);
-    hipLaunchKernelGGL((softmax_kernel<DT, false>), a.rows, kBlock, 0, stream, a);
+  if (!grad) return launch_rows<DT, false>(a, stream);
+  launch_rows<DT, true>(a, stream);
+  if (a.dhidden) {
+    hipLaunchKernelGGL(dhidden_kernel<DT>, blocks, kGemmThreads, kGemmLds, stream, a);
+    hipLaunchKernelGGL(join_kernel<DT>, dim3(a.rows, (a.dim / 4 + kBlock - 1) / kBlock), kBlock, 0, stream, a);
   }
+  if (a.dweight) hipLaunchKernelGGL(dweight_kernel<DT>, a.padded / 256 * nt, kGemmThreads, kGemmLds, stream, a);
 }
 
 }  // namespace
@@ -471,8 +639,9 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   a.weight_stride = p->weight_stride;
   a.vocab = p->vocab;
   a.dim = p->dim;
-  a.tiles = (p->vocab + 255) / 256;
-  a.padded = a.tiles * 256;
+  a.tiles = s.tiles;
+  a.shift = s.shift;
+  a.padded = (p->vocab + 255) / 256 * 256;
   a.inv_temperature = 1.0 / p->temperature;
   a.coef = p->grad_scale / (p->divisor * p->temperature);
   a.c = (float)(kLog2e / p->temperature);
@@ -487,7 +656,10 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   a.kept = reinterpret_cast<uint16_t*>(ws + s.kept);
   a.stats = reinterpret_cast<f32x2*>(ws + s.stats);
   a.held = reinterpret_cast<uint16_t*>(ws + s.held);
+  a.part = reinterpret_cast<float*>(ws + s.part);
   a.sum = reinterpret_cast<float*>(ws + s.sum);
+  if (p->n_rows > 0 && p->n_rows <= std::min<uint64_t>(kTicketRows, s.piece)) a.stats_out = p->stats;
+  a.inv_divisor = 1.0 / p->divisor;
   double* terms = reinterpret_cast<double*>(ws + s.terms);
   uint8_t* counts = reinterpret_cast<uint8_t*>(ws + s.counts);
   // without rows, one empty piece: dweight is then zero
@@ -504,17 +676,18 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
     a.terms = terms + row;
     a.counts = counts + row;
     if (a.rows > 0) {
-      if (p->dtype == ZERO_F16) launch_piece<ZERO_F16>(a, grad, stream);
-      else launch_piece<ZERO_BF16>(a, grad, stream);
+      if (p->dtype == ZERO_F16) launch_piece<ZERO_F16>(a, grad, s.blocks, stream);
+      else launch_piece<ZERO_BF16>(a, grad, s.blocks, stream);
     } else if (a.dweight) {
       hipLaunchKernelGGL(prepare_kernel, 1, 1024, 0, stream, a);
       const uint32_t nt = (a.dim + 255) / 256;
-      if (p->dtype == ZERO_F16) hipLaunchKernelGGL(dweight_kernel<ZERO_F16>, a.tiles * nt, kGemmThreads, kGemmLds, stream, a);
-      else hipLaunchKernelGGL(dweight_kernel<ZERO_BF16>, a.tiles * nt, kGemmThreads, kGemmLds, stream, a);
+      if (p->dtype == ZERO_F16) hipLaunchKernelGGL(dweight_kernel<ZERO_F16>, a.padded / 256 * nt, kGemmThreads, kGemmLds, stream, a);
+      else hipLaunchKernelGGL(dweight_kernel<ZERO_BF16>, a.padded / 256 * nt, kGemmThreads, kGemmLds, stream, a);
     }
     if ((rc = launch_status(who))) return rc;
     row += a.rows;
   } while (row < p->n_rows);
-  hipLaunchKernelGGL(loss_kernel, 1, 1024, 0, stream, terms, counts, p->n_rows, 1.0 / p->divisor, p->stats);
+  if (a.stats_out) return ZERO_OK;
+  hipLaunchKernelGGL(loss_kernel, 1, kBlock, 0, stream, terms, counts, p->n_rows, a.inv_divisor, p->stats);
   return launch_status(who);
 }
