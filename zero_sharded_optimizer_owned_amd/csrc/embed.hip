@@ -184,12 +184,12 @@ __global__ void __launch_bounds__(kBlock) scatter_kernel(const SortArgs a) {
 // ---------------------------------------------------------------------------
 // Sums over the sorted positions.
 //
-// They are cut into tiles of kTile.  A run of equal tokens that lies within a
+// They are cut into tiles of 8 or 32.  A run of equal tokens that lies within a
 // tile is summed and written there; one that a tile's end cuts leaves partial
 // sums (fp32), the tile's first run in slot 0, its last one in slot 1, which
 // join_kernel adds in the order of the tiles.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kTile = 32;
+constexpr uint32_t kFewTokens = 4096, kFewTile = 8, kTile = 32;
 
 struct GradArgs {
   const uint32_t *keys, *at;  // sorted
@@ -197,30 +197,37 @@ struct GradArgs {
   void* dtable;
   float* partial;  // [tiles][2][vecs * N]
   uint64_t stride;
-  uint32_t n, vocab, dim, vecs;
+  uint32_t n, vocab, dim, vecs, tile;
   float scale;
   bool accumulate;
 };
 
+// dtable's row `key`, vector v of dout's: as it is, in OUT's vectors.
 template <int DT, int OUT>
-__device__ __forceinline__ void write_row(const GradArgs& a, uint32_t key, uint32_t v, const float (&sum)[Lane<DT>::N]) {
-  constexpr int N = Lane<DT>::N;
-  typedef typename Vec<OUT>::T T;
-  T* row = static_cast<T*>(a.dtable) + (uint64_t)key * a.stride;
-  float x[N];
+struct Old {
+  static constexpr int kVecs = DT == OUT ? 1 : 2;  // a 16-bit gradient into an fp32 table: two for one
+  u32x4 q[kVecs];
+  __device__ __forceinline__ void load(const void* row, uint32_t v, uint32_t dim) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) x[k] = sum[k] * a.scale;
-  if constexpr (OUT == DT) {
-    if (a.accumulate) {
-      const u32x4 old = load_cut<OUT>(row, v, a.dim);
+    for (int h = 0; h < kVecs; ++h) q[h] = load_cut<OUT>(row, v * kVecs + h, dim);
+  }
+  __device__ __forceinline__ float get(int k) const { return Lane<OUT>::get(q[k / Lane<OUT>::N], k % Lane<OUT>::N); }
+};
+
+template <int DT, int OUT>
+__device__ __forceinline__ void write_row(const GradArgs& a, uint32_t key, uint32_t v, const float (&sum)[Lane<DT>::N],
+                                          const Old<DT, OUT>& old) {
+  constexpr int M = Lane<OUT>::N;
+  typename Vec<OUT>::T* row = static_cast<typename Vec<OUT>::T*>(a.dtable) + (uint64_t)key * a.stride;
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[k] += Lane<OUT>::get(old, k);
+  for (int h = 0; h < Old<DT, OUT>::kVecs; ++h) {
+    float x[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+      x[k] = sum[h * M + k] * a.scale;
+      if (a.accumulate) x[k] += old.get(h * M + k);
     }
-    store_cut<OUT>(row, v, a.dim, x);
-  } else {  // a 16-bit gradient into an fp32 table
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (v * N + k < a.dim) row[v * N + k] = a.accumulate ? row[v * N + k] + x[k] : x[k];
+    store_cut<OUT>(row, v * Old<DT, OUT>::kVecs + h, a.dim, x);
   }
 }
 
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(kBlock) sum_kernel(const GradArgs a) {
   constexpr int N = Lane<DT>::N;
   typedef typename Vec<DT>::T T;
   __shared__ uint32_t key[kTile + 2], at[kTile];
-  const uint32_t begin = blockIdx.x * kTile, end = min(begin + kTile, a.n), n = end - begin;
+  const uint32_t begin = blockIdx.x * a.tile, end = min(begin + a.tile, a.n), n = end - begin;
   // key[0] and key[n + 1]: the neighbours' (a number that no key has, at the ends)
   for (uint32_t i = threadIdx.x; i < n + 2; i += kBlock) {
     const int64_t p = (int64_t)begin + i - 1;
@@ -240,14 +247,19 @@ __global__ void __launch_bounds__(kBlock) sum_kernel(const GradArgs a) {
   for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.vecs; v += gridDim.y * kBlock) {
     float sum[N] = {};
     bool cut = key[0] == key[1];  // the run at hand began in an earlier tile
-    constexpr uint32_t B = 8;     // rows in flight
+    constexpr uint32_t B = 8;     // rows in flight, and the rows they are added to
     for (uint32_t i0 = 0; i0 < n; i0 += B) {
       u32x4 r[B];
+      Old<DT, OUT> old[B];
 #pragma unroll
       for (uint32_t j = 0; j < B; ++j) {
+        const uint32_t i = i0 + j;
         r[j] = u32x4{0, 0, 0, 0};
-        if (i0 + j < n && key[i0 + j + 1] < a.vocab)
-          r[j] = load_cut<DT>(static_cast<const T*>(a.dout) + (uint64_t)at[i0 + j] * a.dim, v, a.dim);
+        if (i < n && key[i + 1] < a.vocab) {
+          r[j] = load_cut<DT>(static_cast<const T*>(a.dout) + (uint64_t)at[i] * a.dim, v, a.dim);
+          if (a.accumulate && key[i + 2] != key[i + 1])
+            old[j].load(static_cast<typename Vec<OUT>::T*>(a.dtable) + (uint64_t)key[i + 1] * a.stride, v, a.dim);
+        }
       }
 #pragma unroll
       for (uint32_t j = 0; j < B; ++j) {
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kBlock) sum_kernel(const GradArgs a) {
 #pragma unroll
         for (int k = 0; k < N; ++k) sum[k] += Lane<DT>::get(r[j], k);
         const bool last = key[i + 2] != k0;
-        if (last && !cut) write_row<DT, OUT>(a, k0, v, sum);
+        if (last && !cut) write_row<DT, OUT>(a, k0, v, sum, old[j]);
         else if (last || i + 1 == n) {
           f32x4* to = reinterpret_cast<f32x4*>(a.partial + (((uint64_t)blockIdx.x * 2 + (cut ? 0 : 1)) * a.vecs + v) * N);
 #pragma unroll
@@ -274,48 +286,6 @@ __global__ void __launch_bounds__(kBlock) sum_kernel(const GradArgs a) {
   }
 }
 
-// Tile b's last run, where it began in the tile and goes on behind it.
-template <int DT, int OUT>
-__global__ void __launch_bounds__(kBlock) join_kernel(const GradArgs a) {
-  constexpr int N = Lane<DT>::N;
-  const uint32_t begin = blockIdx.x * kTile, end = begin + kTile;
-  if (end >= a.n) return;
-  const uint32_t key = a.keys[end - 1];
-  if (key >= a.vocab || a.keys[end] != key) return;           // ends here
-  if (begin > 0 && a.keys[begin - 1] == key) return;  // began earlier
-  // the run's last tile: the first whose last key is another one
-  uint32_t last = blockIdx.x + 1;
-  while ((uint64_t)(last + 1) * kTile <= a.n && a.keys[(last + 1) * kTile - 1] == key &&
-         (uint64_t)(last + 1) * kTile < a.n && a.keys[(last + 1) * kTile] == key)
-    ++last;
-  for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.vecs; v += gridDim.y * kBlock) {
-    float sum[N];
-    const auto part = [&](uint32_t tile, uint32_t slot, int k) {
-      return reinterpret_cast<const f32x4*>(a.partial + (((uint64_t)tile * 2 + slot) * a.vecs + v) * N)[k];
-    };
-#pragma unroll
-    for (int k = 0; k < N / 4; ++k) {
-      const f32x4 p = part(blockIdx.x, 1, k);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[4 * k + j] = p[j];
-    }
-#pragma unroll 8
-    for (uint32_t b = blockIdx.x + 1; b <= last; ++b) {
-#pragma unroll
-      for (int k = 0; k < N / 4; ++k) {
-        const f32x4 p = part(b, 0, k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[4 * k + j] += p[j];
-      }
-    }
-    write_row<DT, OUT>(a, key, v, sum);
-  }
-}
-
-// The rows of the table that no token names are zero.  A block takes kFillRows
-// of them and finds the sorted keys of that range by bisection, 64 probes at a time.
-constexpr uint32_t kFillRows = 16;
-
 // The first position in [lo, hi] whose key is at least x (hi: none), for a whole wavefront.
 __device__ __forceinline__ uint32_t first_at_least(const uint32_t* keys, uint32_t lo, uint32_t hi, uint32_t x) {
   const uint32_t lane = threadIdx.x & 63;
@@ -328,6 +298,59 @@ __device__ __forceinline__ uint32_t first_at_least(const uint32_t* keys, uint32_
   }
   return lo;
 }
+
+// Tile b's last run, where it began in the tile and goes on behind it.
+template <int DT, int OUT>
+__global__ void __launch_bounds__(kBlock) join_kernel(const GradArgs a) {
+  constexpr int N = Lane<DT>::N;
+  const uint32_t begin = blockIdx.x * a.tile, end = begin + a.tile;
+  if (end >= a.n) return;
+  const uint32_t key = a.keys[end - 1];
+  if (key >= a.vocab || a.keys[end] != key) return;   // ends here
+  if (begin > 0 && a.keys[begin - 1] == key) return;  // began earlier
+  const uint32_t last = (first_at_least(a.keys, end, a.n, key + 1) - 1) / a.tile;  // the run's last tile
+  for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.vecs; v += gridDim.y * kBlock) {
+    float sum[N];
+    Old<DT, OUT> old;
+    if (a.accumulate)
+      old.load(static_cast<typename Vec<OUT>::T*>(a.dtable) + (uint64_t)key * a.stride, v, a.dim);
+    const auto part = [&](uint32_t tile, uint32_t slot, int k) {
+      return reinterpret_cast<const f32x4*>(a.partial + (((uint64_t)tile * 2 + slot) * a.vecs + v) * N)[k];
+    };
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+      const f32x4 p = part(blockIdx.x, 1, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[4 * k + j] = p[j];
+    }
+    uint32_t b = blockIdx.x + 1;
+    constexpr uint32_t B = 8;  // partial rows in flight
+    for (; b + B <= last + 1; b += B) {
+      f32x4 p[B][N / 4];
+#pragma unroll
+      for (uint32_t i = 0; i < B; ++i)
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) p[i][k] = part(b + i, 0, k);
+#pragma unroll
+      for (uint32_t i = 0; i < B; ++i)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] += p[i][k / 4][k % 4];
+    }
+    for (; b <= last; ++b) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const f32x4 p = part(b, 0, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[4 * k + j] += p[j];
+      }
+    }
+    write_row<DT, OUT>(a, key, v, sum, old);
+  }
+}
+
+// The rows of the table that no token names are zero.  A block takes kFillRows
+// of them and finds the sorted keys of that range by bisection, 64 probes at a time.
+constexpr uint32_t kFillRows = 16;
 
 template <int OUT, bool NT>
 __global__ void __launch_bounds__(kBlock) fill_kernel(const GradArgs a, uint32_t vecs) {
@@ -364,6 +387,144 @@ __global__ void __launch_bounds__(kBlock) fill_kernel(const GradArgs a, uint32_t
 }
 
 // ---------------------------------------------------------------------------
+// All of it in one launch, for up to kOneSort tokens: block 0 sorts in LDS, by
+// the same steps with 16 wavefronts, and the others meanwhile write the zeros.
+// A block of those goes over all tokens for the rows of its own that are named.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kOneSort = 16384, kOneThreads = 1024, kOneWaves = 16, kOneRounds = kOneSort / kOneThreads;
+constexpr uint32_t kMapRows = 1u << 16;
+
+struct OneArgs {
+  const int64_t* tokens;
+  uint32_t *keys, *at;  // sorted
+  uint32_t n, vocab, bits, passes;
+  void* dtable;  // of the zeros
+  uint64_t stride;
+  uint32_t dim, vecs, shift;  // 1 << shift lanes to a row
+};
+
+__device__ __forceinline__ void sort_in_lds(const OneArgs& a, uint32_t* keys, uint16_t* at, uint16_t (*count)[kDigits],
+                                            uint32_t* sums) {
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const uint32_t rounds = (a.n + kOneThreads - 1) / kOneThreads, begin = wave * rounds * 64 + lane;
+  for (uint32_t pass = 0, done = 0; pass < a.passes; ++pass) {
+    const uint32_t bits = (a.bits - done + a.passes - pass - 1) / (a.passes - pass), digits = 1u << bits;
+    uint32_t key[kOneRounds], from[kOneRounds], rank[kOneRounds];
+#pragma unroll
+    for (uint32_t r = 0; r < kOneRounds; ++r) {
+      const uint32_t i = begin + r * 64;
+      key[r] = from[r] = 0;
+      if (r < rounds && i < a.n) {
+        if (pass == 0) {
+          const int64_t token = a.tokens[i];
+          key[r] = token >= 0 && token < (int64_t)a.vocab ? (uint32_t)token : a.vocab;
+          from[r] = i;
+        } else {
+          key[r] = keys[i];
+          from[r] = at[i];
+        }
+      }
+    }
+    for (uint32_t i = t; i < kOneWaves * kDigits / 2; i += kOneThreads) reinterpret_cast<uint32_t*>(count)[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t r = 0; r < kOneRounds; ++r) {
+      if (r < rounds) {
+        const bool has = begin + r * 64 < a.n;
+        const uint32_t d = key[r] >> done & (digits - 1);
+        uint64_t same = __ballot(has);
+        for (uint32_t b = 0; b < bits; ++b) {
+          const uint64_t one = __ballot(d >> b & 1);
+          same &= (d >> b & 1) ? one : ~one;
+        }
+        const uint32_t before = __popcll(same & ((1ull << lane) - 1));
+        const uint32_t seen = count[wave][d];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (has && before == 0) count[wave][d] = (uint16_t)(seen + __popcll(same));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        rank[r] = seen + before;
+      }
+    }
+    __syncthreads();
+    // thread 2 d + h: digit d, wavefronts 8 h .. 8 h + 7
+    const uint32_t d = t / 2, w0 = t % 2 * 8;
+    uint32_t sum = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < 8; ++w) sum += count[w0 + w][d];
+    const uint32_t own = sum;
+#pragma unroll
+    for (uint32_t s = 1; s < 64; s <<= 1) {
+      const uint32_t up = __shfl_up(sum, s, 64);
+      if (lane >= s) sum += up;
+    }
+    if (lane == 63) sums[wave] = sum;
+    __syncthreads();
+    uint32_t to = sum - own;
+    for (uint32_t w = 0; w < wave; ++w) to += sums[w];
+#pragma unroll
+    for (uint32_t w = 0; w < 8; ++w) {
+      const uint32_t c = count[w0 + w][d];
+      count[w0 + w][d] = (uint16_t)to;
+      to += c;
+    }
+    __syncthreads();
+    const bool last = pass + 1 == a.passes;
+#pragma unroll
+    for (uint32_t r = 0; r < kOneRounds; ++r) {
+      if (r < rounds && begin + r * 64 < a.n) {
+        const uint32_t p = count[wave][key[r] >> done & (digits - 1)] + rank[r];
+        if (last) {
+          a.keys[p] = key[r];
+          a.at[p] = from[r];
+        } else {
+          keys[p] = key[r];
+          at[p] = (uint16_t)from[r];
+        }
+      }
+    }
+    __syncthreads();
+    done += bits;
+  }
+}
+
+template <int OUT, bool NT>
+__global__ void __launch_bounds__(kOneThreads) one_sort_kernel(const OneArgs a) {
+  typedef typename Vec<OUT>::T T;
+  __shared__ uint32_t keys[kOneSort];
+  __shared__ uint16_t at[kOneSort], count[kOneWaves][kDigits];
+  __shared__ uint32_t sums[kOneWaves];
+  if (blockIdx.x == 0) {
+    sort_in_lds(a, keys, at, count, sums);
+    return;
+  }
+  const uint32_t t = threadIdx.x, blocks = gridDim.x - 1;
+  const uint32_t per = (uint32_t)(((uint64_t)a.vocab + blocks - 1) / blocks);
+  const uint64_t begin = (uint64_t)(blockIdx.x - 1) * per, end = min(begin + per, (uint64_t)a.vocab);
+  uint32_t* named = keys;  // one bit to a row
+  const float zero[Lane<OUT>::N] = {};
+  for (uint64_t row0 = begin; row0 < end; row0 += kMapRows) {
+    const uint32_t rows = (uint32_t)min((uint64_t)kMapRows, end - row0);
+    __syncthreads();
+    for (uint32_t i = t; i < (rows + 31) / 32; i += kOneThreads) named[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = t; i < a.n; i += kOneThreads) {
+      const uint64_t r = (uint64_t)a.tokens[i] - row0;
+      if (r < rows) atomicOr(&named[r / 32], 1u << (r % 32));
+    }
+    __syncthreads();
+    const uint32_t lanes = 1u << a.shift;
+    for (uint32_t r = t >> a.shift; r < rows; r += kOneThreads >> a.shift) {
+      if (named[r / 32] >> (r % 32) & 1) continue;
+      T* row = static_cast<T*>(a.dtable) + (row0 + r) * a.stride;
+      for (uint32_t v = t & (lanes - 1); v < a.vecs; v += lanes) store_cut<OUT, NT>(row, v, a.dim, zero);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kMaxDim = 1u << 20;
@@ -373,12 +534,13 @@ uint64_t up256(uint64_t n) { return (n + 255) / 256 * 256; }
 // Workspace: two copies of (keys, positions), the histogram, the partial sums.
 struct Space {
   uint64_t keys[2], at[2], hist, partial, bytes;
-  uint32_t blocks, tiles, row;  // row: floats of a partial row
+  uint32_t blocks, tile, tiles, row;  // row: floats of a partial row
 };
 Space space_of(uint64_t n, uint32_t dim) {
   Space s;
   s.blocks = (uint32_t)((n + kSortKeys - 1) / kSortKeys);
-  s.tiles = (uint32_t)((n + kTile - 1) / kTile);
+  s.tile = n <= kFewTokens ? kFewTile : kTile;
+  s.tiles = (uint32_t)((n + s.tile - 1) / s.tile);
   s.row = (dim + 7) / 8 * 8;
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes) {
@@ -487,39 +649,56 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
   g.dim = p->dim;
   g.scale = (float)p->scale;
   g.accumulate = p->accumulate != 0;
+  g.tile = s.tile;
+  const bool nt = past_cache((uint64_t)p->vocab * p->dim * dtype_bytes(p->table_dtype));
+  const bool one = g.n > 0 && g.n <= kOneSort;
   if (g.n > 0) {
     // keys are 0 .. vocab: passes of equal width, 9 bits at most
     uint32_t bits = 1;
     while (bits < 32 && p->vocab >> bits) ++bits;
     const uint32_t passes = (bits + kMaxBits - 1) / kMaxBits;
-    SortArgs a = {p->tokens, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<uint32_t*>(ws + s.hist),
-                  g.n, p->vocab, s.blocks, 0, 0};
-    for (uint32_t i = 0, done = 0; i < passes; ++i) {
-      a.shift = done;
-      a.bits = (bits - done + passes - i - 1) / (passes - i);
-      done += a.bits;
-      a.keys_out = reinterpret_cast<uint32_t*>(ws + s.keys[i & 1]);
-      a.at_out = reinterpret_cast<uint32_t*>(ws + s.at[i & 1]);
-      hipLaunchKernelGGL(histogram_kernel, s.blocks, kBlock, 0, stream, a);
-      hipLaunchKernelGGL(scatter_kernel, s.blocks, kBlock, 0, stream, a);
-      a.tokens = nullptr;
-      a.keys = a.keys_out;
-      a.at = a.at_out;
+    uint32_t* const keys[2] = {reinterpret_cast<uint32_t*>(ws + s.keys[0]), reinterpret_cast<uint32_t*>(ws + s.keys[1])};
+    uint32_t* const at[2] = {reinterpret_cast<uint32_t*>(ws + s.at[0]), reinterpret_cast<uint32_t*>(ws + s.at[1])};
+    if (one) {
+      with_dtype(p->table_dtype, [&](auto dt) {
+        constexpr int OUT = decltype(dt)::value;
+        const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
+        OneArgs a = {p->tokens, keys[0], at[0], g.n, p->vocab, bits, passes, p->dtable, p->stride, p->dim, vecs, 0};
+        while ((1u << a.shift) < vecs && a.shift < 6) ++a.shift;
+        const uint32_t grid = g.accumulate ? 1 : 1 + std::min(p->vocab, 255u);
+        if (nt) hipLaunchKernelGGL((one_sort_kernel<OUT, true>), grid, kOneThreads, 0, stream, a);
+        else hipLaunchKernelGGL((one_sort_kernel<OUT, false>), grid, kOneThreads, 0, stream, a);
+      });
+      g.keys = keys[0];
+      g.at = at[0];
+    } else {
+      SortArgs a = {p->tokens, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<uint32_t*>(ws + s.hist),
+                    g.n, p->vocab, s.blocks, 0, 0};
+      for (uint32_t i = 0, done = 0; i < passes; ++i) {
+        a.shift = done;
+        a.bits = (bits - done + passes - i - 1) / (passes - i);
+        done += a.bits;
+        a.keys_out = keys[i & 1];
+        a.at_out = at[i & 1];
+        hipLaunchKernelGGL(histogram_kernel, s.blocks, kBlock, 0, stream, a);
+        hipLaunchKernelGGL(scatter_kernel, s.blocks, kBlock, 0, stream, a);
+        a.tokens = nullptr;
+        a.keys = a.keys_out;
+        a.at = a.at_out;
+      }
+      g.keys = a.keys;
+      g.at = a.at;
     }
     if ((rc = launch_status(who))) return rc;
-    g.keys = a.keys;
-    g.at = a.at;
     g.partial = reinterpret_cast<float*>(ws + s.partial);
   }
-  if (!g.accumulate) {
+  if (!g.accumulate && !one) {
     const uint32_t grid = (uint32_t)std::min<uint64_t>((p->vocab + kFillRows - 1) / kFillRows, 1u << 20);
     with_dtype(p->table_dtype, [&](auto dt) {
       constexpr int OUT = decltype(dt)::value;
       const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
-      if (past_cache((uint64_t)p->vocab * p->dim * dtype_bytes(p->table_dtype)))
-        hipLaunchKernelGGL((fill_kernel<OUT, true>), grid, kBlock, 0, stream, g, vecs);
-      else
-        hipLaunchKernelGGL((fill_kernel<OUT, false>), grid, kBlock, 0, stream, g, vecs);
+      if (nt) hipLaunchKernelGGL((fill_kernel<OUT, true>), grid, kBlock, 0, stream, g, vecs);
+      else hipLaunchKernelGGL((fill_kernel<OUT, false>), grid, kBlock, 0, stream, g, vecs);
     });
     if ((rc = launch_status(who))) return rc;
   }

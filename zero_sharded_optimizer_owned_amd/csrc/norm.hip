@@ -295,27 +295,31 @@ __global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const Back
   }
 }
 
-// dgain[d] = sum of the partial rows, in their order within 8 groups of them.
-constexpr int kFoldColumns = 32;
+// dgain[d] = sum of the partial rows: a block takes 32 columns, each of its 32
+// groups of lanes every 32nd row.
+constexpr int kFoldColumns = 32, kFoldGroups = 32;
 __device__ __forceinline__ void store_any(int dtype, void* p, uint64_t e, float x) {
   if (dtype == ZERO_F16) Vec<ZERO_F16>::store1(p, e, x);
   else if (dtype == ZERO_BF16) Vec<ZERO_BF16>::store1(p, e, x);
   else Vec<ZERO_F32>::store1(p, e, x);
 }
-__global__ void __launch_bounds__(kBlock) fold_kernel(const float* partial, uint32_t n, uint32_t dim, void* dgain, int dtype) {
-  __shared__ double s[kBlock];
+__global__ void __launch_bounds__(kFoldColumns * kFoldGroups) fold_kernel(const float* partial, uint32_t n, uint32_t dim,
+                                                                          void* dgain, int dtype) {
+  __shared__ double s[kFoldGroups][kFoldColumns];
   const uint32_t c = threadIdx.x % kFoldColumns, g = threadIdx.x / kFoldColumns;
   const uint32_t d = blockIdx.x * kFoldColumns + c;
   double sum = 0.0;
-  if (d < dim)
-    for (uint32_t i = g; i < n; i += kBlock / kFoldColumns) sum += (double)partial[(uint64_t)i * dim + d];
-  s[threadIdx.x] = sum;
-  __syncthreads();
-  if (g == 0 && d < dim) {
-#pragma unroll
-    for (uint32_t i = 1; i < kBlock / kFoldColumns; ++i) sum += s[i * kFoldColumns + c];
-    store_any(dtype, dgain, d, (float)sum);
+  if (d < dim) {
+#pragma unroll 8
+    for (uint32_t i = g; i < n; i += kFoldGroups) sum += (double)partial[(uint64_t)i * dim + d];
   }
+  s[g][c] = sum;
+  __syncthreads();
+  for (uint32_t half = kFoldGroups / 2; half > 0; half /= 2) {
+    if (g < half) s[g][c] += s[g + half][c];
+    __syncthreads();
+  }
+  if (g == 0 && d < dim) store_any(dtype, dgain, d, (float)s[0][c]);
 }
 
 // ---------------------------------------------------------------------------
@@ -328,10 +332,10 @@ void by_width(uint32_t dim, F fn) {
   const auto go = [&](auto w, auto v) { fn(w, v); };
   if (vecs <= 64) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
   else if (vecs <= 128) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
-  else if (vecs <= 256) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-  else if (vecs <= 512) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
+  else if (vecs <= 256) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
+  else if (vecs <= 512) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   else if (vecs <= 1024) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
-  else if (vecs <= 2048) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{});
+  else if (vecs <= 2048) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
   else if constexpr (DT == ZERO_F32) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
 }
 
@@ -344,9 +348,9 @@ int check_rows(uint64_t n_rows, uint32_t dim, int dtype, const char* who) {
 
 uint32_t scales_of(uint32_t dim) { return (dim + ZERO_QBLOCK - 1) / ZERO_QBLOCK; }
 
-// Blocks of the backward pass: two to a CU, so that each partial row stands for
+// Blocks of the backward pass, so that each partial row stands for
 // many rows and the fold stays short.
-constexpr uint64_t kBackwardBlocks = 512;
+constexpr uint64_t kBackwardBlocks = 1024;
 
 }  // namespace
 }  // namespace zs
@@ -467,7 +471,8 @@ extern "C" int zero_rms_norm_backward(const zero_rms_norm_backward_args* p, hipS
     });
     if ((rc = launch_status(who))) return rc;
   }
-  hipLaunchKernelGGL(fold_kernel, (p->dim + kFoldColumns - 1) / kFoldColumns, kBlock, 0, stream,
+  hipLaunchKernelGGL(fold_kernel, (p->dim + kFoldColumns - 1) / kFoldColumns, kFoldColumns * kFoldGroups, 0,
+                     stream,
                      static_cast<const float*>(p->workspace), parts, p->dim, p->dgain, p->dtype);
   return launch_status(who);
 }
