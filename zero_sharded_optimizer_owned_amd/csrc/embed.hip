@@ -499,26 +499,32 @@ __global__ void __launch_bounds__(kOneThreads) one_sort_kernel(const OneArgs a) 
     sort_in_lds(a, keys, at, count, sums);
     return;
   }
-  const uint32_t t = threadIdx.x, blocks = gridDim.x - 1;
-  const uint32_t per = (uint32_t)(((uint64_t)a.vocab + blocks - 1) / blocks);
-  const uint64_t begin = (uint64_t)(blockIdx.x - 1) * per, end = min(begin + per, (uint64_t)a.vocab);
+  // unit by unit in turn, a unit being the rows that the block writes at a time
+  const uint32_t t = threadIdx.x, blocks = gridDim.x - 1, b = blockIdx.x - 1, lanes = 1u << a.shift;
+  const uint32_t unit = kOneThreads >> a.shift, units = kMapRows / unit;
   uint32_t* named = keys;  // one bit to a row
   const float zero[Lane<OUT>::N] = {};
-  for (uint64_t row0 = begin; row0 < end; row0 += kMapRows) {
-    const uint32_t rows = (uint32_t)min((uint64_t)kMapRows, end - row0);
+  const uint64_t all = ((uint64_t)a.vocab + unit - 1) / unit;
+  for (uint64_t first = b; first < all; first += (uint64_t)blocks * units) {
+    const uint32_t n = (uint32_t)min((all - first + blocks - 1) / blocks, (uint64_t)units);  // units of this round
     __syncthreads();
-    for (uint32_t i = t; i < (rows + 31) / 32; i += kOneThreads) named[i] = 0;
+    for (uint32_t i = t; i < (n * unit + 31) / 32; i += kOneThreads) named[i] = 0;
     __syncthreads();
 #pragma unroll 4
     for (uint32_t i = t; i < a.n; i += kOneThreads) {
-      const uint64_t r = (uint64_t)a.tokens[i] - row0;
-      if (r < rows) atomicOr(&named[r / 32], 1u << (r % 32));
+      const int64_t token = a.tokens[i];
+      if (token < 0 || token >= (int64_t)a.vocab) continue;
+      const uint32_t u = (uint32_t)token / unit, turn = u / blocks;
+      if (u % blocks != b || u < first || (turn - (uint32_t)first / blocks) >= n) continue;
+      const uint32_t bit = (turn - (uint32_t)first / blocks) * unit + (uint32_t)token % unit;
+      atomicOr(&named[bit / 32], 1u << (bit % 32));
     }
     __syncthreads();
-    const uint32_t lanes = 1u << a.shift;
-    for (uint32_t r = t >> a.shift; r < rows; r += kOneThreads >> a.shift) {
-      if (named[r / 32] >> (r % 32) & 1) continue;
-      T* row = static_cast<T*>(a.dtable) + (row0 + r) * a.stride;
+    for (uint32_t i = 0; i < n; ++i) {
+      const uint32_t in = t >> a.shift, bit = i * unit + in;
+      const uint64_t r = (first + (uint64_t)i * blocks) * unit + in;
+      if (r >= a.vocab || (named[bit / 32] >> (bit % 32) & 1)) continue;
+      T* row = static_cast<T*>(a.dtable) + r * a.stride;
       for (uint32_t v = t & (lanes - 1); v < a.vecs; v += lanes) store_cut<OUT, NT>(row, v, a.dim, zero);
     }
   }
@@ -665,7 +671,7 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
         const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
         OneArgs a = {p->tokens, keys[0], at[0], g.n, p->vocab, bits, passes, p->dtable, p->stride, p->dim, vecs, 0};
         while ((1u << a.shift) < vecs && a.shift < 6) ++a.shift;
-        const uint32_t grid = g.accumulate ? 1 : 1 + std::min(p->vocab, 255u);
+        const uint32_t grid = g.accumulate ? 1 : 256u;
         if (nt) hipLaunchKernelGGL((one_sort_kernel<OUT, true>), grid, kOneThreads, 0, stream, a);
         else hipLaunchKernelGGL((one_sort_kernel<OUT, false>), grid, kOneThreads, 0, stream, a);
       });

@@ -302,41 +302,45 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
 }
 
 // The same for up to 16 rows, bound by the reading of the weights: a wavefront
-// takes 16 columns and reads their weights straight into registers, 16 bytes
-// to a lane, kFewSteps steps of 32 k in flight; the rows' hidden states come
-// from the caches.  Tiles are 64 columns, so that a vocabulary of 32,000 makes
-// 500 blocks.
-constexpr uint32_t kFewRows = 16, kFewShift = 6;
-constexpr int kFewSteps = 8;
+// reads the weights of 16 columns straight into registers, 16 bytes to a lane,
+// kFewSteps steps of 32 k in flight; the rows' hidden states come from the
+// caches.  The four wavefronts of a block take turns along k.
+constexpr uint32_t kFewRows = 16, kFewShift = 4;
+constexpr int kFewSteps = 4;
 
 template <int DT, bool KEEP>
 __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
-  __shared__ float red[2][kWavesPerBlock][16];
+  __shared__ f32x4 share[kWavesPerBlock - 1][64];
   const uint32_t live = a.meta->live, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (live == 0) return;
-  const uint32_t tn = blockIdx.x, column = tn * 64 + wave * 16, row = lane % 16, k0 = lane / 16 * 8;
+  const uint32_t tn = blockIdx.x, column = tn * 16, row = lane % 16, k0 = lane / 16 * 8;
   const bool has = row < live, in = column + lane % 16 < a.vocab;
   const uint16_t* w = static_cast<const uint16_t*>(a.weight) + (uint64_t)(in ? column + lane % 16 : 0) * a.weight_stride + k0;
   const uint16_t* h = a.kept + (uint64_t)(has ? row : 0) * a.dim + k0;
   f32x4 acc = {0, 0, 0, 0};
-  uint32_t k = 0;
-  for (; k + 32 * kFewSteps <= a.dim; k += 32 * kFewSteps) {
+  for (uint32_t k = wave * 32 * kFewSteps; k < a.dim; k += kWavesPerBlock * 32 * kFewSteps) {
     u32x4 x[kFewSteps], y[kFewSteps];
+    if (k + 32 * kFewSteps <= a.dim) {
 #pragma unroll
-    for (int i = 0; i < kFewSteps; ++i) x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + k + 32 * i));
+      for (int i = 0; i < kFewSteps; ++i) x[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w + k + 32 * i));
 #pragma unroll
-    for (int i = 0; i < kFewSteps; ++i) y[i] = has ? *reinterpret_cast<const u32x4*>(h + k + 32 * i) : u32x4{0, 0, 0, 0};
+      for (int i = 0; i < kFewSteps; ++i) y[i] = has ? *reinterpret_cast<const u32x4*>(h + k + 32 * i) : u32x4{0, 0, 0, 0};
+    } else {
+#pragma unroll
+      for (int i = 0; i < kFewSteps; ++i) {
+        const bool on = k + k0 + 32 * i < a.dim;
+        x[i] = on ? *reinterpret_cast<const u32x4*>(w + k + 32 * i) : u32x4{0, 0, 0, 0};
+        y[i] = on && has ? *reinterpret_cast<const u32x4*>(h + k + 32 * i) : u32x4{0, 0, 0, 0};
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kFewSteps; ++i) acc = mfma16<DT>(x[i], y[i], acc);
   }
-  for (; k < a.dim; k += 32) {
-    u32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-    if (k + k0 < a.dim) {
-      x = *reinterpret_cast<const u32x4*>(w + k);
-      if (has) y = *reinterpret_cast<const u32x4*>(h + k);
-    }
-    acc = mfma16<DT>(x, y, acc);
-  }
+  if (wave > 0) share[wave - 1][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int i = 0; i < kWavesPerBlock - 1; ++i) acc += share[i][lane];
   // acc[x]: column + 4 (lane / 16) + x of row lane % 16
   const uint32_t n0 = column + lane / 16 * 4;
   float top = -INFINITY;
@@ -345,10 +349,6 @@ __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
     if (n0 + x < a.vocab) top = fmaxf(top, acc[x]);
   top = fmaxf(top, __shfl_xor(top, 16, 64));
   top = fmaxf(top, __shfl_xor(top, 32, 64));
-  if (lane < 16) red[0][wave][lane] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWavesPerBlock; ++i) top = fmaxf(top, red[0][i][row]);
   const float m = top == -INFINITY ? 0.0f : top;
   const uint32_t target = has ? a.target[row] : 0xFFFFFFFFu;
   float sum = 0.0f, e[4];
@@ -363,14 +363,8 @@ __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
                      e[3] * kTileExp);
   sum += __shfl_xor(sum, 16, 64);
   sum += __shfl_xor(sum, 32, 64);
-  if (lane < 16) red[1][wave][lane] = sum;
-  __syncthreads();
-  if (threadIdx.x < live && tn < a.tiles) {  // the blocks behind the vocabulary only store zeros
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWavesPerBlock; ++i) sum += red[1][i][threadIdx.x];
-    a.stats[(uint64_t)threadIdx.x * a.tiles + tn] = f32x2{top, sum};
-  }
+  // the blocks behind the vocabulary only store zeros
+  if (lane < live && lane < 16 && tn < a.tiles) a.stats[(uint64_t)lane * a.tiles + tn] = f32x2{top, sum};
 }
 
 // ---------------------------------------------------------------------------
@@ -634,7 +628,7 @@ int check_matrix(const void* p, uint64_t rows, uint32_t dim, uint64_t stride, co
 
 template <int DT, bool KEEP>
 void launch_rows(const HeadArgs& a, hipStream_t stream) {
-  if (a.shift == kFewShift) hipLaunchKernelGGL((few_logits_kernel<DT, KEEP>), a.padded / 64, kBlock, 0, stream, a);
+  if (a.shift == kFewShift) hipLaunchKernelGGL((few_logits_kernel<DT, KEEP>), a.padded >> kFewShift, kBlock, 0, stream, a);
   else
     hipLaunchKernelGGL((logits_kernel<DT, KEEP>), (a.rows + 255) / 256 * a.tiles, kGemmThreads, kGemmLds, stream, a);
   // with few rows, parts of them: 1024 blocks, of 2048 columns at least

@@ -44,7 +44,7 @@ struct BackwardArgs {
   const uint8_t* codes;
   const float *scales, *rstd;
   void *dx, *dgain;
-  float* partial;  // [gridDim.x][dim]
+  float* partial;  // [gridDim.x][dim up to a multiple of 8]
   uint64_t n_rows;
   uint32_t dim, blocks;
 };
@@ -195,24 +195,18 @@ __global__ void __launch_bounds__(Place<W>::kThreads) restore_kernel(const NormA
   }
 }
 
-// A block goes over rows blockIdx, blockIdx + gridDim, ... (four at a time where
-// a wavefront takes a row), adds up dy n in registers and leaves one partial
-// row for fold_kernel.
+// One row of the backward pass in registers.
 template <int DT, int W, int VPT, bool KEPT>
-__global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const BackwardArgs a) {
-  constexpr int N = Lane<DT>::N;
-  typedef typename Vec<DT>::T T;
-  __shared__ double part[W];
-  __shared__ float share[W == 1 ? 3 * 64 * N : 1];
-  const uint32_t t = Place<W>::lane();
-  float dg[VPT][N] = {};
-  for (uint64_t row = (uint64_t)blockIdx.x * Place<W>::kRows + Place<W>::row(); row < a.n_rows;
-       row += (uint64_t)gridDim.x * Place<W>::kRows) {
+struct Held {
+  static constexpr int N = Lane<DT>::N;
+  u32x4 d[VPT], up[VPT], h[KEPT ? 1 : VPT];
+  u32x2 c[KEPT ? VPT : 1];
+  float s[KEPT ? VPT : 1], rstd;
+
+  __device__ __forceinline__ void load(const BackwardArgs& a, uint64_t row, uint32_t t) {
+    typedef typename Vec<DT>::T T;
     const uint64_t at = row * a.dim;
-    const float rstd = a.rstd[row];
-    u32x4 d[VPT], h[VPT], up[VPT];
-    u32x2 c[VPT];
-    float s[VPT];
+    rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const uint32_t v = t + i * 64 * W;
@@ -232,26 +226,45 @@ __global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const Back
 #pragma unroll
       for (int i = 0; i < VPT; ++i) up[i] = u32x4{0, 0, 0, 0};
     }
-    const auto normalised = [&](int i, float (&n)[N]) {
-      if constexpr (KEPT) {
-        float x[8];
-        decode8(c[i], x);
+  }
+  __device__ __forceinline__ void normalised(int i, float (&n)[N]) const {
+    if constexpr (KEPT) {
+      float x[8];
+      decode8(c[i], x);
 #pragma unroll
-        for (int k = 0; k < N; ++k) n[k] = x[k] * s[i] * rstd;
-      } else {
+      for (int k = 0; k < N; ++k) n[k] = x[k] * s[i] * rstd;
+    } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k) n[k] = Lane<DT>::get(h[i], k) * rstd;
-      }
-    };
+      for (int k = 0; k < N; ++k) n[k] = Lane<DT>::get(h[i], k) * rstd;
+    }
+  }
+};
+
+// A block goes over rows blockIdx, blockIdx + gridDim, ... (four at a time where
+// a wavefront takes a row), adds up dy n in registers and leaves one partial
+// row for fold_kernel.
+template <int DT, int W, int VPT, bool KEPT>
+__global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const BackwardArgs a) {
+  constexpr int N = Lane<DT>::N;
+  typedef typename Vec<DT>::T T;
+  __shared__ double part[W];
+  __shared__ float share[W == 1 ? 3 * 64 * N : 1];
+  const uint32_t t = Place<W>::lane();
+  float dg[VPT][N] = {};
+  const uint64_t step = (uint64_t)gridDim.x * Place<W>::kRows;
+  uint64_t row = (uint64_t)blockIdx.x * Place<W>::kRows + Place<W>::row();
+  for (; row < a.n_rows; row += step) {
+    Held<DT, W, VPT, KEPT> x;
+    x.load(a, row, t);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const u32x4 g = load_cut<DT>(a.gain, t + i * 64 * W, a.dim);
       float n[N], p = 0.0f;
-      normalised(i, n);
+      x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float q = Lane<DT>::get(d[i], k) * n[k];
+        const float q = Lane<DT>::get(x.d[i], k) * n[k];
         dg[i][k] += q;
         p = fmaf(q, Lane<DT>::get(g, k), p);
       }
@@ -263,14 +276,15 @@ __global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const Back
       const uint32_t v = t + i * 64 * W;
       const u32x4 g = load_cut<DT>(a.gain, v, a.dim);
       float n[N], y[N];
-      normalised(i, n);
+      x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        y[k] = fmaf(rstd, fmaf(-n[k], mean, Lane<DT>::get(d[i], k) * Lane<DT>::get(g, k)), Lane<DT>::get(up[i], k));
-      store_cut<DT>(static_cast<T*>(a.dx) + at, v, a.dim, y);
+        y[k] = fmaf(x.rstd, fmaf(-n[k], mean, Lane<DT>::get(x.d[i], k) * Lane<DT>::get(g, k)), Lane<DT>::get(x.up[i], k));
+      store_cut<DT>(static_cast<T*>(a.dx) + row * a.dim, v, a.dim, y);
     }
   }
   // the block's wavefronts together, a vector of each at a time
+  const uint64_t at = (uint64_t)blockIdx.x * ((a.dim + 7) / 8 * 8);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const uint32_t v = t + i * 64 * W;
@@ -289,9 +303,11 @@ __global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const Back
       }
       if (w > 0) continue;
     }
+    if (v * N < a.dim) {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (v * N + k < a.dim) a.partial[(uint64_t)blockIdx.x * a.dim + v * N + k] = dg[i][k];
+      for (int k = 0; k < N; k += 4)
+        *reinterpret_cast<f32x4*>(a.partial + at + v * N + k) = f32x4{dg[i][k], dg[i][k + 1], dg[i][k + 2], dg[i][k + 3]};
+    }
   }
 }
 
@@ -308,10 +324,11 @@ __global__ void __launch_bounds__(kFoldColumns * kFoldGroups) fold_kernel(const 
   __shared__ double s[kFoldGroups][kFoldColumns];
   const uint32_t c = threadIdx.x % kFoldColumns, g = threadIdx.x / kFoldColumns;
   const uint32_t d = blockIdx.x * kFoldColumns + c;
+  const uint32_t row = (dim + 7) / 8 * 8;
   double sum = 0.0;
   if (d < dim) {
 #pragma unroll 8
-    for (uint32_t i = g; i < n; i += kFoldGroups) sum += (double)partial[(uint64_t)i * dim + d];
+    for (uint32_t i = g; i < n; i += kFoldGroups) sum += (double)partial[(uint64_t)i * row + d];
   }
   s[g][c] = sum;
   __syncthreads();
@@ -348,9 +365,15 @@ int check_rows(uint64_t n_rows, uint32_t dim, int dtype, const char* who) {
 
 uint32_t scales_of(uint32_t dim) { return (dim + ZERO_QBLOCK - 1) / ZERO_QBLOCK; }
 
-// Blocks of the backward pass, so that each partial row stands for
-// many rows and the fold stays short.
+// Blocks of the backward pass.  Each leaves a partial row of dgain in fp32, so
+// from 512 groups of rows on a block takes two of them, and from 2048 on more:
+// 999 rows of 5003 fp16 25 us in 999 blocks, 20 in 512, 25 in 256; 16,384 rows of
+// 4096 bf16 (the restored output included) 144 us in 2048 blocks, 138 in 1024,
+// 141 in 512.
 constexpr uint64_t kBackwardBlocks = 1024;
+uint64_t backward_blocks(uint64_t groups) {
+  return std::min(kBackwardBlocks, groups <= 512 ? groups : std::max<uint64_t>(512, groups / 2));
+}
 
 }  // namespace
 }  // namespace zs
@@ -426,7 +449,7 @@ extern "C" int zero_rms_norm_workspace_bytes(uint64_t n_rows, uint32_t dim, uint
   if (!bytes) return fail(ZERO_EINVAL, "zero_rms_norm_workspace_bytes: bytes is NULL");
   if (dim == 0 || dim > kMaxDim)
     return fail(ZERO_EINVAL, "zero_rms_norm_workspace_bytes: dim %u outside [1, %u]", dim, kMaxDim);
-  *bytes = std::max<uint64_t>(std::min(n_rows, kBackwardBlocks), 1) * dim * 4;
+  *bytes = std::max<uint64_t>(std::min(n_rows, kBackwardBlocks), 1) * ((dim + 7) / 8 * 8) * 4;
   return ZERO_OK;
 }
 
@@ -447,7 +470,7 @@ extern "C" int zero_rms_norm_backward(const zero_rms_norm_backward_args* p, hipS
     if (!multiple_of(p->dy, b) || !multiple_of(p->gain, b) || !multiple_of(p->h, b) || !multiple_of(p->upstream, b) ||
         !multiple_of(p->dx, b) || !multiple_of(p->rstd, 4) || !multiple_of(p->scales, 4))
       return fail(ZERO_EINVAL, "%s: an array is not aligned to its elements", who);
-    const uint64_t need = blocks * p->dim * 4;
+    const uint64_t need = blocks * ((p->dim + 7) / 8 * 8) * 4;
     if (!p->workspace) return fail(ZERO_EINVAL, "%s: workspace is NULL", who);
     if (p->workspace_bytes < need)
       return fail(ZERO_EINVAL, "%s: workspace needs %llu bytes, got %zu", who, (unsigned long long)need, p->workspace_bytes);
@@ -462,7 +485,7 @@ extern "C" int zero_rms_norm_backward(const zero_rms_norm_backward_args* p, hipS
       constexpr int DT = decltype(dt)::value;
       by_width<DT>(p->dim, [&](auto w, auto v) {
         constexpr int W = decltype(w)::value, VPT = decltype(v)::value;
-        parts = (uint32_t)std::min<uint64_t>((p->n_rows + Place<W>::kRows - 1) / Place<W>::kRows, kBackwardBlocks);
+        parts = (uint32_t)backward_blocks((p->n_rows + Place<W>::kRows - 1) / Place<W>::kRows);
         if (p->codes)
           hipLaunchKernelGGL((backward_kernel<DT, W, VPT, true>), parts, Place<W>::kThreads, 0, stream, a);
         else
