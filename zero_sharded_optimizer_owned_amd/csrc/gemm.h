@@ -33,9 +33,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGemmThreads = 512;
-constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+#ifndef NOSB
+#define SCHED __builtin_amdgcn_sched_barrier(0);
+#else
+#define SCHED
+#endif
+constexpr int kTileK = 64;
 constexpr int kOperandBytes = 256 * kTileK * 2;
-constexpr int kGemmLds = 4 * kOperandBytes;
+constexpr int kSlotBytes = 2 * kOperandBytes;  // a step's tiles; two steps lie in LDS
+constexpr int kGemmLds = 2 * kSlotBytes;
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: reads zero
 
 template <int DT>
@@ -48,10 +54,17 @@ __device__ __forceinline__ f32x4 mfma16(const u32x4 a, const u32x4 b, const f32x
 
 typedef __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, lds_char* to) {
-  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7FFFFFFF, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, offset, 0, 0, 0);
+// The next 16 bytes of each lane from base + offset to LDS address `to` + 16 lane.
+// Written in assembly because the compiler, which cannot tell the slots apart,
+// would let every read of LDS wait for all loads under way; gemm_tile waits for
+// the step that it reads.  The instruction has no output register.
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, uint32_t to) {
+  const u32x4 buffer = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32), 0x7FFFFFFFu, 0x00020000u};
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(buffer)
+               : "m0");
 }
+
+__device__ __forceinline__ uint32_t wave_of_block() { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 
 // k contiguous.  `base`: row 0 of the tile; rows from `rows` on and k from
 // `depth` (a multiple of 8) on are zero.  256 rows are under 2 GB.
@@ -72,8 +85,8 @@ struct Rows {
       offset[i] = row < rows ? (uint32_t)(row * stride * 2) + k * 2 : kNowhere;
     }
   }
-  __device__ __forceinline__ void load(uint32_t k0, lds_char* tile) const {
-    const uint32_t wave = threadIdx.x >> 6;
+  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile) const {
+    const uint32_t wave = wave_of_block();
     const bool in = k0 + k < depth;
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_to_lds(base + (uint64_t)k0 * 2, in ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
@@ -106,8 +119,8 @@ struct Columns {
     }
   }
   static __device__ __forceinline__ uint32_t swizzle(uint32_t row) { return (row % 4) << 1 | (row / 8 % 2) << 3; }
-  __device__ __forceinline__ void load(uint32_t k0, lds_char* tile) const {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile) const {
+    const uint32_t lane = threadIdx.x & 63, wave = wave_of_block();
     const char* at = base + k0 * stride * 2;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -133,47 +146,61 @@ struct Columns {
 };
 
 // acc[i][j][x]: m = 128 (wave / 4) + 16 i + lane % 16, n = 64 (wave % 4) + 16 j +
-// 4 (lane / 16) + x.  k runs over [k_begin, k_end), k_begin a multiple of 64.
+// 4 (lane / 16) + x.  k runs over [k_begin, k_end), k_begin a multiple of
+// 64; both operands are zero from k_end on.
 typedef f32x4 Acc[8][4];
 
 template <int DT, class P, class Q>
 __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_begin, uint32_t k_end, lds_char* lds, Acc& acc) {
-  const uint32_t wave = threadIdx.x >> 6, m0 = wave / 4 * 128, n0 = wave % 4 * 64;
+  const uint32_t wave = wave_of_block(), m0 = wave / 4 * 128, n0 = wave % 4 * 64;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   if (k_begin >= k_end) return;
-  lds_char* now = lds;
-  lds_char* next = lds + 2 * kOperandBytes;
-  p.load(k_begin, now);
-  q.load(k_begin, now + kOperandBytes);
-  for (uint32_t k = k_begin; k < k_end; k += kTileK) {
-    // this wavefront's loads of the step have arrived and its reads of the
-    // other half are done; behind the barrier that holds for all of them
+  // Half steps of 32 k.  A half step's fragments are read during the one
+  // before: those of Q into registers of their own, those of P each behind the
+  // last product of the one it replaces.  In the second half the next step's
+  // tiles are read, behind a barrier at which they have arrived and this step's
+  // are no longer read, so that the loads of the step after it can begin.
+  u32x4 a[2][4], b[8];
+  const uint32_t base = (uint32_t)(uintptr_t)lds;
+  uint32_t now = 0;
+  const auto load = [&](uint32_t k, uint32_t slot) {
+    p.load(k, base + slot);
+    q.load(k, base + slot + kOperandBytes);
+  };
+  const auto arrive = [&]() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (k + kTileK < k_end) {
-      p.load(k + kTileK, next);
-      q.load(k + kTileK, next + kOperandBytes);
+  };
+  load(k_begin, 0);
+  arrive();
+  if (k_begin + kTileK < k_end) load(k_begin + kTileK, kSlotBytes);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a[0][j] = Q::fragment(lds + kOperandBytes, n0 + 16 * j, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = P::fragment(lds, m0 + 16 * i, 0);
+  const auto half = [&](uint32_t h, const lds_char* from) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[h ^ 1][j] = Q::fragment(from + kOperandBytes, n0 + 16 * j, h ^ 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(a[h][j], b[i], acc[i][j]);
+      b[i] = P::fragment(from, m0 + 16 * i, h ^ 1);
+      SCHED
     }
-#pragma unroll
-    for (uint32_t kk = 0; kk < 2; ++kk) {
-      u32x4 a[4], b[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = Q::fragment(now + kOperandBytes, n0 + 16 * j, kk);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = P::fragment(now, m0 + 16 * i, kk);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(a[j], b[i], acc[i][j]);
-    }
-    lds_char* t = now;
-    now = next;
-    next = t;
+  };
+  for (uint32_t k = k_begin; k < k_end; k += kTileK) {
+    half(0, lds + now);
+    arrive();
+    if (k + 2 * kTileK < k_end) load(k + 2 * kTileK, now);
+    now ^= kSlotBytes;
+    half(1, lds + now);  // behind the last step, of whatever lies there
   }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 }
 
 }  // namespace zs

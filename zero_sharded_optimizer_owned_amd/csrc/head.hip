@@ -482,11 +482,12 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
     tile_of(b % (mt * nt), mt, nt, &tm, &tn);
     Rows p;
     Columns q;
-    p.begin(a.held, (uint64_t)tm * 256, live, a.padded, a.padded);
-    q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, a.vocab);
+    const uint32_t k_end = min((split + 1) * per * 64, a.vocab);
+    p.begin(a.held, (uint64_t)tm * 256, live, a.padded, (k_end + 7) / 8 * 8);  // the columns behind the vocabulary hold zeros
+    q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, k_end);
     Acc acc;
     __syncthreads();
-    gemm_tile<DT>(p, q, split * per * 64, min((split + 1) * per * 64, a.vocab), (lds_char*)lds, acc);
+    gemm_tile<DT>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
     const float f = a.meta->factor;
