@@ -33,11 +33,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kGemmThreads = 512;
-#ifndef NOSB
-#define SCHED __builtin_amdgcn_sched_barrier(0);
-#else
-#define SCHED
-#endif
 constexpr int kTileK = 64;
 constexpr int kOperandBytes = 256 * kTileK * 2;
 constexpr int kSlotBytes = 2 * kOperandBytes;  // a step's tiles; two steps lie in LDS
@@ -85,11 +80,11 @@ struct Rows {
       offset[i] = row < rows ? (uint32_t)(row * stride * 2) + k * 2 : kNowhere;
     }
   }
-  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile) const {
+  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i0, int i1) const {
     const uint32_t wave = wave_of_block();
     const bool in = k0 + k < depth;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_to_lds(base + (uint64_t)k0 * 2, in ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
+    for (int i = i0; i < i1; ++i) load_to_lds(base + (uint64_t)k0 * 2, in ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
   }
   // Eight k from 32 kk + 8 (lane / 16) on of row r0 + lane % 16.
   static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
@@ -119,11 +114,11 @@ struct Columns {
     }
   }
   static __device__ __forceinline__ uint32_t swizzle(uint32_t row) { return (row % 4) << 1 | (row / 8 % 2) << 3; }
-  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile) const {
+  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i0, int i1) const {
     const uint32_t lane = threadIdx.x & 63, wave = wave_of_block();
     const char* at = base + k0 * stride * 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = i0; i < i1; ++i) {
       const uint32_t row = (wave * 4 + i) * 2 + lane / 32;
       load_to_lds(at, k0 + row < depth ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
     }
@@ -166,23 +161,23 @@ __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_beg
   u32x4 a[2][4], b[8];
   const uint32_t base = (uint32_t)(uintptr_t)lds;
   uint32_t now = 0;
-  const auto load = [&](uint32_t k, uint32_t slot) {
-    p.load(k, base + slot);
-    q.load(k, base + slot + kOperandBytes);
+  const auto load = [&](uint32_t k, uint32_t slot, int i0, int i1) {
+    p.load(k, base + slot, i0, i1);
+    q.load(k, base + slot + kOperandBytes, i0, i1);
   };
   const auto arrive = [&]() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  load(k_begin, 0);
+  load(k_begin, 0, 0, 4);
   arrive();
-  if (k_begin + kTileK < k_end) load(k_begin + kTileK, kSlotBytes);
+  load(k_begin + kTileK, kSlotBytes, 0, 4);
 #pragma unroll
   for (int j = 0; j < 4; ++j) a[0][j] = Q::fragment(lds + kOperandBytes, n0 + 16 * j, 0);
 #pragma unroll
   for (int i = 0; i < 8; ++i) b[i] = P::fragment(lds, m0 + 16 * i, 0);
-  const auto half = [&](uint32_t h, const lds_char* from) {
+  const auto half = [&](uint32_t h, const lds_char* from, uint32_t k) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) a[h ^ 1][j] = Q::fragment(from + kOperandBytes, n0 + 16 * j, h ^ 1);
 #pragma unroll
@@ -190,17 +185,17 @@ __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_beg
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(a[h][j], b[i], acc[i][j]);
       b[i] = P::fragment(from, m0 + 16 * i, h ^ 1);
-      SCHED
+      if (h == 1 && i < 4) load(k + 2 * kTileK, now ^ kSlotBytes, i, i + 1);
+      __builtin_amdgcn_sched_barrier(0);  // in this order: left to itself the compiler reads just before the use
     }
   };
   for (uint32_t k = k_begin; k < k_end; k += kTileK) {
-    half(0, lds + now);
+    half(0, lds + now, k);
     arrive();
-    if (k + 2 * kTileK < k_end) load(k + 2 * kTileK, now);
     now ^= kSlotBytes;
-    half(1, lds + now);  // behind the last step, of whatever lies there
+    half(1, lds + now, k);  // behind the last step, of zeros that are not used
   }
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
 }  // namespace zs

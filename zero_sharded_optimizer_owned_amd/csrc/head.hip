@@ -475,37 +475,36 @@ template <int DT>
 __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
   const uint32_t live = a.meta->live, splits = a.meta->splits, mt = (live + 255) / 256, nt = (a.dim + 255) / 256;
+  if (live == 0) return;
   const uint32_t steps = (a.vocab + 63) / 64, per = (steps + splits - 1) / splits;
-  for (uint32_t b = blockIdx.x; b < mt * nt * splits; b += gridDim.x) {
-    const uint32_t split = b / (mt * nt);
-    uint32_t tm, tn;
-    tile_of(b % (mt * nt), mt, nt, &tm, &tn);
-    Rows p;
-    Columns q;
-    const uint32_t k_end = min((split + 1) * per * 64, a.vocab);
-    p.begin(a.held, (uint64_t)tm * 256, live, a.padded, (k_end + 7) / 8 * 8);  // the columns behind the vocabulary hold zeros
-    q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, k_end);
-    Acc acc;
-    __syncthreads();
-    gemm_tile<DT>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
-    const float f = a.meta->factor;
+  const uint32_t split = blockIdx.x / (mt * nt);
+  if (split >= splits) return;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x % (mt * nt), mt, nt, &tm, &tn);
+  const uint32_t k_end = min((split + 1) * per * 64, a.vocab);
+  Rows p;
+  Columns q;
+  p.begin(a.held, (uint64_t)tm * 256, live, a.padded, (k_end + 7) / 8 * 8);  // the columns behind the vocabulary hold zeros
+  q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, k_end);
+  Acc acc;
+  gemm_tile<DT>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  const float f = a.meta->factor;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
-      if (row >= live) continue;
-      const uint64_t at = a.row_of[row] * a.dhidden_stride;
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
+    if (row >= live) continue;
+    const uint64_t at = a.row_of[row] * a.dhidden_stride;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t n = n0 + 16 * j;
-        if (n >= a.dim) continue;
-        if (splits > 1) {
-          *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
-        } else {
-          const f32x4 x = acc[i][j] * f;
-          store4<DT>(a.dhidden, at + n, x[0], x[1], x[2], x[3]);
-        }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t n = n0 + 16 * j;
+      if (n >= a.dim) continue;
+      if (splits > 1) {
+        *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
+      } else {
+        const f32x4 x = acc[i][j] * f;
+        store4<DT>(a.dhidden, at + n, x[0], x[1], x[2], x[3]);
       }
     }
   }
@@ -576,6 +575,7 @@ struct Space {
 Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_rows, bool grad) {
   Space s = {};
   s.piece = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(n_rows, piece_rows));
+  static_assert(kFewShift == 4, "the statistics below are of 16-column tiles");
   s.shift = s.piece <= kFewRows ? kFewShift : 8;
   s.tiles = (vocab + (1u << s.shift) - 1) >> s.shift;
   const uint64_t p = s.piece, padded = (vocab + 255) / 256 * 256;
@@ -593,7 +593,8 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.terms = take(n_rows * 8);
   s.counts = take(n_rows);
   s.kept = take(p * dim * 2);
-  s.stats = take(p * s.tiles * 8);
+  // the most of any number of rows up to p: a workspace serves fewer rows too
+  s.stats = take(std::max(p * ((vocab + 255) / 256), std::min<uint64_t>(p, kFewRows) * ((vocab + 15) / 16)) * 8);
   s.held = take(grad ? p * padded * 2 : 0);
   uint64_t part = 0;  // dhidden's parts, for whatever number of rows counts
   s.blocks = 0;
