@@ -1,10 +1,12 @@
 // Matrix products on the matrix cores: out[m][n] = sum over k of P[m][k] Q[n][k],
 // operands in 16 bits, sums in fp32.
 //
-// A block of 512 threads makes a 256 x 256 tile, k in steps of 64.  Its eight
-// wavefronts take 128 x 64 each (two in m, four in n).  A step's tile of each
-// operand (32 KB) is loaded straight into LDS, 16 bytes to a lane, one step
-// ahead of the products; two steps fill 128 KB of LDS.
+// A block of 512 threads makes an M x 256 tile, k in steps of 64.  With M = 256 its
+// eight wavefronts take 128 x 64 each (two in m, four in n).  Fewer rows take
+// M = 128 (64 x 64 each) or M = 64 (64 x 32 each, all eight in n): those products
+// are bound by the reading of Q, and the smaller tile leaves LDS for more steps
+// under way.  A step's tiles (128 bytes for each m and n) are loaded straight into
+// LDS, 16 bytes to a lane, one step (M = 256), two or three steps ahead.
 //
 // An operand is laid out either with k contiguous (Rows: element (r, k) at r
 // stride + k) or with r contiguous (Columns: at k stride + r).  Rows' tiles hold
@@ -32,11 +34,30 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+__device__ __forceinline__ uint32_t wave_of_block() { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+
 constexpr int kGemmThreads = 512;
-constexpr int kTileK = 64;
-constexpr int kOperandBytes = 256 * kTileK * 2;
-constexpr int kSlotBytes = 2 * kOperandBytes;  // a step's tiles; two steps lie in LDS
-constexpr int kGemmLds = 2 * kSlotBytes;
+constexpr int kWaves = kGemmThreads / 64;
+constexpr int kTileN = 256, kTileK = 64;
+
+// Tiles of M rows with `Slots` steps in LDS.
+template <int M, int Slots>
+struct Tile {
+  static constexpr int kM = M, kSlots = Slots;
+  static constexpr int kBytesP = M * kTileK * 2, kSlotBytes = kBytesP + kTileN * kTileK * 2, kLds = Slots * kSlotBytes;
+  static constexpr int kWavesM = M == 64 ? 1 : 2, kWavesN = kWaves / kWavesM;
+  static constexpr int kWaveM = M / kWavesM, kWaveN = kTileN / kWavesN;  // of one wavefront
+  static constexpr int kI = kWaveM / 16, kJ = kWaveN / 16;
+  static constexpr int kLoads = M / 64 + kTileN / 64;  // a wavefront's, of a step
+  typedef f32x4 Acc[kI][kJ];
+  // acc[i][j][x] is m = row(i), n = column(j) + x of the tile
+  static __device__ __forceinline__ uint32_t row(int i) {
+    return wave_of_block() / kWavesN * kWaveM + 16 * i + threadIdx.x % 16;
+  }
+  static __device__ __forceinline__ uint32_t column(int j) {
+    return wave_of_block() % kWavesN * kWaveN + 16 * j + threadIdx.x % 64 / 16 * 4;
+  }
+};
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: reads zero
 
 template <int DT>
@@ -59,32 +80,29 @@ __device__ __forceinline__ void load_to_lds(const char* base, uint32_t offset, u
                : "m0");
 }
 
-__device__ __forceinline__ uint32_t wave_of_block() { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
-
-// k contiguous.  `base`: row 0 of the tile; rows from `rows` on and k from
+// R rows, k contiguous.  `base`: row 0 of the tile; rows from `rows` on and k from
 // `depth` (a multiple of 8) on are zero.  256 rows are under 2 GB.
+template <int R>
 struct Rows {
+  static constexpr int kLoads = R / 64;  // of each wavefront: 8 rows of 128 bytes
   const char* base;
-  uint32_t offset[4], k;
+  uint32_t offset[kLoads], k;
   uint32_t depth;
 
   __device__ __forceinline__ void begin(const void* p, uint64_t row0, uint32_t n_rows, uint64_t stride, uint32_t depth_) {
     base = static_cast<const char*>(p) + row0 * stride * 2;
     depth = depth_;
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t rows = n_rows > row0 ? (uint32_t)min((uint64_t)n_rows - row0, (uint64_t)256) : 0;
+    const uint32_t rows = n_rows > row0 ? (uint32_t)min((uint64_t)n_rows - row0, (uint64_t)R) : 0;
     k = ((lane % 8) ^ (lane / 8)) * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t row = (wave * 4 + i) * 8 + lane / 8;
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t row = (wave * kLoads + i) * 8 + lane / 8;
       offset[i] = row < rows ? (uint32_t)(row * stride * 2) + k * 2 : kNowhere;
     }
   }
-  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i0, int i1) const {
-    const uint32_t wave = wave_of_block();
-    const bool in = k0 + k < depth;
-#pragma unroll
-    for (int i = i0; i < i1; ++i) load_to_lds(base + (uint64_t)k0 * 2, in ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
+  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i) const {
+    load_to_lds(base + (uint64_t)k0 * 2, k0 + k < depth ? offset[i] : kNowhere, tile + (wave_of_block() * kLoads + i) * 1024);
   }
   // Eight k from 32 kk + 8 (lane / 16) on of row r0 + lane % 16.
   static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
@@ -93,35 +111,39 @@ struct Rows {
   }
 };
 
-// r contiguous.  `base`: column r0 of row 0; columns from `columns` (a multiple
-// of 8) on and k from `depth` on are zero.
+// R columns, r contiguous.  `base`: column r0 of row 0; columns from `columns` (a
+// multiple of 8) on and k from `depth` on are zero.
+template <int R>
 struct Columns {
+  static constexpr int kLoads = R / 64, kPieces = R / 8;  // of each wavefront; of a row of 2 R bytes
   const char* base;
   uint64_t stride;
-  uint32_t offset[4];
+  uint32_t offset[kLoads];
   uint32_t depth;
 
+  static __device__ __forceinline__ uint32_t row_of(int i) {
+    return (wave_of_block() * kLoads + i) * (64 / kPieces) + threadIdx.x % 64 / kPieces;
+  }
   __device__ __forceinline__ void begin(const void* p, uint64_t column0, uint32_t n_columns, uint64_t stride_, uint32_t depth_) {
     base = static_cast<const char*>(p) + column0 * 2;
     stride = stride_;
     depth = depth_;
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const uint32_t columns = n_columns > column0 ? (uint32_t)min((uint64_t)n_columns - column0, (uint64_t)256) : 0;
+    const uint32_t columns = n_columns > column0 ? (uint32_t)min((uint64_t)n_columns - column0, (uint64_t)R) : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t row = (wave * 4 + i) * 2 + lane / 32, c = (lane % 32) ^ swizzle(row);
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t row = row_of(i), c = (threadIdx.x % kPieces) ^ swizzle(row);
       offset[i] = c * 8 < columns ? (uint32_t)(row * stride * 2) + c * 16 : kNowhere;
     }
   }
-  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) { return (row % 4) << 1 | (row / 8 % 2) << 3; }
-  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i0, int i1) const {
-    const uint32_t lane = threadIdx.x & 63, wave = wave_of_block();
-    const char* at = base + k0 * stride * 2;
-#pragma unroll
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t row = (wave * 4 + i) * 2 + lane / 32;
-      load_to_lds(at, k0 + row < depth ? offset[i] : kNowhere, tile + (wave * 4 + i) * 1024);
-    }
+  // A transposing read takes 32 bytes of each of 4 rows, and two groups of 16
+  // lanes at a time rows 8 apart: all in different banks.
+  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+    if constexpr (R == 64) return ((row % 4) ^ (row / 8 % 2)) << 1;  // two rows to a line of 64 banks
+    else return (row % 4) << 1 | (row / 8 % 2) << 3;
+  }
+  __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i) const {
+    load_to_lds(base + k0 * stride * 2, k0 + row_of(i) < depth ? offset[i] : kNowhere,
+                tile + (wave_of_block() * kLoads + i) * 1024);
   }
   static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
     const uint32_t lane = threadIdx.x & 63;
@@ -131,7 +153,7 @@ struct Columns {
       const uint32_t row = 32 * kk + 8 * (lane / 16) + 4 * h + lane % 16 / 4;
       const uint32_t piece = (r0 / 8 + lane % 4 / 2) ^ swizzle(row);
       const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4*)(tile + row * 512 + piece * 16 + lane % 2 * 8));
+          (__attribute__((address_space(3))) s16x4*)(tile + row * (2 * R) + piece * 16 + lane % 2 * 8));
       const u32x2 w = __builtin_bit_cast(u32x2, q);
       f[2 * h] = w[0];
       f[2 * h + 1] = w[1];
@@ -140,60 +162,83 @@ struct Columns {
   }
 };
 
-// acc[i][j][x]: m = 128 (wave / 4) + 16 i + lane % 16, n = 64 (wave % 4) + 16 j +
-// 4 (lane / 16) + x.  k runs over [k_begin, k_end), k_begin a multiple of
-// 64; both operands are zero from k_end on.
-typedef f32x4 Acc[8][4];
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N == 0 || N == 6 || N == 10, "a count the assembly is written for");
+  if constexpr (N == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  else if constexpr (N == 6) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
+}
 
-template <int DT, class P, class Q>
-__device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_begin, uint32_t k_end, lds_char* lds, Acc& acc) {
-  const uint32_t wave = wave_of_block(), m0 = wave / 4 * 128, n0 = wave % 4 * 64;
+// k runs over [k_begin, k_end), k_begin a multiple of 64; both operands are zero
+// from k_end on.
+template <int DT, class T, class P, class Q>
+__device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_begin, uint32_t k_end, lds_char* lds,
+                                          typename T::Acc& acc) {
+  constexpr int I = T::kI, J = T::kJ;
+  static_assert(P::kLoads + Q::kLoads == T::kLoads, "operands of the tile's sizes");
+  const uint32_t m0 = wave_of_block() / T::kWavesN * T::kWaveM, n0 = wave_of_block() % T::kWavesN * T::kWaveN;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < I; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   if (k_begin >= k_end) return;
   // Half steps of 32 k.  A half step's fragments are read during the one
   // before: those of Q into registers of their own, those of P each behind the
   // last product of the one it replaces.  In the second half the next step's
   // tiles are read, behind a barrier at which they have arrived and this step's
-  // are no longer read, so that the loads of the step after it can begin.
-  u32x4 a[2][4], b[8];
+  // are no longer read, so that the loads of a later step can take its slot.
+  u32x4 a[2][J], b[I];
   const uint32_t base = (uint32_t)(uintptr_t)lds;
-  uint32_t now = 0;
-  const auto load = [&](uint32_t k, uint32_t slot, int i0, int i1) {
-    p.load(k, base + slot, i0, i1);
-    q.load(k, base + slot + kOperandBytes, i0, i1);
+  const auto load = [&](uint32_t k, uint32_t slot, int i) {  // this wavefront's i-th load of a step
+    if (i < P::kLoads) p.load(k, base + slot, i);
+    else q.load(k, base + slot + T::kBytesP, i - P::kLoads);
   };
   const auto arrive = [&]() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    wait_loads<(T::kSlots - 2) * T::kLoads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  load(k_begin, 0, 0, 4);
+  uint32_t k_load = k_begin;
+#pragma unroll
+  for (int s = 0; s < T::kSlots - 1; ++s) {
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) load(k_load, s * T::kSlotBytes, i);
+    k_load += kTileK;
+  }
   arrive();
-  load(k_begin + kTileK, kSlotBytes, 0, 4);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) a[0][j] = Q::fragment(lds + kOperandBytes, n0 + 16 * j, 0);
+  for (int i = 0; i < T::kLoads; ++i) load(k_load, (T::kSlots - 1) * T::kSlotBytes, i);
+  k_load += kTileK;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = P::fragment(lds, m0 + 16 * i, 0);
-  const auto half = [&](uint32_t h, const lds_char* from, uint32_t k) {
+  for (int j = 0; j < J; ++j) a[0][j] = Q::fragment(lds + T::kBytesP, n0 + 16 * j, 0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[h ^ 1][j] = Q::fragment(from + kOperandBytes, n0 + 16 * j, h ^ 1);
+  for (int i = 0; i < I; ++i) b[i] = P::fragment(lds, m0 + 16 * i, 0);
+  uint32_t now = 0;
+  const auto half = [&](uint32_t h, const lds_char* from, uint32_t free) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < J; ++j) a[h ^ 1][j] = Q::fragment(from + T::kBytesP, n0 + 16 * j, h ^ 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<DT>(a[h][j], b[i], acc[i][j]);
+    for (int i = 0; i < I; ++i) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) acc[i][j] = mfma16<DT>(a[h][j], b[i], acc[i][j]);
       b[i] = P::fragment(from, m0 + 16 * i, h ^ 1);
-      if (h == 1 && i < 4) load(k + 2 * kTileK, now ^ kSlotBytes, i, i + 1);
+      if (h == 1) {
+        constexpr int kEach = (T::kLoads + I / 2 - 1) / (I / 2);  // within the first half of the products
+#pragma unroll
+        for (int l = i * kEach; l < (i + 1) * kEach; ++l)
+          if (l < T::kLoads) load(k_load, free, l);
+      }
       __builtin_amdgcn_sched_barrier(0);  // in this order: left to itself the compiler reads just before the use
     }
   };
   for (uint32_t k = k_begin; k < k_end; k += kTileK) {
-    half(0, lds + now, k);
+    half(0, lds + now, 0);
     arrive();
-    now ^= kSlotBytes;
-    half(1, lds + now, k);  // behind the last step, of zeros that are not used
+    const uint32_t free = now;
+    now = now + T::kSlotBytes == T::kLds ? 0 : now + T::kSlotBytes;
+    half(1, lds + now, free);  // behind the last step, of zeros that are not used
+    k_load += kTileK;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }

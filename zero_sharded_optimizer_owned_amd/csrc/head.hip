@@ -68,7 +68,7 @@ struct HeadArgs {
   float* part;                // [splits][rows][dim]: dhidden's sums over parts of the vocabulary
   float* sum;                 // fp32 dweight of the pieces so far
   int first, last;            // whether the piece is the first, the last
-  uint8_t splits[64];         // for live rows in (256 i, 256 i + 256]
+  uint8_t splits[64];         // of i + 1 tiles of rows that count
   float* stats_out;           // few rows: the last block of softmax_kernel writes the loss
   double inv_divisor;
 };
@@ -90,6 +90,15 @@ inline uint32_t splits_of(uint32_t m_tiles, uint32_t vocab, uint32_t dim) {
   }
   return best;
 }
+
+// The products' tiles by the piece's rows.  For few rows the reading of the weights
+// bounds logits and dhidden, and the writing of their gradient dweight, whose
+// tiles are then of 64 columns, so that two blocks share a CU.
+typedef Tile<256, 2> Wide;
+typedef Tile<128, 3> Middle;
+typedef Tile<64, 4> Narrow;
+typedef Tile<64, 2> Short;
+__host__ __device__ inline uint32_t tile_rows(uint32_t rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
 
 // ---------------------------------------------------------------------------
 // The rows that count, in order.
@@ -132,7 +141,7 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
   if (lane == 0) most[wave] = top;
   __syncthreads();
   for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
-  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), before ? a.splits[(before - 1) / 256] : 1u, 0};
+  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), before ? a.splits[(before - 1) / tile_rows(a.rows)] : 1u, 0};
   for (uint32_t i = t; i < before; i += 1024) {
     const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f;
     a.omega[i] = top > 0.0f ? w / top : w;  // all weights 0 or not finite
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kBlock) prepare_few_kernel(const HeadArgs a) {
     at += counts;
   }
   if (blockIdx.x == 0 && t == 0)
-    *a.meta = Meta{live, (float)(a.coef * (double)top / kHeld), live ? a.splits[(live - 1) / 256] : 1u, 0};
+    *a.meta = Meta{live, (float)(a.coef * (double)top / kHeld), live ? a.splits[(live - 1) / tile_rows(a.rows)] : 1u, 0};
   __syncthreads();
   gather_row(a, blockIdx.x, mine, a.dhidden && out);
 }
@@ -236,68 +245,76 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, ui
 // ---------------------------------------------------------------------------
 // Product one.
 // ---------------------------------------------------------------------------
-template <int DT, bool KEEP>
+template <int DT, class T, bool KEEP>
 __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t live = a.meta->live, mt = (live + 255) / 256;
+  const uint32_t live = a.meta->live, mt = (live + T::kM - 1) / T::kM;
   if (blockIdx.x >= mt * a.tiles) return;
   uint32_t tm, tn;
   tile_of(blockIdx.x, mt, a.tiles, &tm, &tn);
-  Rows p, q;
-  p.begin(a.kept, (uint64_t)tm * 256, live, a.dim, a.dim);
+  Rows<T::kM> p;
+  Rows<256> q;
+  p.begin(a.kept, (uint64_t)tm * T::kM, live, a.dim, a.dim);
   q.begin(a.weight, (uint64_t)tn * 256, a.vocab, a.weight_stride, a.dim);
-  Acc acc;
-  gemm_tile<DT>(p, q, 0, a.dim, (lds_char*)lds, acc);
-  // the tile's maximum of each row, over the four wavefronts that share it
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t m0 = wave / 4 * 128 + lane % 16, n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  typename T::Acc acc;
+  gemm_tile<DT, T>(p, q, 0, a.dim, (lds_char*)lds, acc);
+  // the tile's maximum of each row, over the wavefronts that share it
+  constexpr int W = T::kWavesN;
+  const uint32_t lane = threadIdx.x & 63, share = wave_of_block() % W * T::kM;
   float* red = reinterpret_cast<float*>(lds);
+  const auto most = [&](uint32_t r) {
+    float m = red[r];
+#pragma unroll
+    for (int w = 1; w < W; ++w) m = fmaxf(m, red[w * T::kM + r]);
+    return m;
+  };
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < T::kI; ++i) {
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < T::kJ; ++j)
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        if (n0 + 16 * j + x < a.vocab) top = fmaxf(top, acc[i][j][x]);
+        if (tn * 256 + T::column(j) + x < a.vocab) top = fmaxf(top, acc[i][j][x]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    if (lane < 16) red[wave % 4 * 256 + m0 + 16 * i] = top;
+    if (lane < 16) red[share + T::row(i)] = top;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t r = m0 + 16 * i, row = tm * 256 + r;
+  for (int i = 0; i < T::kI; ++i) {
+    const uint32_t r = T::row(i), row = tm * T::kM + r;
     const bool has = row < live;
-    const float top = fmaxf(fmaxf(red[r], red[256 + r]), fmaxf(red[512 + r], red[768 + r]));
-    const float m = top == -INFINITY ? 0.0f : top;
+    const float top = most(r), m = top == -INFINITY ? 0.0f : top;
     const uint32_t target = has ? a.target[row] : 0xFFFFFFFFu;
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < T::kJ; ++j) {
+      const uint32_t n0 = tn * 256 + T::column(j);
       float e[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const uint32_t n = n0 + 16 * j + x;
+        const uint32_t n = n0 + x;
         e[x] = n < a.vocab ? __builtin_amdgcn_exp2f((acc[i][j][x] - m) * a.c) : 0.0f;
         if (n == target) a.said[row] = acc[i][j][x];
         else sum += e[x];
       }
       if (KEEP && has)
-        store4<ZERO_F16>(a.held, (uint64_t)row * a.padded + n0 + 16 * j, e[0] * kTileExp, e[1] * kTileExp, e[2] * kTileExp,
+        store4<ZERO_F16>(a.held, (uint64_t)row * a.padded + n0, e[0] * kTileExp, e[1] * kTileExp, e[2] * kTileExp,
                          e[3] * kTileExp);
     }
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
-    if (lane < 16) red[1024 + wave % 4 * 256 + r] = sum;
+    if (lane < 16) red[W * T::kM + share + r] = sum;
   }
   __syncthreads();
-  if (threadIdx.x < 256 && tm * 256 + threadIdx.x < live) {
+  if (threadIdx.x < T::kM && tm * T::kM + threadIdx.x < live) {
     const uint32_t r = threadIdx.x;
-    const float top = fmaxf(fmaxf(red[r], red[256 + r]), fmaxf(red[512 + r], red[768 + r]));
-    const float* s = red + 1024 + r;
-    a.stats[(uint64_t)(tm * 256 + r) * a.tiles + tn] = f32x2{top, s[0] + s[256] + s[512] + s[768]};
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) sum += red[(W + w) * T::kM + r];
+    a.stats[(uint64_t)(tm * T::kM + r) * a.tiles + tn] = f32x2{most(r), sum};
   }
 }
 
@@ -471,10 +488,10 @@ __global__ void __launch_bounds__(kBlock) loss_kernel(const double* terms, const
 // ---------------------------------------------------------------------------
 // Products two and three.
 // ---------------------------------------------------------------------------
-template <int DT>
+template <int DT, class T>
 __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t live = a.meta->live, splits = a.meta->splits, mt = (live + 255) / 256, nt = (a.dim + 255) / 256;
+  const uint32_t live = a.meta->live, splits = a.meta->splits, mt = (live + T::kM - 1) / T::kM, nt = (a.dim + 255) / 256;
   if (live == 0) return;
   const uint32_t steps = (a.vocab + 63) / 64, per = (steps + splits - 1) / splits;
   const uint32_t split = blockIdx.x / (mt * nt);
@@ -482,23 +499,22 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   uint32_t tm, tn;
   tile_of(blockIdx.x % (mt * nt), mt, nt, &tm, &tn);
   const uint32_t k_end = min((split + 1) * per * 64, a.vocab);
-  Rows p;
-  Columns q;
-  p.begin(a.held, (uint64_t)tm * 256, live, a.padded, (k_end + 7) / 8 * 8);  // the columns behind the vocabulary hold zeros
+  Rows<T::kM> p;
+  Columns<256> q;
+  // the columns behind the vocabulary hold zeros
+  p.begin(a.held, (uint64_t)tm * T::kM, live, a.padded, (k_end + 7) / 8 * 8);
   q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, k_end);
-  Acc acc;
-  gemm_tile<DT>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  typename T::Acc acc;
+  gemm_tile<DT, T>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
   const float f = a.meta->factor;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
+  for (int i = 0; i < T::kI; ++i) {
+    const uint32_t row = tm * T::kM + T::row(i);
     if (row >= live) continue;
     const uint64_t at = a.row_of[row] * a.dhidden_stride;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t n = n0 + 16 * j;
+    for (int j = 0; j < T::kJ; ++j) {
+      const uint32_t n = tn * 256 + T::column(j);
       if (n >= a.dim) continue;
       if (splits > 1) {
         *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
@@ -529,27 +545,26 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
   }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs a) {
+template <int DT, class T>
+__global__ void __launch_bounds__(kGemmThreads, T::kM == 64 ? 4 : 2) dweight_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t live = a.meta->live, mt = a.padded / 256, nt = (a.dim + 255) / 256;
+  const uint32_t live = a.meta->live, mt = (a.vocab + T::kM - 1) / T::kM, nt = (a.dim + 255) / 256;
   uint32_t tm, tn;
   tile_of(blockIdx.x, mt, nt, &tm, &tn);
-  Columns p, q;
-  p.begin(a.held, (uint64_t)tm * 256, a.padded, a.padded, live);
+  Columns<T::kM> p;
+  Columns<256> q;
+  p.begin(a.held, (uint64_t)tm * T::kM, a.padded, a.padded, live);
   q.begin(a.kept, (uint64_t)tn * 256, a.dim, a.dim, live);
-  Acc acc;
-  gemm_tile<DT>(p, q, 0, live, (lds_char*)lds, acc);
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t n0 = tn * 256 + wave % 4 * 64 + lane / 16 * 4;
+  typename T::Acc acc;
+  gemm_tile<DT, T>(p, q, 0, live, (lds_char*)lds, acc);
   const float f = a.meta->factor;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t row = tm * 256 + wave / 4 * 128 + 16 * i + lane % 16;
+  for (int i = 0; i < T::kI; ++i) {
+    const uint32_t row = tm * T::kM + T::row(i);
     if (row >= a.vocab) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t n = n0 + 16 * j;
+    for (int j = 0; j < T::kJ; ++j) {
+      const uint32_t n = tn * 256 + T::column(j);
       if (n >= a.dim) continue;
       f32x4 x = acc[i][j] * f;
       f32x4* sum = reinterpret_cast<f32x4*>(a.sum + (uint64_t)row * a.dim + n);
@@ -567,8 +582,7 @@ constexpr uint32_t kMaxDim = 1u << 15;
 
 struct Space {
   uint64_t meta, row_of, target, omega, said, terms, counts, kept, held, stats, part, sum, bytes;
-  uint8_t splits[64];
-  uint32_t piece, tiles, shift, blocks;  // blocks: most of dhidden's product
+  uint32_t piece, tiles, shift;
 };
 
 // Where the pieces of `piece_rows` rows have their intermediates.
@@ -597,12 +611,12 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.stats = take(std::max(p * ((vocab + 255) / 256), std::min<uint64_t>(p, kFewRows) * ((vocab + 15) / 16)) * 8);
   s.held = take(grad ? p * padded * 2 : 0);
   uint64_t part = 0;  // dhidden's parts, for whatever number of rows counts
-  s.blocks = 0;
-  for (uint32_t m = 256; grad && m < p + 256; m += 256) {
-    const uint32_t n = splits_of(m / 256, vocab, dim);
-    s.splits[m / 256 - 1] = (uint8_t)n;
-    if (n > 1) part = std::max(part, n * std::min<uint64_t>(m, p));
-    s.blocks = std::max(s.blocks, m / 256 * ((dim + 255) / 256) * n);
+  for (uint64_t rows : {(uint64_t)64, (uint64_t)128, p}) {  // the last piece may be smaller, and so may a later call
+    const uint32_t t = tile_rows((uint32_t)std::min(rows, p));
+    for (uint32_t m = t; grad && m < std::min(rows, p) + t; m += t) {
+      const uint32_t n = splits_of(m / t, vocab, dim);
+      if (n > 1) part = std::max(part, n * std::min<uint64_t>(m, std::min(rows, p)));
+    }
   }
   s.part = take(part * dim * 4);
   s.sum = take(grad && n_rows > p ? (uint64_t)vocab * dim * 4 : 0);
@@ -628,19 +642,46 @@ int check_matrix(const void* p, uint64_t rows, uint32_t dim, uint64_t stride, co
   return ZERO_OK;
 }
 
+// Calls fn with the tile of a piece's rows.
+template <typename F>
+void by_tile(uint32_t rows, F fn) {
+  if (tile_rows(rows) == 64) fn(Narrow{});
+  else if (tile_rows(rows) == 128) fn(Middle{});
+  else fn(Wide{});
+}
+
 template <int DT, bool KEEP>
 void launch_rows(const HeadArgs& a, hipStream_t stream) {
-  if (a.shift == kFewShift) hipLaunchKernelGGL((few_logits_kernel<DT, KEEP>), a.padded >> kFewShift, kBlock, 0, stream, a);
-  else
-    hipLaunchKernelGGL((logits_kernel<DT, KEEP>), (a.rows + 255) / 256 * a.tiles, kGemmThreads, kGemmLds, stream, a);
+  if (a.shift == kFewShift) {
+    hipLaunchKernelGGL((few_logits_kernel<DT, KEEP>), a.padded >> kFewShift, kBlock, 0, stream, a);
+  } else {
+    by_tile(a.rows, [&](auto tile) {
+      typedef decltype(tile) T;
+      hipLaunchKernelGGL((logits_kernel<DT, T, KEEP>), (a.rows + T::kM - 1) / T::kM * a.tiles, kGemmThreads, T::kLds, stream, a);
+    });
+  }
   // with few rows, parts of them: 1024 blocks, of 2048 columns at least
   const uint32_t parts = KEEP ? std::min((a.padded + 2047) / 2048, std::max(1024 / a.rows, 1u)) : 1;
   hipLaunchKernelGGL((softmax_kernel<DT, KEEP>), dim3(a.rows, parts), kBlock, 0, stream, a);
 }
 
 template <int DT>
-void launch_piece(const HeadArgs& a, bool grad, uint32_t blocks, hipStream_t stream) {
+void launch_dweight(const HeadArgs& a, hipStream_t stream) {
   const uint32_t nt = (a.dim + 255) / 256;
+  if (a.rows <= 128)
+    hipLaunchKernelGGL((dweight_kernel<DT, Short>), (a.vocab + 63) / 64 * nt, kGemmThreads, Short::kLds, stream, a);
+  else
+    hipLaunchKernelGGL((dweight_kernel<DT, Wide>), (a.vocab + 255) / 256 * nt, kGemmThreads, Wide::kLds, stream, a);
+}
+
+template <int DT>
+void launch_piece(HeadArgs a, bool grad, hipStream_t stream) {
+  const uint32_t nt = (a.dim + 255) / 256;
+  uint32_t blocks = 0;  // the most that dhidden's product has, whatever number of rows counts
+  for (uint32_t i = 0; grad && i * tile_rows(a.rows) < a.rows; ++i) {
+    a.splits[i] = (uint8_t)splits_of(i + 1, a.vocab, a.dim);
+    blocks = std::max(blocks, (i + 1) * nt * a.splits[i]);
+  }
   if (a.rows <= kGatherRows) {
     hipLaunchKernelGGL(prepare_few_kernel, a.rows, kBlock, 0, stream, a);
   } else {
@@ -650,10 +691,13 @@ void launch_piece(const HeadArgs& a, bool grad, uint32_t blocks, hipStream_t str
   if (!grad) return launch_rows<DT, false>(a, stream);
   launch_rows<DT, true>(a, stream);
   if (a.dhidden) {
-    hipLaunchKernelGGL(dhidden_kernel<DT>, blocks, kGemmThreads, kGemmLds, stream, a);
+    by_tile(a.rows, [&](auto tile) {
+      typedef decltype(tile) T;
+      hipLaunchKernelGGL((dhidden_kernel<DT, T>), blocks, kGemmThreads, T::kLds, stream, a);
+    });
     hipLaunchKernelGGL(join_kernel<DT>, dim3(a.rows, (a.dim / 4 + kBlock - 1) / kBlock), kBlock, 0, stream, a);
   }
-  if (a.dweight) hipLaunchKernelGGL(dweight_kernel<DT>, a.padded / 256 * nt, kGemmThreads, kGemmLds, stream, a);
+  if (a.dweight) launch_dweight<DT>(a, stream);
 }
 
 }  // namespace
@@ -709,7 +753,6 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   a.weight_stride = p->weight_stride;
   a.vocab = p->vocab;
   a.dim = p->dim;
-  std::copy(s.splits, s.splits + 64, a.splits);
   a.tiles = s.tiles;
   a.shift = s.shift;
   a.padded = (p->vocab + 255) / 256 * 256;
@@ -747,13 +790,12 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
     a.terms = terms + row;
     a.counts = counts + row;
     if (a.rows > 0) {
-      if (p->dtype == ZERO_F16) launch_piece<ZERO_F16>(a, grad, s.blocks, stream);
-      else launch_piece<ZERO_BF16>(a, grad, s.blocks, stream);
+      if (p->dtype == ZERO_F16) launch_piece<ZERO_F16>(a, grad, stream);
+      else launch_piece<ZERO_BF16>(a, grad, stream);
     } else if (a.dweight) {
       hipLaunchKernelGGL(prepare_kernel, 1, 1024, 0, stream, a);
-      const uint32_t nt = (a.dim + 255) / 256;
-      if (p->dtype == ZERO_F16) hipLaunchKernelGGL(dweight_kernel<ZERO_F16>, a.padded / 256 * nt, kGemmThreads, kGemmLds, stream, a);
-      else hipLaunchKernelGGL(dweight_kernel<ZERO_BF16>, a.padded / 256 * nt, kGemmThreads, kGemmLds, stream, a);
+      if (p->dtype == ZERO_F16) launch_dweight<ZERO_F16>(a, stream);
+      else launch_dweight<ZERO_BF16>(a, stream);
     }
     if ((rc = launch_status(who))) return rc;
     row += a.rows;
