@@ -243,4 +243,38 @@ __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_beg
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
+// A tile in 16 bits goes to memory by way of LDS, so that a row's 512 bytes are
+// stored by 32 lanes in one go (a lane of the products holds 8 of them).  16-byte
+// piece c of row m lies at piece c ^ m % 32: all banks at once, both ways.
+template <int DT>
+__device__ __forceinline__ void put_quad(char* lds, uint32_t m, uint32_t n, const f32x4 x) {
+  *reinterpret_cast<u32x2*>(lds + m * 512 + ((n / 8) ^ (m % 32)) * 16 + n % 8 * 2) =
+      u32x2{Vec<DT>::pack(x[0], x[1]), Vec<DT>::pack(x[2], x[3])};
+}
+
+// `row(m)`: where row m of the tile begins, NULL for none; columns from `columns`
+// (a multiple of 8) on are left out.
+template <int M, typename F>
+__device__ __forceinline__ void store_rows(const char* lds, uint32_t columns, F row) {
+  const uint32_t c = threadIdx.x % 32;
+#pragma unroll 4
+  for (uint32_t m = threadIdx.x / 32; m < M; m += kGemmThreads / 32) {
+    uint16_t* to = row(m);
+    if (to && c * 8 < columns)
+      *reinterpret_cast<u32x4*>(to + c * 8) = *reinterpret_cast<const u32x4*>(lds + m * 512 + (c ^ (m % 32)) * 16);
+  }
+}
+
+// The tile times f.  The caller's wavefronts are done with LDS.
+template <int DT, class T, typename F>
+__device__ __forceinline__ void store_tile(const typename T::Acc& acc, float f, uint32_t columns, char* lds, F row) {
+  static_assert(T::kM * kTileN * 2 <= T::kLds, "the tile in 16 bits");
+#pragma unroll
+  for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::kJ; ++j) put_quad<DT>(lds, T::row(i), T::column(j), acc[i][j] * f);
+  __syncthreads();
+  store_rows<T::kM>(lds, columns, row);
+}
+
 }  // namespace zs

@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
   // the tile's maximum of each row, over the wavefronts that share it
   constexpr int W = T::kWavesN;
   const uint32_t lane = threadIdx.x & 63, share = wave_of_block() % W * T::kM;
-  float* red = reinterpret_cast<float*>(lds);
+  float* red = reinterpret_cast<float*>(lds + T::kM * 512);  // behind the tile's exponentials in 16 bits
   const auto most = [&](uint32_t r) {
     float m = red[r];
 #pragma unroll
@@ -300,9 +300,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
         if (n == target) a.said[row] = acc[i][j][x];
         else sum += e[x];
       }
-      if (KEEP && has)
-        store4<ZERO_F16>(a.held, (uint64_t)row * a.padded + n0, e[0] * kTileExp, e[1] * kTileExp, e[2] * kTileExp,
-                         e[3] * kTileExp);
+      if constexpr (KEEP) put_quad<ZERO_F16>(lds, r, T::column(j), f32x4{e[0], e[1], e[2], e[3]} * kTileExp);
     }
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
@@ -316,6 +314,18 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
     for (int w = 0; w < W; ++w) sum += red[(W + w) * T::kM + r];
     a.stats[(uint64_t)(tm * T::kM + r) * a.tiles + tn] = f32x2{most(r), sum};
   }
+  if constexpr (KEEP)
+    store_rows<T::kM>(lds, 256, [&](uint32_t m) {
+      const uint32_t row = tm * T::kM + m;
+      return row < live ? a.held + (uint64_t)row * a.padded + tn * 256 : nullptr;
+    });
+}
+
+// LDS of that: the products' slots, then the exponentials and two numbers of each row and wavefront.
+template <class T>
+constexpr uint32_t logits_lds() {
+  constexpr uint32_t after = T::kM * 512 + 2 * T::kWavesN * T::kM * 4;
+  return after > (uint32_t)T::kLds ? after : T::kLds;
 }
 
 // The same for up to 16 rows, bound by the reading of the weights: a wavefront
@@ -506,22 +516,23 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, k_end);
   typename T::Acc acc;
   gemm_tile<DT, T>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
-  const float f = a.meta->factor;
+  if (splits == 1) {
+    __syncthreads();
+    uint16_t* out = static_cast<uint16_t*>(a.dhidden) + tn * 256;
+    store_tile<DT, T>(acc, a.meta->factor, a.dim - tn * 256, lds, [&](uint32_t m) {
+      const uint32_t row = tm * T::kM + m;
+      return row < live ? out + a.row_of[row] * a.dhidden_stride : nullptr;
+    });
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < T::kI; ++i) {
     const uint32_t row = tm * T::kM + T::row(i);
     if (row >= live) continue;
-    const uint64_t at = a.row_of[row] * a.dhidden_stride;
 #pragma unroll
     for (int j = 0; j < T::kJ; ++j) {
       const uint32_t n = tn * 256 + T::column(j);
-      if (n >= a.dim) continue;
-      if (splits > 1) {
-        *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
-      } else {
-        const f32x4 x = acc[i][j] * f;
-        store4<DT>(a.dhidden, at + n, x[0], x[1], x[2], x[3]);
-      }
+      if (n < a.dim) *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
     }
   }
 }
@@ -558,6 +569,15 @@ __global__ void __launch_bounds__(kGemmThreads, T::kM == 64 ? 4 : 2) dweight_ker
   typename T::Acc acc;
   gemm_tile<DT, T>(p, q, 0, live, (lds_char*)lds, acc);
   const float f = a.meta->factor;
+  if (a.first && a.last) {
+    __syncthreads();
+    uint16_t* out = static_cast<uint16_t*>(a.dweight) + tn * 256;
+    store_tile<DT, T>(acc, f, a.dim - tn * 256, lds, [&](uint32_t m) {
+      const uint32_t row = tm * T::kM + m;
+      return row < a.vocab ? out + row * a.dweight_stride : nullptr;
+    });
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < T::kI; ++i) {
     const uint32_t row = tm * T::kM + T::row(i);
@@ -657,7 +677,8 @@ void launch_rows(const HeadArgs& a, hipStream_t stream) {
   } else {
     by_tile(a.rows, [&](auto tile) {
       typedef decltype(tile) T;
-      hipLaunchKernelGGL((logits_kernel<DT, T, KEEP>), (a.rows + T::kM - 1) / T::kM * a.tiles, kGemmThreads, T::kLds, stream, a);
+      hipLaunchKernelGGL((logits_kernel<DT, T, KEEP>), (a.rows + T::kM - 1) / T::kM * a.tiles, kGemmThreads, logits_lds<T>(),
+                         stream, a);
     });
   }
   // with few rows, parts of them: 1024 blocks, of 2048 columns at least
