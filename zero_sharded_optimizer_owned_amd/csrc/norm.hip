@@ -247,40 +247,40 @@ template <int DT, int W, int VPT, bool KEPT>
 __global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const BackwardArgs a) {
   constexpr int N = Lane<DT>::N;
   typedef typename Vec<DT>::T T;
-  __shared__ double part[W];
+  __shared__ double part[2][W];  // in turn, so that a row needs one barrier
   __shared__ float share[W == 1 ? 3 * 64 * N : 1];
   const uint32_t t = Place<W>::lane();
   float dg[VPT][N] = {};
+  u32x4 gain[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) gain[i] = load_cut<DT>(a.gain, t + i * 64 * W, a.dim);
   const uint64_t step = (uint64_t)gridDim.x * Place<W>::kRows;
-  uint64_t row = (uint64_t)blockIdx.x * Place<W>::kRows + Place<W>::row();
-  for (; row < a.n_rows; row += step) {
+  uint32_t turn = 0;
+  for (uint64_t row = (uint64_t)blockIdx.x * Place<W>::kRows + Place<W>::row(); row < a.n_rows; row += step, turn ^= 1) {
     Held<DT, W, VPT, KEPT> x;
     x.load(a, row, t);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const u32x4 g = load_cut<DT>(a.gain, t + i * 64 * W, a.dim);
       float n[N], p = 0.0f;
       x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const float q = Lane<DT>::get(x.d[i], k) * n[k];
         dg[i][k] += q;
-        p = fmaf(q, Lane<DT>::get(g, k), p);
+        p = fmaf(q, Lane<DT>::get(gain[i], k), p);
       }
       sum += (double)p;
     }
-    const float mean = (float)(row_sum<W>(sum, part) / (double)a.dim);
+    const float mean = (float)(row_sum<W, false>(sum, part[turn]) / (double)a.dim);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const uint32_t v = t + i * 64 * W;
-      const u32x4 g = load_cut<DT>(a.gain, v, a.dim);
       float n[N], y[N];
       x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        y[k] = fmaf(x.rstd, fmaf(-n[k], mean, Lane<DT>::get(x.d[i], k) * Lane<DT>::get(g, k)), Lane<DT>::get(x.up[i], k));
-      store_cut<DT>(static_cast<T*>(a.dx) + row * a.dim, v, a.dim, y);
+        y[k] = fmaf(x.rstd, fmaf(-n[k], mean, Lane<DT>::get(x.d[i], k) * Lane<DT>::get(gain[i], k)), Lane<DT>::get(x.up[i], k));
+      store_cut<DT>(static_cast<T*>(a.dx) + row * a.dim, t + i * 64 * W, a.dim, y);
     }
   }
   // the block's wavefronts together, a vector of each at a time
