@@ -10,8 +10,8 @@
 //
 // All of it is bound by HBM: a row is read once, stays in registers (a lane
 // holds up to eight 16-byte vectors) and is written once.  A wavefront takes a
-// row where the row fits one, so that rows need no barrier; longer rows take 4
-// or 8 wavefronts.
+// row where the row fits one, so that rows need no barrier; longer rows take 4,
+// 8 or 16 wavefronts.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -53,7 +53,7 @@ typedef u32x2 __attribute__((aligned(1))) u32x2_any;
 typedef uint32_t __attribute__((aligned(1))) u32_any;
 
 // N codes of a row from element v N on.
-template <int N>
+template <int N, bool WHOLE>
 __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t v, uint32_t dim, const float (&x)[N]) {
   float y[8];
 #pragma unroll
@@ -63,21 +63,21 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint32_t v, uint32_t d
   if (e + N <= dim) {
     if constexpr (N == 8) *reinterpret_cast<u32x2_any*>(row + e) = c;
     else *reinterpret_cast<u32_any*>(row + e) = c[0];
-  } else {
+  } else if (!WHOLE) {
 #pragma unroll
     for (uint32_t k = 0; k < N; ++k)
       if (e + k < dim) row[e + k] = (uint8_t)(c[k >> 2] >> (8 * (k & 3)));
   }
 }
 
-template <int N>
+template <int N, bool WHOLE>
 __device__ __forceinline__ u32x2 load_codes(const uint8_t* row, uint32_t v, uint32_t dim) {
   const uint32_t e = v * N;
   u32x2 c = {0, 0};
   if (e + N <= dim) {
     if constexpr (N == 8) c = *reinterpret_cast<const u32x2_any*>(row + e);
     else c[0] = *reinterpret_cast<const u32_any*>(row + e);
-  } else if (e < dim) {
+  } else if (!WHOLE && e < dim) {
 #pragma unroll
     for (uint32_t k = 0; k < N; ++k)
       if (e + k < dim) c[k >> 2] |= (uint32_t)row[e + k] << (8 * (k & 3));
@@ -94,7 +94,8 @@ struct Place {
 };
 
 // VPT vectors to a lane: lane t of a row's 64 W holds vectors t, t + 64 W, ...
-template <int DT, int W, int VPT>
+// WHOLE: rows are whole vectors.
+template <int DT, int W, int VPT, bool WHOLE>
 __global__ void __launch_bounds__(Place<W>::kThreads) norm_kernel(const NormArgs a) {
   constexpr int N = Lane<DT>::N;
   typedef typename Vec<DT>::T T;
@@ -105,10 +106,10 @@ __global__ void __launch_bounds__(Place<W>::kThreads) norm_kernel(const NormArgs
     const uint64_t at = row * a.dim;
     u32x4 h[VPT], r[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) h[i] = load_cut<DT>(static_cast<const T*>(a.x) + at, t + i * 64 * W, a.dim);
+    for (int i = 0; i < VPT; ++i) h[i] = load_cut<DT, WHOLE>(static_cast<const T*>(a.x) + at, t + i * 64 * W, a.dim);
     if (a.residual) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) r[i] = load_cut<DT>(static_cast<const T*>(a.residual) + at, t + i * 64 * W, a.dim);
+      for (int i = 0; i < VPT; ++i) r[i] = load_cut<DT, WHOLE>(static_cast<const T*>(a.residual) + at, t + i * 64 * W, a.dim);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
 #pragma unroll
@@ -138,11 +139,11 @@ __global__ void __launch_bounds__(Place<W>::kThreads) norm_kernel(const NormArgs
       float x[N], y[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) x[k] = Lane<DT>::get(h[i], k);
-      if (a.h) store_cut<DT>(static_cast<T*>(a.h) + at, v, a.dim, x);
-      const u32x4 g = load_cut<DT>(a.gain, v, a.dim);
+      if (a.h) store_cut<DT, false, WHOLE>(static_cast<T*>(a.h) + at, v, a.dim, x);
+      const u32x4 g = load_cut<DT, WHOLE>(a.gain, v, a.dim);
 #pragma unroll
       for (int k = 0; k < N; ++k) y[k] = x[k] * rstd * Lane<DT>::get(g, k);
-      store_cut<DT>(static_cast<T*>(a.out) + at, v, a.dim, y);
+      store_cut<DT, false, WHOLE>(static_cast<T*>(a.out) + at, v, a.dim, y);
       if (a.codes) {
         // magnitudes by their bits, where NaN is largest
         uint32_t top = 0;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(Place<W>::kThreads) norm_kernel(const NormArgs
         float c[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) c[k] = x[k] * inv;
-        store_codes<N>(a.codes + at, v, a.dim, c);
+        store_codes<N, WHOLE>(a.codes + at, v, a.dim, c);
         if (v % (128 / N) == 0 && v * N < a.dim)
           a.scales[row * a.blocks + v * N / 128] = live ? m * (1.0f / kE4m3Max) + (m - m) : 0.0f;  // not finite: NaN
       }
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(Place<W>::kThreads) norm_kernel(const NormArgs
 }
 
 // y = n gain from the kept form.
-template <int DT, int W, int VPT>
+template <int DT, int W, int VPT, bool WHOLE>
 __global__ void __launch_bounds__(Place<W>::kThreads) restore_kernel(const NormArgs a) {
   constexpr int N = Lane<DT>::N;
   typedef typename Vec<DT>::T T;
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(Place<W>::kThreads) restore_kernel(const NormA
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const uint32_t v = t + i * 64 * W;
-      c[i] = load_codes<N>(a.codes + at, v, a.dim);
+      c[i] = load_codes<N, WHOLE>(a.codes + at, v, a.dim);
       s[i] = v * N < a.dim ? a.scales[row * a.blocks + v * N / 128] : 0.0f;
     }
 #pragma unroll
@@ -187,16 +188,16 @@ __global__ void __launch_bounds__(Place<W>::kThreads) restore_kernel(const NormA
       const uint32_t v = t + i * 64 * W;
       float x[8], y[N];
       decode8(c[i], x);
-      const u32x4 g = load_cut<DT>(a.gain, v, a.dim);
+      const u32x4 g = load_cut<DT, WHOLE>(a.gain, v, a.dim);
 #pragma unroll
       for (int k = 0; k < N; ++k) y[k] = x[k] * s[i] * rstd * Lane<DT>::get(g, k);
-      store_cut<DT>(static_cast<T*>(a.out) + at, v, a.dim, y);
+      store_cut<DT, false, WHOLE>(static_cast<T*>(a.out) + at, v, a.dim, y);
     }
   }
 }
 
 // One row of the backward pass in registers.
-template <int DT, int W, int VPT, bool KEPT>
+template <int DT, int W, int VPT, bool KEPT, bool WHOLE>
 struct Held {
   static constexpr int N = Lane<DT>::N;
   u32x4 d[VPT], up[VPT], h[KEPT ? 1 : VPT];
@@ -210,18 +211,18 @@ struct Held {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const uint32_t v = t + i * 64 * W;
-      d[i] = load_cut<DT>(static_cast<const T*>(a.dy) + at, v, a.dim);
+      d[i] = load_cut<DT, WHOLE>(static_cast<const T*>(a.dy) + at, v, a.dim);
       if constexpr (KEPT) {
-        c[i] = load_codes<N>(a.codes + at, v, a.dim);
+        c[i] = load_codes<N, WHOLE>(a.codes + at, v, a.dim);
         s[i] = v * N < a.dim ? a.scales[row * a.blocks + v * N / 128] : 0.0f;
       } else {
-        h[i] = load_cut<DT>(static_cast<const T*>(a.h) + at, v, a.dim);
+        h[i] = load_cut<DT, WHOLE>(static_cast<const T*>(a.h) + at, v, a.dim);
       }
     }
     if (a.upstream) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
-        up[i] = load_cut<DT>(static_cast<const T*>(a.upstream) + at, t + i * 64 * W, a.dim);
+        up[i] = load_cut<DT, WHOLE>(static_cast<const T*>(a.upstream) + at, t + i * 64 * W, a.dim);
     } else {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) up[i] = u32x4{0, 0, 0, 0};
@@ -240,68 +241,79 @@ struct Held {
   }
 };
 
-// A block goes over rows blockIdx, blockIdx + gridDim, ... (four at a time where
-// a wavefront takes a row), adds up dy n in registers and leaves one partial
-// row for fold_kernel.
-template <int DT, int W, int VPT, bool KEPT>
-__global__ void __launch_bounds__(Place<W>::kThreads) backward_kernel(const BackwardArgs a) {
-  constexpr int N = Lane<DT>::N;
+// The backward pass's block: kRows rows at a time, of kLanes threads each.
+template <int W, int VPT>
+struct Group {
+  static constexpr int kLanes = 64 * W, kRows = W == 1 ? 4 : W == 4 && VPT <= 2 ? 2 : 1, kThreads = kLanes * kRows;
+};
+
+// A block goes over groups of rows blockIdx, blockIdx + gridDim, ..., adds up
+// dy n in registers and leaves one partial row for fold_kernel.
+template <int DT, int W, int VPT, bool KEPT, bool WHOLE>
+__global__ void __launch_bounds__((Group<W, VPT>::kThreads)) backward_kernel(const BackwardArgs a) {
+  constexpr int N = Lane<DT>::N, kLanes = Group<W, VPT>::kLanes, kRows = Group<W, VPT>::kRows;
   typedef typename Vec<DT>::T T;
-  __shared__ double part[2][W];  // in turn, so that a row needs one barrier
-  __shared__ float share[W == 1 ? 3 * 64 * N : 1];
-  const uint32_t t = Place<W>::lane();
+  __shared__ double part[2][kRows][W];  // in turn, so that a row needs one barrier
+  __shared__ float share[kRows > 1 ? (kRows - 1) * kLanes * N : 1];
+  const uint32_t t = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
   float dg[VPT][N] = {};
-  u32x4 gain[VPT];
+  // kept in registers, but for blocks of 16 wavefronts, which have few
+  u32x4 held[W < 16 ? VPT : 1];
+  const auto gain_at = [&](int i) { return load_cut<DT, WHOLE>(a.gain, t + i * kLanes, a.dim); };
+  if constexpr (W < 16) {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) gain[i] = load_cut<DT>(a.gain, t + i * 64 * W, a.dim);
-  const uint64_t step = (uint64_t)gridDim.x * Place<W>::kRows;
+    for (int i = 0; i < VPT; ++i) held[i] = gain_at(i);
+  }
   uint32_t turn = 0;
-  for (uint64_t row = (uint64_t)blockIdx.x * Place<W>::kRows + Place<W>::row(); row < a.n_rows; row += step, turn ^= 1) {
-    Held<DT, W, VPT, KEPT> x;
+  for (uint64_t row0 = (uint64_t)blockIdx.x * kRows; row0 < a.n_rows; row0 += (uint64_t)gridDim.x * kRows, turn ^= 1) {
+    const bool has = row0 + g < a.n_rows;
+    const uint64_t row = has ? row0 + g : row0;  // behind the last row: one that is not counted
+    Held<DT, W, VPT, KEPT, WHOLE> x;
     x.load(a, row, t);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      const u32x4 gain = W < 16 ? held[i % (W < 16 ? VPT : 1)] : gain_at(i);
       float n[N], p = 0.0f;
       x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const float q = Lane<DT>::get(x.d[i], k) * n[k];
-        dg[i][k] += q;
-        p = fmaf(q, Lane<DT>::get(gain[i], k), p);
+        dg[i][k] += has ? q : 0.0f;
+        p = fmaf(q, Lane<DT>::get(gain, k), p);
       }
       sum += (double)p;
     }
-    const float mean = (float)(row_sum<W, false>(sum, part[turn]) / (double)a.dim);
+    const float mean = (float)(row_sum<W, false>(sum, part[turn][g]) / (double)a.dim);
+    if (!has) continue;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
+      const u32x4 gain = W < 16 ? held[i % (W < 16 ? VPT : 1)] : gain_at(i);
       float n[N], y[N];
       x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        y[k] = fmaf(x.rstd, fmaf(-n[k], mean, Lane<DT>::get(x.d[i], k) * Lane<DT>::get(gain[i], k)), Lane<DT>::get(x.up[i], k));
-      store_cut<DT>(static_cast<T*>(a.dx) + row * a.dim, t + i * 64 * W, a.dim, y);
+        y[k] = fmaf(x.rstd, fmaf(-n[k], mean, Lane<DT>::get(x.d[i], k) * Lane<DT>::get(gain, k)), Lane<DT>::get(x.up[i], k));
+      store_cut<DT, false, WHOLE>(static_cast<T*>(a.dx) + row * a.dim, t + i * kLanes, a.dim, y);
     }
   }
-  // the block's wavefronts together, a vector of each at a time
+  // the block's rows together, a vector of each at a time
   const uint64_t at = (uint64_t)blockIdx.x * ((a.dim + 7) / 8 * 8);
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const uint32_t v = t + i * 64 * W;
-    if constexpr (W == 1) {
-      const uint32_t w = threadIdx.x >> 6;
+    const uint32_t v = t + i * kLanes;
+    if constexpr (kRows > 1) {
       __syncthreads();
-      if (w > 0) {
+      if (g > 0) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) share[((w - 1) * N + k) * 64 + t] = dg[i][k];
+        for (int k = 0; k < N; ++k) share[((g - 1) * N + k) * kLanes + t] = dg[i][k];
       }
       __syncthreads();
-      if (w == 0) {
+      if (g > 0) continue;
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          dg[i][k] += share[k * 64 + t] + share[(N + k) * 64 + t] + share[(2 * N + k) * 64 + t];
-      }
-      if (w > 0) continue;
+      for (int r = 0; r < kRows - 1; ++r)
+#pragma unroll
+        for (int k = 0; k < N; ++k) dg[i][k] += share[(r * N + k) * kLanes + t];
     }
     if (v * N < a.dim) {
 #pragma unroll
@@ -346,14 +358,17 @@ __global__ void __launch_bounds__(kFoldColumns * kFoldGroups) fold_kernel(const 
 template <int DT, typename F>
 void by_width(uint32_t dim, F fn) {
   const uint32_t vecs = (dim + Lane<DT>::N - 1) / Lane<DT>::N;
-  const auto go = [&](auto w, auto v) { fn(w, v); };
+  const auto go = [&](auto w, auto v) {
+    if (dim % Lane<DT>::N == 0) fn(w, v, std::true_type{});
+    else fn(w, v, std::false_type{});
+  };
   if (vecs <= 64) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
   else if (vecs <= 128) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
   else if (vecs <= 256) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
   else if (vecs <= 512) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   else if (vecs <= 1024) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
   else if (vecs <= 2048) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
-  else if constexpr (DT == ZERO_F32) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+  else if constexpr (DT == ZERO_F32) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
 }
 
 int check_rows(uint64_t n_rows, uint32_t dim, int dtype, const char* who) {
@@ -366,14 +381,10 @@ int check_rows(uint64_t n_rows, uint32_t dim, int dtype, const char* who) {
 uint32_t scales_of(uint32_t dim) { return (dim + ZERO_QBLOCK - 1) / ZERO_QBLOCK; }
 
 // Blocks of the backward pass.  Each leaves a partial row of dgain in fp32, so
-// from 512 groups of rows on a block takes two of them, and from 2048 on more:
-// 999 rows of 5003 fp16 25 us in 999 blocks, 20 in 512, 25 in 256; 16,384 rows of
-// 4096 bf16 (the restored output included) 144 us in 2048 blocks, 138 in 1024,
-// 141 in 512.
-constexpr uint64_t kBackwardBlocks = 1024;
-uint64_t backward_blocks(uint64_t groups) {
-  return std::min(kBackwardBlocks, groups <= 512 ? groups : std::max<uint64_t>(512, groups / 2));
-}
+// there are 512 at most: 16,384 rows of 4096 bf16 (the restored output included)
+// 133 us in 512 blocks of two rows at a time, 136 in 768, 138 in 1024; 999 rows of
+// 5003 fp16, a row at a time, 25 us in 999 blocks, 20 in 512, 25 in 256.
+constexpr uint64_t kBackwardBlocks = 512;
 
 }  // namespace
 }  // namespace zs
@@ -400,10 +411,11 @@ extern "C" int zero_rms_norm(const void* x, const void* residual, const void* ga
   const NormArgs a = {x, residual, gain, h, out, codes, scales, rstd, n_rows, dim, scales_of(dim), eps};
   with_dtype(dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    by_width<DT>(dim, [&](auto w, auto v) {
+    by_width<DT>(dim, [&](auto w, auto v, auto whole) {
       constexpr int W = decltype(w)::value, VPT = decltype(v)::value;
+      constexpr bool WHOLE = decltype(whole)::value;
       const uint64_t blocks = (n_rows + Place<W>::kRows - 1) / Place<W>::kRows;
-      hipLaunchKernelGGL((norm_kernel<DT, W, VPT>), chunk_grid(std::min<uint64_t>(blocks, 1u << 20), 0),
+      hipLaunchKernelGGL((norm_kernel<DT, W, VPT, WHOLE>), chunk_grid(std::min<uint64_t>(blocks, 1u << 20), 0),
                          Place<W>::kThreads, 0, stream, a);
     });
   });
@@ -434,10 +446,11 @@ extern "C" int zero_rms_norm_restore(const uint8_t* codes, const float* scales, 
   a.blocks = scales_of(dim);
   with_dtype(dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
-    by_width<DT>(dim, [&](auto w, auto v) {
+    by_width<DT>(dim, [&](auto w, auto v, auto whole) {
       constexpr int W = decltype(w)::value, VPT = decltype(v)::value;
+      constexpr bool WHOLE = decltype(whole)::value;
       const uint64_t blocks = (n_rows + Place<W>::kRows - 1) / Place<W>::kRows;
-      hipLaunchKernelGGL((restore_kernel<DT, W, VPT>), chunk_grid(std::min<uint64_t>(blocks, 1u << 20), 0),
+      hipLaunchKernelGGL((restore_kernel<DT, W, VPT, WHOLE>), chunk_grid(std::min<uint64_t>(blocks, 1u << 20), 0),
                          Place<W>::kThreads, 0, stream, a);
     });
   });
@@ -483,13 +496,15 @@ extern "C" int zero_rms_norm_backward(const zero_rms_norm_backward_args* p, hipS
                             static_cast<float*>(p->workspace), p->n_rows, p->dim, scales_of(p->dim)};
     with_dtype(p->dtype, [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
-      by_width<DT>(p->dim, [&](auto w, auto v) {
+      by_width<DT>(p->dim, [&](auto w, auto v, auto whole) {
         constexpr int W = decltype(w)::value, VPT = decltype(v)::value;
-        parts = (uint32_t)backward_blocks((p->n_rows + Place<W>::kRows - 1) / Place<W>::kRows);
+        constexpr bool WHOLE = decltype(whole)::value;
+        typedef Group<W, VPT> G;
+        parts = (uint32_t)std::min<uint64_t>((p->n_rows + G::kRows - 1) / G::kRows, kBackwardBlocks);
         if (p->codes)
-          hipLaunchKernelGGL((backward_kernel<DT, W, VPT, true>), parts, Place<W>::kThreads, 0, stream, a);
+          hipLaunchKernelGGL((backward_kernel<DT, W, VPT, true, WHOLE>), parts, G::kThreads, 0, stream, a);
         else
-          hipLaunchKernelGGL((backward_kernel<DT, W, VPT, false>), parts, Place<W>::kThreads, 0, stream, a);
+          hipLaunchKernelGGL((backward_kernel<DT, W, VPT, false, WHOLE>), parts, G::kThreads, 0, stream, a);
       });
     });
     if ((rc = launch_status(who))) return rc;

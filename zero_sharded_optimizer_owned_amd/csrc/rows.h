@@ -60,14 +60,15 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t x) {
 }
 
 // Elements [v N, v N + N) of a row of `dim` elements at `row`, N = Lane<DT>::N;
-// those past the row's end are zero and are not touched.
-template <int DT>
+// those past the row's end are zero and are not touched.  WHOLE: dim is a
+// multiple of N (the loads of single elements cost registers even where none runs).
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ u32x4 load_cut(const void* row, uint32_t v, uint32_t dim) {
   constexpr uint32_t N = Lane<DT>::N;
   const uint32_t e = v * N;
   if (e + N <= dim) return load16_any(row, v);
   u32x4 r = {0, 0, 0, 0};
-  if (e < dim) {
+  if (!WHOLE && e < dim) {
     const typename Vec<DT>::T* p = static_cast<const typename Vec<DT>::T*>(row);
 #pragma unroll
     for (uint32_t k = 0; k < N; ++k) {
@@ -80,12 +81,12 @@ __device__ __forceinline__ u32x4 load_cut(const void* row, uint32_t v, uint32_t 
   return r;
 }
 
-template <int DT, bool NT = false>
+template <int DT, bool NT = false, bool WHOLE = false>
 __device__ __forceinline__ void store_cut(void* row, uint32_t v, uint32_t dim, const float (&x)[Lane<DT>::N]) {
   constexpr uint32_t N = Lane<DT>::N;
   const uint32_t e = v * N;
   if (e + N <= dim) store16_any<DT, NT>(row, v, x);
-  else
+  else if (!WHOLE)
 #pragma unroll
     for (uint32_t k = 0; k < N; ++k)
       if (e + k < dim) Vec<DT>::store1(row, e + k, x[k]);
