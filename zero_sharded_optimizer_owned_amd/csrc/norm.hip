@@ -10,8 +10,8 @@
 //
 // All of it is bound by HBM: a row is read once, stays in registers (a lane
 // holds up to eight 16-byte vectors) and is written once.  A wavefront takes a
-// row where the row fits one, so that rows need no barrier; longer rows take 4,
-// 8 or 16 wavefronts.
+// row where the row fits one, so that rows need no barrier; longer rows take 4
+// or 8 wavefronts.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -257,10 +257,10 @@ __global__ void __launch_bounds__((Group<W, VPT>::kThreads)) backward_kernel(con
   __shared__ float share[kRows > 1 ? (kRows - 1) * kLanes * N : 1];
   const uint32_t t = threadIdx.x % kLanes, g = threadIdx.x / kLanes;
   float dg[VPT][N] = {};
-  // kept in registers, but for blocks of 16 wavefronts, which have few
-  u32x4 held[W < 16 ? VPT : 1];
+  // in registers, but for rows that fill them by themselves
+  u32x4 held[VPT < 8 ? VPT : 1];
   const auto gain_at = [&](int i) { return load_cut<DT, WHOLE>(a.gain, t + i * kLanes, a.dim); };
-  if constexpr (W < 16) {
+  if constexpr (VPT < 8) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) held[i] = gain_at(i);
   }
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__((Group<W, VPT>::kThreads)) backward_kernel(con
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const u32x4 gain = W < 16 ? held[i % (W < 16 ? VPT : 1)] : gain_at(i);
+      const u32x4 gain = VPT < 8 ? held[i % (VPT < 8 ? VPT : 1)] : gain_at(i);
       float n[N], p = 0.0f;
       x.normalised(i, n);
 #pragma unroll
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__((Group<W, VPT>::kThreads)) backward_kernel(con
     if (!has) continue;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const u32x4 gain = W < 16 ? held[i % (W < 16 ? VPT : 1)] : gain_at(i);
+      const u32x4 gain = VPT < 8 ? held[i % (VPT < 8 ? VPT : 1)] : gain_at(i);
       float n[N], y[N];
       x.normalised(i, n);
 #pragma unroll
@@ -359,8 +359,11 @@ template <int DT, typename F>
 void by_width(uint32_t dim, F fn) {
   const uint32_t vecs = (dim + Lane<DT>::N - 1) / Lane<DT>::N;
   const auto go = [&](auto w, auto v) {
-    if (dim % Lane<DT>::N == 0) fn(w, v, std::true_type{});
-    else fn(w, v, std::false_type{});
+    // (with eight vectors to a lane the kernels of whole vectors spill registers)
+    if constexpr (decltype(v)::value < 8) {
+      if (dim % Lane<DT>::N == 0) return fn(w, v, std::true_type{});
+    }
+    fn(w, v, std::false_type{});
   };
   if (vecs <= 64) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
   else if (vecs <= 128) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{});
@@ -368,7 +371,7 @@ void by_width(uint32_t dim, F fn) {
   else if (vecs <= 512) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
   else if (vecs <= 1024) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
   else if (vecs <= 2048) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
-  else if constexpr (DT == ZERO_F32) go(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
+  else if constexpr (DT == ZERO_F32) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
 }
 
 int check_rows(uint64_t n_rows, uint32_t dim, int dtype, const char* who) {

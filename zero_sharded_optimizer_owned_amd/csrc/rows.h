@@ -30,15 +30,15 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x + __shfl_xor(x, 32, 64);
 }
 
-// Sum over the W wavefronts of a row, in every thread.  `part` holds W
-// numbers; the caller's block is one row when W > 1.  SYNC: part may still be
+// Sum over the W wavefronts of a row, in every thread.  `part` holds the row's W
+// numbers; a block's rows begin at multiples of W wavefronts.  SYNC: part may still be
 // read from a sum before.
 template <int W, bool SYNC = true>
 __device__ __forceinline__ double row_sum(double x, double* part) {
   x = wave_sum(x);
   if constexpr (W > 1) {
     if constexpr (SYNC) __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
+    if ((threadIdx.x & 63) == 0) part[(threadIdx.x >> 6) % W] = x;
     __syncthreads();
     x = 0.0;
 #pragma unroll
