@@ -40,6 +40,15 @@ constexpr int kGemmThreads = 512;
 constexpr int kWaves = kGemmThreads / 64;
 constexpr int kTileN = 256, kTileK = 64;
 
+// threadIdx.x, not to be recognised as such: what is computed from it behind a
+// product would otherwise be computed before it and kept in registers meanwhile,
+// of which the sums leave few.
+__device__ __forceinline__ uint32_t thread_anew() {
+  uint32_t t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 // Tiles of M rows with `Slots` steps in LDS.
 template <int M, int Slots>
 struct Tile {
@@ -50,12 +59,12 @@ struct Tile {
   static constexpr int kI = kWaveM / 16, kJ = kWaveN / 16;
   static constexpr int kLoads = M / 64 + kTileN / 64;  // a wavefront's, of a step
   typedef f32x4 Acc[kI][kJ];
-  // acc[i][j][x] is m = row(i), n = column(j) + x of the tile
-  static __device__ __forceinline__ uint32_t row(int i) {
-    return wave_of_block() / kWavesN * kWaveM + 16 * i + threadIdx.x % 16;
+  // acc[i][j][x] of thread t is m = row(i, t), n = column(j, t) + x of the tile
+  static __device__ __forceinline__ uint32_t row(int i, uint32_t t) {
+    return wave_of_block() / kWavesN * kWaveM + 16 * i + t % 16;
   }
-  static __device__ __forceinline__ uint32_t column(int j) {
-    return wave_of_block() % kWavesN * kWaveN + 16 * j + threadIdx.x % 64 / 16 * 4;
+  static __device__ __forceinline__ uint32_t column(int j, uint32_t t) {
+    return wave_of_block() % kWavesN * kWaveN + 16 * j + t % 64 / 16 * 4;
   }
 };
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: reads zero
@@ -105,8 +114,8 @@ struct Rows {
     load_to_lds(base + (uint64_t)k0 * 2, k0 + k < depth ? offset[i] : kNowhere, tile + (wave_of_block() * kLoads + i) * 1024);
   }
   // Eight k from 32 kk + 8 (lane / 16) on of row r0 + lane % 16.
-  static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
-    const uint32_t lane = threadIdx.x & 63, row = r0 + lane % 16, piece = (lane / 16 + 4 * kk) ^ (row % 8);
+  static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk, uint32_t lane) {
+    const uint32_t row = r0 + lane % 16, piece = (lane / 16 + 4 * kk) ^ (row % 8);
     return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(tile + row * 128 + piece * 16);
   }
 };
@@ -145,8 +154,7 @@ struct Columns {
     load_to_lds(base + k0 * stride * 2, k0 + row_of(i) < depth ? offset[i] : kNowhere,
                 tile + (wave_of_block() * kLoads + i) * 1024);
   }
-  static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk) {
-    const uint32_t lane = threadIdx.x & 63;
+  static __device__ __forceinline__ u32x4 fragment(const lds_char* tile, uint32_t r0, uint32_t kk, uint32_t lane) {
     u32x4 f;
 #pragma unroll
     for (uint32_t h = 0; h < 2; ++h) {
@@ -170,18 +178,22 @@ __device__ __forceinline__ void wait_loads() {
   else asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
 }
 
-// k runs over [k_begin, k_end), k_begin a multiple of 64; both operands are zero
-// from k_end on.
+template <class T>
+__device__ __forceinline__ void clear(typename T::Acc& acc) {
+#pragma unroll
+  for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::kJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+}
+
+// Adds to acc.  k runs over [k_begin, k_end), k_begin a multiple of 64; both
+// operands are zero from k_end on.
 template <int DT, class T, class P, class Q>
 __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_begin, uint32_t k_end, lds_char* lds,
                                           typename T::Acc& acc) {
   constexpr int I = T::kI, J = T::kJ;
   static_assert(P::kLoads + Q::kLoads == T::kLoads, "operands of the tile's sizes");
   const uint32_t m0 = wave_of_block() / T::kWavesN * T::kWaveM, n0 = wave_of_block() % T::kWavesN * T::kWaveN;
-#pragma unroll
-  for (int i = 0; i < I; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   if (k_begin >= k_end) return;
   // Half steps of 32 k.  A half step's fragments are read during the one
   // before: those of Q into registers of their own, those of P each behind the
@@ -189,7 +201,7 @@ __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_beg
   // tiles are read, behind a barrier at which they have arrived and this step's
   // are no longer read, so that the loads of a later step can take its slot.
   u32x4 a[2][J], b[I];
-  const uint32_t base = (uint32_t)(uintptr_t)lds;
+  const uint32_t base = (uint32_t)(uintptr_t)lds, lane = threadIdx.x & 63;
   const auto load = [&](uint32_t k, uint32_t slot, int i) {  // this wavefront's i-th load of a step
     if (i < P::kLoads) p.load(k, base + slot, i);
     else q.load(k, base + slot + T::kBytesP, i - P::kLoads);
@@ -211,18 +223,18 @@ __device__ __forceinline__ void gemm_tile(const P& p, const Q& q, uint32_t k_beg
   for (int i = 0; i < T::kLoads; ++i) load(k_load, (T::kSlots - 1) * T::kSlotBytes, i);
   k_load += kTileK;
 #pragma unroll
-  for (int j = 0; j < J; ++j) a[0][j] = Q::fragment(lds + T::kBytesP, n0 + 16 * j, 0);
+  for (int j = 0; j < J; ++j) a[0][j] = Q::fragment(lds + T::kBytesP, n0 + 16 * j, 0, lane);
 #pragma unroll
-  for (int i = 0; i < I; ++i) b[i] = P::fragment(lds, m0 + 16 * i, 0);
+  for (int i = 0; i < I; ++i) b[i] = P::fragment(lds, m0 + 16 * i, 0, lane);
   uint32_t now = 0;
   const auto half = [&](uint32_t h, const lds_char* from, uint32_t free) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) a[h ^ 1][j] = Q::fragment(from + T::kBytesP, n0 + 16 * j, h ^ 1);
+    for (int j = 0; j < J; ++j) a[h ^ 1][j] = Q::fragment(from + T::kBytesP, n0 + 16 * j, h ^ 1, lane);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
 #pragma unroll
       for (int j = 0; j < J; ++j) acc[i][j] = mfma16<DT>(a[h][j], b[i], acc[i][j]);
-      b[i] = P::fragment(from, m0 + 16 * i, h ^ 1);
+      b[i] = P::fragment(from, m0 + 16 * i, h ^ 1, lane);
       if (h == 1) {
         constexpr int kEach = (T::kLoads + I / 2 - 1) / (I / 2);  // within the first half of the products
 #pragma unroll
@@ -255,10 +267,10 @@ __device__ __forceinline__ void put_quad(char* lds, uint32_t m, uint32_t n, cons
 // `row(m)`: where row m of the tile begins, NULL for none; columns from `columns`
 // (a multiple of 8) on are left out.
 template <int M, typename F>
-__device__ __forceinline__ void store_rows(const char* lds, uint32_t columns, F row) {
-  const uint32_t c = threadIdx.x % 32;
+__device__ __forceinline__ void store_rows(const char* lds, uint32_t columns, uint32_t t, F row) {
+  const uint32_t c = t % 32;
 #pragma unroll 4
-  for (uint32_t m = threadIdx.x / 32; m < M; m += kGemmThreads / 32) {
+  for (uint32_t m = t / 32; m < M; m += kGemmThreads / 32) {
     uint16_t* to = row(m);
     if (to && c * 8 < columns)
       *reinterpret_cast<u32x4*>(to + c * 8) = *reinterpret_cast<const u32x4*>(lds + m * 512 + (c ^ (m % 32)) * 16);
@@ -267,14 +279,14 @@ __device__ __forceinline__ void store_rows(const char* lds, uint32_t columns, F 
 
 // The tile times f.  The caller's wavefronts are done with LDS.
 template <int DT, class T, typename F>
-__device__ __forceinline__ void store_tile(const typename T::Acc& acc, float f, uint32_t columns, char* lds, F row) {
+__device__ __forceinline__ void store_tile(const typename T::Acc& acc, float f, uint32_t columns, char* lds, uint32_t t, F row) {
   static_assert(T::kM * kTileN * 2 <= T::kLds, "the tile in 16 bits");
 #pragma unroll
   for (int i = 0; i < T::kI; ++i)
 #pragma unroll
-    for (int j = 0; j < T::kJ; ++j) put_quad<DT>(lds, T::row(i), T::column(j), acc[i][j] * f);
+    for (int j = 0; j < T::kJ; ++j) put_quad<DT>(lds, T::row(i, t), T::column(j, t), acc[i][j] * f);
   __syncthreads();
-  store_rows<T::kM>(lds, columns, row);
+  store_rows<T::kM>(lds, columns, t, row);
 }
 
 }  // namespace zs

@@ -18,7 +18,10 @@
 //   dhidden, dweight  products two and three
 // dx is held as (softmax - onehot) w / max|w| 2^14 in 16 bits; the common factor
 // comes back in the epilogues, so that fp16 keeps probabilities down to 2^-38
-// whatever the loss scale.
+// whatever the loss scale.  The entry at the target, as a rule far larger than the
+// others, whose roundings average out in the sums, would leave its own rounding in
+// both gradients: what it loses in 16 bits is kept beside it and goes into dhidden in
+// the epilogue, into dweight as further terms of the product.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -61,6 +64,7 @@ struct HeadArgs {
   Meta* meta;
   uint32_t *row_of, *target;  // of each row that counts
   float *omega, *said;        // w / max|w|; the target's logit
+  float* rest;                // what dx's entry at the target loses in 16 bits
   double* terms;              // w lp of the piece's rows
   uint8_t* counts;            // of the piece's rows
   uint16_t *kept, *held;      // rows that count [rows][dim8]; exponentials, then dx [rows][padded]
@@ -257,10 +261,11 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
   p.begin(a.kept, (uint64_t)tm * T::kM, live, a.dim, a.dim);
   q.begin(a.weight, (uint64_t)tn * 256, a.vocab, a.weight_stride, a.dim);
   typename T::Acc acc;
+  clear<T>(acc);
   gemm_tile<DT, T>(p, q, 0, a.dim, (lds_char*)lds, acc);
   // the tile's maximum of each row, over the wavefronts that share it
   constexpr int W = T::kWavesN;
-  const uint32_t lane = threadIdx.x & 63, share = wave_of_block() % W * T::kM;
+  const uint32_t t = thread_anew(), lane = t & 63, share = wave_of_block() % W * T::kM;
   float* red = reinterpret_cast<float*>(lds + T::kM * 512);  // behind the tile's exponentials in 16 bits
   const auto most = [&](uint32_t r) {
     float m = red[r];
@@ -276,22 +281,22 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
     for (int j = 0; j < T::kJ; ++j)
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        if (tn * 256 + T::column(j) + x < a.vocab) top = fmaxf(top, acc[i][j][x]);
+        if (tn * 256 + T::column(j, t) + x < a.vocab) top = fmaxf(top, acc[i][j][x]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    if (lane < 16) red[share + T::row(i)] = top;
+    if (lane < 16) red[share + T::row(i, t)] = top;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < T::kI; ++i) {
-    const uint32_t r = T::row(i), row = tm * T::kM + r;
+    const uint32_t r = T::row(i, t), row = tm * T::kM + r;
     const bool has = row < live;
     const float top = most(r), m = top == -INFINITY ? 0.0f : top;
     const uint32_t target = has ? a.target[row] : 0xFFFFFFFFu;
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < T::kJ; ++j) {
-      const uint32_t n0 = tn * 256 + T::column(j);
+      const uint32_t n0 = tn * 256 + T::column(j, t);
       float e[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -300,22 +305,22 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
         if (n == target) a.said[row] = acc[i][j][x];
         else sum += e[x];
       }
-      if constexpr (KEEP) put_quad<ZERO_F16>(lds, r, T::column(j), f32x4{e[0], e[1], e[2], e[3]} * kTileExp);
+      if constexpr (KEEP) put_quad<ZERO_F16>(lds, r, T::column(j, t), f32x4{e[0], e[1], e[2], e[3]} * kTileExp);
     }
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
     if (lane < 16) red[W * T::kM + share + r] = sum;
   }
   __syncthreads();
-  if (threadIdx.x < T::kM && tm * T::kM + threadIdx.x < live) {
-    const uint32_t r = threadIdx.x;
+  if (t < T::kM && tm * T::kM + t < live) {
+    const uint32_t r = t;
     float sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) sum += red[(W + w) * T::kM + r];
     a.stats[(uint64_t)(tm * T::kM + r) * a.tiles + tn] = f32x2{most(r), sum};
   }
   if constexpr (KEEP)
-    store_rows<T::kM>(lds, 256, [&](uint32_t m) {
+    store_rows<T::kM>(lds, 256, t, [&](uint32_t m) {
       const uint32_t row = tm * T::kM + m;
       return row < live ? a.held + (uint64_t)row * a.padded + tn * 256 : nullptr;
     });
@@ -455,6 +460,8 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
       const float omega = a.omega[row] * kHeld;
       const float unit = (float)((double)omega / all) * (1.0f / kTileExp);
       const float other = -(float)((double)omega * (sum / all));  // at the target: p - 1, without cancellation
+      if (t == 0 && blockIdx.y == 0)
+        a.rest[row] = other - Vec<DT>::get(typename Vec<DT>::Raw{u32x4{Vec<DT>::pack(other, 0.0f), 0, 0, 0}}, 0);
       uint16_t* held = a.held + (uint64_t)row * a.padded;
       for (uint32_t first = tile0; first < tile1; first += kPartTiles) {
         const uint32_t end = min(first + kPartTiles, tile1);
@@ -515,11 +522,31 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   p.begin(a.held, (uint64_t)tm * T::kM, live, a.padded, (k_end + 7) / 8 * 8);
   q.begin(a.weight, (uint64_t)tn * 256, a.dim, a.weight_stride, k_end);
   typename T::Acc acc;
+  clear<T>(acc);
   gemm_tile<DT, T>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
+  const uint32_t t = thread_anew();
+  if (split == 0) {  // what the targets' entries lost
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i) {
+      const uint32_t row = tm * T::kM + T::row(i, t);
+      if (row >= live) continue;
+      const float rest = a.rest[row];
+      const uint16_t* w = static_cast<const uint16_t*>(a.weight) + a.target[row] * a.weight_stride;
+#pragma unroll
+      for (int j = 0; j < T::kJ; ++j) {
+        const uint32_t n = tn * 256 + T::column(j, t);
+        if (n >= a.dim) continue;
+        const u32x2 v = *reinterpret_cast<const u32x2*>(w + n);
+        const typename Vec<DT>::Raw r = {u32x4{v[0], v[1], 0, 0}};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(rest, Vec<DT>::get(r, x), acc[i][j][x]);
+      }
+    }
+  }
   if (splits == 1) {
     __syncthreads();
     uint16_t* out = static_cast<uint16_t*>(a.dhidden) + tn * 256;
-    store_tile<DT, T>(acc, a.meta->factor, a.dim - tn * 256, lds, [&](uint32_t m) {
+    store_tile<DT, T>(acc, a.meta->factor, a.dim - tn * 256, lds, t, [&](uint32_t m) {
       const uint32_t row = tm * T::kM + m;
       return row < live ? out + a.row_of[row] * a.dhidden_stride : nullptr;
     });
@@ -527,11 +554,11 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   }
 #pragma unroll
   for (int i = 0; i < T::kI; ++i) {
-    const uint32_t row = tm * T::kM + T::row(i);
+    const uint32_t row = tm * T::kM + T::row(i, t);
     if (row >= live) continue;
 #pragma unroll
     for (int j = 0; j < T::kJ; ++j) {
-      const uint32_t n = tn * 256 + T::column(j);
+      const uint32_t n = tn * 256 + T::column(j, t);
       if (n < a.dim) *reinterpret_cast<f32x4*>(a.part + ((uint64_t)split * live + row) * a.dim + n) = acc[i][j];
     }
   }
@@ -556,23 +583,92 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
   }
 }
 
+// What the targets' entries lost, as terms of dweight's product: of the rows whose
+// target lies in the tile, in their order and 64 at a time, P holds the residual at
+// the target's column (zeros elsewhere) and Q the row's hidden state.
+template <int DT, class T>
+__device__ __forceinline__ void add_rests(const HeadArgs& a, uint32_t live, uint32_t tm, uint32_t tn, char* lds,
+                                          uint32_t t, typename T::Acc& acc) {
+  typedef Columns<T::kM> P;
+  typedef Columns<256> Q;
+  constexpr uint32_t kList = 1024;
+  static_assert(T::kSlotBytes + kList * 4 + kWaves * 4 <= T::kLds, "the list lies in the second slot");
+  uint32_t* list = reinterpret_cast<uint32_t*>(lds + T::kSlotBytes);  // rows, the i-th at i % kList
+  uint32_t* part = list + kList;
+  const uint32_t lane = t & 63, wave = wave_of_block();
+  const uint32_t m0 = wave / T::kWavesN * T::kWaveM, n0 = wave % T::kWavesN * T::kWaveN;
+  uint32_t found = 0, used = 0;
+  for (uint32_t r0 = 0; r0 < live; r0 += kGemmThreads) {
+    const uint32_t r = r0 + t;
+    const uint64_t hits = __ballot(r < live && a.target[r < live ? r : 0] - tm * T::kM < (uint32_t)T::kM);
+    __syncthreads();
+    if (lane == 0) part[wave] = (uint32_t)__popcll(hits);
+    __syncthreads();
+    uint32_t at = found + (uint32_t)__popcll(hits & ((1ull << lane) - 1));
+    for (uint32_t w = 0; w < kWaves; ++w) {
+      at += w < wave ? part[w] : 0;
+      found += part[w];
+    }
+    if (hits >> lane & 1) list[at % kList] = r;
+    const bool last = r0 + kGemmThreads >= live;
+    while (found - used >= 64 || (last && found > used)) {
+      const uint32_t n = min(found - used, 64u);
+      // zeros, and the hidden states
+#pragma unroll 1
+      for (uint32_t i = t; i < T::kBytesP / 16; i += kGemmThreads) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
+      __syncthreads();
+#pragma unroll 1
+      for (uint32_t i = t; i < 64 * 32; i += kGemmThreads) {
+        const uint32_t k = i / 32, c = i % 32, column = tn * 256 + c * 8;
+        u32x4 v = {0, 0, 0, 0};
+        if (k < n && column < a.dim) v = *reinterpret_cast<const u32x4*>(a.kept + (uint64_t)list[(used + k) % kList] * a.dim + column);
+        *reinterpret_cast<u32x4*>(lds + T::kBytesP + k * 512 + (c ^ Q::swizzle(k)) * 16) = v;
+      }
+      if (t < n) {
+        const uint32_t k = t, row = list[(used + k) % kList], m = a.target[row] - tm * T::kM;
+        *reinterpret_cast<uint16_t*>(lds + k * (2 * T::kM) + ((m / 8) ^ P::swizzle(k)) * 16 + m % 8 * 2) =
+            (uint16_t)Vec<DT>::pack(a.rest[row], 0.0f);
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (uint32_t kk = 0; kk < 2; ++kk) {
+        u32x4 q[T::kJ];
+#pragma unroll
+        for (int j = 0; j < T::kJ; ++j) q[j] = Q::fragment((lds_char*)lds + T::kBytesP, n0 + 16 * j, kk, lane);
+#pragma unroll
+        for (int i = 0; i < T::kI; ++i) {
+          const u32x4 p = P::fragment((lds_char*)lds, m0 + 16 * i, kk, lane);
+#pragma unroll
+          for (int j = 0; j < T::kJ; ++j) acc[i][j] = mfma16<DT>(q[j], p, acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);  // few registers are left beside the sums
+        }
+      }
+      __syncthreads();
+      used += n;
+    }
+  }
+}
+
 template <int DT, class T>
 __global__ void __launch_bounds__(kGemmThreads, T::kM == 64 ? 4 : 2) dweight_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
   const uint32_t live = a.meta->live, mt = (a.vocab + T::kM - 1) / T::kM, nt = (a.dim + 255) / 256;
   uint32_t tm, tn;
   tile_of(blockIdx.x, mt, nt, &tm, &tn);
+  typename T::Acc acc;
+  clear<T>(acc);
+  add_rests<DT, T>(a, live, tm, tn, lds, thread_anew(), acc);
   Columns<T::kM> p;
   Columns<256> q;
   p.begin(a.held, (uint64_t)tm * T::kM, a.padded, a.padded, live);
   q.begin(a.kept, (uint64_t)tn * 256, a.dim, a.dim, live);
-  typename T::Acc acc;
   gemm_tile<DT, T>(p, q, 0, live, (lds_char*)lds, acc);
+  const uint32_t t = thread_anew();
   const float f = a.meta->factor;
   if (a.first && a.last) {
     __syncthreads();
     uint16_t* out = static_cast<uint16_t*>(a.dweight) + tn * 256;
-    store_tile<DT, T>(acc, f, a.dim - tn * 256, lds, [&](uint32_t m) {
+    store_tile<DT, T>(acc, f, a.dim - tn * 256, lds, t, [&](uint32_t m) {
       const uint32_t row = tm * T::kM + m;
       return row < a.vocab ? out + row * a.dweight_stride : nullptr;
     });
@@ -580,11 +676,11 @@ __global__ void __launch_bounds__(kGemmThreads, T::kM == 64 ? 4 : 2) dweight_ker
   }
 #pragma unroll
   for (int i = 0; i < T::kI; ++i) {
-    const uint32_t row = tm * T::kM + T::row(i);
+    const uint32_t row = tm * T::kM + T::row(i, t);
     if (row >= a.vocab) continue;
 #pragma unroll
     for (int j = 0; j < T::kJ; ++j) {
-      const uint32_t n = tn * 256 + T::column(j);
+      const uint32_t n = tn * 256 + T::column(j, t);
       if (n >= a.dim) continue;
       f32x4 x = acc[i][j] * f;
       f32x4* sum = reinterpret_cast<f32x4*>(a.sum + (uint64_t)row * a.dim + n);
@@ -601,7 +697,7 @@ __global__ void __launch_bounds__(kGemmThreads, T::kM == 64 ? 4 : 2) dweight_ker
 constexpr uint32_t kMaxDim = 1u << 15;
 
 struct Space {
-  uint64_t meta, row_of, target, omega, said, terms, counts, kept, held, stats, part, sum, bytes;
+  uint64_t meta, row_of, target, omega, said, rest, terms, counts, kept, held, stats, part, sum, bytes;
   uint32_t piece, tiles, shift;
 };
 
@@ -624,6 +720,7 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.target = take(p * 4);
   s.omega = take(p * 4);
   s.said = take(p * 4);
+  s.rest = take(grad ? p * 4 : 0);
   s.terms = take(n_rows * 8);
   s.counts = take(n_rows);
   s.kept = take(p * dim * 2);
@@ -788,6 +885,7 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   a.target = reinterpret_cast<uint32_t*>(ws + s.target);
   a.omega = reinterpret_cast<float*>(ws + s.omega);
   a.said = reinterpret_cast<float*>(ws + s.said);
+  a.rest = reinterpret_cast<float*>(ws + s.rest);
   a.kept = reinterpret_cast<uint16_t*>(ws + s.kept);
   a.stats = reinterpret_cast<f32x2*>(ws + s.stats);
   a.held = reinterpret_cast<uint16_t*>(ws + s.held);
