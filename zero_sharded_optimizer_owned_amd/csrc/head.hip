@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   clear<T>(acc);
   gemm_tile<DT, T>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
   const uint32_t t = thread_anew();
-  if (split == 0) {  // what the targets' entries lost
+  if (splits == 1) {  // what the targets' entries lost
 #pragma unroll
     for (int i = 0; i < T::kI; ++i) {
       const uint32_t row = tm * T::kM + T::row(i, t);
@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   }
 }
 
-// dhidden from the sums over parts of the vocabulary, in their order.
+// dhidden from the sums over parts of the vocabulary, in their order, and what the
+// target's entry lost.
 template <int DT>
 __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
   const uint32_t live = a.meta->live, splits = a.meta->splits;
@@ -572,11 +573,16 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
   const float f = a.meta->factor;
   for (uint32_t row = blockIdx.x; row < live; row += gridDim.x) {
     const uint64_t at = a.row_of[row] * a.dhidden_stride;
+    const float rest = a.rest[row];
+    const u32x2* w = reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.weight) + a.target[row] * a.weight_stride);
     for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.dim / 4; v += gridDim.y * kBlock) {
       f32x4 x = {0, 0, 0, 0};
 #pragma unroll 8
       for (uint32_t s = 0; s < splits; ++s)
         x += *reinterpret_cast<const f32x4*>(a.part + ((uint64_t)s * live + row) * a.dim + v * 4);
+      const typename Vec<DT>::Raw r = {u32x4{w[v][0], w[v][1], 0, 0}};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = fmaf(rest, Vec<DT>::get(r, k), x[k]);
       x *= f;
       store4<DT>(a.dhidden, at + v * 4, x[0], x[1], x[2], x[3]);
     }
@@ -591,34 +597,54 @@ __device__ __forceinline__ void add_rests(const HeadArgs& a, uint32_t live, uint
                                           uint32_t t, typename T::Acc& acc) {
   typedef Columns<T::kM> P;
   typedef Columns<256> Q;
-  constexpr uint32_t kList = 1024;
-  static_assert(T::kSlotBytes + kList * 4 + kWaves * 4 <= T::kLds, "the list lies in the second slot");
+  constexpr uint32_t kList = 4096, kEach = 4;  // consecutive rows to a thread
+  static_assert(T::kBytesP == 64 * 2 * T::kM, "half of the bytes of P are 32 rows");
+  static_assert(T::kSlotBytes + kList * 4 + 2 * kWaves * 4 <= T::kLds, "the list lies in the second slot");
   uint32_t* list = reinterpret_cast<uint32_t*>(lds + T::kSlotBytes);  // rows, the i-th at i % kList
-  uint32_t* part = list + kList;
+  uint32_t* parts = list + kList;  // the wavefronts' counts, in turn
   const uint32_t lane = t & 63, wave = wave_of_block();
   const uint32_t m0 = wave / T::kWavesN * T::kWaveM, n0 = wave % T::kWavesN * T::kWaveN;
-  uint32_t found = 0, used = 0;
-  for (uint32_t r0 = 0; r0 < live; r0 += kGemmThreads) {
-    const uint32_t r = r0 + t;
-    const uint64_t hits = __ballot(r < live && a.target[r < live ? r : 0] - tm * T::kM < (uint32_t)T::kM);
+  uint32_t found = 0, used = 0, turn = 0, next[kEach];
+#pragma unroll
+  for (uint32_t i = 0; i < kEach; ++i) next[i] = kEach * t + i < live ? a.target[kEach * t + i] : 0xFFFFFFFFu;
+  for (uint32_t r0 = 0; r0 < live; r0 += kEach * kGemmThreads, turn ^= kWaves) {
+    const uint32_t r = r0 + kEach * t, ahead = r + kEach * kGemmThreads;
+    uint32_t target[kEach];
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+      target[i] = next[i];
+      next[i] = ahead + i < live ? a.target[ahead + i] : 0xFFFFFFFFu;
+    }
+    uint32_t mine = 0, before = 0, all = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+      const bool hit = target[i] != 0xFFFFFFFFu && target[i] - tm * T::kM < (uint32_t)T::kM;
+      const uint64_t hits = __ballot(hit);
+      mine |= (uint32_t)hit << i;
+      before += (uint32_t)__popcll(hits & ((1ull << lane) - 1));
+      all += (uint32_t)__popcll(hits);
+    }
+    const bool last = r0 + kEach * kGemmThreads >= live;
+    uint32_t* part = parts + turn;
+    if (lane == 0) part[wave] = all;
     __syncthreads();
-    if (lane == 0) part[wave] = (uint32_t)__popcll(hits);
-    __syncthreads();
-    uint32_t at = found + (uint32_t)__popcll(hits & ((1ull << lane) - 1));
+    uint32_t at = found + before;
     for (uint32_t w = 0; w < kWaves; ++w) {
       at += w < wave ? part[w] : 0;
       found += part[w];
     }
-    if (hits >> lane & 1) list[at % kList] = r;
-    const bool last = r0 + kGemmThreads >= live;
+    if (found == used) continue;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i)
+      if (mine >> i & 1) list[at++ % kList] = r + i;
     while (found - used >= 64 || (last && found > used)) {
-      const uint32_t n = min(found - used, 64u);
+      const uint32_t n = min(found - used, 64u), halves = (n + 31) / 32;
       // zeros, and the hidden states
-#pragma unroll 1
-      for (uint32_t i = t; i < T::kBytesP / 16; i += kGemmThreads) *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
+      for (uint32_t i = t; i < T::kBytesP / 32 * halves; i += kGemmThreads)
+        *reinterpret_cast<u32x4*>(lds + i * 16) = u32x4{0, 0, 0, 0};
       __syncthreads();
-#pragma unroll 1
-      for (uint32_t i = t; i < 64 * 32; i += kGemmThreads) {
+#pragma unroll 2
+      for (uint32_t i = t; i < halves * 32 * 32; i += kGemmThreads) {
         const uint32_t k = i / 32, c = i % 32, column = tn * 256 + c * 8;
         u32x4 v = {0, 0, 0, 0};
         if (k < n && column < a.dim) v = *reinterpret_cast<const u32x4*>(a.kept + (uint64_t)list[(used + k) % kList] * a.dim + column);
@@ -631,7 +657,7 @@ __device__ __forceinline__ void add_rests(const HeadArgs& a, uint32_t live, uint
       }
       __syncthreads();
 #pragma unroll 1
-      for (uint32_t kk = 0; kk < 2; ++kk) {
+      for (uint32_t kk = 0; kk < halves; ++kk) {
         u32x4 q[T::kJ];
 #pragma unroll
         for (int j = 0; j < T::kJ; ++j) q[j] = Q::fragment((lds_char*)lds + T::kBytesP, n0 + 16 * j, kk, lane);
