@@ -948,18 +948,28 @@ def _matrix(t, name: str, dev: int, dtype=None, shape=None):
 
 def _kind(t, name: str) -> int:
     """The dtype code of a float16, bfloat16 or float32 tensor."""
-    torch = _torch()
-    if t.dtype not in (torch.float16, torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
-    return _dtype_code(t)
+    code = _dtype_codes.get(t.dtype) if _dtype_codes else None
+    if code is None:
+        torch = _torch()
+        if t.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+            raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+        code = _dtype_code(t)
+    return code
 
 
 def _dense(t, name: str, dtype, shape, dev: int) -> int:
     """The address of a contiguous tensor of one dtype and shape."""
-    p = _addr(t, name, dtype, 0, dev)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _dev(t, name, dtype)
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return p
+    return t.data_ptr()
+
+
+def _dense_rows(t, name: str, dev: int):
+    """(address, shape) of a contiguous [rows, dim] tensor on device `dev`."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    return _dense(t, name, t.dtype, t.shape, dev), t.shape
 
 
 def zero_embedding(table, tokens, out, *, scale: float = 1.0) -> None:
@@ -1028,13 +1038,15 @@ def zero_rms_norm(x, gain, out, *, residual=None, h=None, eps: float = 1e-6, rst
     torch = _torch()
     dt = _kind(x, "x")
     dev, stream = _device_stream()
-    px, n, d, stride = _matrix(x, "x", dev)
-    _dense(x, "x", x.dtype, (n, d), dev)
+    px, shape = _dense_rows(x, "x", dev)
+    n, d = shape
     if (residual is None) != (h is None):
         raise ValueError("residual and h go together")
-    same = lambda t, name: None if t is None else _dense(t, name, x.dtype, (n, d), dev)  # noqa: E731
-    _check(lib().zero_rms_norm(px, same(residual, "residual"), _dense(gain, "gain", x.dtype, (d,), dev), dt, n, d, eps,
-                               same(h, "h"), same(out, "out"),
+    pr, ph = None, None
+    if residual is not None:
+        pr, ph = _dense(residual, "residual", x.dtype, shape, dev), _dense(h, "h", x.dtype, shape, dev)
+    _check(lib().zero_rms_norm(px, pr, _dense(gain, "gain", x.dtype, (d,), dev), dt, n, d, eps, ph,
+                               _dense(out, "out", x.dtype, shape, dev),
                                None if rstd is None else _dense(rstd, "rstd", torch.float32, (n,), dev),
                                *_kept(codes, scales, n, d, dev), stream))
 
@@ -1045,8 +1057,7 @@ def zero_rms_norm_restore(codes, scales, rstd, gain, out) -> None:
     torch = _torch()
     dt = _kind(out, "out")
     dev, stream = _device_stream()
-    p, n, d, _ = _matrix(out, "out", dev)
-    _dense(out, "out", out.dtype, (n, d), dev)
+    p, (n, d) = _dense_rows(out, "out", dev)
     _check(lib().zero_rms_norm_restore(*_kept(codes, scales, n, d, dev),
                                        _dense(rstd, "rstd", torch.float32, (n,), dev),
                                        _dense(gain, "gain", out.dtype, (d,), dev), dt, n, d, p, stream))
@@ -1069,11 +1080,11 @@ def zero_rms_norm_backward(dy, gain, rstd, dx, dgain, *, workspace, h=None, code
     torch = _torch()
     dt = _kind(dy, "dy")
     dev, stream = _device_stream()
-    p, n, d, _ = _matrix(dy, "dy", dev)
-    _dense(dy, "dy", dy.dtype, (n, d), dev)
+    p, shape = _dense_rows(dy, "dy", dev)
+    n, d = shape
     if (h is None) == (codes is None):
         raise ValueError("either h or codes and scales")
-    same = lambda t, name: None if t is None else _dense(t, name, dy.dtype, (n, d), dev)  # noqa: E731
+    same = lambda t, name: None if t is None else _dense(t, name, dy.dtype, shape, dev)  # noqa: E731
     row = lambda t, name: _dense(t, name, dy.dtype, (d,), dev)  # noqa: E731
     a = RmsNormBackwardArgs(p, row(gain, "gain"), same(h, "h"), *_kept(codes, scales, n, d, dev),
                             _dense(rstd, "rstd", torch.float32, (n,), dev), same(upstream, "upstream"), dt, n, d,
