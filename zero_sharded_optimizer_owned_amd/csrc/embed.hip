@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kBlock) fill_kernel(const GradArgs a, uint32_t
 
 // ---------------------------------------------------------------------------
 // All of it in one launch, for up to kOneSort tokens: block 0 sorts in LDS, by
-// the same steps with 16 wavefronts, and the others meanwhile write the zeros.
+// the same steps with 16 wavefronts (few tokens: several blocks, by counting), and
+// the others meanwhile write the zeros.
 // A block of those goes over all tokens for the rows of its own that are named.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kOneSort = 16384, kOneThreads = 1024, kOneWaves = 16, kOneRounds = kOneSort / kOneThreads;
@@ -397,11 +398,42 @@ constexpr uint32_t kMapRows = 1u << 16;
 struct OneArgs {
   const int64_t* tokens;
   uint32_t *keys, *at;  // sorted
-  uint32_t n, vocab, bits, passes;
+  uint32_t n, vocab, bits, passes, sorters;  // sorters: the blocks that sort
   void* dtable;  // of the zeros
   uint64_t stride;
   uint32_t dim, vecs, shift;  // 1 << shift lanes to a row
 };
+
+// Few tokens: a block finds the places of 64 of them, 16 lanes to a token, by
+// going over all keys (333 tokens: 3 us, where two passes of one block take 9).
+constexpr uint32_t kCountTokens = 1024, kCountEach = 64;
+
+__device__ __forceinline__ void sort_by_counting(const OneArgs& a, uint32_t* keys) {
+  const uint32_t t = threadIdx.x;
+  uint32_t key = 0xFFFFFFFFu;  // behind all others
+  if (t < a.n) {
+    const int64_t token = a.tokens[t];
+    key = token >= 0 && token < (int64_t)a.vocab ? (uint32_t)token : a.vocab;
+  }
+  keys[t] = key;
+  __syncthreads();
+  const uint32_t i = blockIdx.x * kCountEach + t / 16;
+  const uint32_t own = keys[min(i, kCountTokens - 1)];
+  uint32_t place = 0;
+  for (uint32_t j0 = t % 16 * 4; j0 < a.n; j0 += 64) {
+    const u32x4 k = *reinterpret_cast<const u32x4*>(keys + j0);
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) place += (k[j] < own) | ((k[j] == own) & (j0 + j < i));
+  }
+  place += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)place, 0x128, 0xF, 0xF, false);  // row_ror:8, 4, 2, 1
+  place += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)place, 0x124, 0xF, 0xF, false);
+  place += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)place, 0x122, 0xF, 0xF, false);
+  place += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)place, 0x121, 0xF, 0xF, false);
+  if (t % 16 == 0 && i < a.n) {
+    a.keys[place] = own;
+    a.at[place] = i;
+  }
+}
 
 __device__ __forceinline__ void sort_in_lds(const OneArgs& a, uint32_t* keys, uint16_t* at, uint16_t (*count)[kDigits],
                                             uint32_t* sums) {
@@ -492,15 +524,16 @@ __device__ __forceinline__ void sort_in_lds(const OneArgs& a, uint32_t* keys, ui
 template <int OUT, bool NT>
 __global__ void __launch_bounds__(kOneThreads) one_sort_kernel(const OneArgs a) {
   typedef typename Vec<OUT>::T T;
-  __shared__ uint32_t keys[kOneSort];
+  __shared__ __align__(16) uint32_t keys[kOneSort];
   __shared__ uint16_t at[kOneSort], count[kOneWaves][kDigits];
   __shared__ uint32_t sums[kOneWaves];
-  if (blockIdx.x == 0) {
-    sort_in_lds(a, keys, at, count, sums);
+  if (blockIdx.x < a.sorters) {
+    if (a.n <= kCountTokens) sort_by_counting(a, keys);
+    else sort_in_lds(a, keys, at, count, sums);
     return;
   }
   // unit by unit in turn, a unit being the rows that the block writes at a time
-  const uint32_t t = threadIdx.x, blocks = gridDim.x - 1, b = blockIdx.x - 1, lanes = 1u << a.shift;
+  const uint32_t t = threadIdx.x, blocks = gridDim.x - a.sorters, b = blockIdx.x - a.sorters, lanes = 1u << a.shift;
   const uint32_t unit = kOneThreads >> a.shift, units = kMapRows / unit;
   uint32_t* named = keys;  // one bit to a row
   const float zero[Lane<OUT>::N] = {};
@@ -669,9 +702,9 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
       with_dtype(p->table_dtype, [&](auto dt) {
         constexpr int OUT = decltype(dt)::value;
         const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
-        OneArgs a = {p->tokens, keys[0], at[0], g.n, p->vocab, bits, passes, p->dtable, p->stride, p->dim, vecs, 0};
+        OneArgs a = {p->tokens, keys[0], at[0], g.n, p->vocab, bits, passes, g.n <= kCountTokens ? (g.n + kCountEach - 1) / kCountEach : 1, p->dtable, p->stride, p->dim, vecs, 0};
         while ((1u << a.shift) < vecs && a.shift < 6) ++a.shift;
-        const uint32_t grid = g.accumulate ? 1 : 256u;
+        const uint32_t grid = g.accumulate ? a.sorters : 256;
         if (nt) hipLaunchKernelGGL((one_sort_kernel<OUT, true>), grid, kOneThreads, 0, stream, a);
         else hipLaunchKernelGGL((one_sort_kernel<OUT, false>), grid, kOneThreads, 0, stream, a);
       });
