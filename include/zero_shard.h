@@ -864,9 +864,10 @@ typedef struct {
  *   dhidden, dweight = grad_scale * d loss / d hidden, d weight
  * A target outside [0, vocab) (say -100) marks a row that counts for nothing: logp
  * 0, no loss, zero dhidden, its hidden state unread.  Products add in fp32.  The
- * gradients' second factor, softmax - onehot, is rounded to dtype once more on the
- * way (from 11 significant bits), relative to the largest |row_weight|.  Logits
- * that are NaN or +inf give NaN; -inf has probability 0.
+ * gradients' first factor, softmax - onehot, passes through 11 significant bits and
+ * then those of dtype, relative to the largest |row_weight|; its entries at the
+ * targets count in full.  Logits that are NaN or +inf give NaN; -inf has
+ * probability 0.
  * Rows go in pieces of piece_rows; per row of a piece the workspace holds vocab 16-bit
  * values (without gradients: vocab / 32 bytes) and the hidden state, and with more than
  * one piece fp32 sums of dweight.

@@ -34,7 +34,7 @@ struct EmbedArgs {
 };
 
 // 2^SH threads to a row, one vector each at a time.
-template <int DT, bool NT>
+template <int DT>
 __global__ void __launch_bounds__(kBlock) embed_kernel(const EmbedArgs a, const uint32_t shift) {
   constexpr int N = Lane<DT>::N;
   typedef typename Vec<DT>::T T;
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kBlock) embed_kernel(const EmbedArgs a, const 
 #pragma unroll
         for (int k = 0; k < N; ++k) x[k] = Lane<DT>::get(r, k) * a.scale;
       }
-      store_cut<DT, NT>(to, v, a.dim, x);
+      store_cut<DT>(to, v, a.dim, x);
     }
   }
 }
@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kBlock) scatter_kernel(const SortArgs a) {
 // ---------------------------------------------------------------------------
 // Sums over the sorted positions.
 //
-// They are cut into tiles of 8 or 32.  A run of equal tokens that lies within a
+// They are cut into tiles of 8 or, from kFewTokens on, 32 (onto a gradient of 4096
+// columns bf16: 4096 tokens 40 us with 8, 42 with 32; 8192 tokens 68 and 58).  A run of equal tokens that lies within a
 // tile is summed and written there; one that a tile's end cuts leaves partial
 // sums (fp32), the tile's first run in slot 0, its last one in slot 1, which
 // join_kernel adds in the order of the tiles.
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const GradArgs a) {
 // of them and finds the sorted keys of that range by bisection, 64 probes at a time.
 constexpr uint32_t kFillRows = 16;
 
-template <int OUT, bool NT>
+template <int OUT>
 __global__ void __launch_bounds__(kBlock) fill_kernel(const GradArgs a, uint32_t vecs) {
   constexpr int N = Lane<OUT>::N;
   typedef typename Vec<OUT>::T T;
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kBlock) fill_kernel(const GradArgs a, uint32_t
     for (uint32_t r = 0; r < rows; ++r) {
       if (skip >> r & 1) continue;
       T* row = static_cast<T*>(a.dtable) + (uint64_t)(row0 + r) * a.stride;
-      for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) store_cut<OUT, NT>(row, v, a.dim, zero);
+      for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) store_cut<OUT>(row, v, a.dim, zero);
     }
   }
 }
@@ -521,7 +522,7 @@ __device__ __forceinline__ void sort_in_lds(const OneArgs& a, uint32_t* keys, ui
   }
 }
 
-template <int OUT, bool NT>
+template <int OUT>
 __global__ void __launch_bounds__(kOneThreads) one_sort_kernel(const OneArgs a) {
   typedef typename Vec<OUT>::T T;
   __shared__ __align__(16) uint32_t keys[kOneSort];
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kOneThreads) one_sort_kernel(const OneArgs a) 
       const uint64_t r = (first + (uint64_t)i * blocks) * unit + in;
       if (r >= a.vocab || (named[bit / 32] >> (bit % 32) & 1)) continue;
       T* row = static_cast<T*>(a.dtable) + r * a.stride;
-      for (uint32_t v = t & (lanes - 1); v < a.vecs; v += lanes) store_cut<OUT, NT>(row, v, a.dim, zero);
+      for (uint32_t v = t & (lanes - 1); v < a.vecs; v += lanes) store_cut<OUT>(row, v, a.dim, zero);
     }
   }
 }
@@ -609,9 +610,6 @@ int check_table(const void* table, int dtype, uint32_t vocab, uint32_t dim, uint
   return ZERO_OK;
 }
 
-// Bytes past which what is written will not be found in the 256 MB memory-side cache.
-bool past_cache(uint64_t bytes) { return bytes > (uint64_t(256) << 20); }
-
 }  // namespace
 }  // namespace zs
 
@@ -637,10 +635,7 @@ extern "C" int zero_embedding(const void* table, int dtype, uint32_t vocab, uint
     const EmbedArgs a = {table, tokens, out, n_tokens, stride, vocab, dim, vecs, (float)scale};
     const uint64_t rows = kBlock >> shift;
     const uint32_t grid = chunk_grid((n_tokens + rows - 1) / rows, 0);
-    if (past_cache(n_tokens * dim * dtype_bytes(dtype)))
-      hipLaunchKernelGGL((embed_kernel<DT, true>), grid, kBlock, 0, stream, a, shift);
-    else
-      hipLaunchKernelGGL((embed_kernel<DT, false>), grid, kBlock, 0, stream, a, shift);
+    hipLaunchKernelGGL(embed_kernel<DT>, grid, kBlock, 0, stream, a, shift);
   });
   return launch_status(who);
 }
@@ -689,8 +684,10 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
   g.scale = (float)p->scale;
   g.accumulate = p->accumulate != 0;
   g.tile = s.tile;
-  const bool nt = past_cache((uint64_t)p->vocab * p->dim * dtype_bytes(p->table_dtype));
-  const bool one = g.n > 0 && g.n <= kOneSort;
+  // Alone, one block's sort takes longer than several blocks' passes from some 10,000
+  // tokens on (onto a gradient: 8192 tokens 58 us and 61, 16,384 tokens 115 and 103);
+  // beside the zeros it costs nothing (16,384 tokens of 128,000 x 4096 258 and 274).
+  const bool one = g.n > 0 && g.n <= (g.accumulate ? kOneSort / 2 : kOneSort);
   if (g.n > 0) {
     // keys are 0 .. vocab: passes of equal width, 9 bits at most
     uint32_t bits = 1;
@@ -702,11 +699,11 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
       with_dtype(p->table_dtype, [&](auto dt) {
         constexpr int OUT = decltype(dt)::value;
         const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
-        OneArgs a = {p->tokens, keys[0], at[0], g.n, p->vocab, bits, passes, g.n <= kCountTokens ? (g.n + kCountEach - 1) / kCountEach : 1, p->dtable, p->stride, p->dim, vecs, 0};
+        const uint32_t sorters = g.n <= kCountTokens ? (g.n + kCountEach - 1) / kCountEach : 1;
+        OneArgs a = {p->tokens, keys[0], at[0], g.n, p->vocab, bits, passes, sorters, p->dtable, p->stride, p->dim, vecs, 0};
         while ((1u << a.shift) < vecs && a.shift < 6) ++a.shift;
         const uint32_t grid = g.accumulate ? a.sorters : 256;
-        if (nt) hipLaunchKernelGGL((one_sort_kernel<OUT, true>), grid, kOneThreads, 0, stream, a);
-        else hipLaunchKernelGGL((one_sort_kernel<OUT, false>), grid, kOneThreads, 0, stream, a);
+        hipLaunchKernelGGL(one_sort_kernel<OUT>, grid, kOneThreads, 0, stream, a);
       });
       g.keys = keys[0];
       g.at = at[0];
@@ -736,8 +733,7 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
     with_dtype(p->table_dtype, [&](auto dt) {
       constexpr int OUT = decltype(dt)::value;
       const uint32_t vecs = (p->dim + Lane<OUT>::N - 1) / Lane<OUT>::N;
-      if (nt) hipLaunchKernelGGL((fill_kernel<OUT, true>), grid, kBlock, 0, stream, g, vecs);
-      else hipLaunchKernelGGL((fill_kernel<OUT, false>), grid, kBlock, 0, stream, g, vecs);
+      hipLaunchKernelGGL(fill_kernel<OUT>, grid, kBlock, 0, stream, g, vecs);
     });
     if ((rc = launch_status(who))) return rc;
   }

@@ -2,11 +2,11 @@
 // operands in 16 bits, sums in fp32.
 //
 // A block of 512 threads makes an M x 256 tile, k in steps of 64.  With M = 256 its
-// eight wavefronts take 128 x 64 each (two in m, four in n).  Fewer rows take
-// M = 128 (64 x 64 each) or M = 64 (64 x 32 each, all eight in n): those products
-// are bound by the reading of Q, and the smaller tile leaves LDS for more steps
-// under way.  A step's tiles (128 bytes for each m and n) are loaded straight into
-// LDS, 16 bytes to a lane, one step (M = 256), two or three steps ahead.
+// eight wavefronts take 128 x 64 each (two in m, four in n).  Up to 128 rows take
+// M = 128 (64 x 64 each): those products are bound by the reading of Q, and the
+// smaller tile leaves LDS for one more step under way.  A step's tiles (128 bytes
+// for each m and n) are loaded straight into LDS, 16 bytes to a lane, one step
+// (M = 256) or two ahead.
 //
 // An operand is laid out either with k contiguous (Rows: element (r, k) at r
 // stride + k) or with r contiguous (Columns: at k stride + r).  Rows' tiles hold
@@ -54,7 +54,7 @@ template <int M, int Slots>
 struct Tile {
   static constexpr int kM = M, kSlots = Slots;
   static constexpr int kBytesP = M * kTileK * 2, kSlotBytes = kBytesP + kTileN * kTileK * 2, kLds = Slots * kSlotBytes;
-  static constexpr int kWavesM = M == 64 ? 1 : 2, kWavesN = kWaves / kWavesM;
+  static constexpr int kWavesM = 2, kWavesN = kWaves / kWavesM;
   static constexpr int kWaveM = M / kWavesM, kWaveN = kTileN / kWavesN;  // of one wavefront
   static constexpr int kI = kWaveM / 16, kJ = kWaveN / 16;
   static constexpr int kLoads = M / 64 + kTileN / 64;  // a wavefront's, of a step
@@ -147,8 +147,7 @@ struct Columns {
   // A transposing read takes 32 bytes of each of 4 rows, and two groups of 16
   // lanes at a time rows 8 apart: all in different banks.
   static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    if constexpr (R == 64) return ((row % 4) ^ (row / 8 % 2)) << 1;  // two rows to a line of 64 banks
-    else return (row % 4) << 1 | (row / 8 % 2) << 3;
+    return (row % 4) << 1 | (row / 8 % 2) << 3;
   }
   __device__ __forceinline__ void load(uint32_t k0, uint32_t tile, int i) const {
     load_to_lds(base + k0 * stride * 2, k0 + row_of(i) < depth ? offset[i] : kNowhere,
@@ -170,12 +169,12 @@ struct Columns {
   }
 };
 
+// Until at most N of this wavefront's loads are under way, and its reads of LDS are done.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
-  static_assert(N == 0 || N == 6 || N == 10, "a count the assembly is written for");
+  static_assert(N == 0 || N == 6, "a count the assembly is written for");
   if constexpr (N == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  else if constexpr (N == 6) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
-  else asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
 }
 
 template <class T>

@@ -96,13 +96,12 @@ inline uint32_t splits_of(uint32_t m_tiles, uint32_t vocab, uint32_t dim) {
 }
 
 // The products' tiles by the piece's rows.  For few rows the reading of the weights
-// bounds logits and dhidden, and the writing of their gradient dweight, whose
-// tiles are then of 64 columns, so that two blocks share a CU.
+// bounds logits and dhidden (scores of 100 rows of 32,000 x 4096 bf16: 89 us with
+// 128 rows to a tile, 120 with 256; 200 rows 121 with 256; tiles of 64 rows for up to
+// 64 gained 1%).
 typedef Tile<256, 2> Wide;
 typedef Tile<128, 3> Middle;
-typedef Tile<64, 4> Narrow;
-typedef Tile<64, 2> Short;
-__host__ __device__ inline uint32_t tile_rows(uint32_t rows) { return rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+__host__ __device__ inline uint32_t tile_rows(uint32_t rows) { return rows <= 128 ? 128 : 256; }
 
 // ---------------------------------------------------------------------------
 // The rows that count, in order.
@@ -333,11 +332,13 @@ constexpr uint32_t logits_lds() {
   return after > (uint32_t)T::kLds ? after : T::kLds;
 }
 
-// The same for up to 16 rows, bound by the reading of the weights: a wavefront
+// The same for up to kFewRows rows, bound by the reading of the weights: a wavefront
 // reads the weights of 16 columns straight into registers, 16 bytes to a lane,
 // kFewSteps steps of 32 k in flight; the rows' hidden states come from the
-// caches.  The four wavefronts of a block take turns along k.
-constexpr uint32_t kFewRows = 16, kFewShift = 4;
+// caches.  The four wavefronts of a block take turns along k.  (One row of 32,000 x
+// 4096 bf16 64 us with it, 77 with the products' tiles; 16 rows 79 and 78: the
+// hidden states, read by every wavefront, then cost as much as the barriers saved.)
+constexpr uint32_t kFewRows = 8, kFewShift = 4;
 constexpr int kFewSteps = 4;
 
 template <int DT, bool KEEP>
@@ -676,7 +677,7 @@ __device__ __forceinline__ void add_rests(const HeadArgs& a, uint32_t live, uint
 }
 
 template <int DT, class T>
-__global__ void __launch_bounds__(kGemmThreads, T::kM == 64 ? 4 : 2) dweight_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
   const uint32_t live = a.meta->live, mt = (a.vocab + T::kM - 1) / T::kM, nt = (a.dim + 255) / 256;
   uint32_t tm, tn;
@@ -754,7 +755,7 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.stats = take(std::max(p * ((vocab + 255) / 256), std::min<uint64_t>(p, kFewRows) * ((vocab + 15) / 16)) * 8);
   s.held = take(grad ? p * padded * 2 : 0);
   uint64_t part = 0;  // dhidden's parts, for whatever number of rows counts
-  for (uint64_t rows : {(uint64_t)64, (uint64_t)128, p}) {  // the last piece may be smaller, and so may a later call
+  for (uint64_t rows : {(uint64_t)128, p}) {  // the last piece may be smaller, and so may a later call
     const uint32_t t = tile_rows((uint32_t)std::min(rows, p));
     for (uint32_t m = t; grad && m < std::min(rows, p) + t; m += t) {
       const uint32_t n = splits_of(m / t, vocab, dim);
@@ -788,8 +789,7 @@ int check_matrix(const void* p, uint64_t rows, uint32_t dim, uint64_t stride, co
 // Calls fn with the tile of a piece's rows.
 template <typename F>
 void by_tile(uint32_t rows, F fn) {
-  if (tile_rows(rows) == 64) fn(Narrow{});
-  else if (tile_rows(rows) == 128) fn(Middle{});
+  if (tile_rows(rows) == 128) fn(Middle{});
   else fn(Wide{});
 }
 
@@ -811,11 +811,8 @@ void launch_rows(const HeadArgs& a, hipStream_t stream) {
 
 template <int DT>
 void launch_dweight(const HeadArgs& a, hipStream_t stream) {
-  const uint32_t nt = (a.dim + 255) / 256;
-  if (a.rows <= 128)
-    hipLaunchKernelGGL((dweight_kernel<DT, Short>), (a.vocab + 63) / 64 * nt, kGemmThreads, Short::kLds, stream, a);
-  else
-    hipLaunchKernelGGL((dweight_kernel<DT, Wide>), (a.vocab + 255) / 256 * nt, kGemmThreads, Wide::kLds, stream, a);
+  const uint32_t tiles = (a.vocab + 255) / 256 * ((a.dim + 255) / 256);
+  hipLaunchKernelGGL((dweight_kernel<DT, Wide>), tiles, kGemmThreads, Wide::kLds, stream, a);
 }
 
 template <int DT>
