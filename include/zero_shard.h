@@ -738,7 +738,9 @@ int zero_preference_workspace_bytes(uint64_t n_rows, uint32_t n_pairs, uint64_t 
  * The model's two ends, and what its backward pass keeps.
  *
  * Tables and rows are F16, BF16 or F32.  Sums are fp32 or wider, in an order that
- * depends on the sizes alone, so results are identical run to run.
+ * depends on the sizes alone, so results are identical run to run.  A workspace's
+ * contents do not matter before a call and mean nothing after it; one made for some
+ * size serves smaller ones; calls that overlap need one each.
  * -------------------------------------------------------------------------- */
 
 /* ----------------------------------------------------------------------------
@@ -747,8 +749,8 @@ int zero_preference_workspace_bytes(uint64_t n_rows, uint32_t n_pairs, uint64_t 
  * table[vocab] of `dim` elements each, row v from element v * stride; out dense.
  * Neither needs alignment beyond its elements'.  vocab < 2^31, dim <= 2^20.
  * n_tokens == 0 is a no-op.
- * Errors: EINVAL (bad dtype, vocab or dim, stride < dim, scale not finite, NULL
- * or misaligned arrays); EHIP.
+ * Errors: EINVAL (bad dtype, vocab or dim, stride < dim, scale not finite in fp32,
+ * NULL or misaligned arrays); EHIP.
  * -------------------------------------------------------------------------- */
 int zero_embedding(const void *table, int dtype, uint32_t vocab, uint32_t dim, uint64_t stride,
                    const int64_t *tokens, uint64_t n_tokens, double scale, void *out, hipStream_t stream);
@@ -758,7 +760,7 @@ typedef struct {
   const void *dout; /* [n_tokens][dim], dense */
   int32_t dtype;
   const int64_t *tokens;
-  uint64_t n_tokens; /* below 2^31 */
+  uint64_t n_tokens; /* at most 2^28 */
   uint32_t vocab, dim;
   double scale;
   void *dtable;     /* row v from element v * stride */

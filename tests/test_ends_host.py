@@ -41,7 +41,7 @@ EMBED = [P, zs.ZERO_BF16, 100, 16, 16, P, 5, 1.0, P, None]
 @pytest.mark.parametrize("at, bad, word", [
     (0, None, "table"), (0, P + 1, "aligned"), (1, 0, "dtype"), (1, 4, "dtype"), (2, 0, "vocab"), (2, 1 << 31, "vocab"),
     (3, 0, "dim"), (3, (1 << 20) + 1, "dim"), (4, 15, "overlap"), (5, None, "tokens"), (5, P + 4, "aligned"),
-    (6, 1 << 62, "overflows"), (7, NAN, "scale"), (7, INF, "scale"), (8, None, "out"), (8, P + 1, "aligned"),
+    (6, 1 << 62, "overflows"), (7, NAN, "scale"), (7, INF, "scale"), (7, 1e39, "scale"), (8, None, "out"), (8, P + 1, "aligned"),
     (4, 1 << 62, "overflows"),
 ])
 def test_embedding_refuses(at, bad, word):
@@ -61,7 +61,8 @@ EMBED_GRAD = dict(dout=P, dtype=zs.ZERO_F16, tokens=P, n_tokens=5, vocab=100, di
     (dict(table_dtype=zs.ZERO_BF16), "dtable"), (dict(dtype=zs.ZERO_F32), "dtable"), (dict(tokens=None), "tokens"),
     (dict(tokens=P + 4), "aligned"), (dict(vocab=0), "vocab"), (dict(dim=0), "dim"), (dict(scale=NAN), "scale"),
     (dict(dtable=None), "table"), (dict(dtable=P + 1), "aligned"), (dict(stride=15), "overlap"),
-    (dict(n_tokens=1 << 31), "n_tokens"), (dict(workspace=None), "workspace"), (dict(workspace_bytes=64), "needs"),
+    (dict(n_tokens=(1 << 28) + 1), "n_tokens"), (dict(scale=1e39), "scale"), (dict(workspace=None), "workspace"),
+    (dict(workspace_bytes=64), "needs"),
     (dict(workspace=P + 64), "256"),
 ])
 def test_embedding_grad_refuses(changes, word):

@@ -22,7 +22,8 @@ SUB = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134, "f32": 2.0 ** -150}
 SHAPES = [(1, 1, 1, 0), (1, 7, 8, 0), (2, 3, 9, 11), (5, 10, 3, 0), (64, 4, 16, 0), (65, 300, 31, 40), (333, 1000, 100, 0),
           (1000, 17, 257, 0), (4095, 513, 64, 0), (4097, 50_001, 33, 0), (16_384, 262_143, 5, 0), (16_385, 900, 24, 25),
           (20_000, 3, 40, 0), (33_000, 600_000, 4, 0), (700, 90, 5003, 0), (40, 12, 20_000, 0),
-          (1024, 90, 12, 0), (1025, 90, 12, 0), (8192, 300, 20, 0), (8193, 300, 20, 0)]
+          (1024, 90, 12, 0), (1025, 90, 12, 0), (8192, 300, 20, 0), (8193, 300, 20, 0), (131_072, 70_000, 3, 0), (131_073, 40, 4, 0),
+          (700_001, 1000, 2, 0)]
 
 
 @pytest.fixture(scope="module", autouse=True)

@@ -127,3 +127,40 @@ def test_steps_run_and_write_back():
             a, b = max(off, lo), min(off + n, hi)
             if a < b:
                 assert torch.equal(t.params[a:b], dense[at + a - off:at + b - off].half())
+
+
+def test_two_streams_at_once_with_a_workspace_each():
+    """Two calls of each operator under way at a time leave what each leaves alone."""
+    g = torch.Generator().manual_seed(8)
+    n, v, d = 300, 2000, 256
+    mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    sides = [dict(h=mk(n, d), w=mk(v, d) / 16, dy=mk(n, d), gain=mk(d), t=torch.randint(0, v, (n,), generator=g).to(DEV),
+                  ws=(zs.linear_cross_entropy_workspace(n, v, d), zs.rms_norm_workspace(n, d), zs.embedding_workspace(n, v, d)))
+             for _ in range(2)]
+
+    def call(s):
+        e = lambda *k: torch.empty(*k, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+        f = lambda *k: torch.empty(*k, device=DEV)  # noqa: E731
+        o = dict(y=e(n, d), rstd=f(n), stats=f(2), logp=f(n), dh=e(n, d), dw=e(v, d), dx=e(n, d), dg=e(d), dt=e(v, d))
+        zs.zero_rms_norm(s["h"], s["gain"], o["y"], rstd=o["rstd"])
+        zs.zero_linear_cross_entropy(o["y"], s["w"], s["t"], divisor=2.0, stats=o["stats"], logp=o["logp"], dhidden=o["dh"],
+                                     dweight=o["dw"], workspace=s["ws"][0])
+        zs.zero_rms_norm_backward(o["dh"], s["gain"], o["rstd"], o["dx"], o["dg"], workspace=s["ws"][1], h=s["h"])
+        zs.zero_embedding_grad(o["dx"], s["t"], o["dt"], workspace=s["ws"][2])
+        return o
+
+    alone = []
+    for s in sides:
+        alone.append(call(s))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    both = []
+    for s, stream in zip(sides, streams):
+        with torch.cuda.stream(stream):
+            both.append(call(s))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        for k in a:
+            assert torch.equal(a[k], b[k]), k

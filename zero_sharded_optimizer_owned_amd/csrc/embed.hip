@@ -71,7 +71,8 @@ struct SortArgs {
   const int64_t* tokens;      // the first pass reads these,
   const uint32_t *keys, *at;  // the others these
   uint32_t *keys_out, *at_out;
-  uint32_t* hist;  // [1 << bits][blocks]
+  uint32_t* hist;    // [1 << bits][blocks], of many blocks counts of the blocks before
+  uint32_t* totals;  // [1 << bits], of many blocks
   uint32_t n, vocab, blocks, shift, bits;
 };
 
@@ -97,6 +98,34 @@ __global__ void __launch_bounds__(kBlock) histogram_kernel(const SortArgs a) {
   }
   __syncthreads();
   for (uint32_t d = threadIdx.x; d < digits; d += kBlock) a.hist[(uint64_t)d * a.blocks + blockIdx.x] = count[d];
+}
+
+// Of many blocks: a digit's counts become those of the blocks before, one block to
+// a digit.  (Few blocks add them up themselves: a launch less, and what each then
+// reads grows with their square.)
+constexpr uint32_t kScanBlocks = 64;
+__global__ void __launch_bounds__(kBlock) scan_kernel(const SortArgs a) {
+  __shared__ uint32_t sums[kWavesPerBlock];
+  const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  uint32_t* row = a.hist + (uint64_t)blockIdx.x * a.blocks;
+  uint32_t before = 0;
+  for (uint32_t b0 = 0; b0 < a.blocks; b0 += kBlock) {
+    const uint32_t own = b0 + t < a.blocks ? row[b0 + t] : 0;
+    uint32_t sum = own;
+#pragma unroll
+    for (uint32_t s = 1; s < 64; s <<= 1) {
+      const uint32_t up = __shfl_up(sum, s, 64);
+      if (lane >= s) sum += up;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = sum;
+    __syncthreads();
+    for (uint32_t w = 0; w < wave; ++w) sum += sums[w];
+    if (b0 + t < a.blocks) row[b0 + t] = before + sum - own;
+#pragma unroll
+    for (uint32_t w = 0; w < kWavesPerBlock; ++w) before += sums[w];
+  }
+  if (t == 0) a.totals[blockIdx.x] = before;
 }
 
 __global__ void __launch_bounds__(kBlock) scatter_kernel(const SortArgs a) {
@@ -138,7 +167,11 @@ __global__ void __launch_bounds__(kBlock) scatter_kernel(const SortArgs a) {
 #pragma unroll
   for (uint32_t j = 0; j < 2; ++j) {
     const uint32_t d = 2 * t + j;
-    if (d < digits)
+    if (d >= digits) continue;
+    if (a.blocks > kScanBlocks) {
+      mine[j] = a.hist[(uint64_t)d * a.blocks + blockIdx.x];
+      total[j] = a.totals[d];
+    } else
       for (uint32_t b = 0; b < a.blocks; ++b) {
         const uint32_t c = a.hist[(uint64_t)d * a.blocks + b];
         mine[j] += b < blockIdx.x ? c : 0;
@@ -568,12 +601,13 @@ __global__ void __launch_bounds__(kOneThreads) one_sort_kernel(const OneArgs a) 
 // Host side.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kMaxDim = 1u << 20;
+constexpr uint64_t kMaxTokens = 1u << 28;  // of the gradient: a launch's threads fit 32 bits
 
 uint64_t up256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // Workspace: two copies of (keys, positions), the histogram, the partial sums.
 struct Space {
-  uint64_t keys[2], at[2], hist, partial, bytes;
+  uint64_t keys[2], at[2], hist, totals, partial, bytes;
   uint32_t blocks, tile, tiles, row;  // row: floats of a partial row
 };
 Space space_of(uint64_t n, uint32_t dim) {
@@ -593,6 +627,7 @@ Space space_of(uint64_t n, uint32_t dim) {
     s.at[i] = take(n * 4);
   }
   s.hist = take((uint64_t)kDigits * s.blocks * 4);
+  s.totals = take(kDigits * 4);
   s.partial = take((uint64_t)s.tiles * 2 * s.row * 4);
   s.bytes = std::max<uint64_t>(at, 256);
   return s;
@@ -621,7 +656,7 @@ extern "C" int zero_embedding(const void* table, int dtype, uint32_t vocab, uint
   clear_error();
   int rc = check_table(table, dtype, vocab, dim, stride, who);
   if (rc) return rc;
-  if (!std::isfinite(scale)) return fail(ZERO_EINVAL, "%s: scale must be finite", who);
+  if (!std::isfinite((float)scale)) return fail(ZERO_EINVAL, "%s: scale must be finite in fp32", who);
   if (n_tokens > UINT64_MAX / 8 / dim) return fail(ZERO_EINVAL, "%s: n_tokens * dim overflows", who);
   if (n_tokens == 0) return ZERO_OK;
   if (!tokens || !multiple_of(tokens, 8) || !out || !multiple_of(out, dtype_bytes(dtype)))
@@ -645,7 +680,7 @@ extern "C" int zero_embedding_workspace_bytes(uint64_t n_tokens, uint32_t dim, u
   clear_error();
   if (!bytes) return fail(ZERO_EINVAL, "%s: bytes is NULL", who);
   if (dim == 0 || dim > kMaxDim) return fail(ZERO_EINVAL, "%s: dim %u outside [1, 2^20]", who, dim);
-  if (n_tokens > (uint64_t)INT32_MAX) return fail(ZERO_ERANGE, "%s: n_tokens beyond 2^31 - 1", who);
+  if (n_tokens > kMaxTokens) return fail(ZERO_ERANGE, "%s: n_tokens beyond 2^28", who);
   *bytes = space_of(n_tokens, dim).bytes;
   return ZERO_OK;
 }
@@ -659,8 +694,8 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
   if (!known_dtype(p->dtype)) return fail(ZERO_EINVAL, "%s: unknown dtype %d", who, p->dtype);
   if (p->table_dtype != p->dtype && p->table_dtype != ZERO_F32)
     return fail(ZERO_EINVAL, "%s: dtable must have the dtype of dout or fp32", who);
-  if (!std::isfinite(p->scale)) return fail(ZERO_EINVAL, "%s: scale must be finite", who);
-  if (p->n_tokens > (uint64_t)INT32_MAX) return fail(ZERO_EINVAL, "%s: n_tokens beyond 2^31 - 1", who);
+  if (!std::isfinite((float)p->scale)) return fail(ZERO_EINVAL, "%s: scale must be finite in fp32", who);
+  if (p->n_tokens > kMaxTokens) return fail(ZERO_EINVAL, "%s: n_tokens beyond 2^28", who);
   const Space s = space_of(p->n_tokens, p->dim);
   if (p->n_tokens > 0) {
     if (!p->dout || !p->tokens || !multiple_of(p->dout, dtype_bytes(p->dtype)) || !multiple_of(p->tokens, 8))
@@ -709,7 +744,7 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
       g.at = at[0];
     } else {
       SortArgs a = {p->tokens, nullptr, nullptr, nullptr, nullptr, reinterpret_cast<uint32_t*>(ws + s.hist),
-                    g.n, p->vocab, s.blocks, 0, 0};
+                    reinterpret_cast<uint32_t*>(ws + s.totals), g.n, p->vocab, s.blocks, 0, 0};
       for (uint32_t i = 0, done = 0; i < passes; ++i) {
         a.shift = done;
         a.bits = (bits - done + passes - i - 1) / (passes - i);
@@ -717,6 +752,7 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
         a.keys_out = keys[i & 1];
         a.at_out = at[i & 1];
         hipLaunchKernelGGL(histogram_kernel, s.blocks, kBlock, 0, stream, a);
+        if (s.blocks > kScanBlocks) hipLaunchKernelGGL(scan_kernel, 1u << a.bits, kBlock, 0, stream, a);
         hipLaunchKernelGGL(scatter_kernel, s.blocks, kBlock, 0, stream, a);
         a.tokens = nullptr;
         a.keys = a.keys_out;
