@@ -21,7 +21,12 @@
 // whatever the loss scale.  The entry at the target, as a rule far larger than the
 // others, whose roundings average out in the sums, would leave its own rounding in
 // both gradients: what it loses in 16 bits is kept beside it and goes into dhidden in
-// the epilogue, into dweight as further terms of the product.
+// the epilogue, into dweight as further terms of the product (rms error of 8192 rows
+// of 128,000 x 4096 bf16 against 64 bits: 1.66e-3 and 1.38e-3, which is the outputs'
+// own rounding; 2.00e-3 and 1.73e-3 without).
+//
+// That step takes 19.2 ms: the products 18.3, softmax 0.72 (3.6 GB read and written,
+// 4.9 TB/s), the join of dhidden's parts 0.11, the rest 0.08.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
