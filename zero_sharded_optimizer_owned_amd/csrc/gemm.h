@@ -21,15 +21,16 @@
 // The products are formed with Q first, so that a lane's four results are four
 // consecutive n of one m.
 //
-// Measured in a training step of 6963 rows that count, 128,000 x 4096, bf16 (7.3
-// TFLOP each): logits 6.2 ms, dhidden 5.7, dweight 6.3, 1.16 to 1.28 PFLOP/s, the
-// matrix cores busy in 57 to 65% of the cycles (a library product of the first
+// Measured in a training step of 6962 rows that count, 128,000 x 4096, bf16 (7.3
+// TFLOP each): logits 6.2 ms, dhidden 5.8, dweight 6.4, 1.15 to 1.25 PFLOP/s, the
+// matrix cores busy in 56 to 64% of the cycles (a library product of the first
 // shape alone: 1.43).  What bounds it is the way of the tiles into LDS, 64 KB a
-// step: with half of the products left out the first still takes 92% of its time,
-// without the loads 78%.  256 x 256 is the largest tile whose sums fit the
+// step: in scores of 4096 such rows an earlier form took 3.21 ms, 2.94 with half of
+// the products left out, 2.49 without the loads.  256 x 256 is the largest tile whose sums fit the
 // registers.  Slower: 128 rows to a tile for all (13%: half as much again to load),
-// steps of 32 k with five under way (2%: requests of 64 bytes), 32 x 32 products
-// (3%), four wavefronts of 128 x 128 (8%: sums moved between register files).
+// 32 x 32 products (4%), four wavefronts of 128 x 128 (7 to 10%: sums moved between
+// register files).  Steps of 32 k with five under way, in requests of 64 bytes, were
+// no faster.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -25,8 +25,8 @@
 // of 128,000 x 4096 bf16 against 64 bits: 1.66e-3 and 1.38e-3, which is the outputs'
 // own rounding; 2.00e-3 and 1.73e-3 without).
 //
-// That step takes 19.2 ms: the products 18.3, softmax 0.72 (3.6 GB read and written,
-// 4.9 TB/s), the join of dhidden's parts 0.11, the rest 0.08.
+// That step takes 19.2 ms: the products 18.4, softmax 0.72 (3.6 GB read and written,
+// 5.0 TB/s), the join of dhidden's parts 0.11, the rest 0.06.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

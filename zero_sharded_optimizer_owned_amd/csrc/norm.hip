@@ -11,7 +11,7 @@
 // All of it is bound by HBM: a row is read once, stays in registers (a lane
 // holds up to eight 16-byte vectors) and is written once.  16,384 rows of 4096
 // bf16: forward with residual, kept, 0.61 GB in 107 us (5.7 TB/s); restore 0.20 GB
-// in 35; backward 0.40 GB in 95, its fold of 512 partial rows 5.  A wavefront takes a
+// in 35; backward 0.47 GB in 95 (5.0 TB/s), its fold of 512 partial rows 5.  A wavefront takes a
 // row where the row fits one, so that rows need no barrier; longer rows take 4
 // or 8 wavefronts.
 #include <hip/hip_runtime.h>
