@@ -631,7 +631,10 @@ Space space_of(uint64_t n, uint32_t dim) {
   }
   s.hist = take((uint64_t)kDigits * s.blocks * 4);
   s.totals = take(kDigits * 4);
-  s.partial = take((uint64_t)s.tiles * 2 * s.row * 4);
+  // the most of any number of tokens up to n, of which 4096 have as many tiles as
+  // 16,384: a workspace serves fewer tokens too
+  const uint64_t few = (std::min<uint64_t>(n, kFewTokens) + kFewTile - 1) / kFewTile;
+  s.partial = take(std::max<uint64_t>(s.tiles, few) * 2 * s.row * 4);
   s.bytes = std::max<uint64_t>(at, 256);
   return s;
 }
