@@ -777,6 +777,7 @@ typedef struct {
  * accumulate != 0: that is added to dtable[v], rounded once, and rows that no
  * token names are left as they are (a tied table takes its output head's gradient
  * first); else those rows are zero.  Tokens outside [0, vocab) count for nothing.
+ * Up to 32 rows of a token at a time are added in fp32, those sums in fp64.
  * Errors: EINVAL (as zero_embedding; table_dtype neither dtype nor F32, workspace
  * missing, small or misaligned); EHIP.
  * -------------------------------------------------------------------------- */

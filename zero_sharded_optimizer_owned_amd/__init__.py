@@ -1000,7 +1000,8 @@ def zero_embedding_grad(dout, tokens, dtable, *, workspace, scale: float = 1.0, 
     they are: a tied table takes its output head's gradient first); without it those
     rows become zero.  ``dout`` [n, dim]; ``dtable`` [vocabulary, dim] of its dtype or
     float32, rows contiguous at any row stride (a view of a rank's flat gradient).
-    Sums are fp32 in a fixed order.  ``workspace`` from ``embedding_workspace``.
+    Sums have a fixed order: fp32 over up to 32 rows of a token, fp64 over those.
+    ``workspace`` from ``embedding_workspace``.
     """
     dt, table_dt = _kind(dout, "dout"), _kind(dtable, "dtable")
     dev, stream = _device_stream()
