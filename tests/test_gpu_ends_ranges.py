@@ -7,6 +7,7 @@ pytestmark = pytest.mark.gpu
 
 import zero_sharded_optimizer_owned_amd as zs  # noqa: E402
 import test_gpu_embedding as emb  # noqa: E402
+import test_gpu_head as head  # noqa: E402
 
 DEV = "cuda"
 U = 2.0 ** -24
@@ -54,3 +55,39 @@ def test_long_runs_of_one_token(n, dt, out):
     want, _, _ = emb.grad_reference(dout, tokens, v, 0.3, None)
     count = torch.bincount(tokens, minlength=v).double()[:, None]
     emb.within(dtable, want, ((count.clamp(max=32) + 1) + 2) * U * want + emb.half_step(want, out))
+
+
+@pytest.mark.parametrize("grads", ["both", "dhidden"])
+@pytest.mark.parametrize("n, v, d", [(5, 46_811, 64), (40, 46_811, 64), (300, 46_811, 16), (1100, 30_011, 8), (290, 1999, 600)])
+def test_a_row_s_gradient_does_not_depend_on_other_rows_weights(n, v, d, grads):
+    """fp16, row weights from 1 down to 2^-22 of it, dhidden in one part of the vocabulary and in
+    several.  A row keeps softmax - onehot in steps of at most 2^-30 (2^-24 / (2^14 2^-8)), so to
+    half of that, and its exponentials down to 2^-40: 2^-30 of the row's own factor holds both,
+    where what test_gpu_head.py allows is 2^-38 of the largest one."""
+    h, w, t, _ = head.problem(n, v, d, "f16", spread=0.3 * d ** 0.5)
+    w += 0.5  # a mean: what is lost of many small probabilities does not average out
+    size = torch.tensor([1.0, 2.0 ** -22, -2.0 ** -7, 2.0 ** -9, -2.0 ** -15, 0.0, 1.3 * 2.0 ** -20, 2.0 ** -21])
+    i = torch.arange(n)
+    weight = size[torch.where(i < 2, i, (i * 5 + 1) % 8)].to(DEV)
+    h[weight.abs() < 2.0 ** -8] = 0  # equal probabilities
+    t[1] = v // 3
+    args = dict(divisor=1.0, grad_scale=2.0 ** 10)
+    got = head.run(h, w, t, weight, grads=(True, grads == "both"), **args)
+    head.check(h, w, t, weight, got, "f16", **args)
+    if grads == "both":  # dweight alone: the same bits
+        alone = head.run(h, w, t, weight, grads=(False, True), **args)
+        assert torch.equal(alone[3], got[3])
+    hd, wd, at, coef = h.double().cpu(), w.double().cpu(), t.cpu(), weight.double().cpu() * 2.0 ** 10
+    ok = (at >= 0) & (at < v)
+    hd, at, coef, row = hd[ok], at[ok], coef[ok], torch.arange(int(ok.sum()))
+    x = hd @ wd.T
+    lp = torch.log_softmax(x, 1)
+    e = (2 * (d / 32 + 8) * U * (hd.abs() @ wd.abs().T)).max(1).values
+    r = 2 * e + (6 * (x.max(1).values - x.min(1).values) + 40) * U
+    dx = lp.exp()
+    dx[row, at] = torch.expm1(lp[row, at])
+    off = (r[:, None] + 2.01 * 2.0 ** -11) * dx.abs() + 2.0 ** -30
+    off[row, at] = (r + 2.0 ** -18) * dx[row, at].abs() + 2.0 ** -30
+    want = coef[:, None] * (dx @ wd)
+    tol = coef.abs()[:, None] * (off @ wd.abs() + 2 * (v / 32 + 70) * U * (dx.abs() @ wd.abs()))
+    emb.within(got[2][ok.to(DEV)], want, tol + 2.0 ** -11 * (want.abs() + tol) + 2.0 ** -25)

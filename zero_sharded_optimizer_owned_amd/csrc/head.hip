@@ -18,7 +18,10 @@
 //   dhidden, dweight  products two and three
 // dx is held as (softmax - onehot) w / max|w| 2^14 in 16 bits; the common factor
 // comes back in the epilogues, so that fp16 keeps probabilities down to 2^-38
-// whatever the loss scale.  The entry at the target, as a rule far larger than the
+// whatever the loss scale.  Rows of less than 2^-8 of the largest weight would keep
+// fewer of theirs: in fp16 they are held times a power of two while dhidden's
+// product reads them (lift), and without it for dweight's, a sum over all rows.
+// The entry at the target, as a rule far larger than the
 // others, whose roundings average out in the sums, would leave its own rounding in
 // both gradients: what it loses in 16 bits is kept beside it and goes into dhidden in
 // the epilogue, into dweight as further terms of the product (rms error of 8192 rows
@@ -70,6 +73,8 @@ struct HeadArgs {
   uint32_t *row_of, *target;  // of each row that counts
   float *omega, *said;        // w / max|w|; the target's logit
   float* rest;                // what dx's entry at the target loses in 16 bits
+  float* lift;                // fp16: the power of two by which dx is larger for dhidden; NULL: 1
+  float* low;                 // rest without it
   double* terms;              // w lp of the piece's rows
   uint8_t* counts;            // of the piece's rows
   uint16_t *kept, *held;      // rows that count [rows][dim8]; exponentials, then dx [rows][padded]
@@ -107,6 +112,22 @@ inline uint32_t splits_of(uint32_t m_tiles, uint32_t vocab, uint32_t dim) {
 typedef Tile<256, 2> Wide;
 typedef Tile<128, 3> Middle;
 __host__ __device__ inline uint32_t tile_rows(uint32_t rows) { return rows <= 128 ? 128 : 256; }
+
+// fp16: rows of a small weight are lifted so that omega lift is in [1/2, 1) and
+// softmax - onehot is held in steps of 2^-37 of the row's own scale at most, not of
+// the largest weight's; the others' steps are 2^-30 at most and need no second pass
+// over dx (weights of 1 / length up to 256).  Powers of two up to 2^64: no rounding
+// but that of small numbers.
+constexpr float kLowest = 0x1p-8f;
+__device__ __forceinline__ float lift_of(float omega) {
+  const float m = fabsf(omega);
+  const uint32_t e = max(__float_as_uint(m) >> 23, 62u);
+  return m > 0.0f && m < kLowest ? __uint_as_float((253 - e) << 23) : 1.0f;
+}
+__device__ __forceinline__ float inverse_of(float lift) { return __uint_as_float((254u << 23) - __float_as_uint(lift)); }
+__device__ __forceinline__ float in_f16(float x) {
+  return Vec<ZERO_F16>::get(Vec<ZERO_F16>::Raw{u32x4{Vec<ZERO_F16>::pack(x, 0.0f), 0, 0, 0}}, 0);
+}
 
 // ---------------------------------------------------------------------------
 // The rows that count, in order.
@@ -151,8 +172,9 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
   for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
   if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), before ? a.splits[(before - 1) / tile_rows(a.rows)] : 1u, 0};
   for (uint32_t i = t; i < before; i += 1024) {
-    const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f;
-    a.omega[i] = top > 0.0f ? w / top : w;  // all weights 0 or not finite
+    const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f, omega = top > 0.0f ? w / top : w;
+    a.omega[i] = omega;  // w: all weights 0 or not finite
+    if (a.lift) a.lift[i] = lift_of(omega);
   }
 }
 
@@ -219,7 +241,9 @@ __global__ void __launch_bounds__(kBlock) prepare_few_kernel(const HeadArgs a) {
       if (counts) {
         a.row_of[at] = r;
         a.target[at] = (uint32_t)target[j];
-        a.omega[at] = top > 0.0f ? w[j] / top : w[j];
+        const float omega = top > 0.0f ? w[j] / top : w[j];
+        a.omega[at] = omega;
+        if (a.lift) a.lift[at] = lift_of(omega);
       } else {
         a.logp[r] = 0.0f;
         a.terms[r] = 0.0;
@@ -463,11 +487,19 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
       a.terms[from] = lp * (a.row_weight ? (double)a.row_weight[from] : 1.0);
     }
     if constexpr (KEEP) {
-      const float omega = a.omega[row] * kHeld;
+      // lifted, and lowered at once where no product reads it so
+      const float lift = DT == ZERO_F16 && a.lift ? a.lift[row] : 1.0f;
+      const float omega = a.omega[row] * kHeld * lift;
       const float unit = (float)((double)omega / all) * (1.0f / kTileExp);
-      const float other = -(float)((double)omega * (sum / all));  // at the target: p - 1, without cancellation
-      if (t == 0 && blockIdx.y == 0)
-        a.rest[row] = other - Vec<DT>::get(typename Vec<DT>::Raw{u32x4{Vec<DT>::pack(other, 0.0f), 0, 0, 0}}, 0);
+      float other = -(float)((double)omega * (sum / all));  // at the target: p - 1, without cancellation
+      const bool lower = DT == ZERO_F16 && lift != 1.0f && !a.dhidden;
+      const float down = inverse_of(lift);
+      if (lower) other *= down;
+      if (t == 0 && blockIdx.y == 0) {
+        const float rest = other - Vec<DT>::get(typename Vec<DT>::Raw{u32x4{Vec<DT>::pack(other, 0.0f), 0, 0, 0}}, 0);
+        a.rest[row] = rest;
+        if (a.low != a.rest) a.low[row] = rest;
+      }
       uint16_t* held = a.held + (uint64_t)row * a.padded;
       for (uint32_t first = tile0; first < tile1; first += kPartTiles) {
         const uint32_t end = min(first + kPartTiles, tile1);
@@ -484,7 +516,11 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
           const float f = scale[(v - v0) >> (a.shift - 3)];
           float x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = v * 8 + k == target ? other : Vec<ZERO_F16>::get(e, k) * f;
+          for (int k = 0; k < 8; ++k) {
+            float y = Vec<ZERO_F16>::get(e, k) * f;
+            if (lower) y = in_f16(y) * down;  // the roundings of a row that is lowered later
+            x[k] = v * 8 + k == target ? other : y;
+          }
           store8<DT>(held, (uint64_t)v * 8, x);
         }
       }
@@ -546,6 +582,9 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
         const typename Vec<DT>::Raw r = {u32x4{v[0], v[1], 0, 0}};
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(rest, Vec<DT>::get(r, x), acc[i][j][x]);
+        if constexpr (DT == ZERO_F16) {
+          if (a.lift) acc[i][j] *= inverse_of(a.lift[row]);
+        }
       }
     }
   }
@@ -571,26 +610,48 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
 }
 
 // dhidden from the sums over parts of the vocabulary, in their order, and what the
-// target's entry lost.
+// target's entry lost.  Lifted rows of dx are lowered for dweight's product.
 template <int DT>
 __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
   const uint32_t live = a.meta->live, splits = a.meta->splits;
-  if (splits <= 1) return;
+  const bool lower = DT == ZERO_F16 && a.lift && a.dweight;
+  if (splits <= 1 && !lower) return;
   const float f = a.meta->factor;
   for (uint32_t row = blockIdx.x; row < live; row += gridDim.x) {
-    const uint64_t at = a.row_of[row] * a.dhidden_stride;
-    const float rest = a.rest[row];
-    const u32x2* w = reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.weight) + a.target[row] * a.weight_stride);
-    for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.dim / 4; v += gridDim.y * kBlock) {
-      f32x4 x = {0, 0, 0, 0};
+    const float rest = a.rest[row], lift = DT == ZERO_F16 && a.lift ? a.lift[row] : 1.0f, down = inverse_of(lift);
+    const uint32_t target = a.target[row];
+    if (splits > 1) {
+      const uint64_t at = a.row_of[row] * a.dhidden_stride;
+      const u32x2* w = reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.weight) + target * a.weight_stride);
+      for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.dim / 4; v += gridDim.y * kBlock) {
+        f32x4 x = {0, 0, 0, 0};
 #pragma unroll 8
-      for (uint32_t s = 0; s < splits; ++s)
-        x += *reinterpret_cast<const f32x4*>(a.part + ((uint64_t)s * live + row) * a.dim + v * 4);
-      const typename Vec<DT>::Raw r = {u32x4{w[v][0], w[v][1], 0, 0}};
+        for (uint32_t s = 0; s < splits; ++s)
+          x += *reinterpret_cast<const f32x4*>(a.part + ((uint64_t)s * live + row) * a.dim + v * 4);
+        const typename Vec<DT>::Raw r = {u32x4{w[v][0], w[v][1], 0, 0}};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = fmaf(rest, Vec<DT>::get(r, k), x[k]);
-      x *= f;
-      store4<DT>(a.dhidden, at + v * 4, x[0], x[1], x[2], x[3]);
+        for (int k = 0; k < 4; ++k) x[k] = fmaf(rest, Vec<DT>::get(r, k), x[k]);
+        if constexpr (DT == ZERO_F16) x *= down;
+        x *= f;
+        store4<DT>(a.dhidden, at + v * 4, x[0], x[1], x[2], x[3]);
+      }
+    }
+    if constexpr (DT == ZERO_F16) {
+      if (!lower || lift == 1.0f) continue;
+      uint16_t* held = a.held + (uint64_t)row * a.padded;
+      for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.padded / 8; v += gridDim.y * kBlock) {
+        const typename Vec<DT>::Raw e = load8<DT>(held, (uint64_t)v * 8);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[k] = Vec<DT>::get(e, k) * down;
+          if (v * 8 + k == target) {
+            x[k] = (Vec<DT>::get(e, k) + rest) * down;  // what the entry was
+            a.low[row] = x[k] - in_f16(x[k]);
+          }
+        }
+        store8<DT>(held, (uint64_t)v * 8, x);
+      }
     }
   }
 }
@@ -659,7 +720,7 @@ __device__ __forceinline__ void add_rests(const HeadArgs& a, uint32_t live, uint
       if (t < n) {
         const uint32_t k = t, row = list[(used + k) % kList], m = a.target[row] - tm * T::kM;
         *reinterpret_cast<uint16_t*>(lds + k * (2 * T::kM) + ((m / 8) ^ P::swizzle(k)) * 16 + m % 8 * 2) =
-            (uint16_t)Vec<DT>::pack(a.rest[row], 0.0f);
+            (uint16_t)Vec<DT>::pack(a.low[row], 0.0f);
       }
       __syncthreads();
 #pragma unroll 1
@@ -729,7 +790,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs
 constexpr uint32_t kMaxDim = 1u << 15;
 
 struct Space {
-  uint64_t meta, row_of, target, omega, said, rest, terms, counts, kept, held, stats, part, sum, bytes;
+  uint64_t meta, row_of, target, omega, said, rest, lift, low, terms, counts, kept, held, stats, part, sum, bytes;
   uint32_t piece, tiles, shift;
 };
 
@@ -753,6 +814,8 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.omega = take(p * 4);
   s.said = take(p * 4);
   s.rest = take(grad ? p * 4 : 0);
+  s.lift = take(grad ? p * 4 : 0);
+  s.low = take(grad ? p * 4 : 0);
   s.terms = take(n_rows * 8);
   s.counts = take(n_rows);
   s.kept = take(p * dim * 2);
@@ -913,7 +976,11 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   a.target = reinterpret_cast<uint32_t*>(ws + s.target);
   a.omega = reinterpret_cast<float*>(ws + s.omega);
   a.said = reinterpret_cast<float*>(ws + s.said);
-  a.rest = reinterpret_cast<float*>(ws + s.rest);
+  a.rest = a.low = reinterpret_cast<float*>(ws + s.rest);
+  if (grad && p->dtype == ZERO_F16 && p->row_weight) {
+    a.lift = reinterpret_cast<float*>(ws + s.lift);
+    a.low = reinterpret_cast<float*>(ws + s.low);
+  }
   a.kept = reinterpret_cast<uint16_t*>(ws + s.kept);
   a.stats = reinterpret_cast<f32x2*>(ws + s.stats);
   a.held = reinterpret_cast<uint16_t*>(ws + s.held);
