@@ -738,9 +738,10 @@ int zero_preference_workspace_bytes(uint64_t n_rows, uint32_t n_pairs, uint64_t 
  * The model's two ends, and what its backward pass keeps.
  *
  * Tables and rows are F16, BF16 or F32.  Sums are fp32 or wider, in an order that
- * depends on the sizes alone, so results are identical run to run.  A workspace's
- * contents do not matter before a call and mean nothing after it; one made for some
- * size serves smaller ones; calls that overlap need one each.
+ * depends on the sizes and on which tokens and rows count, so results are identical
+ * run to run.  A workspace's contents do not matter before a call and mean nothing
+ * after it; one made for some number of rows or tokens serves fewer of them at the
+ * same other sizes; calls that overlap need one each.
  * -------------------------------------------------------------------------- */
 
 /* ----------------------------------------------------------------------------
@@ -873,8 +874,10 @@ typedef struct {
  * sums of dweight.  Logits that are NaN or +inf give NaN; -inf has
  * probability 0.
  * Rows go in pieces of piece_rows; per row of a piece the workspace holds vocab 16-bit
- * values (without gradients: vocab / 32 bytes) and the hidden state, and with more than
- * one piece fp32 sums of dweight.
+ * values (without gradients: vocab / 32 bytes) and the hidden state, with gradients
+ * (whichever is wanted) fp32 sums of dhidden over up to 64 parts of the vocabulary,
+ * 512 MiB at most, and with more than one piece fp32 sums of dweight.  Fewer columns
+ * can mean more parts: a workspace serves fewer rows, not a smaller dim or vocab.
  * n_rows == 0 writes stats 0 and a zero dweight.
  * Errors: EINVAL (sizes, strides and alignment as above, divisor or temperature
  * not finite and > 0, grad_scale not finite, NULL arrays, workspace missing, small

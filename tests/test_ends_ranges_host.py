@@ -69,3 +69,19 @@ def test_a_workspace_of_the_linear_cross_entropy_serves_fewer_rows(vocab, dim, p
         now = size(fn, n, vocab, dim, piece, grad)
         assert now >= last and now >= size(fn, n, vocab, dim, piece, 0), n
         last = now
+
+
+@pytest.mark.parametrize("n", [1, 77, 256, 2202, 8192, 20_000])
+@pytest.mark.parametrize("vocab, dim", [(16_544, 1936), (16_544, 2096), (32_000, 64), (32_000, 1024), (32_000, 4096), (50_001, 1000),
+                                        (128_000, 4096), (128_000, 16_384), (1 << 20, 8), (1000, 32_768)])
+def test_what_a_workspace_of_the_linear_cross_entropy_holds(n, vocab, dim):
+    """Two bytes a logit of a piece, the hidden states, the tiles' statistics, a few bytes a row, at
+    most 512 MiB for the parts of dhidden's sums, and past one piece the sums of dweight."""
+    fn = zs.lib().zero_linear_cross_entropy_workspace_bytes
+    piece = min(n, 8192)
+    padded = -(-vocab // 256) * 256
+    # up to 8 rows the statistics are of 16 columns: 8 rows' are 0.5 bytes a logit
+    scores = piece * dim * 2 + max(piece * padded // 256, min(piece, 8) * padded // 16) * 8 + 9 * n + 64 * piece + 8192
+    assert size(fn, n, vocab, dim, 8192, 0) <= scores
+    whole = scores + piece * padded * 2 + (512 << 20) + (vocab * dim * 4 if n > piece else 0)
+    assert piece * vocab * 2 <= size(fn, n, vocab, dim, 8192, 1) <= whole
