@@ -847,23 +847,24 @@ def zero_token_logprobs(logits, targets, logp, *, temperature: float = 1.0) -> N
     _check(lib().zero_token_logprobs(*rows, temperature, _addr(logp, "logp", _torch().float32, rows[2], dev), stream))
 
 
-def _workspace(fn, *sizes, device=None):
+def _workspace(fn, *sizes, device=None, clear=False):
+    """A workspace of the size that `fn` gives; zeros where its contents matter (`clear`)."""
     out = np.zeros(1, dtype=np.uint64)
     _check(fn(*sizes, _p(out)))
     torch = _torch()
-    return torch.zeros(int(out[0]), dtype=torch.uint8, device=_device(device))
+    return (torch.zeros if clear else torch.empty)(int(out[0]), dtype=torch.uint8, device=_device(device))
 
 
 def policy_workspace(n_rows: int, device=None):
     """The device workspace of ``zero_policy_loss`` over up to n_rows rows: zeros before
     its first use, then left ready for the next call (one call at a time).  Any other
     contents show as NaN in ``stats``."""
-    return _workspace(lib().zero_policy_workspace_bytes, n_rows, device=device)
+    return _workspace(lib().zero_policy_workspace_bytes, n_rows, device=device, clear=True)
 
 
 def preference_workspace(n_rows: int, n_pairs: int, device=None):
     """The device workspace of ``zero_preference_loss`` over up to n_rows rows and n_pairs pairs."""
-    return _workspace(lib().zero_preference_workspace_bytes, n_rows, n_pairs, device=device)
+    return _workspace(lib().zero_preference_workspace_bytes, n_rows, n_pairs, device=device, clear=True)
 
 
 def zero_policy_loss(logits, targets, *, old_logp, advantage, divisor: float, stats, logp, workspace, ref_logp=None,

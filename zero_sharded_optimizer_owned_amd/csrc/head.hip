@@ -845,12 +845,11 @@ int check_shape(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_ro
   return ZERO_OK;
 }
 
-int check_matrix(const void* p, uint64_t rows, uint32_t dim, uint64_t stride, const char* name, const char* who) {
+int check_matrix(const void* p, uint32_t dim, uint64_t stride, const char* name, const char* who) {
   if (!p || !multiple_of(p, 16) || stride % 8)
     return fail(ZERO_EINVAL, "%s: %s is NULL, or its rows are not 16-byte aligned", who, name);
   if (stride < dim || stride > (1u << 22))
     return fail(ZERO_EINVAL, "%s: %s has a row stride of %llu outside [dim, 2^22]", who, name, (unsigned long long)stride);
-  (void)rows;
   return ZERO_OK;
 }
 
@@ -939,13 +938,13 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   if (p->temperature <= 0.0 || !std::isnormal((float)(kLog2e / p->temperature)))
     return fail(ZERO_EINVAL, "%s: temperature %g is out of range", who, p->temperature);
   if (!p->stats || !multiple_of(p->stats, 4)) return fail(ZERO_EINVAL, "%s: stats is NULL or misaligned", who);
-  if ((rc = check_matrix(p->weight, p->vocab, p->dim, p->weight_stride, "weight", who))) return rc;
-  if (p->dweight && (rc = check_matrix(p->dweight, p->vocab, p->dim, p->dweight_stride, "dweight", who))) return rc;
+  if ((rc = check_matrix(p->weight, p->dim, p->weight_stride, "weight", who))) return rc;
+  if (p->dweight && (rc = check_matrix(p->dweight, p->dim, p->dweight_stride, "dweight", who))) return rc;
   const bool grad = p->dhidden || p->dweight;
   const Space s = space_of(p->n_rows, p->vocab, p->dim, p->piece_rows, grad);
   if (p->n_rows > 0) {
-    if ((rc = check_matrix(p->hidden, p->n_rows, p->dim, p->hidden_stride, "hidden", who))) return rc;
-    if (p->dhidden && (rc = check_matrix(p->dhidden, p->n_rows, p->dim, p->dhidden_stride, "dhidden", who))) return rc;
+    if ((rc = check_matrix(p->hidden, p->dim, p->hidden_stride, "hidden", who))) return rc;
+    if (p->dhidden && (rc = check_matrix(p->dhidden, p->dim, p->dhidden_stride, "dhidden", who))) return rc;
     if (!p->targets || !multiple_of(p->targets, 8)) return fail(ZERO_EINVAL, "%s: targets is NULL or misaligned", who);
     if (!p->logp || !multiple_of(p->logp, 4) || !multiple_of(p->row_weight, 4))
       return fail(ZERO_EINVAL, "%s: logp is NULL, or a per-row array is misaligned", who);

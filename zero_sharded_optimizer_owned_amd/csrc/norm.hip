@@ -45,7 +45,7 @@ struct BackwardArgs {
   const void *dy, *gain, *h, *upstream;
   const uint8_t* codes;
   const float *scales, *rstd;
-  void *dx, *dgain;
+  void* dx;
   float* partial;  // [gridDim.x][dim up to a multiple of 8]
   uint64_t n_rows;
   uint32_t dim, blocks;
@@ -497,7 +497,7 @@ extern "C" int zero_rms_norm_backward(const zero_rms_norm_backward_args* p, hipS
   if ((rc = begin_launch())) return rc;
   uint32_t parts = 0;
   if (p->n_rows > 0) {
-    const BackwardArgs a = {p->dy, p->gain, p->h, p->upstream, p->codes, p->scales, p->rstd, p->dx, p->dgain,
+    const BackwardArgs a = {p->dy, p->gain, p->h, p->upstream, p->codes, p->scales, p->rstd, p->dx,
                             static_cast<float*>(p->workspace), p->n_rows, p->dim, scales_of(p->dim)};
     with_dtype(p->dtype, [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
