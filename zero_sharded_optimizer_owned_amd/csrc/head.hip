@@ -52,7 +52,6 @@ struct Meta {
   uint32_t live;    // rows that count, of the piece
   float factor;     // dx = factor * what is held
   uint32_t splits;  // of dhidden's sums over the vocabulary
-  uint32_t done;    // rows whose terms are stored (few rows only)
 };
 
 struct HeadArgs {
@@ -83,8 +82,6 @@ struct HeadArgs {
   float* sum;                 // fp32 dweight of the pieces so far
   int first, last;            // whether the piece is the first, the last
   uint8_t splits[64];         // of i + 1 tiles of rows that count
-  float* stats_out;           // few rows: the last block of softmax_kernel writes the loss
-  double inv_divisor;
 };
 
 // How many parts the vocabulary of dhidden's product is cut into, so that the
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
   if (lane == 0) most[wave] = top;
   __syncthreads();
   for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
-  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), before ? a.splits[(before - 1) / tile_rows(a.rows)] : 1u, 0};
+  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), before ? a.splits[(before - 1) / tile_rows(a.rows)] : 1u};
   for (uint32_t i = t; i < before; i += 1024) {
     const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f, omega = top > 0.0f ? w / top : w;
     a.omega[i] = omega;  // w: all weights 0 or not finite
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(kBlock) prepare_few_kernel(const HeadArgs a) {
     at += counts;
   }
   if (blockIdx.x == 0 && t == 0)
-    *a.meta = Meta{live, (float)(a.coef * (double)top / kHeld), live ? a.splits[(live - 1) / tile_rows(a.rows)] : 1u, 0};
+    *a.meta = Meta{live, (float)(a.coef * (double)top / kHeld), live ? a.splits[(live - 1) / tile_rows(a.rows)] : 1u};
   __syncthreads();
   gather_row(a, blockIdx.x, mine, a.dhidden && out);
 }
@@ -435,30 +432,11 @@ __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPartTiles = 512;      // most tiles of one part
 
-// Up to this many rows the last block to finish adds up the rows' terms.
-constexpr uint32_t kTicketRows = 128;
-
-__device__ __forceinline__ void loss_of(const double* terms, const uint8_t* counts, uint64_t n, double inv_divisor,
-                                        double* part, float* stats) {
-  double sum = 0.0, count = 0.0;
-  for (uint64_t i = threadIdx.x; i < n; i += kBlock) {
-    sum += terms[i];
-    count += (double)counts[i];
-  }
-  sum = row_sum<kWavesPerBlock>(sum, part);
-  count = row_sum<kWavesPerBlock>(count, part);
-  if (threadIdx.x == 0) {
-    stats[0] = (float)(-sum * inv_divisor);
-    stats[1] = (float)count;
-  }
-}
-
 template <int DT, bool KEEP>
 __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
   __shared__ float scale[KEEP ? kPartTiles : 1];
   __shared__ double part[kWavesPerBlock];
   __shared__ float tops[kWavesPerBlock];
-  __shared__ uint32_t rank;
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, live = a.meta->live;
   // this block's tiles
   const uint32_t per = (a.tiles + gridDim.y - 1) / gridDim.y, tile0 = blockIdx.y * per, tile1 = min(tile0 + per, a.tiles);
@@ -526,22 +504,26 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
       }
     }
   }
-  if (!a.stats_out || blockIdx.y != 0) return;
-  // few rows: a block to each, and one at least; the last one adds up
-  if (t == 0) {
-    __threadfence();
-    rank = atomicAdd(&a.meta->done, 1u);
-  }
-  __syncthreads();
-  if (rank + 1 != gridDim.x) return;
-  __threadfence();
-  loss_of(a.terms, a.counts, a.rows, a.inv_divisor, part, a.stats_out);
 }
 
+// (A launch of its own also for few rows: as the last block's work in softmax_kernel, behind
+// a counter and its fences, the sum made scores of 1 to 128 rows no faster, alone
+// or among others, and 77 rows of 50,001 x 1000 fp16 with gradients 161 us alone
+// instead of 154.)
 __global__ void __launch_bounds__(kBlock) loss_kernel(const double* terms, const uint8_t* counts, uint64_t n, double inv_divisor,
                                                       float* stats) {
   __shared__ double part[kWavesPerBlock];
-  loss_of(terms, counts, n, inv_divisor, part, stats);
+  double sum = 0.0, count = 0.0;
+  for (uint64_t i = threadIdx.x; i < n; i += kBlock) {
+    sum += terms[i];
+    count += (double)counts[i];
+  }
+  sum = row_sum<kWavesPerBlock>(sum, part);
+  count = row_sum<kWavesPerBlock>(count, part);
+  if (threadIdx.x == 0) {
+    stats[0] = (float)(-sum * inv_divisor);
+    stats[1] = (float)count;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -985,8 +967,6 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
   a.held = reinterpret_cast<uint16_t*>(ws + s.held);
   a.part = reinterpret_cast<float*>(ws + s.part);
   a.sum = reinterpret_cast<float*>(ws + s.sum);
-  if (p->n_rows > 0 && p->n_rows <= std::min<uint64_t>(kTicketRows, s.piece)) a.stats_out = p->stats;
-  a.inv_divisor = 1.0 / p->divisor;
   double* terms = reinterpret_cast<double*>(ws + s.terms);
   uint8_t* counts = reinterpret_cast<uint8_t*>(ws + s.counts);
   // without rows, one empty piece: dweight is then zero
@@ -1013,7 +993,6 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
     if ((rc = launch_status(who))) return rc;
     row += a.rows;
   } while (row < p->n_rows);
-  if (a.stats_out) return ZERO_OK;
-  hipLaunchKernelGGL(loss_kernel, 1, kBlock, 0, stream, terms, counts, p->n_rows, a.inv_divisor, p->stats);
+  hipLaunchKernelGGL(loss_kernel, 1, kBlock, 0, stream, terms, counts, p->n_rows, 1.0 / p->divisor, p->stats);
   return launch_status(who);
 }
