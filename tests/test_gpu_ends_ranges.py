@@ -91,3 +91,14 @@ def test_a_row_s_gradient_does_not_depend_on_other_rows_weights(n, v, d, grads):
     want = coef[:, None] * (dx @ wd)
     tol = coef.abs()[:, None] * (off @ wd.abs() + 2 * (v / 32 + 70) * U * (dx.abs() @ wd.abs()))
     emb.within(got[2][ok.to(DEV)], want, tol + 2.0 ** -11 * (want.abs() + tol) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("n", [30_720, 32_768, 32_769, 34_817])
+def test_gradient_at_the_number_of_blocks_that_a_sort_scans(n):
+    v, d = 5000, 8
+    dout = torch.randn(n, d, generator=torch.Generator().manual_seed(n)).to(DEV)
+    tokens = emb.tokens_of(n, v, 3)
+    dtable = torch.empty(v, d, device=DEV)
+    zs.zero_embedding_grad(dout, tokens, dtable, workspace=zs.embedding_workspace(n, v, d))
+    want, tol, _ = emb.grad_reference(dout, tokens, v, 1.0, None)
+    emb.within(dtable, want, tol + emb.half_step(want, "f32"))
