@@ -1094,6 +1094,8 @@ def zero_rms_norm_backward(dy, gain, rstd, dx, dgain, *, workspace, h=None, code
     _check(lib().zero_rms_norm_backward(ct.byref(a), stream))
 
 
+# With gradients, 16,384 rows of 128,000 x 4096 bf16 take 45.3 ms as one piece, 45.5 in
+# pieces of 8192 rows, 47.3 of 4096 and 52.5 of 2048.
 PIECE_ROWS = 8192
 
 
