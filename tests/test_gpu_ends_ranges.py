@@ -102,3 +102,46 @@ def test_gradient_at_the_number_of_blocks_that_a_sort_scans(n):
     zs.zero_embedding_grad(dout, tokens, dtable, workspace=zs.embedding_workspace(n, v, d))
     want, tol, _ = emb.grad_reference(dout, tokens, v, 1.0, None)
     emb.within(dtable, want, tol + emb.half_step(want, "f32"))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n, v, d", [(9, 5, 7), (333, 1000, 100), (9000, 70, 33)])
+def test_half_precision_into_an_fp32_table(n, v, d, accumulate):
+    dout = torch.randn(n, d, generator=torch.Generator().manual_seed(n)).half().to(DEV)
+    tokens = emb.tokens_of(n, v, 3)
+    dtable, _ = emb.table_of(v, d, d + 3, "f32", 9)
+    start = dtable.clone()
+    zs.zero_embedding_grad(dout, tokens, dtable, workspace=zs.embedding_workspace(n, v, d), scale=0.3, accumulate=accumulate)
+    want, tol, _ = emb.grad_reference(dout, tokens, v, 0.3, start if accumulate else None)
+    emb.within(dtable, want, tol + emb.half_step(want, "f32"))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("piece", [8192, 300, 6])
+def test_weights_of_all_sizes_in_pieces(piece, dt):
+    """Pieces whose largest weights differ, one of them with small weights alone."""
+    n, v, d = 700, 5001, 40
+    h, w, t, _ = head.problem(n, v, d, dt)
+    i = torch.arange(n)
+    weight = (torch.where(i % 3 == 0, 2.0 ** -13, 1.0) * torch.where(i >= 300, 1.0, 2.0 ** -20)).to(DEV)
+    got = head.run(h, w, t, weight, piece=piece, grad_scale=2.0 ** 9)
+    head.check(h, w, t, weight, got, dt, grad_scale=2.0 ** 9)
+    # a negligible row's weight: the same log-probabilities, and the others' gradients to the bit
+    weight[1] = 0.0
+    again = head.run(h, w, t, weight, piece=piece, grad_scale=2.0 ** 9)
+    assert torch.equal(again[1], got[1]) and torch.equal(again[2][2:], got[2][2:])
+
+
+def test_weights_that_are_not_finite_beside_small_ones():
+    """fp16: a row of infinite weight is NaN or infinite by itself, the others' gradients are not."""
+    n, v, d = 40, 700, 64
+    h, w, t, weight = head.problem(n, v, d, "f16", ignore=0.0)
+    weight[::2] *= 2.0 ** -14
+    clean = head.run(h, w, t, weight, grad_scale=2.0 ** 9)
+    top = int(weight.argmax())
+    k = 5 if top != 5 else 7
+    weight[k] = float("inf")
+    got = head.run(h, w, t, weight, grad_scale=2.0 ** 9)
+    rest = [i for i in range(n) if i != k]
+    assert torch.equal(got[2][rest], clean[2][rest]) and torch.equal(got[1], clean[1])
+    assert not torch.isfinite(got[2][k]).any() and not torch.isfinite(got[0][0])

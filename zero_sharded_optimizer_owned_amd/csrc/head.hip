@@ -20,13 +20,19 @@
 // comes back in the epilogues, so that fp16 keeps probabilities down to 2^-38
 // whatever the loss scale.  Rows of less than 2^-8 of the largest weight would keep
 // fewer of theirs: in fp16 they are held times a power of two while dhidden's
-// product reads them (lift), and without it for dweight's, a sum over all rows.
-// The entry at the target, as a rule far larger than the
-// others, whose roundings average out in the sums, would leave its own rounding in
-// both gradients: what it loses in 16 bits is kept beside it and goes into dhidden in
-// the epilogue, into dweight as further terms of the product (rms error of 8192 rows
-// of 128,000 x 4096 bf16 against 64 bits: 1.66e-3 and 1.38e-3, which is the outputs'
-// own rounding; 2.00e-3 and 1.73e-3 without).
+// product reads them (lift), and without it for dweight's, a sum over all rows (with
+// half of the rows so small, 8192 rows of 128,000 x 4096 take 2% longer).  The entry
+// at the target, as a rule far larger than the others, whose roundings average out in
+// the sums, would leave its own rounding in both gradients: what it loses in 16 bits is
+// kept beside it and goes into dhidden in the epilogue, into dweight as further terms
+// of the product, in 16 bits once more (rms error of 8192 rows of 128,000 x 4096 bf16
+// against 64 bits: 1.66e-3 and 1.38e-3, which is the outputs' own rounding; 2.00e-3
+// and 1.73e-3 without).
+//
+// Fewer bits than fp32 are choices: the matrix cores multiply 16-bit operands, so dx is
+// rounded to the storage type; the exponentials, which are written and read once
+// between the first product and dx, have 11 bits so as not to take twice that room and
+// time.  Sums, maxima, log-probabilities and the loss have 32 or 64.
 //
 // That step takes 19.2 ms: the products 18.4, softmax 0.72 (3.6 GB read and written,
 // 5.0 TB/s), the join of dhidden's parts 0.11, the rest 0.06.
@@ -885,7 +891,10 @@ void launch_piece(HeadArgs a, bool grad, hipStream_t stream) {
       typedef decltype(tile) T;
       hipLaunchKernelGGL((dhidden_kernel<DT, T>), blocks, kGemmThreads, T::kLds, stream, a);
     });
-    hipLaunchKernelGGL(join_kernel<DT>, dim3(a.rows, (a.dim / 4 + kBlock - 1) / kBlock), kBlock, 0, stream, a);
+    uint32_t parts = (a.dim / 4 + kBlock - 1) / kBlock;
+    if (a.lift && a.dweight)  // which rows are lowered is not known here: with few, parts of them
+      parts = std::max(parts, std::min((a.padded / 8 + 4 * kBlock - 1) / (4 * kBlock), 2048 / a.rows));
+    hipLaunchKernelGGL(join_kernel<DT>, dim3(a.rows, parts), kBlock, 0, stream, a);
   }
   if (a.dweight) launch_dweight<DT>(a, stream);
 }
