@@ -869,12 +869,13 @@ typedef struct {
  * A target outside [0, vocab) (say -100) marks a row that counts for nothing: logp
  * 0, no loss, zero dhidden, its hidden state unread.  Products add in fp32.  The
  * gradients' first factor, softmax - onehot, passes through 11 significant bits and
- * then those of dtype; its entries at the targets count in full.  In F16 it goes down
+ * then those of dtype (twice as many of up to 64 rows and up to dim 16); its entries
+ * at the targets count in full.  In F16 it goes down
  * to 2^-30 in each row of dhidden, and to 2^-38 of the largest |row_weight|'s in the
  * sums of dweight.  Logits that are NaN or +inf give NaN; -inf has
  * probability 0.
  * Rows go in pieces of piece_rows; per row of a piece the workspace holds vocab 16-bit
- * values (without gradients: vocab / 32 bytes) and the hidden state, with gradients
+ * values (two each of up to 64 rows and up to dim 16; without gradients: vocab / 32 bytes) and the hidden state, with gradients
  * (whichever is wanted) fp32 sums of dhidden over up to 64 parts of the vocabulary,
  * 512 MiB at most, and with more than one piece fp32 sums of dweight.  Fewer columns
  * can mean more parts: a workspace serves fewer rows, not a smaller dim or vocab.

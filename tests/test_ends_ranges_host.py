@@ -60,7 +60,7 @@ def test_a_workspace_of_the_norm_s_backward_pass_serves_fewer_rows_and_columns(d
 
 
 @pytest.mark.parametrize("grad", [0, 1])
-@pytest.mark.parametrize("vocab, dim, piece", [(200, 8, 8192), (16_544, 1936, 8192), (32_000, 1088, 300), (128_000, 4096, 16_384),
+@pytest.mark.parametrize("vocab, dim, piece", [(200, 8, 8192), (5001, 16, 300), (5001, 24, 300), (60_000, 16, 16_384), (5001, 72, 50), (16_544, 1936, 8192), (32_000, 1088, 300), (128_000, 4096, 16_384),
                                                (50_001, 1000, 5)])
 def test_a_workspace_of_the_linear_cross_entropy_serves_fewer_rows(vocab, dim, piece, grad):
     fn = zs.lib().zero_linear_cross_entropy_workspace_bytes
@@ -75,7 +75,7 @@ def test_a_workspace_of_the_linear_cross_entropy_serves_fewer_rows(vocab, dim, p
 @pytest.mark.parametrize("vocab, dim", [(16_544, 1936), (16_544, 2096), (32_000, 64), (32_000, 1024), (32_000, 4096), (50_001, 1000),
                                         (128_000, 4096), (128_000, 16_384), (1 << 20, 8), (1000, 32_768)])
 def test_what_a_workspace_of_the_linear_cross_entropy_holds(n, vocab, dim):
-    """Two bytes a logit of a piece, the hidden states, the tiles' statistics, a few bytes a row, at
+    """Two bytes a logit of a piece (four up to 64 rows or dim 16), the hidden states, the tiles' statistics, a few bytes a row, at
     most 512 MiB for the parts of dhidden's sums, and past one piece the sums of dweight."""
     fn = zs.lib().zero_linear_cross_entropy_workspace_bytes
     piece = min(n, 8192)
@@ -83,5 +83,6 @@ def test_what_a_workspace_of_the_linear_cross_entropy_holds(n, vocab, dim):
     # up to 8 rows the statistics are of 16 columns: 8 rows' are 0.5 bytes a logit
     scores = piece * dim * 2 + max(piece * padded // 256, min(piece, 8) * padded // 16) * 8 + 9 * n + 64 * piece + 8192
     assert size(fn, n, vocab, dim, 8192, 0) <= scores
-    whole = scores + piece * padded * 2 + (512 << 20) + (vocab * dim * 4 if n > piece else 0)
-    assert piece * vocab * 2 <= size(fn, n, vocab, dim, 8192, 1) <= whole
+    held = 2 * piece if dim <= 16 else max(piece, 2 * min(piece, 64))
+    whole = scores + held * (padded + dim) * 2 + (512 << 20) + (vocab * dim * 4 if n > piece else 0)
+    assert held * vocab * 2 <= size(fn, n, vocab, dim, 8192, 1) <= whole

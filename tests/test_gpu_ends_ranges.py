@@ -145,3 +145,46 @@ def test_weights_that_are_not_finite_beside_small_ones():
     rest = [i for i in range(n) if i != k]
     assert torch.equal(got[2][rest], clean[2][rest]) and torch.equal(got[1], clean[1])
     assert not torch.isfinite(got[2][k]).any() and not torch.isfinite(got[0][0])
+
+
+@pytest.mark.parametrize("piece", [8192, 70])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("n, v, d", [(1, 3, 8), (2, 2017, 8), (3, 220, 16), (8, 500, 264), (9, 500, 24), (45, 371, 384),
+                                     (64, 1500, 136), (64, 5001, 520), (65, 300, 16), (128, 900, 16), (129, 257, 8),
+                                     (190, 1550, 8), (300, 5001, 16), (1030, 700, 16), (1100, 3278, 8)])
+def test_small_heads_in_two_numbers(n, v, d, dt, weighted, piece):
+    """Up to 64 rows and up to dim 16 softmax - onehot is held in two numbers of the type.  The exponentials' two of
+    11 bits are off by 2^-24, dx's by 2^-24 (fp16) or 2^-18 (bf16: half a step of 8 bits, twice),
+    all relative; what is below fp16's smallest numbers by 2^-38 of the largest factor."""
+    if piece == 70 and n < 128:
+        return
+    h, w, t, weight = head.problem(n, v, d, dt, spread=4.0)
+    if weighted:
+        weight *= torch.where(torch.arange(n, device=DEV) % 2 == 0, -1.0, 2.0 ** -9)
+    else:
+        weight = None
+    scale = 2.0 ** 7 if dt == "f16" else 1.0
+    got = head.run(h, w, t, weight, temperature=0.8, grad_scale=scale, piece=piece)
+    head.check(h, w, t, weight, got, dt, temperature=0.8, grad_scale=scale)
+    for grads in ((True, False), (False, True)):
+        part = head.run(h, w, t, weight, temperature=0.8, grad_scale=scale, piece=piece, grads=grads)
+        for a, b in zip(part, got):
+            assert a is None or torch.equal(a, b)
+    hd, wd, at = h.double().cpu(), w.double().cpu(), t.cpu()
+    ok = (at >= 0) & (at < v)
+    hd, at, row = hd[ok], at[ok], torch.arange(int(ok.sum()))
+    coef = (torch.ones(n, dtype=torch.float64) if weight is None else weight.double().cpu())[ok] * scale / 3.0 / 0.8
+    x = hd @ wd.T / 0.8
+    lp = torch.log_softmax(x, 1)
+    e = (2 * (d / 32 + 8) * U * (hd.abs() @ wd.abs().T) / 0.8).max(1).values
+    z = torch.maximum((x.max(1).values - x.min(1).values).clamp(max=42), -lp[row, at])
+    r = 2 * e + (6 * z + 40) * U
+    dx = coef[:, None] * lp.exp()
+    dx[row, at] = coef * torch.expm1(lp[row, at])
+    eps = torch.finfo(emb.DT[dt]).eps
+    off = (r[:, None] + 2 * U + (2.0 ** -18 if dt == "bf16" else U)) * dx.abs() + 2.0 ** -38 * coef.abs().max()
+    for g, m, o, a, k in ((got[2][ok.to(DEV)], dx, off, wd, v), (got[3], dx.T, off.T, hd, n)):
+        want = m @ a
+        tol = o @ a.abs() + 2 * (2 * k / 32 + 70) * U * (m.abs() @ a.abs())
+        emb.within(g, want, tol + (eps / 2) * (want.abs() + tol) + head.SUB[dt])

@@ -1103,7 +1103,7 @@ def linear_cross_entropy_workspace(n_rows: int, vocab: int, dim: int, *, grad: b
                                    piece_rows: int = PIECE_ROWS, device=None):
     """The device workspace of ``zero_linear_cross_entropy`` over up to n_rows rows.
 
-    With gradients it holds 2 bytes for each logit of ``piece_rows`` rows, up to 512 MiB of
+    With gradients it holds 2 bytes (up to dim 16: 4) for each logit of ``piece_rows`` rows, up to 512 MiB of
     fp32 parts of the sums of ``dhidden`` and, with more rows than that, 4 bytes for each
     weight; without them vocab / 32 bytes a row.  It serves fewer rows of the same
     vocabulary, dim and ``piece_rows``, with or without gradients."""

@@ -68,6 +68,7 @@ struct HeadArgs {
   uint32_t rows, vocab, dim;  // rows: of the piece
   uint32_t tiles, padded;     // tiles of the vocabulary, its columns up to a multiple of 256
   uint32_t shift;             // a tile is 1 << shift columns
+  uint32_t planes;            // 16-bit numbers that a value of dx is held in
   double inv_temperature, coef;  // coef = grad_scale / (divisor temperature)
   float c;                    // log2(e) / temperature
   float* logp;
@@ -82,12 +83,14 @@ struct HeadArgs {
   float* low;                 // rest without it
   double* terms;              // w lp of the piece's rows
   uint8_t* counts;            // of the piece's rows
-  uint16_t *kept, *held;      // rows that count [rows][dim8]; exponentials, then dx [rows][padded]
+  // of the rows that count, `live` of them: kept [planes][live][dim], the hidden states;
+  // held [planes][live][padded], the exponentials, then dx
+  uint16_t *kept, *held;
   f32x2* stats;               // [rows][tiles]: a tile's maximum and sum without the target
-  float* part;                // [splits][rows][dim]: dhidden's sums over parts of the vocabulary
+  float* part;                // [splits][planes][live][dim]: dhidden's sums over parts of the vocabulary
   float* sum;                 // fp32 dweight of the pieces so far
   int first, last;            // whether the piece is the first, the last
-  uint8_t splits[64];         // of i + 1 tiles of rows that count
+  uint8_t splits[128];        // of i + 1 tiles of rows of dx
 };
 
 // How many parts the vocabulary of dhidden's product is cut into, so that the
@@ -116,6 +119,18 @@ typedef Tile<256, 2> Wide;
 typedef Tile<128, 3> Middle;
 __host__ __device__ inline uint32_t tile_rows(uint32_t rows) { return rows <= 128 ? 128 : 256; }
 
+// For few rows and for few columns dx is held in two numbers, the second of what the
+// first loses, as further rows that meet the same hidden states: where little is added
+// up, the roundings of single probabilities show in the gradients.  Of 400 heads of all
+// sizes, held in one number, the error was up to 1.7 times that of fp32 products at
+// dim 8 and 16 and up to 1.45 times of 64 rows or fewer; with two it is the same, and
+// of the rest up to 1.12 times.  Up to 64 rows both numbers fit one tile of 128 rows (8
+// rows of 32,000 x 4096 bf16 239 us instead of 234, 64 rows 275 and 241, of 50,001 x
+// 1000 fp16 149 and 129); past them the second costs as much as the first (8192 rows of
+// 32,000 x 16 bf16 1.57 ms and 0.92).
+constexpr uint32_t kTwoRows = 64, kTwoDim = 16;
+__host__ __device__ inline uint32_t planes_of(uint32_t rows, uint32_t dim) { return rows <= kTwoRows || dim <= kTwoDim ? 2 : 1; }
+
 // fp16: rows of a small weight are lifted so that omega lift is in [1/2, 1) and
 // softmax - onehot is held in steps of 2^-37 of the row's own scale at most, not of
 // the largest weight's; the others' steps are 2^-30 at most and need no second pass
@@ -128,8 +143,19 @@ __device__ __forceinline__ float lift_of(float omega) {
   return m > 0.0f && m < kLowest ? __uint_as_float((253 - e) << 23) : 1.0f;
 }
 __device__ __forceinline__ float inverse_of(float lift) { return __uint_as_float((254u << 23) - __float_as_uint(lift)); }
-__device__ __forceinline__ float in_f16(float x) {
-  return Vec<ZERO_F16>::get(Vec<ZERO_F16>::Raw{u32x4{Vec<ZERO_F16>::pack(x, 0.0f), 0, 0, 0}}, 0);
+template <int DT>
+__device__ __forceinline__ float rounded(float x) {  // to the type
+  return Vec<DT>::get(typename Vec<DT>::Raw{u32x4{Vec<DT>::pack(x, 0.0f), 0, 0, 0}}, 0);
+}
+template <int DT>
+__device__ __forceinline__ float in_planes(float x, uint32_t planes) {  // what one number holds of x, or two
+  const float a = rounded<DT>(x);
+  return planes == 1 ? a : a + rounded<DT>(x - a);
+}
+
+// Parts of dhidden's sums with `live` rows that count.
+__device__ __forceinline__ uint32_t splits_for(const HeadArgs& a, uint32_t live) {
+  return live ? a.splits[(a.planes * live - 1) / tile_rows(a.planes * a.rows)] : 1u;
 }
 
 // ---------------------------------------------------------------------------
@@ -173,7 +199,7 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
   if (lane == 0) most[wave] = top;
   __syncthreads();
   for (uint32_t i = 0; i < 16; ++i) top = fmaxf(top, most[i]);
-  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), before ? a.splits[(before - 1) / tile_rows(a.rows)] : 1u};
+  if (t == 0) *a.meta = Meta{before, (float)(a.coef * (double)top / kHeld), splits_for(a, before)};
   for (uint32_t i = t; i < before; i += 1024) {
     const float w = a.row_weight ? a.row_weight[a.row_of[i]] : 1.0f, omega = top > 0.0f ? w / top : w;
     a.omega[i] = omega;  // w: all weights 0 or not finite
@@ -185,12 +211,14 @@ __global__ void __launch_bounds__(1024) prepare_kernel(const HeadArgs a) {
 // counts the rows by itself (four to a thread), and block i copies the i-th
 // that counts; block 0 stores the lists.  One launch less, about 5 us.
 constexpr uint32_t kGatherRows = 4 * kBlock;
-__device__ __forceinline__ void gather_row(const HeadArgs& a, uint32_t i, uint32_t row, bool zero) {
+__device__ __forceinline__ void gather_row(const HeadArgs& a, uint32_t live, uint32_t i, uint32_t row, bool zero) {
   const uint32_t vecs = a.dim / 8;
   if (row != 0xFFFFFFFFu) {
     const u32x4* from = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.hidden) + row * a.hidden_stride);
-    u32x4* to = reinterpret_cast<u32x4*>(a.kept + (uint64_t)i * a.dim);
-    for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) to[v] = from[v];
+    for (uint32_t p = 0; p < a.planes; ++p) {
+      u32x4* to = reinterpret_cast<u32x4*>(a.kept + ((uint64_t)p * live + i) * a.dim);
+      for (uint32_t v = threadIdx.x; v < vecs; v += kBlock) to[v] = from[v];
+    }
   }
   if (zero) {
     u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.dhidden) + i * a.dhidden_stride);
@@ -255,16 +283,16 @@ __global__ void __launch_bounds__(kBlock) prepare_few_kernel(const HeadArgs a) {
     at += counts;
   }
   if (blockIdx.x == 0 && t == 0)
-    *a.meta = Meta{live, (float)(a.coef * (double)top / kHeld), live ? a.splits[(live - 1) / tile_rows(a.rows)] : 1u};
+    *a.meta = Meta{live, (float)(a.coef * (double)top / kHeld), splits_for(a, live)};
   __syncthreads();
-  gather_row(a, blockIdx.x, mine, a.dhidden && out);
+  gather_row(a, live, blockIdx.x, mine, a.dhidden && out);
 }
 
 // Block i: the i-th row that counts is copied; row i's gradient, if it does not
 // count, is zero.
 __global__ void __launch_bounds__(kBlock) gather_kernel(const HeadArgs a) {
   for (uint32_t i = blockIdx.x; i < a.rows; i += gridDim.x)
-    gather_row(a, i, i < a.meta->live ? a.row_of[i] : 0xFFFFFFFFu, a.dhidden && !a.counts[i]);
+    gather_row(a, a.meta->live, i, i < a.meta->live ? a.row_of[i] : 0xFFFFFFFFu, a.dhidden && !a.counts[i]);
 }
 
 // Tile numbers in an order that keeps a group of tiles on one XCD: each XCD
@@ -278,9 +306,9 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t mt, uint32_t nt, ui
 }
 
 // ---------------------------------------------------------------------------
-// Product one.
+// Product one.  PLANES of the exponentials are kept, in fp16.
 // ---------------------------------------------------------------------------
-template <int DT, class T, bool KEEP>
+template <int DT, class T, int PLANES>
 __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
   const uint32_t live = a.meta->live, mt = (live + T::kM - 1) / T::kM;
@@ -336,7 +364,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
         if (n == target) a.said[row] = acc[i][j][x];
         else sum += e[x];
       }
-      if constexpr (KEEP) put_quad<ZERO_F16>(lds, r, T::column(j, t), f32x4{e[0], e[1], e[2], e[3]} * kTileExp);
+      if constexpr (PLANES > 0) put_quad<ZERO_F16>(lds, r, T::column(j, t), f32x4{e[0], e[1], e[2], e[3]} * kTileExp);
     }
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
@@ -350,11 +378,34 @@ __global__ void __launch_bounds__(kGemmThreads, 2) logits_kernel(const HeadArgs 
     for (int w = 0; w < W; ++w) sum += red[(W + w) * T::kM + r];
     a.stats[(uint64_t)(tm * T::kM + r) * a.tiles + tn] = f32x2{most(r), sum};
   }
-  if constexpr (KEEP)
+  if constexpr (PLANES > 0)
     store_rows<T::kM>(lds, 256, t, [&](uint32_t m) {
       const uint32_t row = tm * T::kM + m;
       return row < live ? a.held + (uint64_t)row * a.padded + tn * 256 : nullptr;
     });
+  if constexpr (PLANES > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i) {
+      const uint32_t r = T::row(i, t);
+      const float top = most(r), m = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int j = 0; j < T::kJ; ++j) {
+        f32x4 rest;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float e = tn * 256 + T::column(j, t) + x < a.vocab ? __builtin_amdgcn_exp2f((acc[i][j][x] - m) * a.c) * kTileExp : 0.0f;
+          rest[x] = e - rounded<ZERO_F16>(e);
+        }
+        put_quad<ZERO_F16>(lds, r, T::column(j, t), rest);
+      }
+    }
+    __syncthreads();
+    store_rows<T::kM>(lds, 256, t, [&](uint32_t m) {
+      const uint32_t row = tm * T::kM + m;
+      return row < live ? a.held + ((uint64_t)live + row) * a.padded + tn * 256 : nullptr;
+    });
+  }
 }
 
 // LDS of that: the products' slots, then the exponentials and two numbers of each row and wavefront.
@@ -373,7 +424,7 @@ constexpr uint32_t logits_lds() {
 constexpr uint32_t kFewRows = 8, kFewShift = 4;
 constexpr int kFewSteps = 4;
 
-template <int DT, bool KEEP>
+template <int DT, int PLANES>
 __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
   __shared__ f32x4 share[kWavesPerBlock - 1][64];
   const uint32_t live = a.meta->live, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -423,9 +474,15 @@ __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
     if (n0 + x == target) a.said[row] = acc[x];
     else sum += e[x];
   }
-  if (KEEP && has)
-    store4<ZERO_F16>(a.held, (uint64_t)row * a.padded + n0, e[0] * kTileExp, e[1] * kTileExp, e[2] * kTileExp,
-                     e[3] * kTileExp);
+  if (PLANES > 0 && has) {
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) {
+      float y[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] = p == 0 ? e[x] * kTileExp : e[x] * kTileExp - rounded<ZERO_F16>(e[x] * kTileExp);
+      store4<ZERO_F16>(a.held, ((uint64_t)p * live + row) * a.padded + n0, y[0], y[1], y[2], y[3]);
+    }
+  }
   sum += __shfl_xor(sum, 16, 64);
   sum += __shfl_xor(sum, 32, 64);
   // the blocks behind the vocabulary only store zeros
@@ -438,9 +495,9 @@ __global__ void __launch_bounds__(kBlock) few_logits_kernel(const HeadArgs a) {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kPartTiles = 512;      // most tiles of one part
 
-template <int DT, bool KEEP>
+template <int DT, int PLANES>
 __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
-  __shared__ float scale[KEEP ? kPartTiles : 1];
+  __shared__ float scale[PLANES > 0 ? kPartTiles : 1];
   __shared__ double part[kWavesPerBlock];
   __shared__ float tops[kWavesPerBlock];
   const uint32_t t = threadIdx.x, lane = t & 63, wave = t >> 6, live = a.meta->live;
@@ -470,7 +527,7 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
       a.logp[from] = (float)lp;
       a.terms[from] = lp * (a.row_weight ? (double)a.row_weight[from] : 1.0);
     }
-    if constexpr (KEEP) {
+    if constexpr (PLANES > 0) {
       // lifted, and lowered at once where no product reads it so
       const float lift = DT == ZERO_F16 && a.lift ? a.lift[row] : 1.0f;
       const float omega = a.omega[row] * kHeld * lift;
@@ -480,11 +537,12 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
       const float down = inverse_of(lift);
       if (lower) other *= down;
       if (t == 0 && blockIdx.y == 0) {
-        const float rest = other - Vec<DT>::get(typename Vec<DT>::Raw{u32x4{Vec<DT>::pack(other, 0.0f), 0, 0, 0}}, 0);
+        const float rest = other - in_planes<DT>(other, PLANES);
         a.rest[row] = rest;
         if (a.low != a.rest) a.low[row] = rest;
       }
-      uint16_t* held = a.held + (uint64_t)row * a.padded;
+      uint16_t* const held = a.held + (uint64_t)row * a.padded;
+      uint16_t* const second = a.held + ((uint64_t)live + row) * a.padded;  // of two
       for (uint32_t first = tile0; first < tile1; first += kPartTiles) {
         const uint32_t end = min(first + kPartTiles, tile1);
         __syncthreads();
@@ -497,15 +555,24 @@ __global__ void __launch_bounds__(kBlock) softmax_kernel(const HeadArgs a) {
 #pragma unroll 4
         for (uint32_t v = v0 + t; v < v1; v += kBlock) {
           const Vec<ZERO_F16>::Raw e = load8<ZERO_F16>(held, (uint64_t)v * 8);
+          Vec<ZERO_F16>::Raw e2 = e;
+          if constexpr (PLANES > 1) e2 = load8<ZERO_F16>(second, (uint64_t)v * 8);
           const float f = scale[(v - v0) >> (a.shift - 3)];
           float x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float y = Vec<ZERO_F16>::get(e, k) * f;
-            if (lower) y = in_f16(y) * down;  // the roundings of a row that is lowered later
+            float y = Vec<ZERO_F16>::get(e, k);
+            if constexpr (PLANES > 1) y += Vec<ZERO_F16>::get(e2, k);
+            y *= f;
+            if (lower) y = in_planes<DT>(y, PLANES) * down;  // the roundings of a row that is lowered later
             x[k] = v * 8 + k == target ? other : y;
           }
           store8<DT>(held, (uint64_t)v * 8, x);
+          if constexpr (PLANES > 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] -= rounded<DT>(x[k]);
+            store8<DT>(second, (uint64_t)v * 8, x);
+          }
         }
       }
     }
@@ -538,7 +605,9 @@ __global__ void __launch_bounds__(kBlock) loss_kernel(const double* terms, const
 template <int DT, class T>
 __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) char lds[];
-  const uint32_t live = a.meta->live, splits = a.meta->splits, mt = (live + T::kM - 1) / T::kM, nt = (a.dim + 255) / 256;
+  const uint32_t live = a.planes * a.meta->live, splits = a.meta->splits;  // rows of dx
+  const uint32_t mt = (live + T::kM - 1) / T::kM, nt = (a.dim + 255) / 256;
+  const bool whole = splits == 1 && a.planes == 1;
   if (live == 0) return;
   const uint32_t steps = (a.vocab + 63) / 64, per = (steps + splits - 1) / splits;
   const uint32_t split = blockIdx.x / (mt * nt);
@@ -555,7 +624,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   clear<T>(acc);
   gemm_tile<DT, T>(p, q, split * per * 64, k_end, (lds_char*)lds, acc);
   const uint32_t t = thread_anew();
-  if (splits == 1) {  // what the targets' entries lost
+  if (whole) {  // what the targets' entries lost
 #pragma unroll
     for (int i = 0; i < T::kI; ++i) {
       const uint32_t row = tm * T::kM + T::row(i, t);
@@ -576,7 +645,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
       }
     }
   }
-  if (splits == 1) {
+  if (whole) {
     __syncthreads();
     uint16_t* out = static_cast<uint16_t*>(a.dhidden) + tn * 256;
     store_tile<DT, T>(acc, a.meta->factor, a.dim - tn * 256, lds, t, [&](uint32_t m) {
@@ -597,24 +666,24 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dhidden_kernel(const HeadArgs
   }
 }
 
-// dhidden from the sums over parts of the vocabulary, in their order, and what the
-// target's entry lost.  Lifted rows of dx are lowered for dweight's product.
+// dhidden from the sums over parts of the vocabulary and of dx's numbers, in their
+// order, and what the target's entry lost.  Lifted rows of dx are lowered for dweight's product.
 template <int DT>
 __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
-  const uint32_t live = a.meta->live, splits = a.meta->splits;
+  const uint32_t live = a.meta->live, parts = a.meta->splits * a.planes;
   const bool lower = DT == ZERO_F16 && a.lift && a.dweight;
-  if (splits <= 1 && !lower) return;
+  if (parts <= 1 && !lower) return;
   const float f = a.meta->factor;
   for (uint32_t row = blockIdx.x; row < live; row += gridDim.x) {
     const float rest = a.rest[row], lift = DT == ZERO_F16 && a.lift ? a.lift[row] : 1.0f, down = inverse_of(lift);
     const uint32_t target = a.target[row];
-    if (splits > 1) {
+    if (parts > 1) {
       const uint64_t at = a.row_of[row] * a.dhidden_stride;
       const u32x2* w = reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.weight) + target * a.weight_stride);
       for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.dim / 4; v += gridDim.y * kBlock) {
         f32x4 x = {0, 0, 0, 0};
 #pragma unroll 8
-        for (uint32_t s = 0; s < splits; ++s)
+        for (uint32_t s = 0; s < parts; ++s)
           x += *reinterpret_cast<const f32x4*>(a.part + ((uint64_t)s * live + row) * a.dim + v * 4);
         const typename Vec<DT>::Raw r = {u32x4{w[v][0], w[v][1], 0, 0}};
 #pragma unroll
@@ -626,19 +695,30 @@ __global__ void __launch_bounds__(kBlock) join_kernel(const HeadArgs a) {
     }
     if constexpr (DT == ZERO_F16) {
       if (!lower || lift == 1.0f) continue;
-      uint16_t* held = a.held + (uint64_t)row * a.padded;
+      uint16_t* const held = a.held + (uint64_t)row * a.padded;
+      uint16_t* const second = a.held + ((uint64_t)live + row) * a.padded;
       for (uint32_t v = blockIdx.y * kBlock + threadIdx.x; v < a.padded / 8; v += gridDim.y * kBlock) {
         const typename Vec<DT>::Raw e = load8<DT>(held, (uint64_t)v * 8);
         float x[8];
 #pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = Vec<DT>::get(e, k);
+        if (a.planes > 1) {
+          const typename Vec<DT>::Raw e2 = load8<DT>(second, (uint64_t)v * 8);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] += Vec<DT>::get(e2, k);
+        }
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
-          x[k] = Vec<DT>::get(e, k) * down;
-          if (v * 8 + k == target) {
-            x[k] = (Vec<DT>::get(e, k) + rest) * down;  // what the entry was
-            a.low[row] = x[k] - in_f16(x[k]);
-          }
+          if (v * 8 + k == target) x[k] += rest;  // what the entry was
+          x[k] *= down;
+          if (v * 8 + k == target) a.low[row] = x[k] - in_planes<DT>(x[k], a.planes);
         }
         store8<DT>(held, (uint64_t)v * 8, x);
+        if (a.planes > 1) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] -= rounded<DT>(x[k]);
+          store8<DT>(second, (uint64_t)v * 8, x);
+        }
       }
     }
   }
@@ -741,9 +821,10 @@ __global__ void __launch_bounds__(kGemmThreads, 2) dweight_kernel(const HeadArgs
   add_rests<DT, T>(a, live, tm, tn, lds, thread_anew(), acc);
   Columns<T::kM> p;
   Columns<256> q;
-  p.begin(a.held, (uint64_t)tm * T::kM, a.padded, a.padded, live);
-  q.begin(a.kept, (uint64_t)tn * 256, a.dim, a.dim, live);
-  gemm_tile<DT, T>(p, q, 0, live, (lds_char*)lds, acc);
+  const uint32_t rows = a.planes * live;  // of dx
+  p.begin(a.held, (uint64_t)tm * T::kM, a.padded, a.padded, rows);
+  q.begin(a.kept, (uint64_t)tn * 256, a.dim, a.dim, rows);
+  gemm_tile<DT, T>(p, q, 0, rows, (lds_char*)lds, acc);
   const uint32_t t = thread_anew();
   const float f = a.meta->factor;
   if (a.first && a.last) {
@@ -790,6 +871,8 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.shift = s.piece <= kFewRows ? kFewShift : 8;
   s.tiles = (vocab + (1u << s.shift) - 1) >> s.shift;
   const uint64_t p = s.piece, padded = (vocab + 255) / 256 * 256;
+  // rows of dx, the most of any number of rows up to p
+  const uint64_t few = std::min<uint64_t>(p, kTwoRows), held = grad ? std::max(planes_of(s.piece, dim) * p, 2 * few) : p;
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes) {
     const uint64_t here = at;
@@ -806,16 +889,17 @@ Space space_of(uint64_t n_rows, uint32_t vocab, uint32_t dim, uint32_t piece_row
   s.low = take(grad ? p * 4 : 0);
   s.terms = take(n_rows * 8);
   s.counts = take(n_rows);
-  s.kept = take(p * dim * 2);
+  s.kept = take(held * dim * 2);
   // the most of any number of rows up to p: a workspace serves fewer rows too
   s.stats = take(std::max(p * ((vocab + 255) / 256), std::min<uint64_t>(p, kFewRows) * ((vocab + 15) / 16)) * 8);
-  s.held = take(grad ? p * padded * 2 : 0);
+  s.held = take(grad ? held * padded * 2 : 0);
   uint64_t part = 0;  // dhidden's parts, for whatever number of rows counts
-  for (uint64_t rows : {(uint64_t)128, p}) {  // the last piece may be smaller, and so may a later call
-    const uint32_t t = tile_rows((uint32_t)std::min(rows, p));
-    for (uint32_t m = t; grad && m < std::min(rows, p) + t; m += t) {
+  for (uint64_t most : {(uint64_t)128, held}) {  // the last piece may be smaller, and so may a later call
+    const uint64_t rows = std::min(most, held);
+    const uint32_t t = tile_rows((uint32_t)rows);
+    for (uint32_t m = t; grad && m < rows + t; m += t) {
       const uint32_t n = splits_of(m / t, vocab, dim);
-      if (n > 1) part = std::max(part, n * std::min<uint64_t>(m, std::min(rows, p)));
+      if (n > 1 || m <= 2 * kTwoRows || dim <= kTwoDim) part = std::max(part, n * std::min<uint64_t>(m, rows));
     }
   }
   s.part = take(part * dim * 4);
@@ -848,20 +932,20 @@ void by_tile(uint32_t rows, F fn) {
   else fn(Wide{});
 }
 
-template <int DT, bool KEEP>
+template <int DT, int PLANES>
 void launch_rows(const HeadArgs& a, hipStream_t stream) {
   if (a.shift == kFewShift) {
-    hipLaunchKernelGGL((few_logits_kernel<DT, KEEP>), a.padded >> kFewShift, kBlock, 0, stream, a);
+    hipLaunchKernelGGL((few_logits_kernel<DT, PLANES>), a.padded >> kFewShift, kBlock, 0, stream, a);
   } else {
     by_tile(a.rows, [&](auto tile) {
       typedef decltype(tile) T;
-      hipLaunchKernelGGL((logits_kernel<DT, T, KEEP>), (a.rows + T::kM - 1) / T::kM * a.tiles, kGemmThreads, logits_lds<T>(),
+      hipLaunchKernelGGL((logits_kernel<DT, T, PLANES>), (a.rows + T::kM - 1) / T::kM * a.tiles, kGemmThreads, logits_lds<T>(),
                          stream, a);
     });
   }
   // with few rows, parts of them: 1024 blocks, of 2048 columns at least
-  const uint32_t parts = KEEP ? std::min((a.padded + 2047) / 2048, std::max(1024 / a.rows, 1u)) : 1;
-  hipLaunchKernelGGL((softmax_kernel<DT, KEEP>), dim3(a.rows, parts), kBlock, 0, stream, a);
+  const uint32_t parts = PLANES > 0 ? std::min((a.padded + 2047) / 2048, std::max(1024 / a.rows, 1u)) : 1;
+  hipLaunchKernelGGL((softmax_kernel<DT, PLANES>), dim3(a.rows, parts), kBlock, 0, stream, a);
 }
 
 template <int DT>
@@ -872,9 +956,9 @@ void launch_dweight(const HeadArgs& a, hipStream_t stream) {
 
 template <int DT>
 void launch_piece(HeadArgs a, bool grad, hipStream_t stream) {
-  const uint32_t nt = (a.dim + 255) / 256;
+  const uint32_t nt = (a.dim + 255) / 256, rows = a.planes * a.rows;
   uint32_t blocks = 0;  // the most that dhidden's product has, whatever number of rows counts
-  for (uint32_t i = 0; grad && i * tile_rows(a.rows) < a.rows; ++i) {
+  for (uint32_t i = 0; grad && i * tile_rows(rows) < rows; ++i) {
     a.splits[i] = (uint8_t)splits_of(i + 1, a.vocab, a.dim);
     blocks = std::max(blocks, (i + 1) * nt * a.splits[i]);
   }
@@ -884,10 +968,11 @@ void launch_piece(HeadArgs a, bool grad, hipStream_t stream) {
     hipLaunchKernelGGL(prepare_kernel, 1, 1024, 0, stream, a);
     hipLaunchKernelGGL(gather_kernel, a.rows, kBlock, 0, stream, a);
   }
-  if (!grad) return launch_rows<DT, false>(a, stream);
-  launch_rows<DT, true>(a, stream);
+  if (!grad) return launch_rows<DT, 0>(a, stream);
+  if (a.planes == 2) launch_rows<DT, 2>(a, stream);
+  else launch_rows<DT, 1>(a, stream);
   if (a.dhidden) {
-    by_tile(a.rows, [&](auto tile) {
+    by_tile(rows, [&](auto tile) {
       typedef decltype(tile) T;
       hipLaunchKernelGGL((dhidden_kernel<DT, T>), blocks, kGemmThreads, T::kLds, stream, a);
     });
@@ -984,6 +1069,7 @@ extern "C" int zero_linear_cross_entropy(const zero_linear_cross_entropy_args* p
     a.rows = (uint32_t)std::min<uint64_t>(s.piece, p->n_rows - row);
     a.first = row == 0;
     a.last = row + a.rows == p->n_rows;
+    a.planes = grad ? planes_of(a.rows, a.dim) : 1;
     a.hidden = static_cast<const uint16_t*>(p->hidden) + row * p->hidden_stride;
     a.targets = p->targets + row;
     a.row_weight = p->row_weight ? p->row_weight + row : nullptr;
