@@ -188,3 +188,29 @@ def test_small_heads_in_two_numbers(n, v, d, dt, weighted, piece):
         want = m @ a
         tol = o @ a.abs() + 2 * (2 * k / 32 + 70) * U * (m.abs() @ a.abs())
         emb.within(g, want, tol + (eps / 2) * (want.abs() + tol) + head.SUB[dt])
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("d", [1, 2, 3, 9])
+def test_norm_of_few_columns_cancels_what_cancels(d, keep):
+    """With one column n = h rstd is near 1 and dx = rstd dy gain (1 - n^2) far less than its two
+    terms, so that e = dy gain has to be the same number in both: as fp32 has n and e, dx is off by
+    the roundings of up to 8 sums of e n (fused: u each of their magnitudes), of the mean (u; of
+    one column none) and by 3 u of itself (the difference is fused)."""
+    n = 4000
+    g = torch.Generator().manual_seed(d)
+    x, dy, gain = (torch.randn(*s, generator=g).to(DEV) for s in ((n, d), (n, d), (d,)))
+    rstd = torch.empty(n, device=DEV)
+    codes, scales = torch.empty(n, d, dtype=torch.float8_e4m3fn, device=DEV), torch.empty(n, 1, device=DEV)
+    zs.zero_rms_norm(x, gain, torch.empty_like(x), rstd=rstd, codes=codes, scales=scales)
+    held = dict(codes=codes, scales=scales) if keep else dict(h=x)
+    dx, dgain = torch.empty_like(x), torch.empty_like(gain)
+    zs.zero_rms_norm_backward(dy, gain, rstd, dx, dgain, workspace=zs.rms_norm_workspace(n, d), **held)
+    # from what the kernel reads, with n and dy gain as fp32 has them, the rest in 64 bits
+    h = codes.float() * scales if keep else x
+    norm, e = (h * rstd[:, None]).double(), (dy * gain).double()
+    r = rstd.double()[:, None]
+    m = (e * norm).mean(1, keepdim=True)
+    want = r * (e - norm * m)
+    tol = U * r * norm.abs() * ((e * norm).abs().mean(1, keepdim=True) * min(d, 8) + (m.abs() if d > 1 else 0)) + 3 * U * want.abs()
+    emb.within(dx, want.cpu(), tol.cpu() + 2.0 ** -150)

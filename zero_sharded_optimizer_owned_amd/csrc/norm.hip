@@ -284,9 +284,9 @@ __global__ void __launch_bounds__((Group<W, VPT>::kThreads)) backward_kernel(con
       x.normalised(i, n);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float q = Lane<DT>::get(x.d[i], k) * n[k];
+        const float d = Lane<DT>::get(x.d[i], k), q = d * n[k];
         dg[i][k] += has ? q : 0.0f;
-        p = fmaf(q, Lane<DT>::get(gain, k), p);
+        p = fmaf(d * Lane<DT>::get(gain, k), n[k], p);  // dn as below: in few columns the two cancel
       }
       sum += (double)p;
     }
