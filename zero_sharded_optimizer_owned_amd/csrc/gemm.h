@@ -22,7 +22,7 @@
 // consecutive n of one m.
 //
 // Measured in a training step of 6962 rows that count, 128,000 x 4096, bf16 (7.3
-// TFLOP each): logits 6.2 ms, dhidden 5.8, dweight 6.4, 1.15 to 1.25 PFLOP/s, the
+// TFLOP each): logits 6.2 to 6.4 ms, dhidden 5.8, dweight 6.4, 1.15 to 1.25 PFLOP/s, the
 // matrix cores busy in 56 to 64% of the cycles (a library product of the first
 // shape alone: 1.43).  What bounds it is the way of the tiles into LDS, 64 KB a
 // step: in scores of 4096 such rows an earlier form took 3.21 ms, 2.94 with half of

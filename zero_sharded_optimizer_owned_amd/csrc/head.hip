@@ -34,8 +34,9 @@
 // between the first product and dx, have 11 bits so as not to take twice that room and
 // time.  Sums, maxima, log-probabilities and the loss have 32 or 64.
 //
-// That step takes 19.2 ms: the products 18.4, softmax 0.72 (3.6 GB read and written,
-// 5.0 TB/s), the join of dhidden's parts 0.11, the rest 0.06.
+// That step takes 19.2 to 20.7 ms from card to card: of 19.2 the products 18.4, softmax
+// 0.72 (3.6 GB read and written, 5.0 TB/s), the join of dhidden's parts 0.11, the rest
+// 0.06.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
