@@ -736,7 +736,9 @@ extern "C" int zero_embedding_grad(const zero_embedding_grad_args* p, hipStream_
   g.tile = s.tile;
   // Alone, one block's sort takes longer than several blocks' passes from some 10,000
   // tokens on (onto a gradient: 8192 tokens 58 us and 61, 16,384 tokens 115 and 103);
-  // beside the zeros it costs nothing (16,384 tokens of 128,000 x 4096 258 and 274).
+  // beside the zeros, which several passes have a launch of their own for, it is no
+  // slower at any size (16,384 tokens of 128,000 x 4096 258 and 274, of 128,000 x 64 66
+  // and 74, of 18,397 x 1 68 both ways; 8193 tokens of that 53 and 64).
   const bool one = g.n > 0 && g.n <= (g.accumulate ? kOneSort / 2 : kOneSort);
   if (g.n > 0) {
     // keys are 0 .. vocab: passes of equal width, 9 bits at most
