@@ -214,3 +214,51 @@ def test_norm_of_few_columns_cancels_what_cancels(d, keep):
     want = r * (e - norm * m)
     tol = U * r * norm.abs() * ((e * norm).abs().mean(1, keepdim=True) * min(d, 8) + (m.abs() if d > 1 else 0)) + 3 * U * want.abs()
     emb.within(dx, want.cpu(), tol.cpu() + 2.0 ** -150)
+
+
+@pytest.mark.parametrize("n, d", [(40, 136), (300, 136), (300, 8)])
+def test_rows_of_small_weight_captured_and_on_two_streams(n, d):
+    """fp16 with lifted rows, in one number and in two: a graph replayed with eager calls between
+    and other inputs, and two calls at once in a workspace each, to the bit."""
+    v = 5001
+    h, w, t, weight = head.problem(n, v, d, "f16")
+    weight *= torch.where(torch.arange(n, device=DEV) % 2 == 0, 1.0, 2.0 ** -14)
+
+    def buffers():
+        return (torch.zeros(2, device=DEV), torch.zeros(n, device=DEV), torch.zeros_like(h), torch.zeros_like(w),
+                zs.linear_cross_entropy_workspace(n, v, d))
+
+    def call(b, x):
+        zs.zero_linear_cross_entropy(x, w, t, row_weight=weight, divisor=2.0, grad_scale=2.0 ** 9, stats=b[0], logp=b[1],
+                                     dhidden=b[2], dweight=b[3], workspace=b[4])
+
+    eager, held, other = buffers(), buffers(), buffers()
+    call(held, h)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(held, h)
+    for _ in range(3):
+        for x in held[:4]:
+            x.zero_()
+        graph.replay()
+        call(eager, h)
+        torch.cuda.synchronize()
+        for a, b in zip(held[:4], eager[:4]):
+            assert torch.equal(a, b)
+        h.mul_(0.9)
+    h2 = h * 0.5
+    call(eager, h2)
+    want = [x.clone() for x in eager[:4]]
+    call(eager, h)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for s, b, x in zip(streams, (held, other), (h, h2)):
+            with torch.cuda.stream(s):
+                call(b, x)
+    torch.cuda.synchronize()
+    for a, b in zip(held[:4], eager[:4]):
+        assert torch.equal(a, b)
+    for a, b in zip(other[:4], want):
+        assert torch.equal(a, b)
